@@ -328,6 +328,39 @@ nf_status nf_layernorm_bwd_noalloc(void* dx, float* dgamma, float* dbeta, const 
                                    const void* gamma, int64_t rows, int64_t hidden,
                                    nf_stream stream);
 
+/* Largest hidden size of the operators with an 8-bit output. */
+#define NF_Q8_MAX_HIDDEN 32768
+
+/* 8-bit formats.  E4M3: 3 mantissa bits, largest value 448.  INT8: two's
+ * complement, -127 to 127. */
+typedef enum { NF_Q8_E4M3 = 0, NF_Q8_INT8 = 1 } nf_q8_format;
+
+/* RMSNorm forward, and the fused residual add + RMSNorm, with an 8-bit
+ * output and its scales: the normalized rows as a product in 8 bits reads
+ * them.  The source pages have no counterpart; the operator is
+ * nf_rmsnorm_fwd / nf_fused_add_rmsnorm with the quantization of its output
+ * in the same pass.  For each row r:
+ *     s_j      = x[r][j]                                  (nf_rmsnorm_q8)
+ *     s_j      = x[r][j] + residual[r][j]; residual[r][j] <- bf16(s_j)   (fused)
+ *     y_j      = s_j * rsqrt(mean_k(s_k^2) + eps) * weight[j]            (fp32)
+ *     scale    = max(max_j |y_j| / Q, 2^-100),  Q = 448 (E4M3) or 127 (INT8)
+ *     q[r][j]  = y_j / scale, rounded to nearest, ties to even
+ * so q * scale stands for y.  group = 0: one scale per row, scale is [rows]
+ * fp32.  group = 128: one scale per 128 columns (the last group may be
+ * shorter), scale is [rows, ceil(hidden / 128)] fp32.  y is not rounded to
+ * bf16 before it is quantized.  A scale whose largest |y| is not finite is
+ * not finite either, and its q are 0; a row whose sum of squares is not
+ * finite in fp32 (a NaN, an infinity, magnitudes beyond about 1e19) has NaN
+ * for every scale.  x is only read; nothing may overlap.  q: [rows, hidden]
+ * bytes, 8-byte aligned; scale 4-byte aligned.  hidden: a multiple of 8 up
+ * to NF_Q8_MAX_HIDDEN.  rows == 0 returns NF_OK.  No workspace. */
+nf_status nf_rmsnorm_q8(void* q, float* scale, const void* x, const void* weight, int64_t rows,
+                        int64_t hidden, float eps, nf_q8_format format, int64_t group,
+                        nf_stream stream);
+nf_status nf_fused_add_rmsnorm_q8(void* q, float* scale, const void* x, void* residual,
+                                  const void* weight, int64_t rows, int64_t hidden, float eps,
+                                  nf_q8_format format, int64_t group, nf_stream stream);
+
 /* Outer normalization: the statistics run down the columns, over the rows
  * (batch normalization of a [rows, hidden] matrix in training mode; the
  * "Llu/ln bwd" discussion lists block- and grid-parallel outer

@@ -48,7 +48,12 @@ DYN_MAX_HIDDEN_BWD = 16384
 LONG_MAX_HIDDEN_FWD = 262144  # grid-parallel cluster path for longer rows
 LONG_MAX_HIDDEN_BWD = 131072
 SPLIT_MAX_HIDDEN = 1 << 26    # NF_SPLIT_MAX_HIDDEN: rows across any number of CTAs
+Q8_MAX_HIDDEN = 32768         # NF_Q8_MAX_HIDDEN: rows with an 8-bit output
 GRID_MAX_ROWS = 8             # the grid family (rows held on chip) takes 1 to 8 rows
+
+NF_Q8_E4M3, NF_Q8_INT8 = 0, 1
+Q8_FORMATS = {"e4m3": NF_Q8_E4M3, "int8": NF_Q8_INT8}
+Q8_GROUP = 128                # columns per scale of the grouped 8-bit output
 
 # Every symbol include/nf.h declares.
 EXPORTS = (
@@ -58,6 +63,7 @@ EXPORTS = (
     "nf_outer_norm_workspace_size", "nf_outer_norm_fwd", "nf_outer_norm_bwd",
     "nf_fused_add_rmsnorm_bwd", "nf_workspace_size", "nf_fused_add_rmsnorm_ws", "nf_rmsnorm_fwd_ws",
     "nf_layernorm_fwd_ws",
+    "nf_rmsnorm_q8", "nf_fused_add_rmsnorm_q8",
     "nf_set_path", "nf_plan_query", "nf_plan_compute", "nf_get_device_status",
     "nf_selftest_wait_timeout", "nf_selftest_grid_timeout", "nf_selftest_floor", "nf_status_string",
     "nf_version",
@@ -109,6 +115,8 @@ def _bind(lib):
         "nf_fused_add_rmsnorm_bwd": (_S, [_P, _P, _P, _P, _P, _P, _I64, _I64, _F, _P, ctypes.c_size_t, _P]),
         "nf_outer_norm_fwd": (_S, [_P, _P, _P, _P, _P, _P, _I64, _I64, _F, _P, ctypes.c_size_t, _P]),
         "nf_outer_norm_bwd": (_S, [_P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _P, ctypes.c_size_t, _P]),
+        "nf_rmsnorm_q8": (_S, [_P, _P, _P, _P, _I64, _I64, _F, _S, _I64, _P]),
+        "nf_fused_add_rmsnorm_q8": (_S, [_P, _P, _P, _P, _P, _I64, _I64, _F, _S, _I64, _P]),
         "nf_set_path": (_S, [_S]),
         "nf_plan_query": (_S, [_S, _I64, _I64, ctypes.POINTER(Plan)]),
         "nf_plan_compute": (_S, [_S, _I64, _I64, ctypes.c_int32, _S, ctypes.POINTER(Plan)]),
@@ -231,6 +239,16 @@ def nf_outer_norm_bwd(dx, dgamma, dbeta, dy, x, mean, rstd, gamma, rows, hidden,
                       workspace_bytes, stream) -> int:
     return lib().nf_outer_norm_bwd(dx, dgamma, dbeta, dy, x, mean, rstd, gamma, rows, hidden,
                                    workspace, workspace_bytes, stream)
+
+
+def nf_rmsnorm_q8(q, scale, x, weight, rows, hidden, eps, format, group, stream) -> int:
+    return lib().nf_rmsnorm_q8(q, scale, x, weight, rows, hidden, eps, format, group, stream)
+
+
+def nf_fused_add_rmsnorm_q8(q, scale, x, residual, weight, rows, hidden, eps, format, group,
+                            stream) -> int:
+    return lib().nf_fused_add_rmsnorm_q8(q, scale, x, residual, weight, rows, hidden, eps, format,
+                                         group, stream)
 
 
 def nf_set_path(path) -> int:
@@ -469,6 +487,85 @@ def outer_norm_bwd(dy, x, mean, rstd, gamma, workspace=None, out=None, stream=No
                              workspace.numel() * workspace.element_size(), _stream(stream)),
            "nf_outer_norm_bwd")
     return dx, dgamma, dbeta
+
+
+def _same_device(first, *rest):
+    """The tensors lie on the current device, whose stream and context the call uses."""
+    import torch
+    dev = first.get_device()
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"tensors are on cuda:{dev}, which is not the current device")
+    for t in rest:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("tensors are on different devices")
+
+
+def _q8_outputs(x, rows, hidden, fmt, group, out, scale):
+    import torch
+    if fmt not in Q8_FORMATS:
+        raise ValueError(f"fmt must be one of {tuple(Q8_FORMATS)}, got {fmt!r}")
+    if group not in (0, Q8_GROUP):
+        raise ValueError(f"group must be 0 (one scale per row) or {Q8_GROUP}, got {group!r}")
+    dtype = torch.float8_e4m3fn if fmt == "e4m3" else torch.int8
+    shape = x.shape[:-1] + (-(-hidden // group),) if group else x.shape[:-1]
+    if out is None:
+        out = torch.empty(x.shape, dtype=dtype, device=x.device)
+    else:
+        _need(out, dtype, "out")
+        if out.shape != x.shape:
+            raise ValueError("out must have x's shape")
+    if scale is None:
+        scale = torch.empty(shape, dtype=torch.float32, device=x.device)
+    else:
+        _need(scale, torch.float32, "scale")
+        if scale.shape != shape:
+            raise ValueError(f"scale must be of shape {tuple(shape)}")
+    return out, scale
+
+
+def rmsnorm_q8(x, weight, eps: float = 1e-6, fmt: str = "e4m3", group: int = 0, out=None,
+               scale=None, stream=None):
+    """RMSNorm with an 8-bit output.  Returns (q, scale): q of x's shape in
+    float8_e4m3fn or int8 (fmt), scale fp32 of shape [...] (one per row) or
+    [..., ceil(hidden / 128)] (group=128); q * scale stands for the
+    normalized rows, which are not rounded to bf16 in between."""
+    import torch
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return rmsnorm_q8(x, weight, eps, fmt, group, out, scale)
+    _need(x, torch.bfloat16, "x")
+    _need(weight, torch.bfloat16, "weight")
+    rows, hidden = _rows_hidden(x)
+    if weight.shape != (hidden,):
+        raise ValueError("shape mismatch")
+    q, scale = _q8_outputs(x, rows, hidden, fmt, group, out, scale)
+    _same_device(x, weight, q, scale)
+    _check(nf_rmsnorm_q8(q.data_ptr(), scale.data_ptr(), x.data_ptr(), weight.data_ptr(), rows,
+                         hidden, eps, Q8_FORMATS[fmt], group, _stream()), "nf_rmsnorm_q8")
+    return q, scale
+
+
+def fused_add_rmsnorm_q8(x, residual, weight, eps: float = 1e-6, fmt: str = "e4m3",
+                         group: int = 0, out=None, scale=None, stream=None):
+    """residual += x in place; returns (q, scale) of rmsnorm(residual) * weight
+    as rmsnorm_q8 does (from the fp32 sums, as fused_add_rmsnorm).  x is left
+    as it was."""
+    import torch
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return fused_add_rmsnorm_q8(x, residual, weight, eps, fmt, group, out, scale)
+    for t, n in ((x, "x"), (residual, "residual"), (weight, "weight")):
+        _need(t, torch.bfloat16, n)
+    rows, hidden = _rows_hidden(x)
+    if residual.shape != x.shape or weight.shape != (hidden,):
+        raise ValueError("shape mismatch")
+    q, scale = _q8_outputs(x, rows, hidden, fmt, group, out, scale)
+    _same_device(x, residual, weight, q, scale)
+    _check(nf_fused_add_rmsnorm_q8(q.data_ptr(), scale.data_ptr(), x.data_ptr(),
+                                   residual.data_ptr(), weight.data_ptr(), rows, hidden, eps,
+                                   Q8_FORMATS[fmt], group, _stream()),
+           "nf_fused_add_rmsnorm_q8")
+    return q, scale
 
 
 def set_path(path):

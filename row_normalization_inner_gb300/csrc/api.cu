@@ -100,19 +100,6 @@ nf_status current_device(int* dev) {
     return NF_OK;
 }
 
-nf_status device_sm_count(int* sms) {
-    int dev;
-    if (nf_status st = current_device(&dev)) return st;
-    int v = g_sm_count[dev].load(std::memory_order_relaxed);
-    if (v <= 0) {
-        if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || v <= 0)
-            return NF_ERR_CUDA;
-        g_sm_count[dev].store(v, std::memory_order_relaxed);
-    }
-    *sms = v;
-    return NF_OK;
-}
-
 nf_status device_status_addr(int** addr) {
     int dev;
     if (nf_status st = current_device(&dev)) return st;
@@ -142,25 +129,6 @@ bool hidden_supported(nf_op op, int64_t h) {
     return hidden_ok(h) || dyn_shape(op, h, &t) || long_shape(op, h, &c, &t, &sl) || split_ok(h);
 }
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-struct Span {
-    const void* p;
-    int64_t bytes;
-};
-
-bool overlap(Span a, Span b) {
-    if (!a.p || !b.p || a.bytes <= 0 || b.bytes <= 0) return false;
-    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
-    return a0 < b0 + static_cast<uintptr_t>(b.bytes) && b0 < a0 + static_cast<uintptr_t>(a.bytes);
-}
-
-// Overlap allowed only as the exact same buffer.
-bool bad_overlap_except_alias(Span out, Span in) {
-    if (out.p == in.p && out.bytes == in.bytes) return false;
-    return overlap(out, in);
-}
-
 nf_status common_checks(nf_op op, int64_t rows, int64_t hidden, float eps, bool check_eps) {
     if (!hidden_supported(op, hidden)) return NF_ERR_UNSUPPORTED_HIDDEN;
     if (rows < 0) return NF_ERR_INVALID_ARG;
@@ -169,8 +137,6 @@ nf_status common_checks(nf_op op, int64_t rows, int64_t hidden, float eps, bool 
     if (check_eps && !(std::isfinite(eps) && eps > 0.f)) return NF_ERR_INVALID_ARG;
     return NF_OK;
 }
-
-nf_status from_cuda(cudaError_t e) { return e == cudaSuccess ? NF_OK : NF_ERR_CUDA; }
 
 // The split and grid families: the launch of a planned call.
 nf_status launch_split_family(const nf_plan& pl, nf_op op, const DynArgs& a, void* workspace,
@@ -283,6 +249,20 @@ floor_copy_kernel(uint4* __restrict__ dst, const uint4* __restrict__ src, int64_
 }
 
 }  // namespace
+
+// (declared in internal.h)
+nf_status device_sm_count(int* sms) {
+    int dev;
+    if (nf_status st = current_device(&dev)) return st;
+    int v = g_sm_count[dev].load(std::memory_order_relaxed);
+    if (v <= 0) {
+        if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || v <= 0)
+            return NF_ERR_CUDA;
+        g_sm_count[dev].store(v, std::memory_order_relaxed);
+    }
+    *sms = v;
+    return NF_OK;
+}
 
 size_t plan_workspace_bytes(int op, int64_t rows, int64_t hidden, int sms, int path, int partials) {
     if (path == NF_PATH_SPLIT) return split_workspace_bytes(op, rows, hidden, sms);

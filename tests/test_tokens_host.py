@@ -1,0 +1,65 @@
+"""Host-side tests of the token-side operators' entry points (no GPU needed):
+every argument is checked before anything is launched."""
+import pytest
+import torch
+
+import row_normalization_inner_gb300 as nf
+
+# Fake, never dereferenced addresses, far enough apart for the sizes below;
+# every call returns from argument validation.
+A, B, C, D, E = (k << 36 for k in range(1, 6))
+BIG = 1 << 62
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from row_normalization_inner_gb300 import build
+    build.build()
+    yield
+
+
+# ---------------------------------------------------------------- 8-bit RMSNorm
+
+def q8(q=A, scale=B, x=C, w=D, rows=4, hidden=256, eps=1e-6, fmt=0, group=0):
+    return nf.nf_rmsnorm_q8(q, scale, x, w, rows, hidden, eps, fmt, group, None)
+
+
+def fused_q8(q=A, scale=B, x=C, res=E, w=D, rows=4, hidden=256, eps=1e-6, fmt=0, group=0):
+    return nf.nf_fused_add_rmsnorm_q8(q, scale, x, res, w, rows, hidden, eps, fmt, group, None)
+
+
+@pytest.mark.parametrize("call", [q8, fused_q8])
+def test_q8_refusals(call):
+    for hidden in (0, 4, 12, -8, 4095, nf.Q8_MAX_HIDDEN + 8):
+        assert call(hidden=hidden) == nf.NF_ERR_UNSUPPORTED_HIDDEN
+    for bad in ({"rows": -1}, {"rows": BIG}, {"eps": 0.0}, {"eps": -1.0}, {"eps": float("nan")},
+                {"eps": float("inf")}, {"fmt": 2}, {"fmt": -1}, {"group": 64}, {"group": -128},
+                {"q": None}, {"scale": None}, {"x": None}, {"w": None}):
+        assert call(**bad) == nf.NF_ERR_INVALID_ARG, bad
+    for bad in ({"q": A + 4}, {"scale": B + 2}, {"x": C + 8}, {"w": D + 2}):
+        assert call(**bad) == nf.NF_ERR_MISALIGNED, bad
+    # nothing may overlap
+    for bad in ({"q": C}, {"q": C + 4 * 256 * 2 - 8}, {"scale": C + 16}, {"scale": A + 4 * 256 - 4},
+                {"q": D}, {"scale": D + 8}):
+        assert call(**bad) == nf.NF_ERR_INVALID_ARG, bad
+    # group scales: 2 per row
+    assert call(scale=A - 4 * 2 * 4 + 4, group=128) == nf.NF_ERR_INVALID_ARG
+    assert call(rows=0, q=None, scale=None, x=None, w=None) == nf.NF_OK
+
+
+def test_q8_fused_residual_refusals():
+    assert fused_q8(res=None) == nf.NF_ERR_INVALID_ARG
+    assert fused_q8(res=E + 2) == nf.NF_ERR_MISALIGNED
+    for res in (C, C + 16, A, D, B):
+        assert fused_q8(res=res) == nf.NF_ERR_INVALID_ARG
+
+
+def test_q8_helper_refusals():
+    x = torch.zeros(2, 64, dtype=torch.bfloat16)
+    w = torch.zeros(64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="CUDA"):
+        nf.rmsnorm_q8(x, w)
+    with pytest.raises(TypeError):
+        nf.rmsnorm_q8(x.float(), w)
+    with pytest.raises(TypeError):
+        nf.fused_add_rmsnorm_q8(None, x, w)
