@@ -361,6 +361,36 @@ nf_status nf_fused_add_rmsnorm_q8(void* q, float* scale, const void* x, void* re
                                   const void* weight, int64_t rows, int64_t hidden, float eps,
                                   nf_q8_format format, int64_t group, nf_stream stream);
 
+/* Element types of the operators that take more than one. */
+typedef enum { NF_BF16 = 0, NF_F32 = 1 } nf_dtype;
+
+/* Embedding lookup with scaling, the rows a residual stream starts from:
+ *     y[i][j] = bf16( scale * table[ids[i]][j] ),   i < tokens, j < hidden
+ * An id outside [0, vocab) (padding) gives a row of zeros.  ids: int32
+ * (id_bytes 4) or int64 (id_bytes 8).  table: [vocab, hidden] bf16, y:
+ * [tokens, hidden] bf16.  hidden: a multiple of 8 up to 2^20; tokens below
+ * 2^31; vocab 1 to 2^30; scale finite.  y overlaps nothing. */
+nf_status nf_embedding_fwd(void* y, const void* ids, int32_t id_bytes, const void* table, int64_t tokens,
+                           int64_t vocab, int64_t hidden, float scale, nf_stream stream);
+
+/* Gradient of the lookup, by sorted tokens:
+ *     g[v][j] = scale * sum over { i : ids[i] = v } of dy[i][j]          (fp32, in token order)
+ *     dtable = g (accumulate 0: every row is written, those without tokens
+ *     with zeros), or dtable += g (accumulate 1: only rows with tokens are
+ *     touched).  Ids outside [0, vocab) contribute nothing.
+ * dtable: [vocab, hidden], NF_F32 or NF_BF16; bf16 sums are rounded once, at
+ * the end.  The tokens are sorted by id in the workspace (16-byte aligned,
+ * at least nf_embedding_bwd_workspace_size(tokens, hidden) bytes on the
+ * device that runs the call, contents irrelevant) and equal ids are summed
+ * in a fixed order, so results are deterministic; how many ids coincide
+ * changes neither the launches nor the workspace.  Sizes as for the lookup.
+ * Nothing may overlap.  tokens == 0 reads nothing (dy, ids and workspace may
+ * be NULL) and, with accumulate 0, writes zeros. */
+size_t nf_embedding_bwd_workspace_size(int64_t tokens, int64_t hidden);
+nf_status nf_embedding_bwd(void* dtable, nf_dtype dtable_type, int32_t accumulate, const void* dy,
+                           const void* ids, int32_t id_bytes, int64_t tokens, int64_t vocab, int64_t hidden,
+                           float scale, void* workspace, size_t workspace_bytes, nf_stream stream);
+
 /* Outer normalization: the statistics run down the columns, over the rows
  * (batch normalization of a [rows, hidden] matrix in training mode; the
  * "Llu/ln bwd" discussion lists block- and grid-parallel outer

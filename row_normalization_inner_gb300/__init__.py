@@ -55,6 +55,8 @@ NF_Q8_E4M3, NF_Q8_INT8 = 0, 1
 Q8_FORMATS = {"e4m3": NF_Q8_E4M3, "int8": NF_Q8_INT8}
 Q8_GROUP = 128                # columns per scale of the grouped 8-bit output
 
+NF_BF16, NF_F32 = 0, 1        # nf_dtype
+
 # Every symbol include/nf.h declares.
 EXPORTS = (
     "nf_fused_add_rmsnorm", "nf_rmsnorm_fwd", "nf_layernorm_fwd",
@@ -64,6 +66,7 @@ EXPORTS = (
     "nf_fused_add_rmsnorm_bwd", "nf_workspace_size", "nf_fused_add_rmsnorm_ws", "nf_rmsnorm_fwd_ws",
     "nf_layernorm_fwd_ws",
     "nf_rmsnorm_q8", "nf_fused_add_rmsnorm_q8",
+    "nf_embedding_fwd", "nf_embedding_bwd_workspace_size", "nf_embedding_bwd",
     "nf_set_path", "nf_plan_query", "nf_plan_compute", "nf_get_device_status",
     "nf_selftest_wait_timeout", "nf_selftest_grid_timeout", "nf_selftest_floor", "nf_status_string",
     "nf_version",
@@ -117,6 +120,9 @@ def _bind(lib):
         "nf_outer_norm_bwd": (_S, [_P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _P, ctypes.c_size_t, _P]),
         "nf_rmsnorm_q8": (_S, [_P, _P, _P, _P, _I64, _I64, _F, _S, _I64, _P]),
         "nf_fused_add_rmsnorm_q8": (_S, [_P, _P, _P, _P, _P, _I64, _I64, _F, _S, _I64, _P]),
+        "nf_embedding_fwd": (_S, [_P, _P, _S, _P, _I64, _I64, _I64, _F, _P]),
+        "nf_embedding_bwd_workspace_size": (ctypes.c_size_t, [_I64, _I64]),
+        "nf_embedding_bwd": (_S, [_P, _S, _S, _P, _P, _S, _I64, _I64, _I64, _F, _P, ctypes.c_size_t, _P]),
         "nf_set_path": (_S, [_S]),
         "nf_plan_query": (_S, [_S, _I64, _I64, ctypes.POINTER(Plan)]),
         "nf_plan_compute": (_S, [_S, _I64, _I64, ctypes.c_int32, _S, ctypes.POINTER(Plan)]),
@@ -249,6 +255,20 @@ def nf_fused_add_rmsnorm_q8(q, scale, x, residual, weight, rows, hidden, eps, fo
                             stream) -> int:
     return lib().nf_fused_add_rmsnorm_q8(q, scale, x, residual, weight, rows, hidden, eps, format,
                                          group, stream)
+
+
+def nf_embedding_fwd(y, ids, id_bytes, table, tokens, vocab, hidden, scale, stream) -> int:
+    return lib().nf_embedding_fwd(y, ids, id_bytes, table, tokens, vocab, hidden, scale, stream)
+
+
+def nf_embedding_bwd_workspace_size(tokens, hidden) -> int:
+    return lib().nf_embedding_bwd_workspace_size(tokens, hidden)
+
+
+def nf_embedding_bwd(dtable, dtable_type, accumulate, dy, ids, id_bytes, tokens, vocab, hidden, scale,
+                     workspace, workspace_bytes, stream) -> int:
+    return lib().nf_embedding_bwd(dtable, dtable_type, accumulate, dy, ids, id_bytes, tokens, vocab,
+                                  hidden, scale, workspace, workspace_bytes, stream)
 
 
 def nf_set_path(path) -> int:
@@ -566,6 +586,81 @@ def fused_add_rmsnorm_q8(x, residual, weight, eps: float = 1e-6, fmt: str = "e4m
                                    Q8_FORMATS[fmt], group, _stream()),
            "nf_fused_add_rmsnorm_q8")
     return q, scale
+
+
+def _need_ids(ids, name):
+    """Bytes per id of a contiguous int32 / int64 CUDA tensor."""
+    import torch
+    if not isinstance(ids, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if ids.dtype not in (torch.int64, torch.int32):
+        raise TypeError(f"{name} must be torch.int32 or torch.int64, got {ids.dtype}")
+    _need(ids, ids.dtype, name)
+    return 8 if ids.dtype == torch.int64 else 4
+
+
+def embedding_fwd(ids, table, scale: float = 1.0, out=None, stream=None):
+    """scale * table[ids], rounded to bf16: a tensor of shape [*ids.shape, hidden].
+    ids int32 or int64; an id outside [0, vocab) gives a row of zeros."""
+    import torch
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return embedding_fwd(ids, table, scale, out)
+    id_bytes = _need_ids(ids, "ids")
+    _need(table, torch.bfloat16, "table")
+    if table.dim() != 2:
+        raise ValueError("table must be [vocab, hidden]")
+    vocab, hidden = table.shape
+    shape = ids.shape + (hidden,)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=table.device)
+    else:
+        _need(out, torch.bfloat16, "out")
+        if out.shape != shape:
+            raise ValueError(f"out must be of shape {tuple(shape)}")
+    _same_device(table, ids, out)
+    _check(nf_embedding_fwd(out.data_ptr(), ids.data_ptr(), id_bytes, table.data_ptr(), ids.numel(),
+                            vocab, hidden, scale, _stream()), "nf_embedding_fwd")
+    return out
+
+
+def embedding_bwd(dy, ids, vocab: int, scale: float = 1.0, dtype=None, accumulate=None, out=None,
+                  workspace=None, stream=None):
+    """Gradient of embedding_fwd for its table: [vocab, hidden], fp32 or bf16
+    (dtype, fp32 unless given), the rows without tokens zero; or, with
+    accumulate (a gradient of that shape), that tensor with the sums added in
+    place.  Equal ids are summed in fp32 in token order: the result is
+    deterministic.  The workspace (nf_embedding_bwd_workspace_size bytes) is
+    allocated here when not given."""
+    import torch
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return embedding_bwd(dy, ids, vocab, scale, dtype, accumulate, out, workspace)
+    id_bytes = _need_ids(ids, "ids")
+    _need(dy, torch.bfloat16, "dy")
+    if dy.dim() < 1 or dy.shape[:-1] != ids.shape:
+        raise ValueError("dy must be of shape [*ids.shape, hidden]")
+    hidden = dy.shape[-1]
+    if accumulate is not None and out is not None:
+        raise ValueError("accumulate is written in place: out cannot be given too")
+    grad = accumulate if accumulate is not None else out
+    if grad is None:
+        grad = torch.empty((vocab, hidden), dtype=dtype or torch.float32, device=dy.device)
+    if grad.dtype not in (torch.float32, torch.bfloat16) or (dtype is not None and grad.dtype != dtype):
+        raise TypeError(f"the gradient must be {dtype or 'torch.float32 or torch.bfloat16'}, got {grad.dtype}")
+    _need(grad, grad.dtype, "the gradient")
+    if grad.shape != (vocab, hidden):
+        raise ValueError(f"the gradient must be of shape {(vocab, hidden)}")
+    tokens = ids.numel()
+    if workspace is None:
+        workspace = torch.empty(max(nf_embedding_bwd_workspace_size(tokens, hidden), 16),
+                                dtype=torch.uint8, device=dy.device)
+    _same_device(dy, ids, grad, workspace)
+    _check(nf_embedding_bwd(grad.data_ptr(), NF_F32 if grad.dtype == torch.float32 else NF_BF16,
+                            int(accumulate is not None), dy.data_ptr(), ids.data_ptr(), id_bytes, tokens,
+                            vocab, hidden, scale, workspace.data_ptr(),
+                            workspace.numel() * workspace.element_size(), _stream()), "nf_embedding_bwd")
+    return grad
 
 
 def set_path(path):

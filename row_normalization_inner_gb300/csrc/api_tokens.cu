@@ -51,6 +51,16 @@ nf_status norm_q8(void* q, float* scale, const void* x, void* residual, bool fus
                                     reinterpret_cast<cudaStream_t>(stream)));
 }
 
+// The sizes an embedding call takes: token numbers and table rows are kept in
+// 32 bits (a row number of the table's size marks tokens without a row).
+nf_status embedding_checks(int64_t tokens, int64_t vocab, int64_t hidden, float scale, int32_t id_bytes) {
+    if (hidden < 8 || hidden % 8 != 0 || hidden > kEmbedMaxHidden) return NF_ERR_UNSUPPORTED_HIDDEN;
+    if (tokens < 0 || tokens > kEmbedMaxTokens || vocab < 1 || vocab > kEmbedMaxVocab)
+        return NF_ERR_INVALID_ARG;
+    if (!std::isfinite(scale) || (id_bytes != 4 && id_bytes != 8)) return NF_ERR_INVALID_ARG;
+    return NF_OK;
+}
+
 }  // namespace
 }  // namespace nf
 
@@ -68,6 +78,51 @@ nf_status nf_fused_add_rmsnorm_q8(void* q, float* scale, const void* x, void* re
                                   const void* weight, int64_t rows, int64_t hidden, float eps,
                                   nf_q8_format format, int64_t group, nf_stream stream) {
     return norm_q8(q, scale, x, residual, true, weight, rows, hidden, eps, format, group, stream);
+}
+
+nf_status nf_embedding_fwd(void* y, const void* ids, int32_t id_bytes, const void* table, int64_t tokens,
+                           int64_t vocab, int64_t hidden, float scale, nf_stream stream) {
+    if (nf_status st = embedding_checks(tokens, vocab, hidden, scale, id_bytes)) return st;
+    if (tokens == 0) return NF_OK;
+    if (!y || !ids || !table) return NF_ERR_INVALID_ARG;
+    if (!aligned(y, 16) || !aligned(table, 16) || !aligned(ids, id_bytes)) return NF_ERR_MISALIGNED;
+    const Span out{y, tokens * hidden * 2};
+    if (overlap(out, {ids, tokens * id_bytes}) || overlap(out, {table, vocab * hidden * 2}))
+        return NF_ERR_INVALID_ARG;
+    return from_cuda(launch_embedding_fwd(y, ids, id_bytes == 8, table, tokens, vocab, hidden, scale,
+                                          reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t nf_embedding_bwd_workspace_size(int64_t tokens, int64_t hidden) {
+    if (tokens <= 0 || tokens > kEmbedMaxTokens || hidden < 8 || hidden % 8 != 0 || hidden > kEmbedMaxHidden)
+        return 0;
+    int sms;
+    if (device_sm_count(&sms) != NF_OK) return 0;
+    return embedding_bwd_workspace(tokens, hidden, sms);
+}
+
+nf_status nf_embedding_bwd(void* dtable, nf_dtype dtable_type, int32_t accumulate, const void* dy,
+                           const void* ids, int32_t id_bytes, int64_t tokens, int64_t vocab, int64_t hidden,
+                           float scale, void* workspace, size_t workspace_bytes, nf_stream stream) {
+    if (nf_status st = embedding_checks(tokens, vocab, hidden, scale, id_bytes)) return st;
+    if ((dtable_type != NF_BF16 && dtable_type != NF_F32) || (accumulate != 0 && accumulate != 1))
+        return NF_ERR_INVALID_ARG;
+    if (tokens == 0 && accumulate) return NF_OK;
+    if (!dtable || (tokens > 0 && (!dy || !ids || !workspace))) return NF_ERR_INVALID_ARG;
+    if (!aligned(dtable, 16) || !aligned(dy, 16) || !aligned(ids, id_bytes) || !aligned(workspace, 16))
+        return NF_ERR_MISALIGNED;
+    int sms;
+    if (nf_status st = device_sm_count(&sms)) return st;
+    const size_t need = tokens ? embedding_bwd_workspace(tokens, hidden, sms) : 0;
+    if (workspace_bytes < need) return NF_ERR_WORKSPACE_TOO_SMALL;
+    const Span grad{dtable, vocab * hidden * (dtable_type == NF_F32 ? 4 : 2)};
+    const Span ws{workspace, static_cast<int64_t>(need)};
+    for (const Span& in : {Span{dy, tokens * hidden * 2}, Span{ids, tokens * id_bytes}})
+        if (overlap(grad, in) || overlap(ws, in)) return NF_ERR_INVALID_ARG;
+    if (overlap(grad, ws)) return NF_ERR_INVALID_ARG;
+    return from_cuda(launch_embedding_bwd(dtable, dtable_type == NF_F32, accumulate != 0, dy, ids, id_bytes == 8,
+                                          tokens, vocab, hidden, scale, workspace, sms,
+                                          reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -26,4 +26,17 @@ struct Q8Args {
 };
 cudaError_t launch_norm_q8(const Q8Args& a, bool int8, bool grouped, int sms, cudaStream_t st);
 
+// Largest embedding calls.
+constexpr int64_t kEmbedMaxHidden = 1 << 20;
+constexpr int64_t kEmbedMaxTokens = 0x7FFFFFFF;
+constexpr int64_t kEmbedMaxVocab = 1 << 30;
+// Embedding lookup: y[i] = bf16(scale * table[ids[i]]).  wide: 64-bit ids.
+cudaError_t launch_embedding_fwd(void* y, const void* ids, bool wide, const void* table, int64_t tokens,
+                                 int64_t vocab, int64_t hidden, float scale, cudaStream_t st);
+// Its gradient: dtable (fp32 or bf16) is overwritten, or added to (add).
+size_t embedding_bwd_workspace(int64_t tokens, int64_t hidden, int sms);
+cudaError_t launch_embedding_bwd(void* dtable, bool f32, bool add, const void* dy, const void* ids, bool wide,
+                                 int64_t tokens, int64_t vocab, int64_t hidden, float scale, void* workspace,
+                                 int sms, cudaStream_t st);
+
 }  // namespace nf

@@ -63,3 +63,54 @@ def test_q8_helper_refusals():
         nf.rmsnorm_q8(x.float(), w)
     with pytest.raises(TypeError):
         nf.fused_add_rmsnorm_q8(None, x, w)
+
+
+# ---------------------------------------------------------------- embedding
+
+def embed(y=A, ids=B, id_bytes=8, table=C, tokens=4, vocab=100, hidden=64, scale=1.0):
+    return nf.nf_embedding_fwd(y, ids, id_bytes, table, tokens, vocab, hidden, scale, None)
+
+
+def embed_grad(grad=A, kind=nf.NF_F32, add=0, dy=B, ids=C, id_bytes=8, tokens=4, vocab=100, hidden=64,
+               scale=1.0, ws=D, ws_bytes=1 << 34):
+    return nf.nf_embedding_bwd(grad, kind, add, dy, ids, id_bytes, tokens, vocab, hidden, scale, ws,
+                               ws_bytes, None)
+
+
+@pytest.mark.parametrize("call", [embed, embed_grad])
+def test_embedding_refusals(call):
+    for hidden in (0, 4, 12, -8, (1 << 20) + 8):
+        assert call(hidden=hidden) == nf.NF_ERR_UNSUPPORTED_HIDDEN
+    for bad in ({"tokens": -1}, {"tokens": 1 << 31}, {"vocab": 0}, {"vocab": -5}, {"vocab": (1 << 30) + 1},
+                {"scale": float("nan")}, {"scale": float("inf")}, {"id_bytes": 2}, {"id_bytes": 0}, {"ids": None}):
+        assert call(**bad) == nf.NF_ERR_INVALID_ARG, bad
+
+
+def test_embedding_fwd_pointers():
+    for bad in ({"y": None}, {"table": None}, {"y": B}, {"y": B + 16}, {"y": C}, {"y": C + 100 * 64 * 2 - 16}):
+        assert embed(**bad) == nf.NF_ERR_INVALID_ARG, bad
+    for bad in ({"y": A + 8}, {"table": C + 2}, {"ids": B + 4}, {"ids": B + 2, "id_bytes": 4}):
+        assert embed(**bad) == nf.NF_ERR_MISALIGNED, bad
+    assert embed(tokens=0, y=None, ids=None, table=None) == nf.NF_OK
+
+
+def test_embedding_bwd_arguments():
+    for bad in ({"grad": None}, {"dy": None}, {"ws": None}, {"kind": 2}, {"kind": -1}, {"add": 2}, {"add": -1}):
+        assert embed_grad(**bad) == nf.NF_ERR_INVALID_ARG, bad
+    for bad in ({"grad": A + 8}, {"dy": B + 2}, {"ids": C + 4}, {"ws": D + 8}):
+        assert embed_grad(**bad) == nf.NF_ERR_MISALIGNED, bad
+    assert embed_grad(tokens=0, add=1, grad=None, dy=None, ids=None, ws=None) == nf.NF_OK
+    assert embed_grad(tokens=0, grad=None) == nf.NF_ERR_INVALID_ARG
+    for tokens, hidden in ((0, 64), (-1, 64), (1 << 31, 64), (4, 12), (4, 0), (4, (1 << 20) + 8)):
+        assert nf.nf_embedding_bwd_workspace_size(tokens, hidden) == 0
+
+
+def test_embedding_helper_refusals():
+    ids = torch.zeros(3, dtype=torch.int64)
+    table = torch.zeros(10, 64, dtype=torch.bfloat16)
+    with pytest.raises(TypeError):
+        nf.embedding_fwd(ids.float(), table)
+    with pytest.raises(ValueError, match="CUDA"):
+        nf.embedding_fwd(ids, table)
+    with pytest.raises(TypeError):
+        nf.embedding_bwd(table[:3], [0, 1, 2], 10)
