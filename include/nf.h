@@ -391,6 +391,49 @@ nf_status nf_embedding_bwd(void* dtable, nf_dtype dtable_type, int32_t accumulat
                            const void* ids, int32_t id_bytes, int64_t tokens, int64_t vocab, int64_t hidden,
                            float scale, void* workspace, size_t workspace_bytes, nf_stream stream);
 
+/* Largest number of alternatives nf_token_logprob_fwd returns. */
+#define NF_TOP_MAX 32
+
+/* Log probabilities of given tokens, with entropy and top alternatives.  For
+ * each row of logits l (rows of `vocab` elements, `stride` elements apart,
+ * NF_BF16 or NF_F32) at a temperature T, with m = max_j l_j and
+ * d_j = (l_j - m) / T:
+ *     log S      = log sum_j exp(d_j)
+ *     logprob    = d_t - log S,  t = targets[r]      (0 where t is outside [0, vocab))
+ *     entropy    = log S - sum_j exp(d_j) d_j / S
+ *     stats[r]   = (m, log S), what the gradient needs
+ *     top_*[r]   = the `top` most probable tokens, the most probable first and
+ *                  the lower id first among equals: their log probability and id
+ * Entries of -infinity are masked: probability 0, never an alternative; where
+ * fewer than `top` entries are left the rest hold (-infinity, -1).  A row with
+ * every entry masked has stats (-inf, -inf), entropy 0, logprob -inf (0 where
+ * t is outside).  A row with a NaN or +infinity has NaN for every value but
+ * m, and ids of -1.  logprob, entropy: [rows] fp32; stats: [rows, 2] fp32,
+ * 8-byte aligned; top_logprob: [rows, top] fp32; top_ids: [rows, top] int64;
+ * top 0 to NF_TOP_MAX (0: both may be NULL).  targets: int32 (id_bytes 4) or
+ * int64 (id_bytes 8).  logits need the alignment of an element only.  vocab 1
+ * to 2^30, stride >= vocab, T from 2^-64 to 2^64.  Elements behind a row's
+ * vocab are not read.  Nothing may overlap.  rows == 0 returns NF_OK.  No
+ * workspace. */
+nf_status nf_token_logprob_fwd(float* logprob, float* entropy, float* stats, float* top_logprob,
+                               int64_t* top_ids, const void* logits, nf_dtype type, int64_t stride,
+                               const void* targets, int32_t id_bytes, int64_t rows, int64_t vocab,
+                               float temperature, int32_t top, nf_stream stream);
+
+/* Gradient of logprob and entropy with respect to the logits.  With
+ * p_j = exp(d_j - log S) from the forward's stats, g = d_logprob[r] (taken as
+ * 0 where t is outside [0, vocab)) and h = d_entropy[r] (NULL: 0):
+ *     dlogits[r][j] = ( g (1[j = t] - p_j) - h p_j (log p_j + entropy[r]) ) / T
+ * in the logits' type, rows `dstride` elements apart; elements behind a row's
+ * vocab are left as they are.  A row with every entry masked gets zeros.
+ * entropy is the forward's, and may be NULL where d_entropy is.  dlogits may
+ * be the logits themselves (same pointer and stride); nothing else may
+ * overlap it.  Sizes as for the forward. */
+nf_status nf_token_logprob_bwd(void* dlogits, int64_t dstride, const void* logits, nf_dtype type,
+                               int64_t stride, const void* targets, int32_t id_bytes, const float* stats,
+                               const float* entropy, const float* d_logprob, const float* d_entropy,
+                               int64_t rows, int64_t vocab, float temperature, nf_stream stream);
+
 /* Outer normalization: the statistics run down the columns, over the rows
  * (batch normalization of a [rows, hidden] matrix in training mode; the
  * "Llu/ln bwd" discussion lists block- and grid-parallel outer

@@ -49,6 +49,7 @@ LONG_MAX_HIDDEN_FWD = 262144  # grid-parallel cluster path for longer rows
 LONG_MAX_HIDDEN_BWD = 131072
 SPLIT_MAX_HIDDEN = 1 << 26    # NF_SPLIT_MAX_HIDDEN: rows across any number of CTAs
 Q8_MAX_HIDDEN = 32768         # NF_Q8_MAX_HIDDEN: rows with an 8-bit output
+TOP_MAX = 32                  # NF_TOP_MAX: alternatives per row of token_logprob_fwd
 GRID_MAX_ROWS = 8             # the grid family (rows held on chip) takes 1 to 8 rows
 
 NF_Q8_E4M3, NF_Q8_INT8 = 0, 1
@@ -67,6 +68,7 @@ EXPORTS = (
     "nf_layernorm_fwd_ws",
     "nf_rmsnorm_q8", "nf_fused_add_rmsnorm_q8",
     "nf_embedding_fwd", "nf_embedding_bwd_workspace_size", "nf_embedding_bwd",
+    "nf_token_logprob_fwd", "nf_token_logprob_bwd",
     "nf_set_path", "nf_plan_query", "nf_plan_compute", "nf_get_device_status",
     "nf_selftest_wait_timeout", "nf_selftest_grid_timeout", "nf_selftest_floor", "nf_status_string",
     "nf_version",
@@ -123,6 +125,8 @@ def _bind(lib):
         "nf_embedding_fwd": (_S, [_P, _P, _S, _P, _I64, _I64, _I64, _F, _P]),
         "nf_embedding_bwd_workspace_size": (ctypes.c_size_t, [_I64, _I64]),
         "nf_embedding_bwd": (_S, [_P, _S, _S, _P, _P, _S, _I64, _I64, _I64, _F, _P, ctypes.c_size_t, _P]),
+        "nf_token_logprob_fwd": (_S, [_P, _P, _P, _P, _P, _P, _S, _I64, _P, _S, _I64, _I64, _F, _S, _P]),
+        "nf_token_logprob_bwd": (_S, [_P, _I64, _P, _S, _I64, _P, _S, _P, _P, _P, _P, _I64, _I64, _F, _P]),
         "nf_set_path": (_S, [_S]),
         "nf_plan_query": (_S, [_S, _I64, _I64, ctypes.POINTER(Plan)]),
         "nf_plan_compute": (_S, [_S, _I64, _I64, ctypes.c_int32, _S, ctypes.POINTER(Plan)]),
@@ -269,6 +273,18 @@ def nf_embedding_bwd(dtable, dtable_type, accumulate, dy, ids, id_bytes, tokens,
                      workspace, workspace_bytes, stream) -> int:
     return lib().nf_embedding_bwd(dtable, dtable_type, accumulate, dy, ids, id_bytes, tokens, vocab,
                                   hidden, scale, workspace, workspace_bytes, stream)
+
+
+def nf_token_logprob_fwd(logprob, entropy, stats, top_logprob, top_ids, logits, type, stride, targets,
+                         id_bytes, rows, vocab, temperature, top, stream) -> int:
+    return lib().nf_token_logprob_fwd(logprob, entropy, stats, top_logprob, top_ids, logits, type,
+                                      stride, targets, id_bytes, rows, vocab, temperature, top, stream)
+
+
+def nf_token_logprob_bwd(dlogits, dstride, logits, type, stride, targets, id_bytes, stats, entropy,
+                         d_logprob, d_entropy, rows, vocab, temperature, stream) -> int:
+    return lib().nf_token_logprob_bwd(dlogits, dstride, logits, type, stride, targets, id_bytes, stats,
+                                      entropy, d_logprob, d_entropy, rows, vocab, temperature, stream)
 
 
 def nf_set_path(path) -> int:
@@ -661,6 +677,103 @@ def embedding_bwd(dy, ids, vocab: int, scale: float = 1.0, dtype=None, accumulat
                             vocab, hidden, scale, workspace.data_ptr(),
                             workspace.numel() * workspace.element_size(), _stream()), "nf_embedding_bwd")
     return grad
+
+
+def _need_logits(t, name):
+    """(nf_dtype, row stride) of a [rows, vocab] CUDA tensor whose rows may be apart."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if t.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be [rows, vocab]")
+    rows, vocab = t.shape
+    stride = t.stride(0) if rows > 1 else max(vocab, 1)
+    if (vocab > 1 and t.stride(1) != 1) or stride < vocab:
+        raise ValueError(f"{name}'s rows must be contiguous and apart")
+    return (NF_F32 if t.dtype == torch.float32 else NF_BF16), stride
+
+
+def _need_rows(t, rows, name):
+    import torch
+    _need(t, torch.float32, name)
+    if t.shape != (rows,):
+        raise ValueError(f"{name} must be of shape {(rows,)}")
+
+
+def token_logprob_fwd(logits, targets, temperature: float = 1.0, top: int = 0, stream=None):
+    """Log probabilities of targets under softmax(logits / temperature).
+
+    logits: [rows, vocab] bf16 or fp32, contiguous within a row; targets:
+    [rows] int32 or int64.  Returns (logprob, entropy, stats, top_logprob,
+    top_ids): fp32 [rows], [rows], [rows, 2] (the row's maximum and the
+    logarithm of its sum of exponentials, for token_logprob_bwd), and the
+    `top` most probable tokens, [rows, top] fp32 and int64 (None with top 0),
+    equal ones by rising id.  Entries of -inf are masked; targets outside
+    [0, vocab) give 0."""
+    import torch
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return token_logprob_fwd(logits, targets, temperature, top)
+    kind, stride = _need_logits(logits, "logits")
+    id_bytes = _need_ids(targets, "targets")
+    rows, vocab = logits.shape
+    if targets.shape != (rows,):
+        raise ValueError(f"targets must be of shape {(rows,)}")
+    if not 0 <= top <= TOP_MAX:
+        raise ValueError(f"top must be 0 to {TOP_MAX}, got {top}")
+    _same_device(logits, targets)
+    dev = logits.device
+    logprob = torch.empty(rows, dtype=torch.float32, device=dev)
+    entropy = torch.empty(rows, dtype=torch.float32, device=dev)
+    stats = torch.empty((rows, 2), dtype=torch.float32, device=dev)
+    top_logprob = top_ids = None
+    if top:
+        top_logprob = torch.empty((rows, top), dtype=torch.float32, device=dev)
+        top_ids = torch.empty((rows, top), dtype=torch.int64, device=dev)
+    _check(nf_token_logprob_fwd(logprob.data_ptr(), entropy.data_ptr(), stats.data_ptr(),
+                                top_logprob.data_ptr() if top else None, top_ids.data_ptr() if top else None,
+                                logits.data_ptr(), kind, stride, targets.data_ptr(), id_bytes, rows, vocab,
+                                temperature, top, _stream()), "nf_token_logprob_fwd")
+    return logprob, entropy, stats, top_logprob, top_ids
+
+
+def token_logprob_bwd(logits, targets, stats, entropy, d_logprob, d_entropy=None,
+                      temperature: float = 1.0, out=None, stream=None):
+    """Gradient of token_logprob_fwd's logprob and entropy for the logits, in
+    their type, given the gradients d_logprob and (optionally) d_entropy and
+    the forward's stats and entropy.  out may be the logits themselves."""
+    import torch
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return token_logprob_bwd(logits, targets, stats, entropy, d_logprob, d_entropy, temperature, out)
+    kind, stride = _need_logits(logits, "logits")
+    id_bytes = _need_ids(targets, "targets")
+    rows, vocab = logits.shape
+    if targets.shape != (rows,):
+        raise ValueError(f"targets must be of shape {(rows,)}")
+    _need(stats, torch.float32, "stats")
+    if stats.shape != (rows, 2):
+        raise ValueError(f"stats must be of shape {(rows, 2)}")
+    _need_rows(d_logprob, rows, "d_logprob")
+    if d_entropy is not None:
+        _need_rows(d_entropy, rows, "d_entropy")
+        _need_rows(entropy, rows, "entropy")
+    if out is None:
+        out = torch.empty((rows, vocab), dtype=logits.dtype, device=logits.device)
+    out_kind, out_stride = _need_logits(out, "out")
+    if out_kind != kind or out.shape != logits.shape:
+        raise ValueError("out must have the logits' type and shape")
+    _same_device(logits, targets, stats, entropy, d_logprob, d_entropy, out)
+    _check(nf_token_logprob_bwd(out.data_ptr(), out_stride, logits.data_ptr(), kind, stride,
+                                targets.data_ptr(), id_bytes, stats.data_ptr(),
+                                None if entropy is None else entropy.data_ptr(), d_logprob.data_ptr(),
+                                None if d_entropy is None else d_entropy.data_ptr(), rows, vocab,
+                                temperature, _stream()), "nf_token_logprob_bwd")
+    return out
 
 
 def set_path(path):

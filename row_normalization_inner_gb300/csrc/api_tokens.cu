@@ -61,6 +61,21 @@ nf_status embedding_checks(int64_t tokens, int64_t vocab, int64_t hidden, float 
     return NF_OK;
 }
 
+nf_status logprob_checks(nf_dtype type, int32_t id_bytes, int64_t rows, int64_t vocab, int64_t stride,
+                         float temperature) {
+    if ((type != NF_BF16 && type != NF_F32) || (id_bytes != 4 && id_bytes != 8)) return NF_ERR_INVALID_ARG;
+    if (rows < 0 || vocab < 1 || vocab > kLogprobMaxVocab || stride < vocab) return NF_ERR_INVALID_ARG;
+    // a row's last element stays addressable, and rows times CTAs per row countable
+    if (stride > INT64_MAX / 32 || rows > (INT64_MAX / 32) / stride) return NF_ERR_INVALID_ARG;
+    if (!(temperature >= 0x1p-64f && temperature <= 0x1p64f)) return NF_ERR_INVALID_ARG;
+    return NF_OK;
+}
+
+// Bytes from a strided matrix's first element to behind its last.
+int64_t strided_bytes(int64_t rows, int64_t vocab, int64_t stride, int64_t size) {
+    return ((rows - 1) * stride + vocab) * size;
+}
+
 }  // namespace
 }  // namespace nf
 
@@ -123,6 +138,59 @@ nf_status nf_embedding_bwd(void* dtable, nf_dtype dtable_type, int32_t accumulat
     return from_cuda(launch_embedding_bwd(dtable, dtable_type == NF_F32, accumulate != 0, dy, ids, id_bytes == 8,
                                           tokens, vocab, hidden, scale, workspace, sms,
                                           reinterpret_cast<cudaStream_t>(stream)));
+}
+
+nf_status nf_token_logprob_fwd(float* logprob, float* entropy, float* stats, float* top_logprob,
+                               int64_t* top_ids, const void* logits, nf_dtype type, int64_t stride,
+                               const void* targets, int32_t id_bytes, int64_t rows, int64_t vocab,
+                               float temperature, int32_t top, nf_stream stream) {
+    if (nf_status st = logprob_checks(type, id_bytes, rows, vocab, stride, temperature)) return st;
+    if (top < 0 || top > kLogprobMaxTop) return NF_ERR_INVALID_ARG;
+    if (rows == 0) return NF_OK;
+    if (!logprob || !entropy || !stats || !logits || !targets || (top && (!top_logprob || !top_ids)))
+        return NF_ERR_INVALID_ARG;
+    const int size = type == NF_F32 ? 4 : 2;
+    if (!aligned(logprob, 4) || !aligned(entropy, 4) || !aligned(stats, 8) || !aligned(logits, size) ||
+        !aligned(targets, id_bytes) || (top && (!aligned(top_logprob, 4) || !aligned(top_ids, 8))))
+        return NF_ERR_MISALIGNED;
+    const Span outs[] = {{logprob, rows * 4}, {entropy, rows * 4}, {stats, rows * 8},
+                         {top ? top_logprob : nullptr, rows * top * 4}, {top ? top_ids : nullptr, rows * top * 8}};
+    const Span ins[] = {{logits, strided_bytes(rows, vocab, stride, size)}, {targets, rows * id_bytes}};
+    for (int i = 0; i < 5; ++i) {
+        for (int j = i + 1; j < 5; ++j)
+            if (overlap(outs[i], outs[j])) return NF_ERR_INVALID_ARG;
+        for (const Span& in : ins)
+            if (overlap(outs[i], in)) return NF_ERR_INVALID_ARG;
+    }
+    int sms;
+    if (nf_status st = device_sm_count(&sms)) return st;
+    return from_cuda(launch_token_logprob_fwd(logprob, entropy, stats, top_logprob, top_ids, logits,
+                                              type == NF_F32, targets, id_bytes == 8, rows, vocab, stride,
+                                              temperature, top, sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+nf_status nf_token_logprob_bwd(void* dlogits, int64_t dstride, const void* logits, nf_dtype type,
+                               int64_t stride, const void* targets, int32_t id_bytes, const float* stats,
+                               const float* entropy, const float* d_logprob, const float* d_entropy,
+                               int64_t rows, int64_t vocab, float temperature, nf_stream stream) {
+    if (nf_status st = logprob_checks(type, id_bytes, rows, vocab, stride, temperature)) return st;
+    if (nf_status st = logprob_checks(type, id_bytes, rows, vocab, dstride, temperature)) return st;
+    if (rows == 0) return NF_OK;
+    if (!dlogits || !logits || !targets || !stats || !d_logprob || (d_entropy && !entropy)) return NF_ERR_INVALID_ARG;
+    const int size = type == NF_F32 ? 4 : 2;
+    if (!aligned(dlogits, size) || !aligned(logits, size) || !aligned(targets, id_bytes) || !aligned(stats, 8) ||
+        !aligned(d_logprob, 4) || !aligned(d_entropy, 4) || (d_entropy && !aligned(entropy, 4)))
+        return NF_ERR_MISALIGNED;
+    const Span out{dlogits, strided_bytes(rows, vocab, dstride, size)};
+    // dlogits may be the logits themselves: every element is read before it is written, by the thread that writes it
+    if (!(dlogits == logits && dstride == stride) && overlap(out, {logits, strided_bytes(rows, vocab, stride, size)}))
+        return NF_ERR_INVALID_ARG;
+    for (const Span& in : {Span{targets, rows * id_bytes}, Span{stats, rows * 8}, Span{d_logprob, rows * 4},
+                           Span{d_entropy, rows * 4}, Span{d_entropy ? entropy : nullptr, rows * 4}})
+        if (overlap(out, in)) return NF_ERR_INVALID_ARG;
+    return from_cuda(launch_token_logprob_bwd(dlogits, logits, type == NF_F32, targets, id_bytes == 8, stats,
+                                              entropy, d_logprob, d_entropy, rows, vocab, stride, dstride,
+                                              temperature, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

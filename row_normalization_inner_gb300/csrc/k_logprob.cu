@@ -1,0 +1,578 @@
+// Log probabilities of given tokens, with entropy and top alternatives, and
+// the gradient of both.
+//
+// Forward, per row of logits l at temperature T, with m = max l and
+// d_j = (l_j - m) / T:
+//     S = sum_j exp(d_j),  U = sum_j exp(d_j) d_j
+//     logprob = d_t - log S,   entropy = log S - U / S,   stats = (m, log S)
+// and the `top` largest logits, a tie going to the lower index.  One pass
+// over the row: a thread keeps a running maximum and rescales its sums where
+// it grows; powers of two stand for powers of e (d in units of ln 2).  d is
+// the difference first and the product after, so that its error is relative
+// to d itself and a probability near 1 keeps its logarithm.
+//
+// Bound by memory: the logits are read once.  A row belongs to a CTA, or,
+// where there are few rows, to a cluster of 2, 4 or 8 CTAs that join their
+// sums through distributed shared memory.
+//
+// The alternatives need no second pass: the maxima of the threads' own
+// elements are known from the sums, and the top-th largest of these maxima
+// is a lower bound for the alternatives.  Only the threads whose maximum
+// reaches it (little more than `top` of them) have their elements read
+// again, from L2; what reaches the bound there is sorted as 64-bit keys
+// (value, then index from the end), all distinct.
+//
+// Backward: with p_j = exp(d_j - log S),
+//     dl_j = ( g (1[j = t] - p_j) - h p_j (log p_j + H) ) / T
+// for gradients g of logprob and h of entropy (H): one read, one write.
+#include <cfloat>
+
+#include <cooperative_groups.h>
+
+#include "common.cuh"
+#include "pairs.cuh"
+#include "pdl.cuh"
+#include "tokens.h"
+
+namespace nf {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+// d is held at this or above: a power of two of it is 0, and its product
+// with 0 is 0 where that of -infinity would be NaN
+constexpr float kLowest = -16384.f;
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// max(x, kLowest), a NaN staying NaN.
+__device__ __forceinline__ float hold(float x) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(kLowest));
+    return y;
+}
+
+// Element access of a 16-byte vector of bf16 or fp32 logits.
+template <bool F32> struct Elem;
+template <> struct Elem<false> {
+    static constexpr int N = 8;
+    using T = uint16_t;
+    static constexpr uint32_t kNone = 0xFF80FF80u;  // -infinity in every element
+    static __device__ __forceinline__ void unpack(uint4 v, float2 (&f)[4]) { unpack8x2(v, f); }
+    static __device__ __forceinline__ uint4 pack(const float2 (&f)[4]) { return pack8x2(f); }
+    static __device__ __forceinline__ float value(uint16_t b) { return __uint_as_float(static_cast<uint32_t>(b) << 16); }
+    static __device__ __forceinline__ uint16_t bits(float f) { return static_cast<uint16_t>(pack2(f, 0.f)); }
+};
+template <> struct Elem<true> {
+    static constexpr int N = 4;
+    using T = float;
+    static constexpr uint32_t kNone = 0xFF800000u;
+    static __device__ __forceinline__ void unpack(uint4 v, float2 (&f)[2]) {
+        f[0] = make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
+        f[1] = make_float2(__uint_as_float(v.z), __uint_as_float(v.w));
+    }
+    static __device__ __forceinline__ uint4 pack(const float2 (&f)[2]) {
+        return make_uint4(__float_as_uint(f[0].x), __float_as_uint(f[0].y), __float_as_uint(f[1].x),
+                          __float_as_uint(f[1].y));
+    }
+    static __device__ __forceinline__ float value(float f) { return f; }
+    static __device__ __forceinline__ float bits(float f) { return f; }
+};
+
+// A row of `n` elements that starts anywhere, as 16-byte vectors counted from
+// the boundary at or below its start: element j is element j + lead of the
+// vectors.  Only the first and the last vector can be partial; their missing
+// elements are neither read nor written.
+template <bool F32>
+struct Row {
+    using E = Elem<F32>;
+    using T = typename E::T;
+    const T* base;  // of element 0
+    int lead;
+    int n;
+    __device__ __forceinline__ Row(const void* p, int64_t offset, int n_) {
+        base = static_cast<const T*>(p) + offset;
+        lead = static_cast<int>((reinterpret_cast<uintptr_t>(base) & 15) / sizeof(T));
+        n = n_;
+    }
+    __device__ __forceinline__ int vectors() const { return (lead + n + E::N - 1) / E::N; }
+    __device__ __forceinline__ bool full(int v) const { return v * E::N >= lead && (v + 1) * E::N <= lead + n; }
+    __device__ __forceinline__ uint4 load(int v) const {
+        const int j0 = v * E::N - lead;
+        if (full(v)) return ld_stream(base + j0);
+        uint4 r = make_uint4(E::kNone, E::kNone, E::kNone, E::kNone);
+        T* e = reinterpret_cast<T*>(&r);
+#pragma unroll
+        for (int k = 0; k < E::N; ++k)
+            if (j0 + k >= 0 && j0 + k < n) e[k] = base[j0 + k];
+        return r;
+    }
+};
+
+// ---- forward ---------------------------------------------------------------------
+constexpr int kFwdMaxThreads = 512;
+constexpr int kFwdBatch = 4;   // vectors in flight per thread
+constexpr int kTopMax = kLogprobMaxTop;
+constexpr int kCand = kFwdMaxThreads * 8 + kTopMax;  // one round's candidates and those kept
+
+// Sums of exponentials of d (units of ln 2) below the maximum m.
+struct Part {
+    float m, s, u;
+};
+
+__device__ __forceinline__ Part join(Part a, Part b, float c) {
+    const float m = fmaxf(a.m, b.m);
+    const float da = hold((a.m - m) * c), db = hold((b.m - m) * c);
+    const float fa = ex2(da), fb = ex2(db);
+    Part r;
+    r.m = m;
+    r.s = a.s * fa + b.s * fb;
+    r.u = fa * (a.u + a.s * da) + fb * (b.u + b.s * db);
+    return r;
+}
+
+// An order-preserving integer of a float, and back.
+__device__ __forceinline__ uint32_t order_of(float f) {
+    const uint32_t b = __float_as_uint(f);
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float float_of(uint32_t o) {
+    return __uint_as_float(o & 0x80000000u ? o & 0x7FFFFFFFu : ~o);
+}
+__device__ __forceinline__ float key_value(uint64_t key) { return float_of(static_cast<uint32_t>(key >> 32)); }
+__device__ __forceinline__ int key_index(uint64_t key) { return static_cast<int>(~static_cast<uint32_t>(key)); }
+
+struct TopShared {
+    uint64_t cand[kCand];
+    uint64_t best[kTopMax];
+    int list[kFwdMaxThreads];
+    int n_cand, n_list;
+};
+
+// The `top` largest of cand[0, n), sorted, to best (0 where there are fewer).
+// Every thread calls; synchronized on return.
+__device__ __forceinline__ void sort_top(uint64_t* cand, int n, int top, uint64_t* best, int* n_kept) {
+    const int t = threadIdx.x, T = blockDim.x;
+    if (n > 256) {
+        // the top-th largest key bit by bit (the keys are distinct), then only what reaches it
+        uint64_t bound = 0;
+        for (int b = 63; b >= 0; --b) {
+            const uint64_t test = bound | (1ull << b);
+            int mine = 0;
+            for (int i = t; i < n; i += T) mine += cand[i] >= test;
+            // counts beyond `top` per thread are cut: only >= top matters
+            int total = 0;
+#pragma unroll
+            for (int bit = 0; bit < 6; ++bit) total += __syncthreads_count((min(mine, 63) >> bit) & 1) << bit;
+            if (total >= top) bound = test;
+        }
+        uint64_t keep[kCand / 64 + 1];
+        int kept = 0;
+        for (int i = t; i < n; i += T)
+            if (cand[i] >= bound && kept < kCand / 64 + 1) keep[kept++] = cand[i];
+        if (t == 0) *n_kept = 0;
+        __syncthreads();
+        const int at = kept ? atomicAdd(n_kept, kept) : 0;
+        for (int i = 0; i < kept; ++i) cand[at + i] = keep[i];
+        __syncthreads();
+        n = *n_kept;
+    }
+    if (t < top) best[t] = 0;
+    __syncthreads();
+    for (int i = t; i < n; i += T) {
+        const uint64_t key = cand[i];
+        int above = 0;
+        for (int k = 0; k < n; ++k) above += cand[k] > key;
+        if (above < top) best[above] = key;
+    }
+    __syncthreads();
+}
+
+struct LogprobFwd {
+    float* logprob;
+    float* entropy;
+    float2* stats;
+    float* top_logprob;
+    int64_t* top_ids;
+    const void* logits;
+    const void* targets;
+    int64_t rows, stride;
+    int vocab, top;
+    float inv_t;
+    bool wide;
+};
+
+__device__ __forceinline__ int64_t target_at(const void* ids, bool wide, int64_t i) {
+    return wide ? static_cast<const int64_t*>(ids)[i] : static_cast<const int32_t*>(ids)[i];
+}
+
+template <bool F32, bool TOP, bool CLUSTER>
+__global__ void __launch_bounds__(kFwdMaxThreads)
+token_logprob_rows(const LogprobFwd a) {
+    using E = Elem<F32>;
+    extern __shared__ __align__(16) unsigned char smem[];
+    TopShared& sh = *reinterpret_cast<TopShared*>(smem);  // only with TOP
+    __shared__ Part warps[kFwdMaxThreads / 32];
+    __shared__ Part mine;
+    const int t = threadIdx.x, T = blockDim.x, lane = t & 31, warp = t >> 5;
+    int ctas = 1, rank = 0;
+    if constexpr (CLUSTER) {
+        ctas = cg::this_cluster().num_blocks();
+        rank = cg::this_cluster().block_rank();
+    }
+    const float c = a.inv_t * kLog2e;
+    const float2 c2 = make_float2(c, c);
+    grid_dep_wait();
+    grid_dep_release();
+    for (int64_t row = blockIdx.x / ctas; row < a.rows; row += gridDim.x / ctas) {
+        const Row<F32> r(a.logits, row * a.stride, a.vocab);
+        const int nv = r.vectors();
+        const int per = (nv + ctas - 1) / ctas;
+        const int v0 = min(nv, rank * per), v1 = min(nv, v0 + per);
+        // the thread's elements: vectors v0 + t + i * T
+        Part p = {-FLT_MAX, 0.f, 0.f};
+        float2 s2 = make_float2(0.f, 0.f), u2 = make_float2(0.f, 0.f);
+        for (int v = v0 + t; v < v1; v += kFwdBatch * T) {
+            uint4 raw[kFwdBatch];
+#pragma unroll
+            for (int k = 0; k < kFwdBatch; ++k)
+                raw[k] = v + k * T < v1 ? r.load(v + k * T) : make_uint4(E::kNone, E::kNone, E::kNone, E::kNone);
+            float top = -FLT_MAX;
+#pragma unroll
+            for (int k = 0; k < kFwdBatch; ++k) {
+                float2 f[E::N / 2];
+                E::unpack(raw[k], f);
+#pragma unroll
+                for (int q = 0; q < E::N / 2; ++q) top = fmaxf(top, fmaxf(f[q].x, f[q].y));
+            }
+            if (top > p.m) {
+                const float d = hold((p.m - top) * c), g = ex2(d);
+                const float2 d2 = make_float2(d, d), g2 = make_float2(g, g);
+                u2 = __fmul2_rn(g2, __ffma2_rn(s2, d2, u2));
+                s2 = __fmul2_rn(s2, g2);
+                p.m = top;
+            }
+            const float2 nm = make_float2(-p.m, -p.m);
+#pragma unroll
+            for (int k = 0; k < kFwdBatch; ++k) {
+                float2 f[E::N / 2];
+                E::unpack(raw[k], f);
+#pragma unroll
+                for (int q = 0; q < E::N / 2; ++q) {
+                    float2 d = __fmul2_rn(__fadd2_rn(f[q], nm), c2);
+                    d = make_float2(hold(d.x), hold(d.y));
+                    const float2 e = make_float2(ex2(d.x), ex2(d.y));
+                    s2 = __fadd2_rn(s2, e);
+                    u2 = __ffma2_rn(e, d, u2);
+                }
+            }
+        }
+        p.s = s2.x + s2.y;
+        p.u = u2.x + u2.y;
+        const float own_max = p.m;
+        // warp, then CTA, then cluster, each in a fixed order
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) {
+            Part o;
+            o.m = __shfl_xor_sync(0xFFFFFFFFu, p.m, off);
+            o.s = __shfl_xor_sync(0xFFFFFFFFu, p.s, off);
+            o.u = __shfl_xor_sync(0xFFFFFFFFu, p.u, off);
+            p = (lane & off) ? join(o, p, c) : join(p, o, c);
+        }
+        if (lane == 0) warps[warp] = p;
+        __syncthreads();
+        if (warp == 0) {
+            p = lane < T / 32 ? warps[lane] : Part{-FLT_MAX, 0.f, 0.f};
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) {
+                Part o;
+                o.m = __shfl_xor_sync(0xFFFFFFFFu, p.m, off);
+                o.s = __shfl_xor_sync(0xFFFFFFFFu, p.s, off);
+                o.u = __shfl_xor_sync(0xFFFFFFFFu, p.u, off);
+                p = (lane & off) ? join(o, p, c) : join(p, o, c);
+            }
+            if (lane == 0) mine = p;
+        }
+        if constexpr (TOP) {
+            // a bound that `top` threads' maxima reach, bit by bit; nearly `top` will do
+            const uint32_t ord = order_of(own_max);
+            uint32_t bound = 0;
+            for (int b = 31; b >= 0; --b) {
+                const uint32_t test = bound | (1u << b);
+                const int n = __syncthreads_count(ord >= test);
+                if (n >= a.top) {
+                    bound = test;
+                    if (n <= a.top + 8) break;
+                }
+            }
+            if (t == 0) sh.n_list = sh.n_cand = 0;
+            __syncthreads();
+            if (ord >= bound) sh.list[atomicAdd(&sh.n_list, 1)] = t;
+            __syncthreads();
+            const int lists = sh.n_list;
+            const int each = (v1 - v0 + T - 1) / T;
+            const int64_t items = static_cast<int64_t>(lists) * each;
+            uint64_t low = static_cast<uint64_t>(bound) << 32;  // keys below are out
+            for (int64_t i0 = 0; i0 < items; i0 += T) {
+                const int64_t i = i0 + t;
+                if (i < items) {
+                    const int v = v0 + sh.list[i % lists] + static_cast<int>(i / lists) * T;
+                    if (v < v1) {
+                        float2 f[E::N / 2];
+                        E::unpack(r.load(v), f);
+                        const int j0 = v * E::N - r.lead;
+#pragma unroll
+                        for (int q = 0; q < E::N; ++q) {
+                            const float x = q & 1 ? f[q / 2].y : f[q / 2].x;
+                            const uint64_t key = (static_cast<uint64_t>(order_of(x)) << 32) | ~static_cast<uint32_t>(j0 + q);
+                            if (x > -INFINITY && key >= low) sh.cand[atomicAdd(&sh.n_cand, 1)] = key;
+                        }
+                    }
+                }
+                __syncthreads();
+                const int n = sh.n_cand;
+                const bool last = i0 + T >= items;
+                // keep the best when the next round might not fit
+                if (last || n + T * E::N > kCand) {
+                    __syncthreads();
+                    sort_top(sh.cand, n, a.top, sh.best, &sh.n_cand);
+                    if (!last) {
+                        const int kept = min(n, a.top);
+                        if (t < kept) sh.cand[t] = sh.best[t];
+                        if (kept == a.top) low = max(low, sh.best[a.top - 1]);
+                        if (t == 0) sh.n_cand = kept;
+                    }
+                }
+                __syncthreads();
+            }
+            if (items == 0) {
+                if (t < a.top) sh.best[t] = 0;
+                __syncthreads();
+            }
+        } else {
+            __syncthreads();
+        }
+        Part all = mine;
+        if constexpr (CLUSTER) {
+            cg::cluster_group cluster = cg::this_cluster();
+            cluster.sync();
+            if (rank == 0) {
+                all = Part{-FLT_MAX, 0.f, 0.f};
+                for (int i = 0; i < ctas; ++i) all = join(all, *cluster.map_shared_rank(&mine, i), c);
+                if constexpr (TOP) {
+                    for (int i = t; i < ctas * a.top; i += T)
+                        sh.cand[i] = cluster.map_shared_rank(&sh, i / a.top)->best[i % a.top];
+                }
+            }
+            cluster.sync();  // the other CTAs' shared memory has been read
+            if constexpr (TOP) {
+                // ranks of missing alternatives (key 0) lie behind all others
+                if (rank == 0) sort_top(sh.cand, ctas * a.top, a.top, sh.best, &sh.n_cand);
+            }
+        }
+        if (rank == 0) {
+            const bool none = all.s == 0.f;   // every entry masked
+            const bool bad = isnan(all.s);
+            const float log_s = logf(all.s);  // -infinity where none
+            if (t == 0) {
+                const int64_t target = target_at(a.targets, a.wide, row);
+                float lp = 0.f;
+                if (target >= 0 && target < a.vocab)
+                    lp = none ? -INFINITY : (E::value(r.base[target]) - all.m) * a.inv_t - log_s;
+                a.logprob[row] = bad ? all.s : lp;
+                a.entropy[row] = none ? 0.f : log_s - kLn2 * (all.u / all.s);
+                a.stats[row] = make_float2(none ? -INFINITY : all.m, log_s);
+            }
+            if constexpr (TOP) {
+                if (t < a.top) {
+                    const uint64_t key = sh.best[t];
+                    a.top_logprob[row * a.top + t] =
+                        bad ? all.s : key ? (key_value(key) - all.m) * a.inv_t - log_s : -INFINITY;
+                    a.top_ids[row * a.top + t] = key && !bad ? key_index(key) : -1;
+                }
+            }
+        }
+        __syncthreads();  // the shared memory is reused by the next row
+    }
+}
+
+// ---- backward --------------------------------------------------------------------
+constexpr int kBwdThreads = 256;
+constexpr int kBwdBatch = 4;
+
+struct LogprobBwd {
+    void* out;
+    const void* logits;
+    const void* targets;
+    const float2* stats;
+    const float* entropy;
+    const float* d_logprob;
+    const float* d_entropy;  // or null
+    int64_t rows, stride, out_stride;
+    int vocab, chunks;       // CTAs of a row
+    float inv_t;
+    bool wide;
+};
+
+template <bool F32>
+__global__ void __launch_bounds__(kBwdThreads)
+token_logprob_grad(const LogprobBwd a) {
+    using E = Elem<F32>;
+    using T = typename E::T;
+    grid_dep_wait();
+    grid_dep_release();
+    const int threads = blockDim.x;
+    const int64_t work = a.rows * a.chunks;
+    for (int64_t w = blockIdx.x; w < work; w += gridDim.x) {
+        const int64_t row = w / a.chunks;
+        const int chunk = static_cast<int>(w - row * a.chunks);
+        const Row<F32> r(a.logits, row * a.stride, a.vocab);
+        T* out = static_cast<T*>(a.out) + row * a.out_stride;
+        const bool same = (reinterpret_cast<uintptr_t>(out) & 15) == (reinterpret_cast<uintptr_t>(r.base) & 15);
+        const int nv = r.vectors();
+        const float2 st = a.stats[row];
+        const int64_t target = target_at(a.targets, a.wide, row);
+        const bool none = st.x == -INFINITY;  // a row without entries: its gradient is 0
+        const bool known = target >= 0 && target < a.vocab && !none;
+        const float g = known ? a.d_logprob[row] : 0.f;
+        const float h = a.d_entropy && !none ? a.d_entropy[row] : 0.f;
+        const float m = none ? 0.f : st.x, log2_s = none ? 0.f : st.y * kLog2e;
+        // dl = p (A + B log2 p), p = 2^(log2 p)
+        const float A = -a.inv_t * (h != 0.f ? fmaf(h, a.entropy[row], g) : g);
+        const float B = -a.inv_t * h * kLn2;
+        const float c = a.inv_t * kLog2e;
+        const float2 c2 = make_float2(c, c), nm = make_float2(-m, -m), ns = make_float2(-log2_s, -log2_s);
+        const float2 A2 = make_float2(A, A), B2 = make_float2(B, B);
+        const int first = chunk * threads * kBwdBatch + threadIdx.x;
+        uint4 raw[kBwdBatch];
+#pragma unroll
+        for (int k = 0; k < kBwdBatch; ++k)
+            if (first + k * threads < nv) raw[k] = r.load(first + k * threads);
+#pragma unroll
+        for (int k = 0; k < kBwdBatch; ++k) {
+            const int v = first + k * threads;
+            if (v >= nv) continue;
+            const int j0 = v * E::N - r.lead;
+            float2 f[E::N / 2];
+            E::unpack(raw[k], f);
+#pragma unroll
+            for (int q = 0; q < E::N / 2; ++q) {
+                float2 d = __fadd2_rn(__fmul2_rn(__fadd2_rn(f[q], nm), c2), ns);
+                d = make_float2(hold(d.x), hold(d.y));
+                const float2 p = make_float2(ex2(d.x), ex2(d.y));
+                f[q] = __fmul2_rn(p, __ffma2_rn(B2, d, A2));
+            }
+            if (known && target >= j0 && target < j0 + E::N) {
+                const int at = static_cast<int>(target - j0);
+#pragma unroll
+                for (int q = 0; q < E::N / 2; ++q) {
+                    if (at == 2 * q) f[q].x = fmaf(g, a.inv_t, f[q].x);
+                    if (at == 2 * q + 1) f[q].y = fmaf(g, a.inv_t, f[q].y);
+                }
+            }
+            if (same && r.full(v)) {
+                st_stream(out + j0, E::pack(f));
+            } else {
+#pragma unroll
+                for (int q = 0; q < E::N; ++q)
+                    if (j0 + q >= 0 && j0 + q < a.vocab) out[j0 + q] = E::bits(q & 1 ? f[q / 2].y : f[q / 2].x);
+            }
+        }
+    }
+}
+
+template <bool F32, bool TOP, bool CLUSTER>
+cudaError_t fwd(const LogprobFwd& a, int threads, int ctas, cudaStream_t st) {
+    const auto k = token_logprob_rows<F32, TOP, CLUSTER>;
+    constexpr size_t smem = TOP ? sizeof(TopShared) : 0;
+    static_assert(sizeof(TopShared) <= 47 * 1024, "within the default limit of shared memory");
+    const int64_t most = 0x7FFFFFFF / ctas;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>((a.rows < most ? a.rows : most) * ctas));
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ctas;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = CLUSTER ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, k, a);
+}
+
+template <bool F32>
+cudaError_t fwd(const LogprobFwd& a, int threads, int ctas, cudaStream_t st) {
+    if (a.top) return ctas > 1 ? fwd<F32, true, true>(a, threads, ctas, st) : fwd<F32, true, false>(a, threads, ctas, st);
+    return ctas > 1 ? fwd<F32, false, true>(a, threads, ctas, st) : fwd<F32, false, false>(a, threads, ctas, st);
+}
+
+}  // namespace
+
+cudaError_t launch_token_logprob_fwd(float* logprob, float* entropy, float* stats, float* top_logprob,
+                                     int64_t* top_ids, const void* logits, bool f32, const void* targets,
+                                     bool wide, int64_t rows, int64_t vocab, int64_t stride, float temperature,
+                                     int top, int sms, cudaStream_t st) {
+    LogprobFwd a{};
+    a.logprob = logprob;
+    a.entropy = entropy;
+    a.stats = reinterpret_cast<float2*>(stats);
+    a.top_logprob = top_logprob;
+    a.top_ids = top_ids;
+    a.logits = logits;
+    a.targets = targets;
+    a.rows = rows;
+    a.stride = stride;
+    a.vocab = static_cast<int>(vocab);
+    a.top = top;
+    a.inv_t = 1.0f / temperature;
+    a.wide = wide;
+    const int64_t nv = vocab / (f32 ? 4 : 8) + 1;
+    int threads = 128;
+    while (threads < kFwdMaxThreads && threads * kFwdBatch < nv) threads *= 2;
+    // few rows: more CTAs per row, while each thread still has a batch
+    int ctas = 1;
+    while (ctas < 8 && rows * ctas * 2 <= 2 * static_cast<int64_t>(sms) && nv >= static_cast<int64_t>(ctas) * 2 * threads)
+        ctas *= 2;
+    return f32 ? fwd<true>(a, threads, ctas, st) : fwd<false>(a, threads, ctas, st);
+}
+
+cudaError_t launch_token_logprob_bwd(void* out, const void* logits, bool f32, const void* targets, bool wide,
+                                     const float* stats, const float* entropy, const float* d_logprob,
+                                     const float* d_entropy, int64_t rows, int64_t vocab, int64_t stride,
+                                     int64_t out_stride, float temperature, cudaStream_t st) {
+    LogprobBwd a{};
+    a.out = out;
+    a.logits = logits;
+    a.targets = targets;
+    a.stats = reinterpret_cast<const float2*>(stats);
+    a.entropy = entropy;
+    a.d_logprob = d_logprob;
+    a.d_entropy = d_entropy;
+    a.rows = rows;
+    a.stride = stride;
+    a.out_stride = out_stride;
+    a.vocab = static_cast<int>(vocab);
+    a.inv_t = 1.0f / temperature;
+    a.wide = wide;
+    const int n = f32 ? 4 : 8;
+    const int64_t nv = (vocab + n - 1) / n + 1;  // an unaligned row takes one more
+    int threads = 32;
+    while (threads < kBwdThreads && threads * kBwdBatch < nv) threads *= 2;
+    a.chunks = static_cast<int>((nv + threads * kBwdBatch - 1) / (threads * kBwdBatch));
+    const int64_t work = rows * a.chunks;
+    const dim3 grid(static_cast<unsigned>(work < 0x7FFFFFFF ? work : 0x7FFFFFFF));
+    return f32 ? launch_with_pdl(token_logprob_grad<true>, grid, dim3(threads), 0, st, a)
+               : launch_with_pdl(token_logprob_grad<false>, grid, dim3(threads), 0, st, a);
+}
+
+}  // namespace nf

@@ -39,4 +39,17 @@ cudaError_t launch_embedding_bwd(void* dtable, bool f32, bool add, const void* d
                                  int64_t tokens, int64_t vocab, int64_t hidden, float scale, void* workspace,
                                  int sms, cudaStream_t st);
 
+// Log probabilities of given tokens with entropy and alternatives (top 0 to
+// kLogprobMaxTop), and the gradient.  Strides in elements.
+constexpr int64_t kLogprobMaxVocab = 1 << 30;
+constexpr int kLogprobMaxTop = 32;
+cudaError_t launch_token_logprob_fwd(float* logprob, float* entropy, float* stats, float* top_logprob,
+                                     int64_t* top_ids, const void* logits, bool f32, const void* targets,
+                                     bool wide, int64_t rows, int64_t vocab, int64_t stride, float temperature,
+                                     int top, int sms, cudaStream_t st);
+cudaError_t launch_token_logprob_bwd(void* out, const void* logits, bool f32, const void* targets, bool wide,
+                                     const float* stats, const float* entropy, const float* d_logprob,
+                                     const float* d_entropy, int64_t rows, int64_t vocab, int64_t stride,
+                                     int64_t out_stride, float temperature, cudaStream_t st);
+
 }  // namespace nf

@@ -114,3 +114,63 @@ def test_embedding_helper_refusals():
         nf.embedding_fwd(ids, table)
     with pytest.raises(TypeError):
         nf.embedding_bwd(table[:3], [0, 1, 2], 10)
+
+
+# ---------------------------------------------------------------- token log probabilities
+
+F = 7 << 36
+G = 8 << 36
+H = 9 << 36
+
+
+def logprob(lp=A, ent=B, stats=C, top_lp=D, top_ids=E, logits=F, kind=nf.NF_BF16, stride=100, targets=G,
+            id_bytes=8, rows=4, vocab=100, temperature=1.0, top=5):
+    return nf.nf_token_logprob_fwd(lp, ent, stats, top_lp, top_ids, logits, kind, stride, targets, id_bytes,
+                                   rows, vocab, temperature, top, None)
+
+
+def logprob_grad(out=A, dstride=100, logits=F, kind=nf.NF_BF16, stride=100, targets=G, id_bytes=8, stats=C,
+                 ent=B, d_lp=D, d_ent=E, rows=4, vocab=100, temperature=1.0):
+    return nf.nf_token_logprob_bwd(out, dstride, logits, kind, stride, targets, id_bytes, stats, ent, d_lp,
+                                   d_ent, rows, vocab, temperature, None)
+
+
+@pytest.mark.parametrize("call", [logprob, logprob_grad])
+def test_logprob_refusals(call):
+    nan, inf = float("nan"), float("inf")
+    for bad in ({"kind": 2}, {"kind": -1}, {"id_bytes": 2}, {"rows": -1}, {"rows": BIG}, {"vocab": 0}, {"vocab": -1},
+                {"vocab": (1 << 30) + 1, "stride": 1 << 31}, {"stride": 99}, {"stride": BIG}, {"stride": -100},
+                {"temperature": 0.0}, {"temperature": -1.0}, {"temperature": nan}, {"temperature": inf},
+                {"temperature": 1e-30}, {"temperature": 1e30}, {"logits": None}, {"targets": None}, {"stats": None}):
+        assert call(**bad) == nf.NF_ERR_INVALID_ARG, bad
+    for bad in ({"logits": F + 1}, {"logits": F + 2, "kind": nf.NF_F32}, {"targets": G + 4}, {"stats": C + 4}):
+        assert call(**bad) == nf.NF_ERR_MISALIGNED, bad
+    assert call(rows=0, logits=None, targets=None, stats=None) == nf.NF_OK
+
+
+def test_logprob_fwd_outputs():
+    for bad in ({"lp": None}, {"ent": None}, {"top_lp": None}, {"top_ids": None}, {"top": -1}, {"top": 33},
+                {"lp": B}, {"lp": F}, {"lp": F + 3 * 200 + 196}, {"ent": G + 8}, {"stats": F + 8}, {"top_lp": F},
+                {"top_ids": D + 16}, {"top_ids": G}, {"top_lp": A + 8}):
+        assert logprob(**bad) == nf.NF_ERR_INVALID_ARG, bad
+    for bad in ({"lp": A + 2}, {"ent": B + 1}, {"top_lp": D + 2}, {"top_ids": E + 4}):
+        assert logprob(**bad) == nf.NF_ERR_MISALIGNED, bad
+
+
+def test_logprob_bwd_outputs():
+    for bad in ({"out": None}, {"d_lp": None}, {"ent": None}, {"dstride": 99}, {"out": F + 2}, {"out": F + 790},
+                {"out": F, "dstride": 108}, {"out": G}, {"out": C}, {"out": B}, {"out": D}, {"out": E}):
+        assert logprob_grad(**bad) == nf.NF_ERR_INVALID_ARG, bad
+    for bad in ({"out": A + 1}, {"d_lp": D + 2}, {"d_ent": E + 2}, {"ent": B + 2}):
+        assert logprob_grad(**bad) == nf.NF_ERR_MISALIGNED, bad
+
+
+def test_logprob_helper_refusals():
+    logits = torch.zeros(3, 10)
+    ids = torch.zeros(3, dtype=torch.int64)
+    with pytest.raises(ValueError, match="CUDA"):
+        nf.token_logprob_fwd(logits, ids)
+    with pytest.raises(TypeError):
+        nf.token_logprob_fwd(logits.double(), ids)
+    with pytest.raises(TypeError):
+        nf.token_logprob_bwd(None, ids, None, None, None)
