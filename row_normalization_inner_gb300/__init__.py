@@ -147,6 +147,8 @@ def _bind(lib):
 def lib():
     """The loaded libnf.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -525,37 +527,86 @@ def outer_norm_bwd(dy, x, mean, rstd, gamma, workspace=None, out=None, stream=No
     return dx, dgamma, dbeta
 
 
-def _same_device(first, *rest):
-    """The tensors lie on the current device, whose stream and context the call uses."""
+# The token-side operators' helpers.  A decode step's call takes 2 us on the
+# GPU, so they spend little on the host: one pass of checks per tensor, the
+# raw stream handle, outputs allocated once the arguments are known to fit.
+
+def _device(t, name, *dtypes):
+    """Device index of a CUDA tensor of one of the types; it must be the
+    current device, whose context and stream the call uses."""
     import torch
-    dev = first.get_device()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
     if dev != torch.cuda.current_device():
-        raise ValueError(f"tensors are on cuda:{dev}, which is not the current device")
-    for t in rest:
-        if t is not None and t.get_device() != dev:
-            raise ValueError("tensors are on different devices")
+        raise ValueError(f"{name} is on cuda:{dev}, which is not the current device")
+    return dev
 
 
-def _q8_outputs(x, rows, hidden, fmt, group, out, scale):
+def _need_on(dev, t, dtype, name, contiguous=True):
     import torch
-    if fmt not in Q8_FORMATS:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA tensor on cuda:{dev}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _stream_on(dev):
+    """The current stream's handle (torch.cuda.current_stream() builds a Stream object first, 3 us)."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _rmsnorm_q8(x, residual, weight, eps, fmt, group, out, scale):
+    import torch
+    bf16 = torch.bfloat16
+    dev = _device(x, "x", bf16)
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
+    _need_on(dev, weight, bf16, "weight")
+    shape = x.shape
+    hidden = shape[-1] if shape else 0
+    rows = x.numel() // hidden if hidden else 0
+    if weight.shape != (hidden,):
+        raise ValueError("weight must be of shape [hidden]")
+    if residual is not None:
+        _need_on(dev, residual, bf16, "residual")
+        if residual.shape != shape:
+            raise ValueError("residual must have x's shape")
+    code = Q8_FORMATS.get(fmt)
+    if code is None:
         raise ValueError(f"fmt must be one of {tuple(Q8_FORMATS)}, got {fmt!r}")
-    if group not in (0, Q8_GROUP):
+    if group != 0 and group != Q8_GROUP:
         raise ValueError(f"group must be 0 (one scale per row) or {Q8_GROUP}, got {group!r}")
-    dtype = torch.float8_e4m3fn if fmt == "e4m3" else torch.int8
-    shape = x.shape[:-1] + (-(-hidden // group),) if group else x.shape[:-1]
-    if out is None:
-        out = torch.empty(x.shape, dtype=dtype, device=x.device)
-    else:
-        _need(out, dtype, "out")
-        if out.shape != x.shape:
+    dtype = torch.float8_e4m3fn if code == NF_Q8_E4M3 else torch.int8
+    if out is not None:
+        _need_on(dev, out, dtype, "out")
+        if out.shape != shape:
             raise ValueError("out must have x's shape")
+    scale_shape = shape[:-1] + (-(-hidden // group),) if group else shape[:-1]
+    if scale is not None:
+        _need_on(dev, scale, torch.float32, "scale")
+        if scale.shape != scale_shape:
+            raise ValueError(f"scale must be of shape {tuple(scale_shape)}")
+    if out is None:
+        out = torch.empty_like(x, dtype=dtype)
     if scale is None:
-        scale = torch.empty(shape, dtype=torch.float32, device=x.device)
+        scale = torch.empty(scale_shape, dtype=torch.float32, device=x.device)
+    if residual is None:
+        _check(nf_rmsnorm_q8(out.data_ptr(), scale.data_ptr(), x.data_ptr(), weight.data_ptr(), rows,
+                             hidden, eps, code, group, _stream_on(dev)), "nf_rmsnorm_q8")
     else:
-        _need(scale, torch.float32, "scale")
-        if scale.shape != shape:
-            raise ValueError(f"scale must be of shape {tuple(shape)}")
+        _check(nf_fused_add_rmsnorm_q8(out.data_ptr(), scale.data_ptr(), x.data_ptr(),
+                                       residual.data_ptr(), weight.data_ptr(), rows, hidden, eps, code,
+                                       group, _stream_on(dev)), "nf_fused_add_rmsnorm_q8")
     return out, scale
 
 
@@ -565,20 +616,11 @@ def rmsnorm_q8(x, weight, eps: float = 1e-6, fmt: str = "e4m3", group: int = 0, 
     float8_e4m3fn or int8 (fmt), scale fp32 of shape [...] (one per row) or
     [..., ceil(hidden / 128)] (group=128); q * scale stands for the
     normalized rows, which are not rounded to bf16 in between."""
-    import torch
     if stream is not None:
+        import torch
         with torch.cuda.stream(stream):
-            return rmsnorm_q8(x, weight, eps, fmt, group, out, scale)
-    _need(x, torch.bfloat16, "x")
-    _need(weight, torch.bfloat16, "weight")
-    rows, hidden = _rows_hidden(x)
-    if weight.shape != (hidden,):
-        raise ValueError("shape mismatch")
-    q, scale = _q8_outputs(x, rows, hidden, fmt, group, out, scale)
-    _same_device(x, weight, q, scale)
-    _check(nf_rmsnorm_q8(q.data_ptr(), scale.data_ptr(), x.data_ptr(), weight.data_ptr(), rows,
-                         hidden, eps, Q8_FORMATS[fmt], group, _stream()), "nf_rmsnorm_q8")
-    return q, scale
+            return _rmsnorm_q8(x, None, weight, eps, fmt, group, out, scale)
+    return _rmsnorm_q8(x, None, weight, eps, fmt, group, out, scale)
 
 
 def fused_add_rmsnorm_q8(x, residual, weight, eps: float = 1e-6, fmt: str = "e4m3",
@@ -587,32 +629,24 @@ def fused_add_rmsnorm_q8(x, residual, weight, eps: float = 1e-6, fmt: str = "e4m
     as rmsnorm_q8 does (from the fp32 sums, as fused_add_rmsnorm).  x is left
     as it was."""
     import torch
+    if residual is None:
+        raise TypeError("residual must be a tensor")
     if stream is not None:
         with torch.cuda.stream(stream):
-            return fused_add_rmsnorm_q8(x, residual, weight, eps, fmt, group, out, scale)
-    for t, n in ((x, "x"), (residual, "residual"), (weight, "weight")):
-        _need(t, torch.bfloat16, n)
-    rows, hidden = _rows_hidden(x)
-    if residual.shape != x.shape or weight.shape != (hidden,):
-        raise ValueError("shape mismatch")
-    q, scale = _q8_outputs(x, rows, hidden, fmt, group, out, scale)
-    _same_device(x, residual, weight, q, scale)
-    _check(nf_fused_add_rmsnorm_q8(q.data_ptr(), scale.data_ptr(), x.data_ptr(),
-                                   residual.data_ptr(), weight.data_ptr(), rows, hidden, eps,
-                                   Q8_FORMATS[fmt], group, _stream()),
-           "nf_fused_add_rmsnorm_q8")
-    return q, scale
+            return _rmsnorm_q8(x, residual, weight, eps, fmt, group, out, scale)
+    return _rmsnorm_q8(x, residual, weight, eps, fmt, group, out, scale)
 
 
-def _need_ids(ids, name):
-    """Bytes per id of a contiguous int32 / int64 CUDA tensor."""
+def _id_bytes(ids, name):
+    """Bytes per id of an int32 / int64 tensor."""
     import torch
     if not isinstance(ids, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
-    if ids.dtype not in (torch.int64, torch.int32):
-        raise TypeError(f"{name} must be torch.int32 or torch.int64, got {ids.dtype}")
-    _need(ids, ids.dtype, name)
-    return 8 if ids.dtype == torch.int64 else 4
+    if ids.dtype is torch.int64:
+        return 8
+    if ids.dtype is torch.int32:
+        return 4
+    raise TypeError(f"{name} must be torch.int32 or torch.int64, got {ids.dtype}")
 
 
 def embedding_fwd(ids, table, scale: float = 1.0, out=None, stream=None):
@@ -622,21 +656,21 @@ def embedding_fwd(ids, table, scale: float = 1.0, out=None, stream=None):
     if stream is not None:
         with torch.cuda.stream(stream):
             return embedding_fwd(ids, table, scale, out)
-    id_bytes = _need_ids(ids, "ids")
-    _need(table, torch.bfloat16, "table")
-    if table.dim() != 2:
-        raise ValueError("table must be [vocab, hidden]")
+    id_bytes = _id_bytes(ids, "ids")
+    dev = _device(table, "table", torch.bfloat16)
+    _need_on(dev, ids, ids.dtype, "ids")
+    if table.dim() != 2 or not table.is_contiguous():
+        raise ValueError("table must be [vocab, hidden] and contiguous")
     vocab, hidden = table.shape
     shape = ids.shape + (hidden,)
     if out is None:
         out = torch.empty(shape, dtype=torch.bfloat16, device=table.device)
     else:
-        _need(out, torch.bfloat16, "out")
+        _need_on(dev, out, torch.bfloat16, "out")
         if out.shape != shape:
             raise ValueError(f"out must be of shape {tuple(shape)}")
-    _same_device(table, ids, out)
     _check(nf_embedding_fwd(out.data_ptr(), ids.data_ptr(), id_bytes, table.data_ptr(), ids.numel(),
-                            vocab, hidden, scale, _stream()), "nf_embedding_fwd")
+                            vocab, hidden, scale, _stream_on(dev)), "nf_embedding_fwd")
     return out
 
 
@@ -652,54 +686,57 @@ def embedding_bwd(dy, ids, vocab: int, scale: float = 1.0, dtype=None, accumulat
     if stream is not None:
         with torch.cuda.stream(stream):
             return embedding_bwd(dy, ids, vocab, scale, dtype, accumulate, out, workspace)
-    id_bytes = _need_ids(ids, "ids")
-    _need(dy, torch.bfloat16, "dy")
-    if dy.dim() < 1 or dy.shape[:-1] != ids.shape:
-        raise ValueError("dy must be of shape [*ids.shape, hidden]")
+    id_bytes = _id_bytes(ids, "ids")
+    dev = _device(dy, "dy", torch.bfloat16)
+    _need_on(dev, ids, ids.dtype, "ids")
+    if dy.dim() < 1 or dy.shape[:-1] != ids.shape or not dy.is_contiguous():
+        raise ValueError("dy must be of shape [*ids.shape, hidden] and contiguous")
     hidden = dy.shape[-1]
     if accumulate is not None and out is not None:
         raise ValueError("accumulate is written in place: out cannot be given too")
     grad = accumulate if accumulate is not None else out
     if grad is None:
         grad = torch.empty((vocab, hidden), dtype=dtype or torch.float32, device=dy.device)
-    if grad.dtype not in (torch.float32, torch.bfloat16) or (dtype is not None and grad.dtype != dtype):
-        raise TypeError(f"the gradient must be {dtype or 'torch.float32 or torch.bfloat16'}, got {grad.dtype}")
-    _need(grad, grad.dtype, "the gradient")
+    elif not isinstance(grad, torch.Tensor):
+        raise TypeError("the gradient must be a tensor")
+    kind = grad.dtype
+    if (kind is not torch.float32 and kind is not torch.bfloat16) or (dtype is not None and kind is not dtype):
+        raise TypeError(f"the gradient must be {dtype or 'torch.float32 or torch.bfloat16'}, got {kind}")
+    _need_on(dev, grad, kind, "the gradient")
     if grad.shape != (vocab, hidden):
         raise ValueError(f"the gradient must be of shape {(vocab, hidden)}")
     tokens = ids.numel()
     if workspace is None:
+        # freed right after the launches: the allocator hands the block to
+        # later work on the same stream only, which runs after these kernels
         workspace = torch.empty(max(nf_embedding_bwd_workspace_size(tokens, hidden), 16),
                                 dtype=torch.uint8, device=dy.device)
-    _same_device(dy, ids, grad, workspace)
-    _check(nf_embedding_bwd(grad.data_ptr(), NF_F32 if grad.dtype == torch.float32 else NF_BF16,
+    else:
+        _need_on(dev, workspace, workspace.dtype, "workspace")
+    _check(nf_embedding_bwd(grad.data_ptr(), NF_F32 if kind is torch.float32 else NF_BF16,
                             int(accumulate is not None), dy.data_ptr(), ids.data_ptr(), id_bytes, tokens,
                             vocab, hidden, scale, workspace.data_ptr(),
-                            workspace.numel() * workspace.element_size(), _stream()), "nf_embedding_bwd")
+                            workspace.numel() * workspace.element_size(), _stream_on(dev)),
+           "nf_embedding_bwd")
     return grad
 
 
-def _need_logits(t, name):
-    """(nf_dtype, row stride) of a [rows, vocab] CUDA tensor whose rows may be apart."""
-    import torch
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a tensor")
-    if t.dtype not in (torch.bfloat16, torch.float32):
-        raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
+def _logits_stride(t, name):
+    """Row stride of a [rows, vocab] tensor whose rows may be apart."""
     if t.dim() != 2:
         raise ValueError(f"{name} must be [rows, vocab]")
     rows, vocab = t.shape
-    stride = t.stride(0) if rows > 1 else max(vocab, 1)
-    if (vocab > 1 and t.stride(1) != 1) or stride < vocab:
+    row_stride, stride = t.stride()
+    if rows <= 1:
+        row_stride = max(vocab, 1)
+    if (vocab > 1 and stride != 1) or row_stride < vocab:
         raise ValueError(f"{name}'s rows must be contiguous and apart")
-    return (NF_F32 if t.dtype == torch.float32 else NF_BF16), stride
+    return row_stride
 
 
-def _need_rows(t, rows, name):
+def _need_rows(dev, t, rows, name):
     import torch
-    _need(t, torch.float32, name)
+    _need_on(dev, t, torch.float32, name)
     if t.shape != (rows,):
         raise ValueError(f"{name} must be of shape {(rows,)}")
 
@@ -718,26 +755,28 @@ def token_logprob_fwd(logits, targets, temperature: float = 1.0, top: int = 0, s
     if stream is not None:
         with torch.cuda.stream(stream):
             return token_logprob_fwd(logits, targets, temperature, top)
-    kind, stride = _need_logits(logits, "logits")
-    id_bytes = _need_ids(targets, "targets")
+    dev = _device(logits, "logits", torch.bfloat16, torch.float32)
+    stride = _logits_stride(logits, "logits")
+    id_bytes = _id_bytes(targets, "targets")
+    _need_on(dev, targets, targets.dtype, "targets")
+    kind = NF_F32 if logits.dtype is torch.float32 else NF_BF16
     rows, vocab = logits.shape
     if targets.shape != (rows,):
         raise ValueError(f"targets must be of shape {(rows,)}")
     if not 0 <= top <= TOP_MAX:
         raise ValueError(f"top must be 0 to {TOP_MAX}, got {top}")
-    _same_device(logits, targets)
-    dev = logits.device
-    logprob = torch.empty(rows, dtype=torch.float32, device=dev)
-    entropy = torch.empty(rows, dtype=torch.float32, device=dev)
-    stats = torch.empty((rows, 2), dtype=torch.float32, device=dev)
-    top_logprob = top_ids = None
+    device, f32 = logits.device, torch.float32
+    logprob = torch.empty(rows, dtype=f32, device=device)
+    entropy = torch.empty(rows, dtype=f32, device=device)
+    stats = torch.empty((rows, 2), dtype=f32, device=device)
+    top_logprob = top_ids = lp_ptr = id_ptr = None
     if top:
-        top_logprob = torch.empty((rows, top), dtype=torch.float32, device=dev)
-        top_ids = torch.empty((rows, top), dtype=torch.int64, device=dev)
-    _check(nf_token_logprob_fwd(logprob.data_ptr(), entropy.data_ptr(), stats.data_ptr(),
-                                top_logprob.data_ptr() if top else None, top_ids.data_ptr() if top else None,
+        top_logprob = torch.empty((rows, top), dtype=f32, device=device)
+        top_ids = torch.empty((rows, top), dtype=torch.int64, device=device)
+        lp_ptr, id_ptr = top_logprob.data_ptr(), top_ids.data_ptr()
+    _check(nf_token_logprob_fwd(logprob.data_ptr(), entropy.data_ptr(), stats.data_ptr(), lp_ptr, id_ptr,
                                 logits.data_ptr(), kind, stride, targets.data_ptr(), id_bytes, rows, vocab,
-                                temperature, top, _stream()), "nf_token_logprob_fwd")
+                                temperature, top, _stream_on(dev)), "nf_token_logprob_fwd")
     return logprob, entropy, stats, top_logprob, top_ids
 
 
@@ -750,29 +789,35 @@ def token_logprob_bwd(logits, targets, stats, entropy, d_logprob, d_entropy=None
     if stream is not None:
         with torch.cuda.stream(stream):
             return token_logprob_bwd(logits, targets, stats, entropy, d_logprob, d_entropy, temperature, out)
-    kind, stride = _need_logits(logits, "logits")
-    id_bytes = _need_ids(targets, "targets")
+    dev = _device(logits, "logits", torch.bfloat16, torch.float32)
+    stride = _logits_stride(logits, "logits")
+    id_bytes = _id_bytes(targets, "targets")
+    _need_on(dev, targets, targets.dtype, "targets")
+    kind = NF_F32 if logits.dtype is torch.float32 else NF_BF16
     rows, vocab = logits.shape
     if targets.shape != (rows,):
         raise ValueError(f"targets must be of shape {(rows,)}")
-    _need(stats, torch.float32, "stats")
+    _need_on(dev, stats, torch.float32, "stats")
     if stats.shape != (rows, 2):
         raise ValueError(f"stats must be of shape {(rows, 2)}")
-    _need_rows(d_logprob, rows, "d_logprob")
+    _need_rows(dev, d_logprob, rows, "d_logprob")
+    ent_ptr = d_ent_ptr = None
     if d_entropy is not None:
-        _need_rows(d_entropy, rows, "d_entropy")
-        _need_rows(entropy, rows, "entropy")
+        _need_rows(dev, d_entropy, rows, "d_entropy")
+        _need_rows(dev, entropy, rows, "entropy")
+        ent_ptr, d_ent_ptr = entropy.data_ptr(), d_entropy.data_ptr()
     if out is None:
         out = torch.empty((rows, vocab), dtype=logits.dtype, device=logits.device)
-    out_kind, out_stride = _need_logits(out, "out")
-    if out_kind != kind or out.shape != logits.shape:
-        raise ValueError("out must have the logits' type and shape")
-    _same_device(logits, targets, stats, entropy, d_logprob, d_entropy, out)
+        out_stride = max(vocab, 1)
+    else:
+        if not isinstance(out, torch.Tensor) or out.dtype is not logits.dtype or out.shape != logits.shape:
+            raise ValueError("out must have the logits' type and shape")
+        _need_on(dev, out, out.dtype, "out", contiguous=False)
+        out_stride = _logits_stride(out, "out")
     _check(nf_token_logprob_bwd(out.data_ptr(), out_stride, logits.data_ptr(), kind, stride,
-                                targets.data_ptr(), id_bytes, stats.data_ptr(),
-                                None if entropy is None else entropy.data_ptr(), d_logprob.data_ptr(),
-                                None if d_entropy is None else d_entropy.data_ptr(), rows, vocab,
-                                temperature, _stream()), "nf_token_logprob_bwd")
+                                targets.data_ptr(), id_bytes, stats.data_ptr(), ent_ptr,
+                                d_logprob.data_ptr(), d_ent_ptr, rows, vocab, temperature,
+                                _stream_on(dev)), "nf_token_logprob_bwd")
     return out
 
 

@@ -91,28 +91,27 @@ __device__ __forceinline__ uint32_t key_of(const void* ids, bool wide, int64_t i
 // Lanes of the warp whose digit is this lane's.
 __device__ __forceinline__ uint32_t lanes_like(uint32_t digit) { return __match_any_sync(0xFFFFFFFFu, digit); }
 
-// Stable ranks of a tile's digits (key >> shift) & mask.  Warp w holds the
-// items [w * 32 * ITEMS, (w + 1) * 32 * ITEMS) of the tile, item k of a lane
-// at k * 32 + lane; bit k of `valid` says whether the lane has it.  counts:
-// kBins of each warp, zeroed here.  On return the low 16 bits of rank[k] are
-// the number of items of the same digit before this one in its warp (the
-// high 16 are kept), counts[w * kBins + d] is the number of items of digit d
-// in the warps before w, and total[d] the tile's items of digit d.  Threads =
-// 32 * warps.
-template <int ITEMS>
-__device__ __forceinline__ void rank_tile(const uint32_t (&key)[ITEMS], uint32_t valid, int shift,
-                                          uint32_t mask, uint16_t* counts, int warps, uint32_t* total,
-                                          uint32_t (&rank)[ITEMS]) {
-    const int t = threadIdx.x, lane = t & 31, warp = t >> 5, threads = warps * 32;
+// Stable ranks of a tile's digits (key >> shift) & (bins - 1).  Warp w holds
+// the items [w * 32 * ITEMS, (w + 1) * 32 * ITEMS) of the tile, item k of a
+// lane at k * 32 + lane; bit k of `valid` says whether the lane has it.
+// counts: `bins` of each warp, zeroed here.  On return the low 16 bits of
+// rank[k] are the number of items of the same digit before this one in its
+// warp (the high 16 are kept), counts[w * bins + d] is the number of items of
+// digit d in the warps before w, and total[d] the tile's items of digit d.
+template <int THREADS, int ITEMS>
+__device__ __forceinline__ void rank_tile(const uint32_t (&key)[ITEMS], uint32_t valid, int shift, int bins,
+                                          uint16_t* counts, uint32_t* total, uint32_t (&rank)[ITEMS]) {
+    constexpr int kWarps = THREADS / 32;
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     uint32_t* words = reinterpret_cast<uint32_t*>(counts);
-    for (int i = t; i < warps * kBins / 2; i += threads) words[i] = 0;
+    for (int i = t; i < kWarps * bins / 2; i += THREADS) words[i] = 0;
     __syncthreads();
-    uint16_t* mine = counts + warp * kBins;
+    uint16_t* mine = counts + warp * bins;
 #pragma unroll
     for (int k = 0; k < ITEMS; ++k) {
         const bool have = (valid >> k) & 1;
         // lanes past the end match each other only
-        const uint32_t d = have ? (key[k] >> shift) & mask : kBins;
+        const uint32_t d = have ? (key[k] >> shift) & (bins - 1) : kBins;
         const uint32_t like = lanes_like(d);
         const int before = __popc(like & ((1u << lane) - 1));
         const uint32_t c = have ? mine[d] : 0;
@@ -122,11 +121,12 @@ __device__ __forceinline__ void rank_tile(const uint32_t (&key)[ITEMS], uint32_t
         rank[k] = (rank[k] & 0xFFFF0000u) | (c + before);
     }
     __syncthreads();
-    for (int d = t; d < kBins; d += threads) {
+    for (int d = t; d < bins; d += THREADS) {
         uint32_t sum = 0;
-        for (int w = 0; w < warps; ++w) {
-            const uint32_t c = counts[w * kBins + d];
-            counts[w * kBins + d] = static_cast<uint16_t>(sum);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const uint32_t c = counts[w * bins + d];
+            counts[w * bins + d] = static_cast<uint16_t>(sum);
             sum += c;
         }
         total[d] = sum;
@@ -134,85 +134,87 @@ __device__ __forceinline__ void rank_tile(const uint32_t (&key)[ITEMS], uint32_t
     __syncthreads();
 }
 
-// Exclusive prefix sum of kBins values in shared memory by the first warp.
-// The caller synchronizes before and after.
-__device__ __forceinline__ void scan_bins(uint32_t* bins) {
-    if (threadIdx.x >= 32) return;
-    constexpr int per = kBins / 32;
-    uint32_t sum = 0;
-    for (int i = 0; i < per; ++i) sum += bins[threadIdx.x * per + i];
-    uint32_t run = sum;
+// Exclusive prefix sum of bins <= 2 * THREADS values in shared memory, by the
+// whole CTA.  The values must be visible on entry; synchronized on return.
+template <int THREADS>
+__device__ __forceinline__ void scan_bins(uint32_t* values, int bins, uint32_t* warp_sums) {
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    const uint32_t a = 2 * t < bins ? values[2 * t] : 0, b = 2 * t + 1 < bins ? values[2 * t + 1] : 0;
+    uint32_t run = a + b;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
         const uint32_t up = __shfl_up_sync(0xFFFFFFFFu, run, off);
-        if (threadIdx.x >= off) run += up;
+        if (lane >= off) run += up;
     }
-    run -= sum;
-    for (int i = 0; i < per; ++i) {
-        const uint32_t c = bins[threadIdx.x * per + i];
-        bins[threadIdx.x * per + i] = run;
-        run += c;
-    }
+    if (lane == 31) warp_sums[warp] = run;
+    __syncthreads();
+    const uint32_t w = lane < warp ? warp_sums[lane] : 0;
+    run += __reduce_add_sync(0xFFFFFFFFu, w);
+    if (2 * t < bins) values[2 * t] = run - a - b;
+    if (2 * t + 1 < bins) values[2 * t + 1] = run - b;
+    __syncthreads();
 }
 
-// One CTA sorts all tokens: every pass in shared memory.
-constexpr int kOneThreads = 1024;
-constexpr int kOneItems = 16;
-constexpr int kSortOne = kOneThreads * kOneItems;  // 16384
-constexpr size_t kOneSmem = kSortOne * 4 + kSortOne * 2 + kOneThreads / 32 * kBins * 2 + kBins * 4;
+// One CTA sorts all tokens: every pass in shared memory.  A thread holds
+// ITEMS of them; small batches take the variant with the fewest.
+constexpr int kSortOne = 16384;
+template <int THREADS, int ITEMS>
+constexpr size_t sort_one_smem(int bins) {
+    return static_cast<size_t>(THREADS) * ITEMS * 6 + static_cast<size_t>(THREADS / 32) * bins * 2 + bins * 4 + 128;
+}
 
-__global__ void __launch_bounds__(kOneThreads)
+template <int THREADS, int ITEMS>
+__global__ void __launch_bounds__(THREADS)
 sort_one(const void* __restrict__ ids, bool wide, int n, int64_t vocab, int bits, int passes,
          uint32_t* __restrict__ keys_out, uint32_t* __restrict__ at_out) {
     extern __shared__ __align__(16) unsigned char smem[];
+    const int bins = 1 << bits;
     uint32_t* keys = reinterpret_cast<uint32_t*>(smem);
-    uint16_t* at = reinterpret_cast<uint16_t*>(keys + kSortOne);  // kSortOne tokens: 16 bits
-    uint16_t* counts = at + kSortOne;
-    uint32_t* total = reinterpret_cast<uint32_t*>(counts + kOneThreads / 32 * kBins);
+    uint32_t* total = keys + THREADS * ITEMS;
+    uint32_t* warp_sums = total + bins;
+    uint16_t* at = reinterpret_cast<uint16_t*>(warp_sums + 32);  // at most kSortOne tokens: 16 bits
+    uint16_t* counts = at + THREADS * ITEMS;
     grid_dep_wait();
     grid_dep_release();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    // small calls use fewer items per thread: warp w holds 32 * items tokens
-    const int items = (n + kOneThreads - 1) / kOneThreads;
-    const uint32_t mask = (1u << bits) - 1;
-    uint32_t key[kOneItems], pr[kOneItems];  // pr: the token in the high 16 bits, its rank in the low
+    uint32_t key[ITEMS], pr[ITEMS];  // pr: the token in the high 16 bits, its rank in the low
     uint32_t valid = 0;
 #pragma unroll
-    for (int k = 0; k < kOneItems; ++k) {
-        const int i = (warp * items + k) * 32 + lane;
-        const bool have = k < items && i < n;
+    for (int k = 0; k < ITEMS; ++k) {
+        const int i = (warp * ITEMS + k) * 32 + lane;
+        const bool have = i < n;
         valid |= static_cast<uint32_t>(have) << k;
         key[k] = have ? key_of(ids, wide, i, vocab) : 0;
         pr[k] = static_cast<uint32_t>(i) << 16;
     }
     for (int p = 0; p < passes; ++p) {
         const int shift = p * bits;
-        rank_tile<kOneItems>(key, valid, shift, mask, counts, kOneThreads / 32, total, pr);
-        scan_bins(total);
-        __syncthreads();
+        rank_tile<THREADS, ITEMS>(key, valid, shift, bins, counts, total, pr);
+        scan_bins<THREADS>(total, bins, warp_sums);
+        const bool last = p == passes - 1;
 #pragma unroll
-        for (int k = 0; k < kOneItems; ++k) {
+        for (int k = 0; k < ITEMS; ++k) {
             if (!((valid >> k) & 1)) continue;
-            const uint32_t d = (key[k] >> shift) & mask;
-            const uint32_t to = total[d] + counts[warp * kBins + d] + (pr[k] & 0xFFFFu);
-            keys[to] = key[k];
-            at[to] = static_cast<uint16_t>(pr[k] >> 16);
+            const uint32_t d = (key[k] >> shift) & (bins - 1);
+            const uint32_t to = total[d] + counts[warp * bins + d] + (pr[k] & 0xFFFFu);
+            if (last) {
+                keys_out[to] = key[k];
+                at_out[to] = pr[k] >> 16;
+            } else {
+                keys[to] = key[k];
+                at[to] = static_cast<uint16_t>(pr[k] >> 16);
+            }
         }
+        if (last) break;
         __syncthreads();
-        if (p == passes - 1) break;
 #pragma unroll
-        for (int k = 0; k < kOneItems; ++k) {
-            const int i = (warp * items + k) * 32 + lane;
+        for (int k = 0; k < ITEMS; ++k) {
+            const int i = (warp * ITEMS + k) * 32 + lane;
             if ((valid >> k) & 1) {
                 key[k] = keys[i];
                 pr[k] = static_cast<uint32_t>(at[i]) << 16;
             }
         }
-        __syncthreads();
-    }
-    for (int i = threadIdx.x; i < n; i += kOneThreads) {
-        keys_out[i] = keys[i];
-        at_out[i] = at[i];
     }
 }
 
@@ -241,8 +243,8 @@ sort_count(const void* __restrict__ ids, bool wide, const uint32_t* __restrict__
         if (ok && __popc(like & ((1u << (threadIdx.x & 31)) - 1)) == 0) atomicAdd(&bins[d], __popc(like));
     }
     __syncthreads();
-    for (int d = threadIdx.x; d < kBins; d += kTileThreads)
-        hist[static_cast<int64_t>(blockIdx.x) * kBins + d] = bins[d];
+    for (int d = threadIdx.x; d < 1 << bits; d += kTileThreads)
+        hist[(static_cast<int64_t>(blockIdx.x) << bits) + d] = bins[d];
 }
 
 __global__ void __launch_bounds__(kTileThreads)
@@ -251,12 +253,12 @@ sort_scatter(const void* __restrict__ ids, bool wide, const uint32_t* __restrict
              const uint32_t* __restrict__ hist, uint32_t* __restrict__ keys_out,
              uint32_t* __restrict__ at_out) {
     __shared__ __align__(4) uint16_t counts[kTileThreads / 32 * kBins];
-    __shared__ uint32_t total[kBins], first[kBins];
+    __shared__ uint32_t total[kBins], first[kBins], warp_sums[32];
     grid_dep_wait();
     grid_dep_release();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t base = static_cast<int64_t>(blockIdx.x) * kTile;
-    const uint32_t mask = (1u << bits) - 1;
+    const int bins = 1 << bits;
     uint32_t key[kTileItems], pos[kTileItems], rank[kTileItems];
     uint32_t valid = 0;
 #pragma unroll
@@ -268,13 +270,13 @@ sort_scatter(const void* __restrict__ ids, bool wide, const uint32_t* __restrict
         pos[k] = !have ? 0 : at_in ? at_in[i] : static_cast<uint32_t>(i);
         rank[k] = 0;
     }
-    rank_tile<kTileItems>(key, valid, shift, mask, counts, kTileThreads / 32, total, rank);
+    rank_tile<kTileThreads, kTileItems>(key, valid, shift, bins, counts, total, rank);
     // all tiles' items of a digit, and those of the tiles before this one
-    for (int d = threadIdx.x; d < kBins; d += kTileThreads) {
+    for (int d = threadIdx.x; d < bins; d += kTileThreads) {
         uint32_t all = 0, before = 0;
 #pragma unroll 8
         for (int i = 0; i < tiles; ++i) {
-            const uint32_t c = hist[static_cast<int64_t>(i) * kBins + d];
+            const uint32_t c = hist[static_cast<int64_t>(i) * bins + d];
             all += c;
             if (i < static_cast<int>(blockIdx.x)) before += c;
         }
@@ -282,13 +284,12 @@ sort_scatter(const void* __restrict__ ids, bool wide, const uint32_t* __restrict
         first[d] = before;
     }
     __syncthreads();
-    scan_bins(total);
-    __syncthreads();
+    scan_bins<kTileThreads>(total, bins, warp_sums);
 #pragma unroll
     for (int k = 0; k < kTileItems; ++k) {
         if (!((valid >> k) & 1)) continue;
-        const uint32_t d = (key[k] >> shift) & mask;
-        const uint32_t to = total[d] + first[d] + counts[warp * kBins + d] + rank[k];
+        const uint32_t d = (key[k] >> shift) & (bins - 1);
+        const uint32_t to = total[d] + first[d] + counts[warp * bins + d] + rank[k];
         keys_out[to] = key[k];
         at_out[to] = pos[k];
     }
@@ -297,6 +298,7 @@ sort_scatter(const void* __restrict__ ids, bool wide, const uint32_t* __restrict
 // ---- the sums --------------------------------------------------------------------
 constexpr int kSumThreads = 128;   // threads of a column slice, 8 columns each
 constexpr int kSumBatch = 4;       // rows of dy in flight per thread
+constexpr int kSumPart = 256;      // tokens whose ids and numbers are staged at once
 constexpr int kZeroRows = 16;      // rows per CTA that writes zeros
 
 struct EmbedBwd {
@@ -311,40 +313,49 @@ struct EmbedBwd {
     float scale;
 };
 
-// One table row's 8 columns (+)= scale * acc.
+// One table row's 8 columns: (old +) scale * acc.  The old values are loaded
+// apart, so that a batch of rows has its loads in flight together.
 template <bool F32, bool ADD>
-__device__ __forceinline__ void put_row(const EmbedBwd& a, uint32_t key, int v, const float2 (&acc)[4]) {
-    const int64_t off = static_cast<int64_t>(key) * a.hidden + static_cast<int64_t>(v) * kVec;
-    const float2 s2 = make_float2(a.scale, a.scale);
-    if constexpr (F32) {
-        float4* p = reinterpret_cast<float4*>(static_cast<float*>(a.dtable) + off);
-        float2 o[4];
-        if constexpr (ADD) {
-            const float4 x = __ldcs(p), y = __ldcs(p + 1);
-            o[0] = make_float2(x.x, x.y);
-            o[1] = make_float2(x.z, x.w);
-            o[2] = make_float2(y.x, y.y);
-            o[3] = make_float2(y.z, y.w);
-        } else {
-            o[0] = o[1] = o[2] = o[3] = make_float2(0.f, 0.f);
-        }
-#pragma unroll
-        for (int q = 0; q < 4; ++q) o[q] = __ffma2_rn(acc[q], s2, o[q]);
-        __stcs(p, make_float4(o[0].x, o[0].y, o[1].x, o[1].y));
-        __stcs(p + 1, make_float4(o[2].x, o[2].y, o[3].x, o[3].y));
-    } else {
-        uint16_t* p = static_cast<uint16_t*>(a.dtable) + off;
-        float2 o[4];
-        if constexpr (ADD) {
-            unpack8x2(ld_stream(p), o);
-        } else {
-            o[0] = o[1] = o[2] = o[3] = make_float2(0.f, 0.f);
-        }
-#pragma unroll
-        for (int q = 0; q < 4; ++q) o[q] = __ffma2_rn(acc[q], s2, o[q]);
-        st_stream(p, pack8x2(o));
+struct Old {
+    static constexpr int N = F32 ? 2 : 1;  // 16-byte vectors
+    uint4 v[ADD ? N : 1];
+    static __device__ __forceinline__ uint4* place(const EmbedBwd& a, uint32_t key, int col) {
+        return static_cast<uint4*>(a.dtable) + (static_cast<int64_t>(key) * (a.hidden / kVec) + col) * N;
     }
-}
+    __device__ __forceinline__ void load(const EmbedBwd& a, uint32_t key, int col) {
+        const uint4* p = place(a, key, col);
+        if constexpr (ADD) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = ld_stream(p + i);
+        }
+    }
+    __device__ __forceinline__ void put(const EmbedBwd& a, uint32_t key, int col, const float2 (&acc)[4]) const {
+        const float2 s2 = make_float2(a.scale, a.scale);
+        float2 o[4];
+        if constexpr (ADD && F32) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                o[2 * i] = make_float2(__uint_as_float(v[i].x), __uint_as_float(v[i].y));
+                o[2 * i + 1] = make_float2(__uint_as_float(v[i].z), __uint_as_float(v[i].w));
+            }
+        } else if constexpr (ADD) {
+            unpack8x2(v[0], o);
+        } else {
+            o[0] = o[1] = o[2] = o[3] = make_float2(0.f, 0.f);
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) o[q] = __ffma2_rn(acc[q], s2, o[q]);
+        uint4* p = place(a, key, col);
+        if constexpr (F32) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                st_stream(p + i, make_uint4(__float_as_uint(o[2 * i].x), __float_as_uint(o[2 * i].y),
+                                            __float_as_uint(o[2 * i + 1].x), __float_as_uint(o[2 * i + 1].y)));
+        } else {
+            st_stream(p, pack8x2(o));
+        }
+    }
+};
 
 __device__ __forceinline__ void put_piece(float* pieces, int v, const float2 (&acc)[4]) {
     float4* p = reinterpret_cast<float4*>(pieces + static_cast<int64_t>(v) * kVec);
@@ -374,6 +385,7 @@ template <bool F32, bool ADD>
 __global__ void __launch_bounds__(kSumThreads)
 embedding_sums(const EmbedBwd a) {
     __shared__ uint32_t touched[kZeroRows];
+    __shared__ uint32_t keys[kSumPart + kSumBatch], at[kSumPart];  // keys: one more than the part's
     __shared__ int64_t range[2];
     grid_dep_wait();
     grid_dep_release();
@@ -400,42 +412,48 @@ embedding_sums(const EmbedBwd a) {
     }
     const int64_t c = static_cast<int64_t>(blockIdx.x) / a.slices;
     const int v = static_cast<int>(blockIdx.x % a.slices) * kSumThreads + threadIdx.x;
-    if (v >= nv) return;
     const int64_t begin = c * a.chunk;
     const int64_t end = begin + a.chunk < a.tokens ? begin + a.chunk : a.tokens;
     const uint32_t none = static_cast<uint32_t>(a.vocab);
     const uint32_t before = begin > 0 ? a.keys[begin - 1] : none;
-    const uint32_t after = end < a.tokens ? a.keys[end] : none;
     const uint32_t first = a.keys[begin];
     float2 acc[4] = {};
-    for (int64_t i = begin; i < end; i += kSumBatch) {
-        uint32_t key[kSumBatch + 1];
-        uint4 d[kSumBatch];
-#pragma unroll
-        for (int k = 0; k < kSumBatch; ++k) {
-            key[k] = i + k < end ? a.keys[i + k] : none;
-            d[k] = make_uint4(0, 0, 0, 0);
-            if (key[k] != none)
-                d[k] = ld_stream(a.dy + (static_cast<int64_t>(a.at[i + k]) * nv + v) * kVec);
+    for (int64_t part = begin; part < end; part += kSumPart) {
+        const int n = static_cast<int>(end - part < kSumPart ? end - part : kSumPart);
+        __syncthreads();  // the part before this one has been read
+        for (int i = threadIdx.x; i < kSumPart + kSumBatch; i += kSumThreads) {
+            keys[i] = part + i < a.tokens && i <= n ? a.keys[part + i] : none;
+            if (i < n) at[i] = a.at[part + i];
         }
-        key[kSumBatch] = i + kSumBatch < end ? a.keys[i + kSumBatch] : after;
-        if (key[0] == none) break;
+        __syncthreads();
+        if (v >= nv) continue;
+        for (int i = 0; i < n; i += kSumBatch) {
+            if (keys[i] == none) break;
+            uint4 d[kSumBatch];
+            Old<F32, ADD> old[kSumBatch];
 #pragma unroll
-        for (int k = 0; k < kSumBatch; ++k) {
-            if (key[k] == none) break;
-            float2 f[4];
-            unpack8x2(d[k], f);
+            for (int k = 0; k < kSumBatch; ++k) {
+                const uint32_t key = keys[i + k];
+                if (i + k >= n || key == none) continue;
+                d[k] = ld_stream(a.dy + (static_cast<int64_t>(at[i + k]) * nv + v) * kVec);
+                if (ADD && keys[i + k + 1] != key && !(key == first && before == first)) old[k].load(a, key, v);
+            }
 #pragma unroll
-            for (int q = 0; q < 4; ++q) acc[q] = __fadd2_rn(acc[q], f[q]);
-            const bool at_end = i + k + 1 == end;
-            const uint32_t next = at_end ? after : key[k + 1];
-            if (next != key[k]) {  // the run ends here
-                if (key[k] == first && before == first) put_piece(a.pieces + c * 2 * a.hidden, v, acc);
-                else put_row<F32, ADD>(a, key[k], v, acc);
-                acc[0] = acc[1] = acc[2] = acc[3] = make_float2(0.f, 0.f);
-            } else if (at_end) {  // it goes on in the next chunk
-                const int slot = key[k] == first && before == first ? 0 : 1;
-                put_piece(a.pieces + (c * 2 + slot) * a.hidden, v, acc);
+            for (int k = 0; k < kSumBatch; ++k) {
+                const uint32_t key = keys[i + k];
+                if (i + k >= n || key == none) break;
+                float2 f[4];
+                unpack8x2(d[k], f);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) acc[q] = __fadd2_rn(acc[q], f[q]);
+                const bool head = key == first && before == first;  // the run began in an earlier chunk
+                if (keys[i + k + 1] != key) {                       // and ends here
+                    if (head) put_piece(a.pieces + c * 2 * a.hidden, v, acc);
+                    else old[k].put(a, key, v, acc);
+                    acc[0] = acc[1] = acc[2] = acc[3] = make_float2(0.f, 0.f);
+                } else if (part + i + k + 1 == end) {               // it goes on in the next chunk
+                    put_piece(a.pieces + (c * 2 + (head ? 0 : 1)) * a.hidden, v, acc);
+                }
             }
         }
     }
@@ -481,7 +499,9 @@ embedding_join(const EmbedBwd a) {
         acc[2] = __fadd2_rn(acc[2], make_float2(y.x, y.y));
         acc[3] = __fadd2_rn(acc[3], make_float2(y.z, y.w));
     }
-    put_row<F32, ADD>(a, key, v, acc);
+    Old<F32, ADD> old;
+    old.load(a, key, v);
+    old.put(a, key, v, acc);
 }
 
 int64_t round16(int64_t b) { return (b + 15) / 16 * 16; }
@@ -519,6 +539,25 @@ Layout layout(int64_t tokens, int64_t hidden, int sms) {
     l.pieces = take(l.chunks * 2 * hidden * 4);
     l.bytes = at;
     return l;
+}
+
+template <int THREADS, int ITEMS>
+cudaError_t sort_in_one(const void* ids, bool wide, int n, int64_t vocab, int bits, int passes, uint32_t* keys,
+                        uint32_t* at, cudaStream_t st) {
+    static_assert(THREADS * ITEMS <= kSortOne && kBins <= 2 * THREADS, "16-bit token numbers; two bins a thread");
+    static std::atomic<bool> set[64];
+    int dev = 0;
+    if (cudaError_t e = cudaGetDevice(&dev)) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    const auto kernel = sort_one<THREADS, ITEMS>;
+    if (!set[dev].load(std::memory_order_acquire)) {
+        if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 static_cast<int>(sort_one_smem<THREADS, ITEMS>(kBins))))
+            return e;
+        set[dev].store(true, std::memory_order_release);
+    }
+    return launch_with_pdl(kernel, dim3(1), dim3(THREADS), sort_one_smem<THREADS, ITEMS>(1 << bits), st, ids, wide, n,
+                           vocab, bits, passes, keys, at);
 }
 
 template <bool F32, bool ADD>
@@ -564,19 +603,11 @@ cudaError_t launch_embedding_bwd(void* dtable, bool f32, bool add, const void* d
     if (tokens == 0) {
         if (add) return cudaSuccess;
     } else if (!l.tiles) {
-        static std::atomic<bool> set[64];
-        int dev = 0;
-        if (cudaError_t e = cudaGetDevice(&dev)) return e;
-        if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-        if (!set[dev].load(std::memory_order_acquire)) {
-            if (cudaError_t e = cudaFuncSetAttribute(sort_one, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                     static_cast<int>(kOneSmem)))
-                return e;
-            set[dev].store(true, std::memory_order_release);
-        }
-        if (cudaError_t e = launch_with_pdl(sort_one, dim3(1), dim3(kOneThreads), kOneSmem, st, ids, wide,
-                                            static_cast<int>(tokens), vocab, bits, passes, u32(l.keys), u32(l.at)))
-            return e;
+        const int n = static_cast<int>(tokens);
+        const cudaError_t e = n <= 2048   ? sort_in_one<512, 4>(ids, wide, n, vocab, bits, passes, u32(l.keys), u32(l.at), st)
+                              : n <= 4096 ? sort_in_one<1024, 4>(ids, wide, n, vocab, bits, passes, u32(l.keys), u32(l.at), st)
+                                          : sort_in_one<1024, 16>(ids, wide, n, vocab, bits, passes, u32(l.keys), u32(l.at), st);
+        if (e != cudaSuccess) return e;
     } else {
         uint32_t *to_keys = u32(l.keys), *to_at = u32(l.at), *other_keys = u32(l.keys2), *other_at = u32(l.at2);
         const uint32_t *from_keys = nullptr, *from_at = nullptr;

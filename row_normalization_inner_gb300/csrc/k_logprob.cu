@@ -66,6 +66,17 @@ template <> struct Elem<false> {
     static constexpr uint32_t kNone = 0xFF80FF80u;  // -infinity in every element
     static __device__ __forceinline__ void unpack(uint4 v, float2 (&f)[4]) { unpack8x2(v, f); }
     static __device__ __forceinline__ uint4 pack(const float2 (&f)[4]) { return pack8x2(f); }
+    // the largest element of N vectors (a NaN is passed over)
+    template <int N>
+    static __device__ __forceinline__ float largest(const uint4 (&v)[N]) {
+        __nv_bfloat162 m = max2(max2(as2(v[0].x), as2(v[0].y)), max2(as2(v[0].z), as2(v[0].w)));
+#pragma unroll
+        for (int k = 1; k < N; ++k)
+            m = max2(m, max2(max2(as2(v[k].x), as2(v[k].y)), max2(as2(v[k].z), as2(v[k].w))));
+        return fmaxf(__low2float(m), __high2float(m));
+    }
+    static __device__ __forceinline__ __nv_bfloat162 as2(uint32_t w) { return *reinterpret_cast<__nv_bfloat162*>(&w); }
+    static __device__ __forceinline__ __nv_bfloat162 max2(__nv_bfloat162 a, __nv_bfloat162 b) { return __hmax2(a, b); }
     static __device__ __forceinline__ float value(uint16_t b) { return __uint_as_float(static_cast<uint32_t>(b) << 16); }
     static __device__ __forceinline__ uint16_t bits(float f) { return static_cast<uint16_t>(pack2(f, 0.f)); }
 };
@@ -80,6 +91,15 @@ template <> struct Elem<true> {
     static __device__ __forceinline__ uint4 pack(const float2 (&f)[2]) {
         return make_uint4(__float_as_uint(f[0].x), __float_as_uint(f[0].y), __float_as_uint(f[1].x),
                           __float_as_uint(f[1].y));
+    }
+    template <int N>
+    static __device__ __forceinline__ float largest(const uint4 (&v)[N]) {
+        float m = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            m = fmaxf(fmaxf(fmaxf(m, __uint_as_float(v[k].x)), fmaxf(__uint_as_float(v[k].y), __uint_as_float(v[k].z))),
+                      __uint_as_float(v[k].w));
+        return m;
     }
     static __device__ __forceinline__ float value(float f) { return f; }
     static __device__ __forceinline__ float bits(float f) { return f; }
@@ -116,7 +136,8 @@ struct Row {
 };
 
 // ---- forward ---------------------------------------------------------------------
-constexpr int kFwdMaxThreads = 512;
+constexpr int kFwdMaxThreads = 256;
+constexpr int kFwdMinCtas = 5;
 constexpr int kFwdBatch = 4;   // vectors in flight per thread
 constexpr int kTopMax = kLogprobMaxTop;
 constexpr int kCand = kFwdMaxThreads * 8 + kTopMax;  // one round's candidates and those kept
@@ -125,6 +146,55 @@ constexpr int kCand = kFwdMaxThreads * 8 + kTopMax;  // one round's candidates a
 struct Part {
     float m, s, u;
 };
+
+// The running sums of a thread.
+struct Sums {
+    float m;
+    float2 s, u;
+};
+
+// Adds a batch of vectors.  Without HOLD an entry of -infinity (or one so far
+// below the maximum that their difference overflows) turns u into NaN, by
+// 0 * -infinity, and is found that way: testing every entry costs more than
+// the rest of its arithmetic allows.
+template <bool F32, bool HOLD, int N>
+__device__ __forceinline__ void add_batch(Sums& p, const uint4 (&raw)[N], float c) {
+    using E = Elem<F32>;
+    const float2 nm = make_float2(-p.m, -p.m), c2 = make_float2(c, c);
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        float2 f[E::N / 2];
+        E::unpack(raw[k], f);
+#pragma unroll
+        for (int q = 0; q < E::N / 2; ++q) {
+            float2 d = __fmul2_rn(__fadd2_rn(f[q], nm), c2);
+            if constexpr (HOLD) d = make_float2(hold(d.x), hold(d.y));
+            const float2 e = make_float2(ex2(d.x), ex2(d.y));
+            p.s = __fadd2_rn(p.s, e);
+            p.u = __ffma2_rn(e, d, p.u);
+        }
+    }
+}
+
+template <bool F32, int N>
+__device__ __forceinline__ void take_batch(Sums& p, const uint4 (&raw)[N], float c, bool& masked) {
+    const float top = Elem<F32>::template largest<N>(raw);
+    if (top > p.m) {
+        const float d = hold((p.m - top) * c), g = ex2(d);
+        const float2 d2 = make_float2(d, d), g2 = make_float2(g, g);
+        p.u = __fmul2_rn(g2, __ffma2_rn(p.s, d2, p.u));
+        p.s = __fmul2_rn(p.s, g2);
+        p.m = top;
+    }
+    const Sums before = p;
+    if (!masked) {
+        add_batch<F32, false, N>(p, raw, c);
+        masked = isnan(p.u.x + p.u.y);  // from here on this thread's row is taken with HOLD
+        if (!masked) return;
+        p = before;
+    }
+    add_batch<F32, true, N>(p, raw, c);
+}
 
 __device__ __forceinline__ Part join(Part a, Part b, float c) {
     const float m = fmaxf(a.m, b.m);
@@ -151,9 +221,32 @@ __device__ __forceinline__ int key_index(uint64_t key) { return static_cast<int>
 struct TopShared {
     uint64_t cand[kCand];
     uint64_t best[kTopMax];
-    int list[kFwdMaxThreads];
+    uint2 span[kFwdMaxThreads / 32];  // each warp's smallest and largest thread maximum, as order_of()
+    int list[kFwdMaxThreads];         // the threads that reach the bound
     int n_cand, n_list;
 };
+
+// The elements of vector v that reach `low`, as keys, to the candidates;
+// sh.n_cand counts those that do not fit too.
+template <bool F32>
+__device__ __forceinline__ void push_top(TopShared& sh, const Row<F32>& r, int v, uint4 raw, uint64_t low) {
+    using E = Elem<F32>;
+    float2 f[E::N / 2];
+    E::unpack(raw, f);
+    const int j0 = v * E::N - r.lead;
+#pragma unroll
+    for (int q = 0; q < E::N; ++q) {
+        const float x = q & 1 ? f[q / 2].y : f[q / 2].x;
+        const uint32_t ord = order_of(x);
+        if (x > -INFINITY && ord >= static_cast<uint32_t>(low >> 32)) {
+            const uint64_t key = (static_cast<uint64_t>(ord) << 32) | ~static_cast<uint32_t>(j0 + q);
+            if (key >= low) {
+                const int at = atomicAdd(&sh.n_cand, 1);
+                if (at < kCand) sh.cand[at] = key;
+            }
+        }
+    }
+}
 
 // The `top` largest of cand[0, n), sorted, to best (0 where there are fewer).
 // Every thread calls; synchronized on return.
@@ -213,7 +306,7 @@ __device__ __forceinline__ int64_t target_at(const void* ids, bool wide, int64_t
 }
 
 template <bool F32, bool TOP, bool CLUSTER>
-__global__ void __launch_bounds__(kFwdMaxThreads)
+__global__ void __launch_bounds__(kFwdMaxThreads, kFwdMinCtas)
 token_logprob_rows(const LogprobFwd a) {
     using E = Elem<F32>;
     extern __shared__ __align__(16) unsigned char smem[];
@@ -227,7 +320,6 @@ token_logprob_rows(const LogprobFwd a) {
         rank = cg::this_cluster().block_rank();
     }
     const float c = a.inv_t * kLog2e;
-    const float2 c2 = make_float2(c, c);
     grid_dep_wait();
     grid_dep_release();
     for (int64_t row = blockIdx.x / ctas; row < a.rows; row += gridDim.x / ctas) {
@@ -236,45 +328,37 @@ token_logprob_rows(const LogprobFwd a) {
         const int per = (nv + ctas - 1) / ctas;
         const int v0 = min(nv, rank * per), v1 = min(nv, v0 + per);
         // the thread's elements: vectors v0 + t + i * T
-        Part p = {-FLT_MAX, 0.f, 0.f};
-        float2 s2 = make_float2(0.f, 0.f), u2 = make_float2(0.f, 0.f);
-        for (int v = v0 + t; v < v1; v += kFwdBatch * T) {
-            uint4 raw[kFwdBatch];
+        Sums sums = {-FLT_MAX, make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        bool masked = false;
+        {
+            // whole vectors; the row's partial first and last ones after them
+            const int f0 = v0 + (v0 < v1 && !r.full(v0)), f1 = v1 - (v1 > f0 && !r.full(v1 - 1));
+            int v = v0 + t < f0 ? v0 + t + T : v0 + t;
+            const uint4* src = reinterpret_cast<const uint4*>(r.base - r.lead);
+            for (; v + (kFwdBatch - 1) * T < f1; v += kFwdBatch * T) {
+                uint4 raw[kFwdBatch];
 #pragma unroll
-            for (int k = 0; k < kFwdBatch; ++k)
-                raw[k] = v + k * T < v1 ? r.load(v + k * T) : make_uint4(E::kNone, E::kNone, E::kNone, E::kNone);
-            float top = -FLT_MAX;
-#pragma unroll
-            for (int k = 0; k < kFwdBatch; ++k) {
-                float2 f[E::N / 2];
-                E::unpack(raw[k], f);
-#pragma unroll
-                for (int q = 0; q < E::N / 2; ++q) top = fmaxf(top, fmaxf(f[q].x, f[q].y));
+                for (int k = 0; k < kFwdBatch; ++k) raw[k] = ld_stream(src + v + k * T);
+                take_batch<F32, kFwdBatch>(sums, raw, c, masked);
             }
-            if (top > p.m) {
-                const float d = hold((p.m - top) * c), g = ex2(d);
-                const float2 d2 = make_float2(d, d), g2 = make_float2(g, g);
-                u2 = __fmul2_rn(g2, __ffma2_rn(s2, d2, u2));
-                s2 = __fmul2_rn(s2, g2);
-                p.m = top;
+            if (v < f1) {
+                uint4 raw[kFwdBatch];
+#pragma unroll
+                for (int k = 0; k < kFwdBatch; ++k)
+                    raw[k] = v + k * T < f1 ? ld_stream(src + v + k * T) : make_uint4(E::kNone, E::kNone, E::kNone, E::kNone);
+                masked = masked || v + (kFwdBatch - 1) * T >= f1;
+                take_batch<F32, kFwdBatch>(sums, raw, c, masked);
             }
-            const float2 nm = make_float2(-p.m, -p.m);
-#pragma unroll
-            for (int k = 0; k < kFwdBatch; ++k) {
-                float2 f[E::N / 2];
-                E::unpack(raw[k], f);
-#pragma unroll
-                for (int q = 0; q < E::N / 2; ++q) {
-                    float2 d = __fmul2_rn(__fadd2_rn(f[q], nm), c2);
-                    d = make_float2(hold(d.x), hold(d.y));
-                    const float2 e = make_float2(ex2(d.x), ex2(d.y));
-                    s2 = __fadd2_rn(s2, e);
-                    u2 = __ffma2_rn(e, d, u2);
-                }
+            if ((t == 0 && v0 < f0) || (f1 < v1 && t == (v1 - 1 - v0) % T)) {
+                uint4 raw[2];
+                raw[0] = raw[1] = make_uint4(E::kNone, E::kNone, E::kNone, E::kNone);
+                if (t == 0 && v0 < f0) raw[0] = r.load(v0);
+                if (f1 < v1 && t == (v1 - 1 - v0) % T) raw[1] = r.load(v1 - 1);
+                masked = true;
+                take_batch<F32, 2>(sums, raw, c, masked);
             }
         }
-        p.s = s2.x + s2.y;
-        p.u = u2.x + u2.y;
+        Part p = {sums.m, sums.s.x + sums.s.y, sums.u.x + sums.u.y};
         const float own_max = p.m;
         // warp, then CTA, then cluster, each in a fixed order
 #pragma unroll
@@ -286,6 +370,11 @@ token_logprob_rows(const LogprobFwd a) {
             p = (lane & off) ? join(o, p, c) : join(p, o, c);
         }
         if (lane == 0) warps[warp] = p;
+        const uint32_t ord = order_of(own_max);
+        if constexpr (TOP) {
+            const uint32_t least = __reduce_min_sync(0xFFFFFFFFu, ord), most = __reduce_max_sync(0xFFFFFFFFu, ord);
+            if (lane == 0) sh.span[warp] = make_uint2(least, most);
+        }
         __syncthreads();
         if (warp == 0) {
             p = lane < T / 32 ? warps[lane] : Part{-FLT_MAX, 0.f, 0.f};
@@ -300,59 +389,73 @@ token_logprob_rows(const LogprobFwd a) {
             if (lane == 0) mine = p;
         }
         if constexpr (TOP) {
-            // a bound that `top` threads' maxima reach, bit by bit; nearly `top` will do
-            const uint32_t ord = order_of(own_max);
-            uint32_t bound = 0;
-            for (int b = 31; b >= 0; --b) {
-                const uint32_t test = bound | (1u << b);
-                const int n = __syncthreads_count(ord >= test);
-                if (n >= a.top) {
+            // A bound that `top` threads' maxima reach, bit by bit below the bits
+            // that all maxima share; a few more than `top` will do.
+            uint32_t low_ord = 0xFFFFFFFFu, high_ord = 0;
+            for (int w = 0; w < T / 32; ++w) {
+                low_ord = min(low_ord, sh.span[w].x);
+                high_ord = max(high_ord, sh.span[w].y);
+            }
+            uint32_t bound = low_ord;
+            if (low_ord != high_ord) {
+                int bit = 31 - __clz(low_ord ^ high_ord);
+                bound = bit == 31 ? 0 : high_ord >> (bit + 1) << (bit + 1);
+                for (; bit >= 0; --bit) {
+                    const uint32_t test = bound | (1u << bit);
+                    const int n = __syncthreads_count(ord >= test);
+                    if (n < a.top) continue;
                     bound = test;
-                    if (n <= a.top + 8) break;
+                    if (n <= a.top + 4) break;
                 }
             }
             if (t == 0) sh.n_list = sh.n_cand = 0;
             __syncthreads();
             if (ord >= bound) sh.list[atomicAdd(&sh.n_list, 1)] = t;
             __syncthreads();
+            // read these threads' elements again
             const int lists = sh.n_list;
             const int each = (v1 - v0 + T - 1) / T;
-            const int64_t items = static_cast<int64_t>(lists) * each;
+            const int items = lists * each;
             uint64_t low = static_cast<uint64_t>(bound) << 32;  // keys below are out
-            for (int64_t i0 = 0; i0 < items; i0 += T) {
-                const int64_t i = i0 + t;
-                if (i < items) {
-                    const int v = v0 + sh.list[i % lists] + static_cast<int>(i / lists) * T;
-                    if (v < v1) {
-                        float2 f[E::N / 2];
-                        E::unpack(r.load(v), f);
-                        const int j0 = v * E::N - r.lead;
+            const auto vector_of = [&](int i) { return v0 + sh.list[i % lists] + i / lists * T; };
+            for (int i0 = t; i0 < items; i0 += kFwdBatch * T) {
+                uint4 raw[kFwdBatch];
+                int at[kFwdBatch];
 #pragma unroll
-                        for (int q = 0; q < E::N; ++q) {
-                            const float x = q & 1 ? f[q / 2].y : f[q / 2].x;
-                            const uint64_t key = (static_cast<uint64_t>(order_of(x)) << 32) | ~static_cast<uint32_t>(j0 + q);
-                            if (x > -INFINITY && key >= low) sh.cand[atomicAdd(&sh.n_cand, 1)] = key;
-                        }
-                    }
+                for (int k = 0; k < kFwdBatch; ++k) {
+                    at[k] = i0 + k * T < items ? vector_of(i0 + k * T) : v1;
+                    if (at[k] < v1) raw[k] = r.load(at[k]);
                 }
-                __syncthreads();
-                const int n = sh.n_cand;
-                const bool last = i0 + T >= items;
-                // keep the best when the next round might not fit
-                if (last || n + T * E::N > kCand) {
+#pragma unroll
+                for (int k = 0; k < kFwdBatch; ++k)
+                    if (at[k] < v1) push_top<F32>(sh, r, at[k], raw[k], low);
+            }
+            __syncthreads();
+            int n = sh.n_cand;
+            __syncthreads();
+            if (n <= kCand) {
+                sort_top(sh.cand, n, a.top, sh.best, &sh.n_cand);
+            } else {
+                // more than fit (many equal elements): again in rounds, keeping
+                // the best of each
+                if (t == 0) sh.n_cand = 0;
+                for (int i0 = 0; i0 < items; i0 += T) {
                     __syncthreads();
-                    sort_top(sh.cand, n, a.top, sh.best, &sh.n_cand);
-                    if (!last) {
+                    const int i = i0 + t;
+                    const int v = i < items ? vector_of(i) : v1;
+                    if (v < v1) push_top<F32>(sh, r, v, r.load(v), low);
+                    __syncthreads();
+                    n = sh.n_cand;
+                    const bool last = i0 + T >= items;
+                    if (last || n + T * E::N > kCand) {  // the next round might not fit
+                        __syncthreads();
+                        sort_top(sh.cand, n, a.top, sh.best, &sh.n_cand);
                         const int kept = min(n, a.top);
                         if (t < kept) sh.cand[t] = sh.best[t];
                         if (kept == a.top) low = max(low, sh.best[a.top - 1]);
                         if (t == 0) sh.n_cand = kept;
                     }
                 }
-                __syncthreads();
-            }
-            if (items == 0) {
-                if (t < a.top) sh.best[t] = 0;
                 __syncthreads();
             }
         } else {

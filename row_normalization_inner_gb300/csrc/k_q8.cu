@@ -54,6 +54,23 @@ __device__ __forceinline__ float scale_of(uint32_t top, float rstd) {
     return v < kScaleMin ? kScaleMin : v;  // false for NaN, which stays
 }
 
+// y / scale = s w * first * second.  rstd stands in y and in the scale alike,
+// so the quotient is s w * (Q / max|s w|): fewer roundings than y / scale has.
+// Where max|s w| is so small that Q over it could overflow, or the scale is
+// the smallest one, the factors are rstd and 1 / scale, one after the other
+// (their product alone could overflow).
+struct Factors {
+    float first, second;
+};
+template <bool INT8>
+__device__ __forceinline__ Factors factors(float top, float rstd, float scale) {
+    Factors f;
+    const bool direct = top >= kScaleMin && scale > kScaleMin;
+    f.first = direct ? 1.f : rstd;
+    f.second = __fdiv_rn(direct ? (INT8 ? 127.f : 448.f) : 1.f, direct ? top : scale);
+    return f;
+}
+
 // A row per blockDim.x threads (a multiple of 32), blockDim.y rows per CTA
 // (more than one only where a row is one warp).  Thread t holds the vectors
 // k * T + t, k < VPT, so 16 neighbouring lanes hold a group of 128 columns.
@@ -152,12 +169,12 @@ norm_q8_rows(const Q8Args a) {
                 scale = scale_of<INT8>(top[k], rstd);
                 if ((t & 15) == 0 && v < NV) a.scale[row * a.groups + v / 16] = scale;
             }
-            const float inv = __frcp_rn(scale);
-            const float2 r2 = make_float2(rstd, rstd), i2 = make_float2(inv, inv);
+            const float t_max = __uint_as_float(GROUPED ? top[k] : row_top);
+            const Factors f = factors<INT8>(t_max, rstd, scale);
+            const float2 f1 = make_float2(f.first, f.first), f2 = make_float2(f.second, f.second);
             float2 o[4];
-            // two products: rstd / scale alone could overflow where the scale is the smallest
 #pragma unroll
-            for (int q = 0; q < 4; ++q) o[q] = __fmul2_rn(__fmul2_rn(p[k][q], r2), i2);
+            for (int q = 0; q < 4; ++q) o[q] = __fmul2_rn(__fmul2_rn(p[k][q], f1), f2);
             uint2 bytes = make_uint2(quant4<INT8>(o[0], o[1]), quant4<INT8>(o[2], o[3]));
             if (!finite_bits(scale)) bytes = make_uint2(0, 0);
             if (v < NV) __stcs(reinterpret_cast<uint2*>(a.q + row * H + v * kVec), bytes);
