@@ -15,12 +15,15 @@
 // where there are few rows, to a cluster of 2, 4 or 8 CTAs that join their
 // sums through distributed shared memory.
 //
-// The alternatives need no second pass: the maxima of the threads' own
-// elements are known from the sums, and the top-th largest of these maxima
-// is a lower bound for the alternatives.  Only the threads whose maximum
-// reaches it (little more than `top` of them) have their elements read
-// again, from L2; what reaches the bound there is sorted as 64-bit keys
-// (value, then index from the end), all distinct.
+// The alternatives need no second pass: the sums need the maximum of every
+// batch of vectors anyway, so each thread leaves the maxima of up to kSlots
+// stretches of its elements in shared memory.  The top-th largest of the
+// threads' maxima is a lower bound for the alternatives; only the stretches
+// that reach it (little more than `top` of them) are read again, from L2,
+// and what reaches the bound there is sorted as 64-bit keys (value, then
+// index from the end), all distinct.  Reading all elements of the threads
+// that reach the bound instead took 85 us more at 4096 x 131072 with 20
+// alternatives.
 //
 // Backward: with p_j = exp(d_j - log S),
 //     dl_j = ( g (1[j = t] - p_j) - h p_j (log p_j + H) ) / T
@@ -137,10 +140,26 @@ struct Row {
 
 // ---- forward ---------------------------------------------------------------------
 constexpr int kFwdMaxThreads = 256;
-constexpr int kFwdMinCtas = 5;
+// Resident CTAs per SM.  Five, at 48 registers, keep more of the row's bytes in
+// flight (8192 x 131072 bf16: 303 us, four 319 us); with the alternatives, and
+// in fp32 (half the arithmetic per byte), four at 64 registers were faster
+// (4096 x 131072 bf16 with 20 alternatives 191 against 211 us, 1000 x 100003
+// fp32 66 against 71 us).
+constexpr int fwd_min_ctas(bool f32, bool top) { return f32 || top ? 4 : 5; }
 constexpr int kFwdBatch = 4;   // vectors in flight per thread
 constexpr int kTopMax = kLogprobMaxTop;
 constexpr int kCand = kFwdMaxThreads * 8 + kTopMax;  // one round's candidates and those kept
+
+// An order-preserving integer of a float, and back.
+__device__ __forceinline__ uint32_t order_of(float f) {
+    const uint32_t b = __float_as_uint(f);
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float float_of(uint32_t o) {
+    return __uint_as_float(o & 0x80000000u ? o & 0x7FFFFFFFu : ~o);
+}
+__device__ __forceinline__ float key_value(uint64_t key) { return float_of(static_cast<uint32_t>(key >> 32)); }
+__device__ __forceinline__ int key_index(uint64_t key) { return static_cast<int>(~static_cast<uint32_t>(key)); }
 
 // Sums of exponentials of d (units of ln 2) below the maximum m.
 struct Part {
@@ -176,8 +195,9 @@ __device__ __forceinline__ void add_batch(Sums& p, const uint4 (&raw)[N], float 
     }
 }
 
+// The batch's largest element.
 template <bool F32, int N>
-__device__ __forceinline__ void take_batch(Sums& p, const uint4 (&raw)[N], float c, bool& masked) {
+__device__ __forceinline__ float take_batch(Sums& p, const uint4 (&raw)[N], float c, bool& masked) {
     const float top = Elem<F32>::template largest<N>(raw);
     if (top > p.m) {
         const float d = hold((p.m - top) * c), g = ex2(d);
@@ -190,40 +210,39 @@ __device__ __forceinline__ void take_batch(Sums& p, const uint4 (&raw)[N], float
     if (!masked) {
         add_batch<F32, false, N>(p, raw, c);
         masked = isnan(p.u.x + p.u.y);  // from here on this thread's row is taken with HOLD
-        if (!masked) return;
+        if (!masked) return top;
         p = before;
     }
     add_batch<F32, true, N>(p, raw, c);
+    return top;
 }
 
-__device__ __forceinline__ Part join(Part a, Part b, float c) {
-    const float m = fmaxf(a.m, b.m);
-    const float da = hold((a.m - m) * c), db = hold((b.m - m) * c);
-    const float fa = ex2(da), fb = ex2(db);
-    Part r;
-    r.m = m;
-    r.s = a.s * fa + b.s * fb;
-    r.u = fa * (a.u + a.s * da) + fb * (b.u + b.s * db);
-    return r;
+// p with the maximum m.
+__device__ __forceinline__ Part rebase(Part p, float m, float c) {
+    const float d = hold((p.m - m) * c), f = ex2(d);
+    return Part{m, p.s * f, f * (p.u + p.s * d)};
 }
 
-// An order-preserving integer of a float, and back.
-__device__ __forceinline__ uint32_t order_of(float f) {
-    const uint32_t b = __float_as_uint(f);
-    return b & 0x80000000u ? ~b : b | 0x80000000u;
+// The warp's sums, in a fixed order, in every lane.
+__device__ __forceinline__ Part warp_join(Part p, float c) {
+    p = rebase(p, float_of(__reduce_max_sync(0xFFFFFFFFu, order_of(p.m))), c);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        p.s += __shfl_xor_sync(0xFFFFFFFFu, p.s, off);
+        p.u += __shfl_xor_sync(0xFFFFFFFFu, p.u, off);
+    }
+    return p;
 }
-__device__ __forceinline__ float float_of(uint32_t o) {
-    return __uint_as_float(o & 0x80000000u ? o & 0x7FFFFFFFu : ~o);
-}
-__device__ __forceinline__ float key_value(uint64_t key) { return float_of(static_cast<uint32_t>(key >> 32)); }
-__device__ __forceinline__ int key_index(uint64_t key) { return static_cast<int>(~static_cast<uint32_t>(key)); }
 
+constexpr int kSlots = 16;
 struct TopShared {
     uint64_t cand[kCand];
     uint64_t best[kTopMax];
-    uint2 span[kFwdMaxThreads / 32];  // each warp's smallest and largest thread maximum, as order_of()
-    int list[kFwdMaxThreads];         // the threads that reach the bound
+    float slot[kSlots][kFwdMaxThreads];         // largest element of each stretch
+    uint32_t thread_max[kFwdMaxThreads];        // of each thread, as order_of()
+    uint16_t list[kSlots * kFwdMaxThreads];     // the stretches that reach the bound: slot * T + thread
     int n_cand, n_list;
+    uint32_t bound;
 };
 
 // The elements of vector v that reach `low`, as keys, to the candidates;
@@ -306,7 +325,7 @@ __device__ __forceinline__ int64_t target_at(const void* ids, bool wide, int64_t
 }
 
 template <bool F32, bool TOP, bool CLUSTER>
-__global__ void __launch_bounds__(kFwdMaxThreads, kFwdMinCtas)
+__global__ void __launch_bounds__(kFwdMaxThreads, fwd_min_ctas(F32, TOP))
 token_logprob_rows(const LogprobFwd a) {
     using E = Elem<F32>;
     extern __shared__ __align__(16) unsigned char smem[];
@@ -330,24 +349,52 @@ token_logprob_rows(const LogprobFwd a) {
         // the thread's elements: vectors v0 + t + i * T
         Sums sums = {-FLT_MAX, make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         bool masked = false;
-        {
-            // whole vectors; the row's partial first and last ones after them
-            const int f0 = v0 + (v0 < v1 && !r.full(v0)), f1 = v1 - (v1 > f0 && !r.full(v1 - 1));
-            int v = v0 + t < f0 ? v0 + t + T : v0 + t;
+        // whole vectors are [f0, f1); a thread's first is v0 + t, or one step
+        // on where that is the row's partial first vector
+        const int f0 = v0 + (v0 < v1 && !r.full(v0)), f1 = v1 - (v1 > f0 && !r.full(v1 - 1));
+        const auto first_of = [&](int thread) { return v0 + thread < f0 ? v0 + thread + T : v0 + thread; };
+        const bool short_row = v1 - v0 <= kFwdBatch * T;  // one batch per thread, the partial vectors with it
+        int shift = 0;                                    // batches per slot, as a power of two
+        while ((v1 - v0) / (kFwdBatch * T) >> shift >= kSlots) ++shift;
+        int slots = 0;
+        if (short_row) {
+            uint4 raw[kFwdBatch];
+#pragma unroll
+            for (int k = 0; k < kFwdBatch; ++k)
+                raw[k] = v0 + t + k * T < v1 ? r.load(v0 + t + k * T) : make_uint4(E::kNone, E::kNone, E::kNone, E::kNone);
+            masked = true;
+            const float top = take_batch<F32, kFwdBatch>(sums, raw, c, masked);
+            if constexpr (TOP) sh.slot[0][t] = top;
+            slots = 1;
+        } else {
             const uint4* src = reinterpret_cast<const uint4*>(r.base - r.lead);
+            int v = first_of(t), batch = 0;
+            float most = -INFINITY;
             for (; v + (kFwdBatch - 1) * T < f1; v += kFwdBatch * T) {
                 uint4 raw[kFwdBatch];
 #pragma unroll
                 for (int k = 0; k < kFwdBatch; ++k) raw[k] = ld_stream(src + v + k * T);
-                take_batch<F32, kFwdBatch>(sums, raw, c, masked);
+                const float top = take_batch<F32, kFwdBatch>(sums, raw, c, masked);
+                if constexpr (TOP) {
+                    most = fmaxf(most, top);
+                    ++batch;
+                    if ((batch & ((1 << shift) - 1)) == 0) {
+                        sh.slot[slots++][t] = most;
+                        most = -INFINITY;
+                    }
+                }
             }
             if (v < f1) {
                 uint4 raw[kFwdBatch];
 #pragma unroll
                 for (int k = 0; k < kFwdBatch; ++k)
                     raw[k] = v + k * T < f1 ? ld_stream(src + v + k * T) : make_uint4(E::kNone, E::kNone, E::kNone, E::kNone);
-                masked = masked || v + (kFwdBatch - 1) * T >= f1;
-                take_batch<F32, kFwdBatch>(sums, raw, c, masked);
+                masked = true;  // the filling
+                most = fmaxf(most, take_batch<F32, kFwdBatch>(sums, raw, c, masked));
+                ++batch;
+            }
+            if constexpr (TOP) {
+                if (slots << shift < batch) sh.slot[slots++][t] = most;
             }
             if ((t == 0 && v0 < f0) || (f1 < v1 && t == (v1 - 1 - v0) % T)) {
                 uint4 raw[2];
@@ -358,77 +405,74 @@ token_logprob_rows(const LogprobFwd a) {
                 take_batch<F32, 2>(sums, raw, c, masked);
             }
         }
-        Part p = {sums.m, sums.s.x + sums.s.y, sums.u.x + sums.u.y};
-        const float own_max = p.m;
         // warp, then CTA, then cluster, each in a fixed order
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) {
-            Part o;
-            o.m = __shfl_xor_sync(0xFFFFFFFFu, p.m, off);
-            o.s = __shfl_xor_sync(0xFFFFFFFFu, p.s, off);
-            o.u = __shfl_xor_sync(0xFFFFFFFFu, p.u, off);
-            p = (lane & off) ? join(o, p, c) : join(p, o, c);
-        }
+        Part p = warp_join(Part{sums.m, sums.s.x + sums.s.y, sums.u.x + sums.u.y}, c);
         if (lane == 0) warps[warp] = p;
-        const uint32_t ord = order_of(own_max);
+        const uint32_t ord = order_of(sums.m);
         if constexpr (TOP) {
-            const uint32_t least = __reduce_min_sync(0xFFFFFFFFu, ord), most = __reduce_max_sync(0xFFFFFFFFu, ord);
-            if (lane == 0) sh.span[warp] = make_uint2(least, most);
+            sh.thread_max[t] = ord;
+            if (t == 0) sh.n_list = sh.n_cand = 0;
         }
         __syncthreads();
         if (warp == 0) {
-            p = lane < T / 32 ? warps[lane] : Part{-FLT_MAX, 0.f, 0.f};
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) {
-                Part o;
-                o.m = __shfl_xor_sync(0xFFFFFFFFu, p.m, off);
-                o.s = __shfl_xor_sync(0xFFFFFFFFu, p.s, off);
-                o.u = __shfl_xor_sync(0xFFFFFFFFu, p.u, off);
-                p = (lane & off) ? join(o, p, c) : join(p, o, c);
-            }
+            p = warp_join(lane < T / 32 ? warps[lane] : Part{-FLT_MAX, 0.f, 0.f}, c);
             if (lane == 0) mine = p;
         }
         if constexpr (TOP) {
-            // A bound that `top` threads' maxima reach, bit by bit below the bits
-            // that all maxima share; a few more than `top` will do.
-            uint32_t low_ord = 0xFFFFFFFFu, high_ord = 0;
-            for (int w = 0; w < T / 32; ++w) {
-                low_ord = min(low_ord, sh.span[w].x);
-                high_ord = max(high_ord, sh.span[w].y);
-            }
-            uint32_t bound = low_ord;
-            if (low_ord != high_ord) {
-                int bit = 31 - __clz(low_ord ^ high_ord);
-                bound = bit == 31 ? 0 : high_ord >> (bit + 1) << (bit + 1);
-                for (; bit >= 0; --bit) {
-                    const uint32_t test = bound | (1u << bit);
-                    const int n = __syncthreads_count(ord >= test);
-                    if (n < a.top) continue;
-                    bound = test;
-                    if (n <= a.top + 4) break;
+            if (warp == T / 32 - 1) {
+                // A bound that `top` threads' maxima reach, bit by bit below the
+                // bits that all maxima share; a few more than `top` will do.
+                constexpr int kEach = kFwdMaxThreads / 32;
+                uint32_t x[kEach];
+                uint32_t least = 0xFFFFFFFFu, most = 0;
+#pragma unroll
+                for (int i = 0; i < kEach; ++i) {
+                    x[i] = i * 32 < T ? sh.thread_max[i * 32 + lane] : 0;
+                    if (i * 32 < T) least = min(least, x[i]);
+                    most = max(most, x[i]);
                 }
+                least = __reduce_min_sync(0xFFFFFFFFu, least);
+                most = __reduce_max_sync(0xFFFFFFFFu, most);
+                uint32_t bound = least;
+                if (least != most) {
+                    int bit = 31 - __clz(least ^ most);
+                    bound = bit == 31 ? 0 : most >> (bit + 1) << (bit + 1);
+                    for (; bit >= 0; --bit) {
+                        const uint32_t test = bound | (1u << bit);
+                        int n = 0;
+#pragma unroll
+                        for (int i = 0; i < kEach; ++i) n += x[i] >= test;
+                        n = __reduce_add_sync(0xFFFFFFFFu, n);
+                        if (n < a.top) continue;
+                        bound = test;
+                        if (n <= a.top + 4) break;
+                    }
+                }
+                if (lane == 0) sh.bound = bound;
             }
-            if (t == 0) sh.n_list = sh.n_cand = 0;
             __syncthreads();
-            if (ord >= bound) sh.list[atomicAdd(&sh.n_list, 1)] = t;
+            const uint32_t bound = sh.bound;
+            if (ord >= bound)
+                for (int i = 0; i < slots; ++i)
+                    if (order_of(sh.slot[i][t]) >= bound) sh.list[atomicAdd(&sh.n_list, 1)] = static_cast<uint16_t>(i * T + t);
             __syncthreads();
-            // read these threads' elements again
-            const int lists = sh.n_list;
-            const int each = (v1 - v0 + T - 1) / T;
-            const int items = lists * each;
+            // read these stretches again, and the partial vectors
+            const int edges = short_row ? 0 : (v0 < f0) + (f1 < v1);
+            const int per_log = shift + 2;  // vectors of a stretch
+            static_assert(kFwdBatch == 4, "per_log");
+            const int items = (sh.n_list << per_log) + edges;
             uint64_t low = static_cast<uint64_t>(bound) << 32;  // keys below are out
-            const auto vector_of = [&](int i) { return v0 + sh.list[i % lists] + i / lists * T; };
-            for (int i0 = t; i0 < items; i0 += kFwdBatch * T) {
-                uint4 raw[kFwdBatch];
-                int at[kFwdBatch];
-#pragma unroll
-                for (int k = 0; k < kFwdBatch; ++k) {
-                    at[k] = i0 + k * T < items ? vector_of(i0 + k * T) : v1;
-                    if (at[k] < v1) raw[k] = r.load(at[k]);
-                }
-#pragma unroll
-                for (int k = 0; k < kFwdBatch; ++k)
-                    if (at[k] < v1) push_top<F32>(sh, r, at[k], raw[k], low);
+            const auto vector_of = [&](int i) {  // v1: none
+                if (i < edges) return i == 0 && v0 < f0 ? v0 : v1 - 1;
+                if (i >= items) return v1;
+                i -= edges;
+                const int code = sh.list[i >> per_log], slot = code / T, thread = code - slot * T;
+                const int v = (short_row ? v0 + thread : first_of(thread)) + ((slot << per_log) + (i & ((1 << per_log) - 1))) * T;
+                return v < (short_row ? v1 : f1) ? v : v1;
+            };
+            for (int i0 = t; i0 < items; i0 += T) {
+                const int v = vector_of(i0);
+                if (v < v1) push_top<F32>(sh, r, v, r.load(v), low);
             }
             __syncthreads();
             int n = sh.n_cand;
@@ -441,8 +485,7 @@ token_logprob_rows(const LogprobFwd a) {
                 if (t == 0) sh.n_cand = 0;
                 for (int i0 = 0; i0 < items; i0 += T) {
                     __syncthreads();
-                    const int i = i0 + t;
-                    const int v = i < items ? vector_of(i) : v1;
+                    const int v = vector_of(i0 + t);
                     if (v < v1) push_top<F32>(sh, r, v, r.load(v), low);
                     __syncthreads();
                     n = sh.n_cand;
@@ -466,8 +509,8 @@ token_logprob_rows(const LogprobFwd a) {
             cg::cluster_group cluster = cg::this_cluster();
             cluster.sync();
             if (rank == 0) {
-                all = Part{-FLT_MAX, 0.f, 0.f};
-                for (int i = 0; i < ctas; ++i) all = join(all, *cluster.map_shared_rank(&mine, i), c);
+                // every warp: lane i takes CTA i's sums
+                all = warp_join(lane < ctas ? *cluster.map_shared_rank(&mine, lane) : Part{-FLT_MAX, 0.f, 0.f}, c);
                 if constexpr (TOP) {
                     for (int i = t; i < ctas * a.top; i += T)
                         sh.cand[i] = cluster.map_shared_rank(&sh, i / a.top)->best[i % a.top];
