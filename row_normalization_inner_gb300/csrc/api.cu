@@ -100,20 +100,6 @@ nf_status current_device(int* dev) {
     return NF_OK;
 }
 
-nf_status device_status_addr(int** addr) {
-    int dev;
-    if (nf_status st = current_device(&dev)) return st;
-    int* p = g_status_addr[dev].load(std::memory_order_acquire);
-    if (!p) {
-        void* q = nullptr;
-        if (cudaGetSymbolAddress(&q, g_device_status) != cudaSuccess || !q) return NF_ERR_CUDA;
-        p = static_cast<int*>(q);
-        g_status_addr[dev].store(p, std::memory_order_release);
-    }
-    *addr = p;
-    return NF_OK;
-}
-
 // A size with kernels specialized at compile time.
 bool hidden_ok(int64_t h) {
     int a, b;
@@ -261,6 +247,20 @@ nf_status device_sm_count(int* sms) {
         g_sm_count[dev].store(v, std::memory_order_relaxed);
     }
     *sms = v;
+    return NF_OK;
+}
+
+nf_status device_status_addr(int** addr) {
+    int dev;
+    if (nf_status st = current_device(&dev)) return st;
+    int* p = g_status_addr[dev].load(std::memory_order_acquire);
+    if (!p) {
+        void* q = nullptr;
+        if (cudaGetSymbolAddress(&q, g_device_status) != cudaSuccess || !q) return NF_ERR_CUDA;
+        p = static_cast<int*>(q);
+        g_status_addr[dev].store(p, std::memory_order_release);
+    }
+    *addr = p;
     return NF_OK;
 }
 

@@ -38,6 +38,7 @@ nf_status norm_q8(void* q, float* scale, const void* x, void* residual, bool fus
     int sms;
     if (nf_status st = device_sm_count(&sms)) return st;
     Q8Args a{};
+    if (nf_status st = device_status_addr(&a.status)) return st;
     a.q = static_cast<uint8_t*>(q);
     a.scale = scale;
     a.x = static_cast<const uint16_t*>(x);

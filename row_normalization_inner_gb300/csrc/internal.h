@@ -11,6 +11,9 @@ namespace nf {
 // SM count of the current device, cached per device.
 nf_status device_sm_count(int* sms);
 
+// Address of the current device's status word, cached per device.
+nf_status device_status_addr(int** addr);
+
 inline nf_status from_cuda(cudaError_t e) { return e == cudaSuccess ? NF_OK : NF_ERR_CUDA; }
 
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }

@@ -21,7 +21,8 @@ struct Q8Args {
     const uint16_t* w;
     int64_t rows;
     int hidden;
-    int groups;  // scales per row
+    int* status;  // the device status word
+    int groups;   // scales per row
     float eps;
 };
 cudaError_t launch_norm_q8(const Q8Args& a, bool int8, bool grouped, int sms, cudaStream_t st);

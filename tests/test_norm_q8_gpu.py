@@ -86,6 +86,33 @@ def test_fused_add_rmsnorm_q8(rows, hidden, fmt, group):
     assert torch.equal(res, r2)
 
 
+# enough rows for every resident CTA to walk several (rows that no CTA count divides), CTAs of 128 to 1024 threads
+@pytest.mark.parametrize("group", [0, 128])
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("rows,hidden", [(2003, 4096), (1501, 5128), (1301, 8192), (1111, 12280), (777, 16392),
+                                         (401, 32768), (3001, 3208)])
+def test_many_rows(rows, hidden, fmt, group):
+    x, w = workloads.rms_inputs(rows, hidden, seed=rows, device="cuda")
+    x[5] = 0
+    x[rows - 1, hidden - 1] = float("nan")
+    keep = x.clone()
+    q, scale = nf.rmsnorm_q8(x, w, EPS, fmt=fmt, group=group)
+    _, v, ref = reference(x[:-1], None, w, fmt, group)
+    check(q[:-1], scale[:-1], v, ref, fmt)
+    assert torch.isnan(scale[-1]).all() and torch.all(bits(q[-1]) == 0)
+    assert torch.all(bits(q[5]) & 0x7F == 0)
+    assert torch.equal(x[:-1], keep[:-1])
+    assert nf.nf_get_device_status(0) == nf.NF_OK  # no wait ran out
+    # in a graph and on rows a larger buffer holds
+    out, sc = torch.empty_like(q), torch.empty_like(scale)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        nf.rmsnorm_q8(x, w, EPS, fmt=fmt, group=group, out=out, scale=sc)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(bits(out), bits(q)) and torch.equal(sc[:-1], scale[:-1])
+
+
 def bits(q):
     return q.view(torch.uint8)
 
