@@ -8,10 +8,10 @@
 // tokens are sorted by id, stably, so that equal ids become a run in token
 // order; every run is summed in fp32 in that order, which makes the result
 // deterministic where atomics on the table would not be.  Launches:
-//   1. the sort: one CTA up to kSortOne tokens (every radix pass in shared
-//      memory), above that two launches per radix pass (digit counts of each
-//      tile, then a stable scatter whose CTAs each add up the counts of the
-//      tiles before theirs);
+//   1. the sort: up to kSortRank tokens by counting, up to kSortCluster radix
+//      passes in the shared memory of one cluster of CTAs, above that two
+//      launches per radix pass (digit counts of each tile, then a stable
+//      scatter whose CTAs each add up the counts of the tiles before theirs);
 //   2. the sums: the sorted tokens are cut into chunks of equal length, a CTA
 //      per chunk and slice of columns.  A run inside one chunk is written at
 //      once; the pieces of a run that crosses chunks go to the workspace.
@@ -21,6 +21,8 @@
 // A chunk rather than a run per CTA, because word frequencies are uneven:
 // one id can hold several percent of a batch.  Bound by memory: dy read
 // once, the rows with tokens (or all rows) written once.
+#include <cooperative_groups.h>
+
 #include <atomic>
 
 #include "common.cuh"
@@ -30,6 +32,8 @@
 
 namespace nf {
 namespace {
+
+namespace cg = cooperative_groups;
 
 __device__ __forceinline__ int64_t id_at(const void* ids, bool wide, int64_t i) {
     return wide ? static_cast<const int64_t*>(ids)[i] : static_cast<const int32_t*>(ids)[i];
@@ -88,10 +92,23 @@ __device__ __forceinline__ uint32_t key_of(const void* ids, bool wide, int64_t i
     return static_cast<uint32_t>(id >= 0 && id < vocab ? id : vocab);
 }
 
-// Lanes of the warp whose digit is this lane's.
-__device__ __forceinline__ uint32_t lanes_like(uint32_t digit) { return __match_any_sync(0xFFFFFFFFu, digit); }
+// Lanes of the warp that have an item and this lane's digit of `bits` bits,
+// from one vote per bit (__match_any_sync took five times as long: the whole
+// sort of 16384 tokens 46 us).
+__device__ __forceinline__ uint32_t lanes_like(uint32_t digit, bool have, int bits) {
+    uint32_t like = __ballot_sync(0xFFFFFFFFu, have);
+#pragma unroll
+    for (int b = 0; b < kBinBits; ++b) {
+        if (b >= bits) break;
+        const bool one = (digit >> b) & 1;
+        const uint32_t ones = __ballot_sync(0xFFFFFFFFu, one);
+        like &= one ? ones : ~ones;
+    }
+    return like;
+}
 
-// Stable ranks of a tile's digits (key >> shift) & (bins - 1).  Warp w holds
+// Stable ranks of a tile's digits, `bits` bits of the key above `shift`
+// (bins = 2^bits).  Warp w holds
 // the items [w * 32 * ITEMS, (w + 1) * 32 * ITEMS) of the tile, item k of a
 // lane at k * 32 + lane; bit k of `valid` says whether the lane has it.
 // counts: `bins` of each warp, zeroed here.  On return the low 16 bits of
@@ -99,10 +116,10 @@ __device__ __forceinline__ uint32_t lanes_like(uint32_t digit) { return __match_
 // warp (the high 16 are kept), counts[w * bins + d] is the number of items of
 // digit d in the warps before w, and total[d] the tile's items of digit d.
 template <int THREADS, int ITEMS>
-__device__ __forceinline__ void rank_tile(const uint32_t (&key)[ITEMS], uint32_t valid, int shift, int bins,
+__device__ __forceinline__ void rank_tile(const uint32_t (&key)[ITEMS], uint32_t valid, int shift, int bits,
                                           uint16_t* counts, uint32_t* total, uint32_t (&rank)[ITEMS]) {
     constexpr int kWarps = THREADS / 32;
-    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5, bins = 1 << bits;
     uint32_t* words = reinterpret_cast<uint32_t*>(counts);
     for (int i = t; i < kWarps * bins / 2; i += THREADS) words[i] = 0;
     __syncthreads();
@@ -110,9 +127,8 @@ __device__ __forceinline__ void rank_tile(const uint32_t (&key)[ITEMS], uint32_t
 #pragma unroll
     for (int k = 0; k < ITEMS; ++k) {
         const bool have = (valid >> k) & 1;
-        // lanes past the end match each other only
-        const uint32_t d = have ? (key[k] >> shift) & (bins - 1) : kBins;
-        const uint32_t like = lanes_like(d);
+        const uint32_t d = (key[k] >> shift) & (bins - 1);
+        const uint32_t like = lanes_like(d, have, bits);
         const int before = __popc(like & ((1u << lane) - 1));
         const uint32_t c = have ? mine[d] : 0;
         __syncwarp();
@@ -122,12 +138,14 @@ __device__ __forceinline__ void rank_tile(const uint32_t (&key)[ITEMS], uint32_t
     }
     __syncthreads();
     for (int d = t; d < bins; d += THREADS) {
+        uint16_t c[kWarps];
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) c[w] = counts[w * bins + d];
         uint32_t sum = 0;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            const uint32_t c = counts[w * bins + d];
             counts[w * bins + d] = static_cast<uint16_t>(sum);
-            sum += c;
+            sum += c[w];
         }
         total[d] = sum;
     }
@@ -155,64 +173,160 @@ __device__ __forceinline__ void scan_bins(uint32_t* values, int bins, uint32_t* 
     __syncthreads();
 }
 
-// One CTA sorts all tokens: every pass in shared memory.  A thread holds
-// ITEMS of them; small batches take the variant with the fewest.
-constexpr int kSortOne = 16384;
-template <int THREADS, int ITEMS>
-constexpr size_t sort_one_smem(int bins) {
-    return static_cast<size_t>(THREADS) * ITEMS * 6 + static_cast<size_t>(THREADS / 32) * bins * 2 + bins * 4 + 128;
-}
+// Up to kSortRank tokens: a token's place is the number of tokens before it
+// in the order, counted against all of them.  A CTA takes 32 tokens, one per
+// lane, its warps each a stretch of the tokens.  4096 tokens take the GPU
+// 17 million comparisons, less than the latency of the radix passes
+// (2000 tokens and 8 columns, all three launches: 13.8 -> 9.5 us).
+constexpr int kSortRank = 4096;
+constexpr int kRankThreads = 256;
 
-template <int THREADS, int ITEMS>
-__global__ void __launch_bounds__(THREADS)
-sort_one(const void* __restrict__ ids, bool wide, int n, int64_t vocab, int bits, int passes,
-         uint32_t* __restrict__ keys_out, uint32_t* __restrict__ at_out) {
-    extern __shared__ __align__(16) unsigned char smem[];
-    const int bins = 1 << bits;
-    uint32_t* keys = reinterpret_cast<uint32_t*>(smem);
-    uint32_t* total = keys + THREADS * ITEMS;
-    uint32_t* warp_sums = total + bins;
-    uint16_t* at = reinterpret_cast<uint16_t*>(warp_sums + 32);  // at most kSortOne tokens: 16 bits
-    uint16_t* counts = at + THREADS * ITEMS;
+__global__ void __launch_bounds__(kRankThreads)
+sort_by_rank(const void* __restrict__ ids, bool wide, int n, int64_t vocab, uint32_t* __restrict__ keys_out,
+             uint32_t* __restrict__ at_out, uint32_t* __restrict__ crossings) {
+    __shared__ __align__(16) uint32_t keys[kSortRank];
+    __shared__ int counts[kRankThreads / 32][32];
     grid_dep_wait();
     grid_dep_release();
+    if (blockIdx.x == 0 && threadIdx.x == 0) *crossings = 0;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    uint32_t key[ITEMS], pr[ITEMS];  // pr: the token in the high 16 bits, its rank in the low
+    const int whole = (n + 3) / 4 * 4;
+    for (int i = threadIdx.x; i < whole; i += kRankThreads)
+        keys[i] = i < n ? key_of(ids, wide, i, vocab) : 0xFFFFFFFFu;  // behind every key
+    __syncthreads();
+    const int block = blockIdx.x * 32, token = block + lane;
+    const uint32_t key = token < n ? keys[token] : 0;
+    // of the tokens before this CTA's, those with the same key come first; of
+    // those behind, they do not (key <= 2^30: no overflow)
+    int count = 0;
+    const uint4* four = reinterpret_cast<const uint4*>(keys);
+    const int per = (whole / 4 + kRankThreads / 32 - 1) / (kRankThreads / 32);
+    const int i0 = warp * per, i1 = min(i0 + per, whole / 4);
+    const auto add = [&](int from, int to, uint32_t bound) {
+#pragma unroll 4
+        for (int i = from; i < to; ++i) {
+            const uint4 k = four[i];
+            count += (k.x < bound) + (k.y < bound) + (k.z < bound) + (k.w < bound);
+        }
+    };
+    const int b0 = block / 4, b1 = min(block / 4 + 8, whole / 4);
+    add(i0, min(i1, b0), key + 1);
+    for (int i = max(i0, b0) * 4; i < min(i1, b1) * 4; ++i) count += keys[i] < key + (i < token);
+    add(max(i0, b1), i1, key);
+    counts[warp][lane] = count;
+    __syncthreads();
+    if (warp == 0 && token < n) {
+#pragma unroll
+        for (int w = 1; w < kRankThreads / 32; ++w) count += counts[w][lane];
+        keys_out[count] = key;
+        at_out[count] = token;
+    }
+}
+
+// Up to kSortCluster tokens: one cluster of 1, 2, 4 or 8 CTAs, every pass in
+// its shared memory.  CTA r holds the places [r * kTile, (r + 1) * kTile) of
+// the order so far.  In a pass a CTA brings its tokens into digit order, the
+// CTAs read each other's digit counts, and every token goes to its place, in
+// whichever CTA that lies, through distributed shared memory: neighbours in
+// digit order go to neighbouring places, where writing them straight from
+// the registers took one transaction each (65536 tokens: 42 us).
+constexpr int kSortThreads = 512;
+constexpr int kSortCtas = 8;
+constexpr int kSortCluster = 32768;
+template <int ITEMS>
+constexpr size_t sort_cluster_smem(int bins) {
+    return static_cast<size_t>(kSortThreads) * ITEMS * 16 + static_cast<size_t>(kSortThreads / 32) * bins * 2 + 3 * bins * 4 + 128;
+}
+
+template <int ITEMS>
+__global__ void __launch_bounds__(kSortThreads, 1)
+sort_cluster(const void* __restrict__ ids, bool wide, int n, int64_t vocab, int bits, int passes,
+             uint32_t* __restrict__ keys_out, uint32_t* __restrict__ at_out, uint32_t* __restrict__ crossings) {
+    constexpr int kTile = kSortThreads * ITEMS;
+    extern __shared__ __align__(16) unsigned char smem[];
+    const int bins = 1 << bits;
+    uint64_t* order = reinterpret_cast<uint64_t*>(smem);  // this CTA's tokens in digit order: (key, token)
+    uint64_t* place = order + kTile;                      // the tokens whose places are this CTA's
+    uint32_t* total = reinterpret_cast<uint32_t*>(place + kTile);  // this CTA's items of each digit
+    uint32_t* local = total + bins;                       // of smaller digits
+    uint32_t* start = local + bins;                       // the place of the digit's first item of this CTA, less local
+    uint32_t* warp_sums = start + bins;
+    uint16_t* counts = reinterpret_cast<uint16_t*>(warp_sums + 32);
+    cg::cluster_group cluster = cg::this_cluster();
+    const int ctas = cluster.num_blocks(), cta = cluster.block_rank();
+    grid_dep_wait();
+    grid_dep_release();
+    if (cta == 0 && threadIdx.x == 0) *crossings = 0;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int held = min(max(n - cta * kTile, 0), kTile);  // places of this CTA
+    uint32_t key[ITEMS], token[ITEMS], rank[ITEMS];
     uint32_t valid = 0;
 #pragma unroll
     for (int k = 0; k < ITEMS; ++k) {
-        const int i = (warp * ITEMS + k) * 32 + lane;
-        const bool have = i < n;
+        const int j = (warp * ITEMS + k) * 32 + lane;
+        const bool have = j < held;
         valid |= static_cast<uint32_t>(have) << k;
-        key[k] = have ? key_of(ids, wide, i, vocab) : 0;
-        pr[k] = static_cast<uint32_t>(i) << 16;
+        token[k] = cta * kTile + j;
+        key[k] = have ? key_of(ids, wide, token[k], vocab) : 0;
+        rank[k] = 0;
     }
     for (int p = 0; p < passes; ++p) {
         const int shift = p * bits;
-        rank_tile<THREADS, ITEMS>(key, valid, shift, bins, counts, total, pr);
-        scan_bins<THREADS>(total, bins, warp_sums);
-        const bool last = p == passes - 1;
+        const auto digit_of = [&](uint32_t k) { return (k >> shift) & (bins - 1); };
+        rank_tile<kSortThreads, ITEMS>(key, valid, shift, bits, counts, total, rank);
+        for (int d = threadIdx.x; d < bins; d += kSortThreads) local[d] = total[d];
+        __syncthreads();
+        scan_bins<kSortThreads>(local, bins, warp_sums);
 #pragma unroll
         for (int k = 0; k < ITEMS; ++k) {
             if (!((valid >> k) & 1)) continue;
-            const uint32_t d = (key[k] >> shift) & (bins - 1);
-            const uint32_t to = total[d] + counts[warp * bins + d] + (pr[k] & 0xFFFFu);
+            const uint32_t d = digit_of(key[k]);
+            order[local[d] + counts[warp * bins + d] + (rank[k] & 0xFFFFu)] = static_cast<uint64_t>(key[k]) << 32 | token[k];
+        }
+        cluster.sync();
+        uint32_t mine[2];  // bins <= 2 * kSortThreads
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int d = threadIdx.x + h * kSortThreads;
+            if (d >= bins) break;
+            uint32_t all = 0, before = 0;
+#pragma unroll
+            for (int i = 0; i < kSortCtas; ++i) {
+                if (i >= ctas) break;
+                const uint32_t c = cluster.map_shared_rank(total, i)[d];
+                all += c;
+                if (i < cta) before += c;
+            }
+            start[d] = all;
+            mine[h] = before - local[d];
+        }
+        __syncthreads();
+        scan_bins<kSortThreads>(start, bins, warp_sums);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int d = threadIdx.x + h * kSortThreads;
+            if (d < bins) start[d] += mine[h];
+        }
+        __syncthreads();
+        const bool last = p == passes - 1;
+        for (int j = threadIdx.x; j < held; j += kSortThreads) {
+            const uint64_t item = order[j];
+            const uint32_t k = static_cast<uint32_t>(item >> 32), to = start[digit_of(k)] + j;
             if (last) {
-                keys_out[to] = key[k];
-                at_out[to] = pr[k] >> 16;
+                keys_out[to] = k;
+                at_out[to] = static_cast<uint32_t>(item);
             } else {
-                keys[to] = key[k];
-                at[to] = static_cast<uint16_t>(pr[k] >> 16);
+                cluster.map_shared_rank(place, to / kTile)[to % kTile] = item;
             }
         }
+        cluster.sync();  // all tokens are placed, and the counts have been read
         if (last) break;
-        __syncthreads();
 #pragma unroll
         for (int k = 0; k < ITEMS; ++k) {
-            const int i = (warp * ITEMS + k) * 32 + lane;
             if ((valid >> k) & 1) {
-                key[k] = keys[i];
-                pr[k] = static_cast<uint32_t>(at[i]) << 16;
+                const uint64_t item = place[(warp * ITEMS + k) * 32 + lane];
+                key[k] = static_cast<uint32_t>(item >> 32);
+                token[k] = static_cast<uint32_t>(item);
             }
         }
     }
@@ -225,22 +339,21 @@ constexpr int kTile = kTileThreads * kTileItems;  // 4096
 
 __global__ void __launch_bounds__(kTileThreads)
 sort_count(const void* __restrict__ ids, bool wide, const uint32_t* __restrict__ keys_in, int64_t n,
-           int64_t vocab, int shift, int bits, uint32_t* __restrict__ hist) {
+           int64_t vocab, int shift, int bits, uint32_t* __restrict__ hist, uint32_t* __restrict__ crossings) {
     __shared__ uint32_t bins[kBins];
     grid_dep_wait();
     grid_dep_release();
+    if (blockIdx.x == 0 && threadIdx.x == 0) *crossings = 0;
     for (int d = threadIdx.x; d < kBins; d += kTileThreads) bins[d] = 0;
     __syncthreads();
     const int64_t base = static_cast<int64_t>(blockIdx.x) * kTile;
 #pragma unroll
     for (int k = 0; k < kTileItems; ++k) {
         const int64_t i = base + k * kTileThreads + threadIdx.x;
-        const bool ok = i < n;
-        const uint32_t key = !ok ? 0 : keys_in ? keys_in[i] : key_of(ids, wide, i, vocab);
-        const uint32_t d = ok ? (key >> shift) & ((1u << bits) - 1) : kBins;
-        // one addition per distinct digit of the warp
-        const uint32_t like = lanes_like(d);
-        if (ok && __popc(like & ((1u << (threadIdx.x & 31)) - 1)) == 0) atomicAdd(&bins[d], __popc(like));
+        if (i < n) {
+            const uint32_t key = keys_in ? keys_in[i] : key_of(ids, wide, i, vocab);
+            atomicAdd(&bins[(key >> shift) & ((1u << bits) - 1)], 1u);  // a count: its order does not matter
+        }
     }
     __syncthreads();
     for (int d = threadIdx.x; d < 1 << bits; d += kTileThreads)
@@ -270,7 +383,7 @@ sort_scatter(const void* __restrict__ ids, bool wide, const uint32_t* __restrict
         pos[k] = !have ? 0 : at_in ? at_in[i] : static_cast<uint32_t>(i);
         rank[k] = 0;
     }
-    rank_tile<kTileThreads, kTileItems>(key, valid, shift, bins, counts, total, rank);
+    rank_tile<kTileThreads, kTileItems>(key, valid, shift, bits, counts, total, rank);
     // all tiles' items of a digit, and those of the tiles before this one
     for (int d = threadIdx.x; d < bins; d += kTileThreads) {
         uint32_t all = 0, before = 0;
@@ -306,40 +419,33 @@ struct EmbedBwd {
     const uint16_t* dy;
     const uint32_t* keys;
     const uint32_t* at;
-    float* pieces;       // [chunks][2][hidden]: a chunk's first and last piece of a crossing run
+    float* pieces;        // [chunks][2][hidden]: a chunk's first and last piece of a crossing run
+    uint32_t* crossings;  // how many chunks a crossing run begins in, then (4 further on) which
     int64_t tokens, vocab;
     int hidden, chunk, slices;
     int64_t chunks;
     float scale;
 };
 
-// One table row's 8 columns: (old +) scale * acc.  The old values are loaded
-// apart, so that a batch of rows has its loads in flight together.
+// One table row's 8 columns: (old +) scale * acc.  A bf16 row's old values are
+// loaded apart, so that a batch of rows has its loads in flight together; an
+// fp32 row is added to in L2 (a row is one thread's, so the order of such
+// additions cannot matter).
 template <bool F32, bool ADD>
 struct Old {
     static constexpr int N = F32 ? 2 : 1;  // 16-byte vectors
-    uint4 v[ADD ? N : 1];
+    uint4 v;
     static __device__ __forceinline__ uint4* place(const EmbedBwd& a, uint32_t key, int col) {
         return static_cast<uint4*>(a.dtable) + (static_cast<int64_t>(key) * (a.hidden / kVec) + col) * N;
     }
     __device__ __forceinline__ void load(const EmbedBwd& a, uint32_t key, int col) {
-        const uint4* p = place(a, key, col);
-        if constexpr (ADD) {
-#pragma unroll
-            for (int i = 0; i < N; ++i) v[i] = ld_stream(p + i);
-        }
+        if constexpr (ADD && !F32) v = ld_stream(place(a, key, col));
     }
     __device__ __forceinline__ void put(const EmbedBwd& a, uint32_t key, int col, const float2 (&acc)[4]) const {
         const float2 s2 = make_float2(a.scale, a.scale);
         float2 o[4];
-        if constexpr (ADD && F32) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                o[2 * i] = make_float2(__uint_as_float(v[i].x), __uint_as_float(v[i].y));
-                o[2 * i + 1] = make_float2(__uint_as_float(v[i].z), __uint_as_float(v[i].w));
-            }
-        } else if constexpr (ADD) {
-            unpack8x2(v[0], o);
+        if constexpr (ADD && !F32) {
+            unpack8x2(v, o);
         } else {
             o[0] = o[1] = o[2] = o[3] = make_float2(0.f, 0.f);
         }
@@ -348,9 +454,14 @@ struct Old {
         uint4* p = place(a, key, col);
         if constexpr (F32) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                st_stream(p + i, make_uint4(__float_as_uint(o[2 * i].x), __float_as_uint(o[2 * i].y),
-                                            __float_as_uint(o[2 * i + 1].x), __float_as_uint(o[2 * i + 1].y)));
+            for (int i = 0; i < 2; ++i) {
+                if constexpr (ADD)
+                    asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p + i), "f"(o[2 * i].x),
+                                 "f"(o[2 * i].y), "f"(o[2 * i + 1].x), "f"(o[2 * i + 1].y) : "memory");
+                else
+                    st_stream(p + i, make_uint4(__float_as_uint(o[2 * i].x), __float_as_uint(o[2 * i].y),
+                                                __float_as_uint(o[2 * i + 1].x), __float_as_uint(o[2 * i + 1].y)));
+            }
         } else {
             st_stream(p, pack8x2(o));
         }
@@ -417,6 +528,12 @@ embedding_sums(const EmbedBwd a) {
     const uint32_t none = static_cast<uint32_t>(a.vocab);
     const uint32_t before = begin > 0 ? a.keys[begin - 1] : none;
     const uint32_t first = a.keys[begin];
+    if (blockIdx.x % a.slices == 0 && threadIdx.x == 0) {
+        const uint32_t key = a.keys[end - 1], after = end < a.tokens ? a.keys[end] : none;
+        // the last run goes on, and began here
+        if (key != none && after == key && !(first == key && before == key))
+            a.crossings[4 + atomicAdd(a.crossings, 1u)] = static_cast<uint32_t>(c);
+    }
     float2 acc[4] = {};
     for (int64_t part = begin; part < end; part += kSumPart) {
         const int n = static_cast<int>(end - part < kSumPart ? end - part : kSumPart);
@@ -459,57 +576,69 @@ embedding_sums(const EmbedBwd a) {
     }
 }
 
-// The runs that cross chunks: the chunk in which a run begins adds its last
-// piece and the first pieces of the chunks the run goes on through, in order.
+// The runs that cross chunks: the last piece of the chunk in which a run
+// begins and the first pieces of the chunks it goes on through, in order.  A
+// CTA takes 32 column vectors of a run; its warps each add a stretch of the
+// pieces, so that a run of thousands of tokens is not one long chain.
+constexpr int kJoinWarps = 8;
 template <bool F32, bool ADD>
-__global__ void __launch_bounds__(kSumThreads)
+__global__ void __launch_bounds__(kJoinWarps * 32)
 embedding_join(const EmbedBwd a) {
-    __shared__ int64_t last;
+    __shared__ float2 sums[kJoinWarps][4][32];
+    // no early release: with the next kernel's CTAs resident beside these, a
+    // call of 4096 tokens and 4096 columns took 32 us instead of 20
     grid_dep_wait();
-    grid_dep_release();
-    const int nv = a.hidden / kVec;
-    const int64_t c = static_cast<int64_t>(blockIdx.x) / a.slices;
-    const int v = static_cast<int>(blockIdx.x % a.slices) * kSumThreads + threadIdx.x;
-    const int64_t begin = c * a.chunk, end = begin + a.chunk;
-    if (end >= a.tokens) return;
-    const uint32_t key = a.keys[end - 1];
-    if (key >= a.vocab || a.keys[end] != key) return;                       // no run goes on
-    if (a.keys[begin] == key && begin > 0 && a.keys[begin - 1] == key) return;  // it began earlier
-    if (threadIdx.x < 32) {
-        const int64_t stop = lower_bound_warp(a.keys, end, a.tokens, key + 1);
-        if (threadIdx.x == 0) last = (stop - 1) / a.chunk;  // the chunk of the run's last token
-    }
-    __syncthreads();
-    if (v >= nv) return;
-    const float* p = a.pieces + (c * 2 + 1) * a.hidden + static_cast<int64_t>(v) * kVec;
-    float2 acc[4];
-    {
-        const float4 x = *reinterpret_cast<const float4*>(p), y = *reinterpret_cast<const float4*>(p + 4);
-        acc[0] = make_float2(x.x, x.y);
-        acc[1] = make_float2(x.z, x.w);
-        acc[2] = make_float2(y.x, y.y);
-        acc[3] = make_float2(y.z, y.w);
-    }
-    p += a.hidden;  // the next chunk's first piece
+    const int nv = a.hidden / kVec, slices = (nv + 31) / 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t work = static_cast<int64_t>(*a.crossings) * slices;
+    for (int64_t w = blockIdx.x; w < work; w += gridDim.x) {
+        const int64_t c = a.crossings[4 + w / slices];
+        const int v = static_cast<int>(w % slices) * 32 + lane;
+        const uint32_t key = a.keys[(c + 1) * a.chunk];
+        int64_t pieces = 1;  // and one for each following chunk that the run's id opens
+        for (;;) {
+            const int64_t at = (c + pieces + lane) * a.chunk;
+            const uint32_t open = __ballot_sync(0xFFFFFFFFu, at < a.tokens && a.keys[at] == key);
+            const int n = open == 0xFFFFFFFFu ? 32 : __ffs(~open) - 1;
+            pieces += n;
+            if (n < 32) break;
+        }
+        const int64_t per = (pieces + kJoinWarps - 1) / kJoinWarps;
+        const int64_t p0 = warp * per, p1 = p0 + per < pieces ? p0 + per : pieces;
+        float2 acc[4] = {};
+        if (v < nv) {
 #pragma unroll 4
-    for (int64_t i = c + 1; i <= last; ++i, p += 2 * static_cast<int64_t>(a.hidden)) {
-        const float4 x = *reinterpret_cast<const float4*>(p), y = *reinterpret_cast<const float4*>(p + 4);
-        acc[0] = __fadd2_rn(acc[0], make_float2(x.x, x.y));
-        acc[1] = __fadd2_rn(acc[1], make_float2(x.z, x.w));
-        acc[2] = __fadd2_rn(acc[2], make_float2(y.x, y.y));
-        acc[3] = __fadd2_rn(acc[3], make_float2(y.z, y.w));
+            for (int64_t i = p0; i < p1; ++i) {
+                const float4* p = reinterpret_cast<const float4*>(a.pieces + ((c + i) * 2 + (i == 0)) * a.hidden + v * kVec);
+                const float4 x = p[0], y = p[1];
+                acc[0] = __fadd2_rn(acc[0], make_float2(x.x, x.y));
+                acc[1] = __fadd2_rn(acc[1], make_float2(x.z, x.w));
+                acc[2] = __fadd2_rn(acc[2], make_float2(y.x, y.y));
+                acc[3] = __fadd2_rn(acc[3], make_float2(y.z, y.w));
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) sums[warp][q][lane] = acc[q];
+        __syncthreads();
+        if (warp == 0 && v < nv) {
+            Old<F32, ADD> old;
+            old.load(a, key, v);
+            for (int i = 1; i < kJoinWarps; ++i)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) acc[q] = __fadd2_rn(acc[q], sums[i][q][lane]);
+            old.put(a, key, v, acc);
+        }
+        __syncthreads();
     }
-    Old<F32, ADD> old;
-    old.load(a, key, v);
-    old.put(a, key, v, acc);
 }
 
 int64_t round16(int64_t b) { return (b + 15) / 16 * 16; }
 
+constexpr int kChunksPerSm = 4;
 // Chunks of the sums: long enough that the pieces stay a small share of dy,
 // short enough that every SM has several.
 int chunk_rows(int64_t tokens, int slices, int sms) {
-    int64_t c = tokens * slices / (static_cast<int64_t>(sms) * 16);
+    int64_t c = tokens * slices / (static_cast<int64_t>(sms) * kChunksPerSm);
     int chunk = 8;
     while (chunk < 256 && chunk * 2 <= c) chunk *= 2;
     while ((tokens + chunk - 1) / chunk * slices > 0x3FFFFFFF) chunk *= 2;
@@ -519,7 +648,7 @@ int chunk_rows(int64_t tokens, int slices, int sms) {
 struct Layout {
     int slices, chunk;
     int64_t chunks, tiles;
-    int64_t keys, at, keys2, at2, hist, pieces, bytes;  // byte offsets, total
+    int64_t keys, at, keys2, at2, hist, crossings, pieces, bytes;  // byte offsets, total
 };
 
 Layout layout(int64_t tokens, int64_t hidden, int sms) {
@@ -528,7 +657,7 @@ Layout layout(int64_t tokens, int64_t hidden, int sms) {
     l.slices = (nv + kSumThreads - 1) / kSumThreads;
     l.chunk = chunk_rows(tokens, l.slices, sms);
     l.chunks = (tokens + l.chunk - 1) / l.chunk;
-    l.tiles = tokens > kSortOne ? (tokens + kTile - 1) / kTile : 0;
+    l.tiles = tokens > kSortCluster ? (tokens + kTile - 1) / kTile : 0;
     int64_t at = 0;
     const auto take = [&at](int64_t bytes) { const int64_t o = at; at += round16(bytes); return o; };
     l.keys = take(tokens * 4);
@@ -536,39 +665,58 @@ Layout layout(int64_t tokens, int64_t hidden, int sms) {
     l.keys2 = take(l.tiles ? tokens * 4 : 0);
     l.at2 = take(l.tiles ? tokens * 4 : 0);
     l.hist = take(l.tiles * kBins * 4);
+    l.crossings = take((4 + l.chunks) * 4);
     l.pieces = take(l.chunks * 2 * hidden * 4);
     l.bytes = at;
     return l;
 }
 
-template <int THREADS, int ITEMS>
-cudaError_t sort_in_one(const void* ids, bool wide, int n, int64_t vocab, int bits, int passes, uint32_t* keys,
-                        uint32_t* at, cudaStream_t st) {
-    static_assert(THREADS * ITEMS <= kSortOne && kBins <= 2 * THREADS, "16-bit token numbers; two bins a thread");
+template <int ITEMS>
+cudaError_t sort_in_cluster(const void* ids, bool wide, int n, int64_t vocab, int bits, int passes, uint32_t* keys,
+                            uint32_t* at, uint32_t* crossings, cudaStream_t st) {
+    static_assert(kSortThreads * ITEMS * kSortCtas <= kSortCluster && kBins <= 2 * kSortThreads, "two bins a thread");
     static std::atomic<bool> set[64];
     int dev = 0;
     if (cudaError_t e = cudaGetDevice(&dev)) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    const auto kernel = sort_one<THREADS, ITEMS>;
+    const auto kernel = sort_cluster<ITEMS>;
     if (!set[dev].load(std::memory_order_acquire)) {
         if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 static_cast<int>(sort_one_smem<THREADS, ITEMS>(kBins))))
+                                                 static_cast<int>(sort_cluster_smem<ITEMS>(kBins))))
             return e;
         set[dev].store(true, std::memory_order_release);
     }
-    return launch_with_pdl(kernel, dim3(1), dim3(THREADS), sort_one_smem<THREADS, ITEMS>(1 << bits), st, ids, wide, n,
-                           vocab, bits, passes, keys, at);
+    unsigned ctas = 1;
+    while (static_cast<int>(ctas) * kSortThreads * ITEMS < n) ctas *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kSortThreads);
+    cfg.dynamicSmemBytes = sort_cluster_smem<ITEMS>(1 << bits);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ctas;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, ids, wide, n, vocab, bits, passes, keys, at, crossings);
 }
 
 template <bool F32, bool ADD>
-cudaError_t sums(const EmbedBwd& e, cudaStream_t st) {
+cudaError_t sums(const EmbedBwd& e, int sms, cudaStream_t st) {
     const int64_t work = e.chunks * e.slices;
     const int64_t zero = ADD ? 0 : (e.vocab + kZeroRows - 1) / kZeroRows;
     if (cudaError_t err = launch_with_pdl(embedding_sums<F32, ADD>, dim3(static_cast<unsigned>(work + zero)),
                                           dim3(kSumThreads), 0, st, e))
         return err;
     if (e.chunks <= 1) return cudaSuccess;
-    return launch_with_pdl(embedding_join<F32, ADD>, dim3(static_cast<unsigned>(work)), dim3(kSumThreads), 0, st, e);
+    // one crossing run per chunk at most; as many CTAs as stay resident take them in turn
+    const int64_t joins = (e.chunks - 1) * ((e.hidden / kVec + 31) / 32), wave = static_cast<int64_t>(sms) * 8;
+    return launch_with_pdl(embedding_join<F32, ADD>, dim3(static_cast<unsigned>(joins < wave ? joins : wave)),
+                           dim3(kJoinWarps * 32), 0, st, e);
 }
 
 }  // namespace
@@ -604,9 +752,11 @@ cudaError_t launch_embedding_bwd(void* dtable, bool f32, bool add, const void* d
         if (add) return cudaSuccess;
     } else if (!l.tiles) {
         const int n = static_cast<int>(tokens);
-        const cudaError_t e = n <= 2048   ? sort_in_one<512, 4>(ids, wide, n, vocab, bits, passes, u32(l.keys), u32(l.at), st)
-                              : n <= 4096 ? sort_in_one<1024, 4>(ids, wide, n, vocab, bits, passes, u32(l.keys), u32(l.at), st)
-                                          : sort_in_one<1024, 16>(ids, wide, n, vocab, bits, passes, u32(l.keys), u32(l.at), st);
+        const auto sort = n <= 4 * kSortThreads * kSortCtas ? sort_in_cluster<4> : sort_in_cluster<8>;
+        const cudaError_t e =
+            n <= kSortRank ? launch_with_pdl(sort_by_rank, dim3((n + 31) / 32), dim3(kRankThreads), 0, st, ids, wide, n,
+                                             vocab, u32(l.keys), u32(l.at), u32(l.crossings))
+                           : sort(ids, wide, n, vocab, bits, passes, u32(l.keys), u32(l.at), u32(l.crossings), st);
         if (e != cudaSuccess) return e;
     } else {
         uint32_t *to_keys = u32(l.keys), *to_at = u32(l.at), *other_keys = u32(l.keys2), *other_at = u32(l.at2);
@@ -614,7 +764,7 @@ cudaError_t launch_embedding_bwd(void* dtable, bool f32, bool add, const void* d
         const dim3 grid(static_cast<unsigned>(l.tiles));
         for (int p = 0; p < passes; ++p) {
             if (cudaError_t e = launch_with_pdl(sort_count, grid, dim3(kTileThreads), 0, st, ids, wide, from_keys,
-                                                tokens, vocab, p * bits, bits, u32(l.hist)))
+                                                tokens, vocab, p * bits, bits, u32(l.hist), u32(l.crossings)))
                 return e;
             if (cudaError_t e = launch_with_pdl(sort_scatter, grid, dim3(kTileThreads), 0, st, ids, wide, from_keys,
                                                 from_at, tokens, vocab, p * bits, bits, static_cast<int>(l.tiles),
@@ -635,6 +785,7 @@ cudaError_t launch_embedding_bwd(void* dtable, bool f32, bool add, const void* d
     e.keys = keys;
     e.at = at;
     e.pieces = reinterpret_cast<float*>(ws + l.pieces);
+    e.crossings = u32(l.crossings);
     e.tokens = tokens;
     e.vocab = vocab;
     e.hidden = static_cast<int>(hidden);
@@ -642,8 +793,8 @@ cudaError_t launch_embedding_bwd(void* dtable, bool f32, bool add, const void* d
     e.slices = l.slices;
     e.chunks = l.chunks;
     e.scale = scale;
-    if (f32) return add ? sums<true, true>(e, st) : sums<true, false>(e, st);
-    return add ? sums<false, true>(e, st) : sums<false, false>(e, st);
+    if (f32) return add ? sums<true, true>(e, sms, st) : sums<true, false>(e, sms, st);
+    return add ? sums<false, true>(e, sms, st) : sums<false, false>(e, sms, st);
 }
 
 }  // namespace nf

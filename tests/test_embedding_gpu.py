@@ -142,6 +142,15 @@ def test_gradient(tokens, vocab, hidden, kind, add, dtype):
         check_grad(got, dy, ids, vocab, 0.5, None)
 
 
+@pytest.mark.parametrize("kind", ["words", "one", "falling"])
+@pytest.mark.parametrize("tokens", [31, 32, 33, 4095, 4096, 8193, 16384, 16390, 32768, 32769, 65537])
+def test_gradient_at_the_borders_of_the_sorts(tokens, kind):
+    vocab, hidden = 3001, 16
+    ids = make_ids(kind, tokens, vocab, tokens)
+    dy = torch.randn(tokens, hidden, generator=gen(tokens), device="cuda").bfloat16()
+    check_grad(nf.embedding_bwd(dy, ids, vocab, 1.0), dy, ids, vocab, 1.0, None)
+
+
 @pytest.mark.parametrize("tokens", [3000, 30000])
 def test_gradient_is_deterministic_and_in_token_order(tokens):
     vocab, hidden = 500, 520
