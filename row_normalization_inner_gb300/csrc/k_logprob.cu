@@ -148,7 +148,6 @@ constexpr int kFwdMaxThreads = 256;
 constexpr int fwd_min_ctas(bool f32, bool top) { return f32 || top ? 4 : 5; }
 constexpr int kFwdBatch = 4;   // vectors in flight per thread
 constexpr int kTopMax = kLogprobMaxTop;
-constexpr int kCand = kFwdMaxThreads * 8 + kTopMax;  // one round's candidates and those kept
 
 // An order-preserving integer of a float, and back.
 __device__ __forceinline__ uint32_t order_of(float f) {
@@ -235,20 +234,38 @@ __device__ __forceinline__ Part warp_join(Part p, float c) {
 }
 
 constexpr int kSlots = 16;
+// The shared memory of the alternatives, laid out for T threads and `slots`
+// stretches of each (rows of one batch need one, and more CTAs then fit).
 struct TopShared {
-    uint64_t cand[kCand];
-    uint64_t best[kTopMax];
-    float slot[kSlots][kFwdMaxThreads];         // largest element of each stretch
-    uint32_t thread_max[kFwdMaxThreads];        // of each thread, as order_of()
-    uint16_t list[kSlots * kFwdMaxThreads];     // the stretches that reach the bound: slot * T + thread
-    int n_cand, n_list;
-    uint32_t bound;
+    uint64_t* best;        // [kTopMax]
+    uint64_t* cand;        // [capacity]: one round's candidates and those kept
+    uint32_t* thread_max;  // [T], as order_of()
+    float* slot;           // [slots][T]: largest element of each stretch
+    uint16_t* list;        // [slots * T]: the stretches that reach the bound, slot * T + thread
+    int *n_cand, *n_list;
+    uint32_t* bound;
+    int capacity;
+    static constexpr __host__ __device__ int room(int threads, int per_vector) { return threads * per_vector + kTopMax; }
+    static constexpr __host__ __device__ size_t bytes(int threads, int per_vector, int slots) {
+        return 16 + 8 * (kTopMax + room(threads, per_vector)) + 4 * threads + 6 * slots * threads;
+    }
+    __device__ __forceinline__ TopShared(unsigned char* at, int threads, int per_vector, int slots) {
+        n_cand = reinterpret_cast<int*>(at);
+        n_list = n_cand + 1;
+        bound = reinterpret_cast<uint32_t*>(n_cand + 2);
+        capacity = room(threads, per_vector);
+        best = reinterpret_cast<uint64_t*>(at + 16);
+        cand = best + kTopMax;
+        thread_max = reinterpret_cast<uint32_t*>(cand + capacity);
+        slot = reinterpret_cast<float*>(thread_max + threads);
+        list = reinterpret_cast<uint16_t*>(slot + slots * threads);
+    }
 };
 
 // The elements of vector v that reach `low`, as keys, to the candidates;
-// sh.n_cand counts those that do not fit too.
+// n_cand counts those that do not fit too.
 template <bool F32>
-__device__ __forceinline__ void push_top(TopShared& sh, const Row<F32>& r, int v, uint4 raw, uint64_t low) {
+__device__ __forceinline__ void push_top(const TopShared& sh, const Row<F32>& r, int v, uint4 raw, uint64_t low) {
     using E = Elem<F32>;
     float2 f[E::N / 2];
     E::unpack(raw, f);
@@ -260,8 +277,8 @@ __device__ __forceinline__ void push_top(TopShared& sh, const Row<F32>& r, int v
         if (x > -INFINITY && ord >= static_cast<uint32_t>(low >> 32)) {
             const uint64_t key = (static_cast<uint64_t>(ord) << 32) | ~static_cast<uint32_t>(j0 + q);
             if (key >= low) {
-                const int at = atomicAdd(&sh.n_cand, 1);
-                if (at < kCand) sh.cand[at] = key;
+                const int at = atomicAdd(sh.n_cand, 1);
+                if (at < sh.capacity) sh.cand[at] = key;
             }
         }
     }
@@ -284,14 +301,16 @@ __device__ __forceinline__ void sort_top(uint64_t* cand, int n, int top, uint64_
             for (int bit = 0; bit < 6; ++bit) total += __syncthreads_count((min(mine, 63) >> bit) & 1) << bit;
             if (total >= top) bound = test;
         }
-        uint64_t keep[kCand / 64 + 1];
-        int kept = 0;
-        for (int i = t; i < n; i += T)
-            if (cand[i] >= bound && kept < kCand / 64 + 1) keep[kept++] = cand[i];
+        // at most 9 of a thread's: n <= 8 T + kTopMax
+        constexpr int kEach = 9;
+        uint64_t keep[kEach];
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) keep[k] = t + k * T < n && cand[t + k * T] >= bound ? cand[t + k * T] : 0;
         if (t == 0) *n_kept = 0;
         __syncthreads();
-        const int at = kept ? atomicAdd(n_kept, kept) : 0;
-        for (int i = 0; i < kept; ++i) cand[at + i] = keep[i];
+#pragma unroll
+        for (int k = 0; k < kEach; ++k)
+            if (keep[k]) cand[atomicAdd(n_kept, 1)] = keep[k];
         __syncthreads();
         n = *n_kept;
     }
@@ -317,6 +336,7 @@ struct LogprobFwd {
     int64_t rows, stride;
     int vocab, top;
     float inv_t;
+    int slots;  // of the alternatives' shared memory
     bool wide;
 };
 
@@ -329,10 +349,10 @@ __global__ void __launch_bounds__(kFwdMaxThreads, fwd_min_ctas(F32, TOP))
 token_logprob_rows(const LogprobFwd a) {
     using E = Elem<F32>;
     extern __shared__ __align__(16) unsigned char smem[];
-    TopShared& sh = *reinterpret_cast<TopShared*>(smem);  // only with TOP
     __shared__ Part warps[kFwdMaxThreads / 32];
     __shared__ Part mine;
     const int t = threadIdx.x, T = blockDim.x, lane = t & 31, warp = t >> 5;
+    const TopShared sh(smem, T, E::N, a.slots);  // only with TOP
     int ctas = 1, rank = 0;
     if constexpr (CLUSTER) {
         ctas = cg::this_cluster().num_blocks();
@@ -364,7 +384,7 @@ token_logprob_rows(const LogprobFwd a) {
                 raw[k] = v0 + t + k * T < v1 ? r.load(v0 + t + k * T) : make_uint4(E::kNone, E::kNone, E::kNone, E::kNone);
             masked = true;
             const float top = take_batch<F32, kFwdBatch>(sums, raw, c, masked);
-            if constexpr (TOP) sh.slot[0][t] = top;
+            if constexpr (TOP) sh.slot[t] = top;
             slots = 1;
         } else {
             const uint4* src = reinterpret_cast<const uint4*>(r.base - r.lead);
@@ -379,7 +399,7 @@ token_logprob_rows(const LogprobFwd a) {
                     most = fmaxf(most, top);
                     ++batch;
                     if ((batch & ((1 << shift) - 1)) == 0) {
-                        sh.slot[slots++][t] = most;
+                        sh.slot[slots++ * T + t] = most;
                         most = -INFINITY;
                     }
                 }
@@ -394,7 +414,7 @@ token_logprob_rows(const LogprobFwd a) {
                 ++batch;
             }
             if constexpr (TOP) {
-                if (slots << shift < batch) sh.slot[slots++][t] = most;
+                if (slots << shift < batch) sh.slot[slots++ * T + t] = most;
             }
             if ((t == 0 && v0 < f0) || (f1 < v1 && t == (v1 - 1 - v0) % T)) {
                 uint4 raw[2];
@@ -411,7 +431,7 @@ token_logprob_rows(const LogprobFwd a) {
         const uint32_t ord = order_of(sums.m);
         if constexpr (TOP) {
             sh.thread_max[t] = ord;
-            if (t == 0) sh.n_list = sh.n_cand = 0;
+            if (t == 0) *sh.n_list = *sh.n_cand = 0;
         }
         __syncthreads();
         if (warp == 0) {
@@ -448,19 +468,19 @@ token_logprob_rows(const LogprobFwd a) {
                         if (n <= a.top + 4) break;
                     }
                 }
-                if (lane == 0) sh.bound = bound;
+                if (lane == 0) *sh.bound = bound;
             }
             __syncthreads();
-            const uint32_t bound = sh.bound;
+            const uint32_t bound = *sh.bound;
             if (ord >= bound)
                 for (int i = 0; i < slots; ++i)
-                    if (order_of(sh.slot[i][t]) >= bound) sh.list[atomicAdd(&sh.n_list, 1)] = static_cast<uint16_t>(i * T + t);
+                    if (order_of(sh.slot[i * T + t]) >= bound) sh.list[atomicAdd(sh.n_list, 1)] = static_cast<uint16_t>(i * T + t);
             __syncthreads();
             // read these stretches again, and the partial vectors
             const int edges = short_row ? 0 : (v0 < f0) + (f1 < v1);
             const int per_log = shift + 2;  // vectors of a stretch
             static_assert(kFwdBatch == 4, "per_log");
-            const int items = (sh.n_list << per_log) + edges;
+            const int items = (*sh.n_list << per_log) + edges;
             uint64_t low = static_cast<uint64_t>(bound) << 32;  // keys below are out
             const auto vector_of = [&](int i) {  // v1: none
                 if (i < edges) return i == 0 && v0 < f0 ? v0 : v1 - 1;
@@ -475,28 +495,28 @@ token_logprob_rows(const LogprobFwd a) {
                 if (v < v1) push_top<F32>(sh, r, v, r.load(v), low);
             }
             __syncthreads();
-            int n = sh.n_cand;
+            int n = *sh.n_cand;
             __syncthreads();
-            if (n <= kCand) {
-                sort_top(sh.cand, n, a.top, sh.best, &sh.n_cand);
+            if (n <= sh.capacity) {
+                sort_top(sh.cand, n, a.top, sh.best, sh.n_cand);
             } else {
                 // more than fit (many equal elements): again in rounds, keeping
                 // the best of each
-                if (t == 0) sh.n_cand = 0;
+                if (t == 0) *sh.n_cand = 0;
                 for (int i0 = 0; i0 < items; i0 += T) {
                     __syncthreads();
                     const int v = vector_of(i0 + t);
                     if (v < v1) push_top<F32>(sh, r, v, r.load(v), low);
                     __syncthreads();
-                    n = sh.n_cand;
+                    n = *sh.n_cand;
                     const bool last = i0 + T >= items;
-                    if (last || n + T * E::N > kCand) {  // the next round might not fit
+                    if (last || n + T * E::N > sh.capacity) {  // the next round might not fit
                         __syncthreads();
-                        sort_top(sh.cand, n, a.top, sh.best, &sh.n_cand);
+                        sort_top(sh.cand, n, a.top, sh.best, sh.n_cand);
                         const int kept = min(n, a.top);
                         if (t < kept) sh.cand[t] = sh.best[t];
                         if (kept == a.top) low = max(low, sh.best[a.top - 1]);
-                        if (t == 0) sh.n_cand = kept;
+                        if (t == 0) *sh.n_cand = kept;
                     }
                 }
                 __syncthreads();
@@ -513,13 +533,13 @@ token_logprob_rows(const LogprobFwd a) {
                 all = warp_join(lane < ctas ? *cluster.map_shared_rank(&mine, lane) : Part{-FLT_MAX, 0.f, 0.f}, c);
                 if constexpr (TOP) {
                     for (int i = t; i < ctas * a.top; i += T)
-                        sh.cand[i] = cluster.map_shared_rank(&sh, i / a.top)->best[i % a.top];
+                        sh.cand[i] = cluster.map_shared_rank(sh.best, i / a.top)[i % a.top];
                 }
             }
             cluster.sync();  // the other CTAs' shared memory has been read
             if constexpr (TOP) {
                 // ranks of missing alternatives (key 0) lie behind all others
-                if (rank == 0) sort_top(sh.cand, ctas * a.top, a.top, sh.best, &sh.n_cand);
+                if (rank == 0) sort_top(sh.cand, ctas * a.top, a.top, sh.best, sh.n_cand);
             }
         }
         if (rank == 0) {
@@ -549,7 +569,10 @@ token_logprob_rows(const LogprobFwd a) {
 }
 
 // ---- backward --------------------------------------------------------------------
-constexpr int kBwdThreads = 256;
+// 128 threads of 40 registers, twelve CTAs an SM: 4096 x 131072 bf16 307 us;
+// 256 threads of 52 registers, four CTAs, 334 us.
+constexpr int kBwdThreads = 128;
+constexpr int kBwdCtas = 12;
 constexpr int kBwdBatch = 4;
 
 struct LogprobBwd {
@@ -567,7 +590,7 @@ struct LogprobBwd {
 };
 
 template <bool F32>
-__global__ void __launch_bounds__(kBwdThreads)
+__global__ void __launch_bounds__(kBwdThreads, kBwdCtas)
 token_logprob_grad(const LogprobBwd a) {
     using E = Elem<F32>;
     using T = typename E::T;
@@ -636,8 +659,9 @@ token_logprob_grad(const LogprobBwd a) {
 template <bool F32, bool TOP, bool CLUSTER>
 cudaError_t fwd(const LogprobFwd& a, int threads, int ctas, cudaStream_t st) {
     const auto k = token_logprob_rows<F32, TOP, CLUSTER>;
-    constexpr size_t smem = TOP ? sizeof(TopShared) : 0;
-    static_assert(sizeof(TopShared) <= 47 * 1024, "within the default limit of shared memory");
+    constexpr int n = Elem<F32>::N;
+    static_assert(TopShared::bytes(kFwdMaxThreads, 8, kSlots) <= 47 * 1024, "within the default limit of shared memory");
+    const size_t smem = TOP ? TopShared::bytes(threads, n, a.slots) : 0;
     const int64_t most = 0x7FFFFFFF / ctas;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>((a.rows < most ? a.rows : most) * ctas));
@@ -689,6 +713,8 @@ cudaError_t launch_token_logprob_fwd(float* logprob, float* entropy, float* stat
     int ctas = 1;
     while (ctas < 8 && rows * ctas * 2 <= 2 * static_cast<int64_t>(sms) && nv >= static_cast<int64_t>(ctas) * 2 * threads)
         ctas *= 2;
+    // a row, or a CTA's share of one, of at most a batch per thread has one stretch (an unaligned row: one vector more)
+    a.slots = (nv + 1 + ctas - 1) / ctas <= threads * kFwdBatch ? 1 : kSlots;
     return f32 ? fwd<true>(a, threads, ctas, st) : fwd<false>(a, threads, ctas, st);
 }
 
