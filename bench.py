@@ -810,7 +810,11 @@ def run_profile_case(spec: str, reps: int):
     """Run `reps` launches of one operation at one size and exit: the small,
     self-contained command the ncu captures use.  spec = OP:ROWSxHIDDEN with
     OP in fused_add_rmsnorm, rmsnorm_fwd, layernorm_fwd, layernorm_bwd,
-    rmsnorm_bwd, fused_add_rmsnorm_bwd, outer_norm_fwd, outer_norm_bwd; an
+    rmsnorm_bwd, fused_add_rmsnorm_bwd, outer_norm_fwd, outer_norm_bwd, or a
+    token-side operator (rmsnorm_q8, fused_add_rmsnorm_q8 and the same with
+    _128 for group scales; embedding_fwd, embedding_bwd, embedding_bwd_add,
+    TOKENSxHIDDEN on a table of 131072 rows; token_logprob_fwd,
+    token_logprob_fwd_top, token_logprob_bwd, ROWSxVOCAB); an
     optional @FAMILY suffix (e.g. @split) forces that kernel family for the
     timed calls (inputs are prepared under the automatic choice)."""
     import row_normalization_inner_gb300 as nf
@@ -860,6 +864,33 @@ def run_profile_case(spec: str, reps: int):
             fn = lambda: nf.outer_norm_fwd(x, g, b, EPS, workspace=ws, out=y)  # noqa: E731
         else:
             fn = lambda: nf.outer_norm_bwd(dy, x, mean, rstd, g, workspace=ws, out=y)  # noqa: E731
+    elif op.removesuffix("_128") in ("rmsnorm_q8", "fused_add_rmsnorm_q8"):
+        x, r, w = workloads.fused_inputs(rows, hidden, residual_scale=4.0, device=dev)
+        group = 128 if op.endswith("_128") else 0
+        q, scale = nf.rmsnorm_q8(x, w, EPS, group=group)
+        if op.startswith("fused"):
+            fn = lambda: nf.fused_add_rmsnorm_q8(x, r, w, EPS, group=group, out=q, scale=scale)  # noqa: E731
+        else:
+            fn = lambda: nf.rmsnorm_q8(x, w, EPS, group=group, out=q, scale=scale)  # noqa: E731
+    elif op.startswith("embedding_"):
+        ids, table, dy = workloads.embedding_inputs(rows, 131072, hidden, device=dev)
+        if op == "embedding_fwd":
+            y = torch.empty_like(dy)
+            fn = lambda: nf.embedding_fwd(ids, table, 1.0, out=y)  # noqa: E731
+        else:
+            grad = torch.zeros(131072, hidden, device=dev)
+            ws = torch.empty(nf.nf_embedding_bwd_workspace_size(rows, hidden), dtype=torch.uint8, device=dev)
+            kw = {"accumulate": grad} if op == "embedding_bwd_add" else {"out": grad}
+            fn = lambda: nf.embedding_bwd(dy, ids, 131072, 1.0, workspace=ws, **kw)  # noqa: E731
+    elif op.startswith("token_logprob_"):
+        logits, targets, d_lp, d_ent = workloads.logprob_inputs(rows, hidden, device=dev)
+        _, ent, stats, _, _ = nf.token_logprob_fwd(logits, targets)
+        if op == "token_logprob_bwd":
+            y = torch.empty_like(logits)
+            fn = lambda: nf.token_logprob_bwd(logits, targets, stats, ent, d_lp, d_ent, out=y)  # noqa: E731
+        else:
+            top = 20 if op.endswith("_top") else 0
+            fn = lambda: nf.token_logprob_fwd(logits, targets, top=top)  # noqa: E731
     else:
         raise SystemExit(f"unknown op {op}")
     nf.set_path(family or "auto")
@@ -867,7 +898,7 @@ def run_profile_case(spec: str, reps: int):
         for _ in range(reps):
             fn()
         torch.cuda.synchronize()
-        plan = "outer" if op.startswith("outer") else nf.nf_plan_query(
+        plan = op.split("_")[0] if op.startswith(("outer", "embedding", "token")) or "_q8" in op else nf.nf_plan_query(
             "rmsnorm_bwd" if op == "fused_add_rmsnorm_bwd" else op, rows, hidden)
     finally:
         nf.set_path("auto")

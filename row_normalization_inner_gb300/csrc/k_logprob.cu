@@ -465,7 +465,7 @@ token_logprob_rows(const LogprobFwd a) {
                         n = __reduce_add_sync(0xFFFFFFFFu, n);
                         if (n < a.top) continue;
                         bound = test;
-                        if (n <= a.top + 4) break;
+                        if (n <= a.top + 8) break;
                     }
                 }
                 if (lane == 0) *sh.bound = bound;
@@ -569,11 +569,16 @@ token_logprob_rows(const LogprobFwd a) {
 }
 
 // ---- backward --------------------------------------------------------------------
-// 128 threads of 40 registers, twelve CTAs an SM: 4096 x 131072 bf16 307 us;
-// 256 threads of 52 registers, four CTAs, 334 us.
-constexpr int kBwdThreads = 128;
-constexpr int kBwdCtas = 12;
+// Two forms.  The largest calls give a CTA of 256 threads kBwdSpan batches of
+// a row in turn (4096 x 131072 bf16, launches one after the other: 317 us;
+// with a CTA per batch 334 us), all others a batch to a CTA of 128 threads
+// (2048 x 131072: 159 against 162 us; 300 x 32003 fp32 in a graph: 10.4
+// against 12.6 us).  Both keep 1536 threads of 40 registers on an SM (four
+// CTAs of 256 threads at 52 registers: 343 us).
 constexpr int kBwdBatch = 4;
+constexpr int kBwdSpan = 4;
+constexpr int64_t kBwdMinWork = 10000;  // CTAs with a span each
+constexpr int bwd_threads(bool spans) { return spans ? 256 : 128; }
 
 struct LogprobBwd {
     void* out;
@@ -584,13 +589,13 @@ struct LogprobBwd {
     const float* d_logprob;
     const float* d_entropy;  // or null
     int64_t rows, stride, out_stride;
-    int vocab, chunks;       // CTAs of a row
+    int vocab, chunks;       // stretches of a row, a CTA each
     float inv_t;
     bool wide;
 };
 
-template <bool F32>
-__global__ void __launch_bounds__(kBwdThreads, kBwdCtas)
+template <bool F32, bool SPANS>
+__global__ void __launch_bounds__(bwd_threads(SPANS), 1536 / bwd_threads(SPANS))
 token_logprob_grad(const LogprobBwd a) {
     using E = Elem<F32>;
     using T = typename E::T;
@@ -618,40 +623,49 @@ token_logprob_grad(const LogprobBwd a) {
         const float c = a.inv_t * kLog2e;
         const float2 c2 = make_float2(c, c), nm = make_float2(-m, -m), ns = make_float2(-log2_s, -log2_s);
         const float2 A2 = make_float2(A, A), B2 = make_float2(B, B);
-        const int first = chunk * threads * kBwdBatch + threadIdx.x;
-        uint4 raw[kBwdBatch];
+        const auto batch = [&](int first) {
+            uint4 raw[kBwdBatch];
 #pragma unroll
-        for (int k = 0; k < kBwdBatch; ++k)
-            if (first + k * threads < nv) raw[k] = r.load(first + k * threads);
+            for (int k = 0; k < kBwdBatch; ++k)
+                if (first + k * threads < nv) raw[k] = r.load(first + k * threads);
 #pragma unroll
-        for (int k = 0; k < kBwdBatch; ++k) {
-            const int v = first + k * threads;
-            if (v >= nv) continue;
-            const int j0 = v * E::N - r.lead;
-            float2 f[E::N / 2];
-            E::unpack(raw[k], f);
-#pragma unroll
-            for (int q = 0; q < E::N / 2; ++q) {
-                float2 d = __fadd2_rn(__fmul2_rn(__fadd2_rn(f[q], nm), c2), ns);
-                d = make_float2(hold(d.x), hold(d.y));
-                const float2 p = make_float2(ex2(d.x), ex2(d.y));
-                f[q] = __fmul2_rn(p, __ffma2_rn(B2, d, A2));
-            }
-            if (known && target >= j0 && target < j0 + E::N) {
-                const int at = static_cast<int>(target - j0);
+            for (int k = 0; k < kBwdBatch; ++k) {
+                const int v = first + k * threads;
+                if (v >= nv) continue;
+                const int j0 = v * E::N - r.lead;
+                float2 f[E::N / 2];
+                E::unpack(raw[k], f);
 #pragma unroll
                 for (int q = 0; q < E::N / 2; ++q) {
-                    if (at == 2 * q) f[q].x = fmaf(g, a.inv_t, f[q].x);
-                    if (at == 2 * q + 1) f[q].y = fmaf(g, a.inv_t, f[q].y);
+                    float2 d = __fadd2_rn(__fmul2_rn(__fadd2_rn(f[q], nm), c2), ns);
+                    d = make_float2(hold(d.x), hold(d.y));
+                    const float2 p = make_float2(ex2(d.x), ex2(d.y));
+                    f[q] = __fmul2_rn(p, __ffma2_rn(B2, d, A2));
+                }
+                if (known && target >= j0 && target < j0 + E::N) {
+                    const int at = static_cast<int>(target - j0);
+#pragma unroll
+                    for (int q = 0; q < E::N / 2; ++q) {
+                        if (at == 2 * q) f[q].x = fmaf(g, a.inv_t, f[q].x);
+                        if (at == 2 * q + 1) f[q].y = fmaf(g, a.inv_t, f[q].y);
+                    }
+                }
+                if (same && r.full(v)) {
+                    st_stream(out + j0, E::pack(f));
+                } else {
+#pragma unroll
+                    for (int q = 0; q < E::N; ++q)
+                        if (j0 + q >= 0 && j0 + q < a.vocab) out[j0 + q] = E::bits(q & 1 ? f[q / 2].y : f[q / 2].x);
                 }
             }
-            if (same && r.full(v)) {
-                st_stream(out + j0, E::pack(f));
-            } else {
-#pragma unroll
-                for (int q = 0; q < E::N; ++q)
-                    if (j0 + q >= 0 && j0 + q < a.vocab) out[j0 + q] = E::bits(q & 1 ? f[q / 2].y : f[q / 2].x);
-            }
+        };
+        const int step = threads * kBwdBatch;
+        if constexpr (SPANS) {
+            const int64_t begin = static_cast<int64_t>(chunk) * kBwdSpan * step;
+            const int end = static_cast<int>(begin + kBwdSpan * step < nv ? begin + kBwdSpan * step : nv);
+            for (int first = static_cast<int>(begin) + threadIdx.x; first < end; first += step) batch(first);
+        } else {
+            batch(chunk * step + threadIdx.x);
         }
     }
 }
@@ -737,14 +751,22 @@ cudaError_t launch_token_logprob_bwd(void* out, const void* logits, bool f32, co
     a.inv_t = 1.0f / temperature;
     a.wide = wide;
     const int n = f32 ? 4 : 8;
-    const int64_t nv = (vocab + n - 1) / n + 1;  // an unaligned row takes one more
-    int threads = 32;
-    while (threads < kBwdThreads && threads * kBwdBatch < nv) threads *= 2;
-    a.chunks = static_cast<int>((nv + threads * kBwdBatch - 1) / (threads * kBwdBatch));
+    // rows that do not all start on a 16-byte boundary can take one vector more
+    const bool even = reinterpret_cast<uintptr_t>(logits) % 16 == 0 && (stride % n == 0 || rows == 1);
+    const int64_t nv = (vocab + n - 1) / n + (even ? 0 : 1);
+    const auto count = [nv](int64_t vectors) { return (nv + vectors - 1) / vectors; };
+    const int64_t stretch = static_cast<int64_t>(bwd_threads(true)) * kBwdBatch * kBwdSpan;
+    const bool spans = nv >= stretch && rows * count(stretch) >= kBwdMinWork;
+    int threads = spans ? bwd_threads(true) : 32;
+    while (threads < bwd_threads(false) && threads * kBwdBatch < nv) threads *= 2;
+    a.chunks = static_cast<int>(count(spans ? stretch : threads * kBwdBatch));
     const int64_t work = rows * a.chunks;
     const dim3 grid(static_cast<unsigned>(work < 0x7FFFFFFF ? work : 0x7FFFFFFF));
-    return f32 ? launch_with_pdl(token_logprob_grad<true>, grid, dim3(threads), 0, st, a)
-               : launch_with_pdl(token_logprob_grad<false>, grid, dim3(threads), 0, st, a);
+    if (spans)
+        return f32 ? launch_with_pdl(token_logprob_grad<true, true>, grid, dim3(threads), 0, st, a)
+                   : launch_with_pdl(token_logprob_grad<false, true>, grid, dim3(threads), 0, st, a);
+    return f32 ? launch_with_pdl(token_logprob_grad<true, false>, grid, dim3(threads), 0, st, a)
+               : launch_with_pdl(token_logprob_grad<false, false>, grid, dim3(threads), 0, st, a);
 }
 
 }  // namespace nf

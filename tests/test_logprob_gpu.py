@@ -247,6 +247,24 @@ def test_gradient_in_place_strided_and_beside(shift, room, kind):
     assert torch.all(whole[:, :shift] == 77) and torch.all(whole[:, shift + vocab:] == 77)
 
 
+@pytest.mark.parametrize("kind,rows,vocab", [("bf16", 2503, 131072 + 5), ("f32", 3400, 50001)])
+def test_gradient_of_large_calls(kind, rows, vocab):
+    # several batches of a row per CTA; checked some rows at a time
+    logits = torch.randn(rows, vocab, generator=gen(7), device="cuda").mul_(3).to(TYPES[kind])
+    targets = torch.randint(0, vocab, (rows,), generator=gen(8), device="cuda")
+    g = torch.randn(rows, generator=gen(9), device="cuda")
+    h = torch.randn(rows, generator=gen(10), device="cuda")
+    _, ent, stats, _, _ = nf.token_logprob_fwd(logits, targets)
+    got = nf.token_logprob_bwd(logits, targets, stats, ent, g, h)
+    for at in (0, 1, 97, rows // 2, rows - 3):
+        part = slice(at, at + 3)
+        want = nf.token_logprob_bwd(logits[part], targets[part], stats[part], ent[part], g[part], h[part])
+        assert torch.equal(got[part], want)
+        check_gradient(logits[part], targets[part], 1.0, True)
+    sums = got.float().sum(1)  # every row's gradient sums to 0
+    assert torch.all(sums.abs() < 0.05 * (1 + g.abs() + h.abs()))
+
+
 def test_gradient_against_differences():
     # central differences of the operator's own forward along random directions: with a step of 2^-6 the
     # third-order term is below (2^-6)^2 / 6 * 30 (third derivatives of log softmax and entropy along a unit

@@ -13,6 +13,7 @@ rows of a 128-row draw so that its cases nest.
 """
 from __future__ import annotations
 
+import math
 from dataclasses import dataclass, field
 
 import torch
@@ -104,6 +105,29 @@ def outer_inputs(rows: int, hidden: int, seed: int = 0, device="cpu"):
     gamma = _draw(g, (hidden,), 1.0, 0.1, device)
     beta = _draw(g, (hidden,), 0.0, 0.1, device)
     return x, dy, gamma, beta
+
+
+def embedding_inputs(tokens: int, vocab: int, hidden: int, seed: int = 0, device="cpu"):
+    """Token ids log-uniform over the vocabulary (density 1 / id), a table ~ N(0, 0.02)
+    and a gradient ~ N(0, 0.01), bf16.  Returns (ids int64, table, dy)."""
+    g = _gen(seed, device)
+    u = torch.rand(tokens, generator=g, dtype=torch.float64, device=device)
+    ids = (torch.exp(u * math.log(vocab + 1.0)).long() - 1).clamp(0, vocab - 1)
+    table = _draw(g, (vocab, hidden), 0.0, 0.02, device)
+    dy = _draw(g, (tokens, hidden), 0.0, 0.01, device)
+    return ids, table, dy
+
+
+def logprob_inputs(rows: int, vocab: int, seed: int = 0, device="cpu"):
+    """Logits ~ N(0, 2.5) bf16, uniform targets, gradients of the log probability
+    ~ N(0, 1) and of the entropy ~ N(0, 0.01), fp32.  Returns (logits, targets,
+    d_logprob, d_entropy)."""
+    g = _gen(seed, device)
+    logits = _draw(g, (rows, vocab), 0.0, 2.5, device)
+    targets = torch.randint(0, vocab, (rows,), generator=g, device=device)
+    d_logprob = torch.randn(rows, generator=g, device=device)
+    d_entropy = torch.randn(rows, generator=g, device=device) * 0.01
+    return logits, targets, d_logprob, d_entropy
 
 
 @dataclass(frozen=True)
