@@ -21,6 +21,13 @@
  * The pages name the operations but print no formulas; each function below
  * states the textbook definition it implements.
  *
+ * Beside the pages' operations stand the operators at the two ends of the
+ * row stream that the norms work on, and its 8-bit form: the norms with an
+ * 8-bit output (nf_rmsnorm_q8, nf_fused_add_rmsnorm_q8), the embedding lookup
+ * and its gradient (nf_embedding_*), and log probabilities of given tokens
+ * with their gradient (nf_token_logprob_*).  They follow the conventions
+ * below except where they say otherwise; nf_set_path does not concern them.
+ *
  * Conventions shared by every entry point
  * ---------------------------------------
  * Layout.   Activations are row-major, contiguous [rows, hidden] arrays of
@@ -378,8 +385,9 @@ nf_status nf_embedding_fwd(void* y, const void* ids, int32_t id_bytes, const voi
  *     dtable = g (accumulate 0: every row is written, those without tokens
  *     with zeros), or dtable += g (accumulate 1: only rows with tokens are
  *     touched).  Ids outside [0, vocab) contribute nothing.
- * dtable: [vocab, hidden], NF_F32 or NF_BF16; bf16 sums are rounded once, at
- * the end.  The tokens are sorted by id in the workspace (16-byte aligned,
+ * dtable: [vocab, hidden], NF_F32 or NF_BF16; a bf16 element is rounded
+ * once, at the end.  Sums added to fp32 elements are added in L2, where a
+ * result below 2^-126 becomes 0.  The tokens are sorted by id in the workspace (16-byte aligned,
  * at least nf_embedding_bwd_workspace_size(tokens, hidden) bytes on the
  * device that runs the call, contents irrelevant) and equal ids are summed
  * in a fixed order, so results are deterministic; how many ids coincide

@@ -156,3 +156,87 @@ def test_serving_step_with_8_bit_rows():
             assert torch.all(top[:, 0][given] >= lp[given] - 1e-5)
             nxt = nf.embedding_fwd(ids[:, 0], m.table, m.scale)   # the next step's rows
             assert torch.equal(nxt, nf.embedding_fwd(ids[:, 0].int(), m.table, m.scale))
+
+
+FRESH = r"""
+import torch
+import row_normalization_inner_gb300 as nf
+g = torch.Generator(device="cuda")
+g.manual_seed(1)
+# the entry points' first calls, at their smallest
+x = torch.randn(2, 64, generator=g, device="cuda").bfloat16()
+w = torch.ones(64, device="cuda").bfloat16()
+nf.rmsnorm_q8(x, w)
+nf.fused_add_rmsnorm_q8(x, x.clone(), w)
+ids = torch.tensor([1, 0], device="cuda")
+nf.embedding_fwd(ids, x)
+nf.embedding_bwd(x, ids, 5)
+lp, ent, stats, _, _ = nf.token_logprob_fwd(x, ids)
+nf.token_logprob_bwd(x, ids, stats, ent, lp)
+torch.cuda.synchronize()
+# other kernels of the same entry points, met for the first time inside a capture
+x = torch.randn(2500, 4104, generator=g, device="cuda").bfloat16()
+r = torch.randn(2500, 4104, generator=g, device="cuda").bfloat16()
+w = torch.randn(4104, generator=g, device="cuda").bfloat16()
+ids = torch.randint(-1, 3000, (2500,), generator=g, device="cuda")
+many = torch.randint(-1, 3000, (40000,), generator=g, device="cuda")
+some = torch.randint(-1, 3000, (20000,), generator=g, device="cuda")
+dy = torch.randn(40000, 64, generator=g, device="cuda").bfloat16()
+table = torch.randn(3000, 4104, generator=g, device="cuda").bfloat16()
+logits = torch.randn(20, 40001, generator=g, device="cuda")
+t = torch.randint(0, 40001, (20,), generator=g, device="cuda").int()
+
+def step():
+    res = r.clone()
+    out = list(nf.rmsnorm_q8(x, w, fmt="int8")) + list(nf.rmsnorm_q8(x, w, group=128))
+    out += list(nf.fused_add_rmsnorm_q8(x, res, w, group=128)) + [res]
+    out += [nf.embedding_fwd(ids, table, 3.0), nf.embedding_bwd(x, ids, 3000, dtype=torch.bfloat16)]
+    out += [nf.embedding_bwd(dy, many, 3000), nf.embedding_bwd(dy[:20000], some, 3000)]
+    lp, ent, stats, top, top_ids = nf.token_logprob_fwd(logits, t, 0.5, top=32)
+    return out + [lp, ent, stats, top, top_ids, nf.token_logprob_bwd(logits, t, stats, ent, lp, ent, 0.5)]
+
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = step()
+graph.replay()
+torch.cuda.synchronize()
+want = step()
+torch.cuda.synchronize()
+assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(got, want))
+assert nf.nf_get_device_status(0) == nf.NF_OK
+print("captured")
+"""
+
+
+def test_kernels_first_met_inside_a_capture():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FRESH], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
+
+
+def test_calls_at_once_on_two_streams():
+    m = Model(tokens=3000, vocab=5003, hidden=1024, seed=3)
+    dy = torch.randn(3000, 1024, device="cuda").bfloat16()
+    logits = torch.randn(3000, 5003, device="cuda")
+
+    def step(ids, targets):
+        y = nf.embedding_fwd(ids, m.table, 2.0)
+        q, scale = nf.rmsnorm_q8(y, m.w, EPS)
+        lp, ent, stats, top, top_ids = nf.token_logprob_fwd(logits, targets, top=8)
+        return [y, q, scale, lp, ent, top, top_ids, nf.embedding_bwd(dy, ids, 5003),
+                nf.token_logprob_bwd(logits, targets, stats, ent, m.d_logprob)]
+    inputs = [(m.ids, m.targets), (m.ids.flip(0), m.targets.flip(0))]
+    want = [step(*i) for i in inputs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in inputs]
+    for _ in range(5):
+        got = []
+        for s, i in zip(streams, inputs):
+            with torch.cuda.stream(s):
+                got.append(step(*i))
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(a, b))
