@@ -601,12 +601,14 @@ def _rmsnorm_q8(x, residual, weight, eps, fmt, group, out, scale):
     if scale is None:
         scale = torch.empty(scale_shape, dtype=torch.float32, device=x.device)
     if residual is None:
-        _check(nf_rmsnorm_q8(out.data_ptr(), scale.data_ptr(), x.data_ptr(), weight.data_ptr(), rows,
-                             hidden, eps, code, group, _stream_on(dev)), "nf_rmsnorm_q8")
+        st = lib().nf_rmsnorm_q8(out.data_ptr(), scale.data_ptr(), x.data_ptr(), weight.data_ptr(), rows,
+                                 hidden, eps, code, group, _stream_on(dev))
     else:
-        _check(nf_fused_add_rmsnorm_q8(out.data_ptr(), scale.data_ptr(), x.data_ptr(),
-                                       residual.data_ptr(), weight.data_ptr(), rows, hidden, eps, code,
-                                       group, _stream_on(dev)), "nf_fused_add_rmsnorm_q8")
+        st = lib().nf_fused_add_rmsnorm_q8(out.data_ptr(), scale.data_ptr(), x.data_ptr(),
+                                           residual.data_ptr(), weight.data_ptr(), rows, hidden, eps,
+                                           code, group, _stream_on(dev))
+    if st:
+        raise NFError(st, "nf_rmsnorm_q8" if residual is None else "nf_fused_add_rmsnorm_q8")
     return out, scale
 
 
@@ -669,8 +671,10 @@ def embedding_fwd(ids, table, scale: float = 1.0, out=None, stream=None):
         _need_on(dev, out, torch.bfloat16, "out")
         if out.shape != shape:
             raise ValueError(f"out must be of shape {tuple(shape)}")
-    _check(nf_embedding_fwd(out.data_ptr(), ids.data_ptr(), id_bytes, table.data_ptr(), ids.numel(),
-                            vocab, hidden, scale, _stream_on(dev)), "nf_embedding_fwd")
+    st = lib().nf_embedding_fwd(out.data_ptr(), ids.data_ptr(), id_bytes, table.data_ptr(), ids.numel(),
+                                vocab, hidden, scale, _stream_on(dev))
+    if st:
+        raise NFError(st, "nf_embedding_fwd")
     return out
 
 
@@ -709,15 +713,16 @@ def embedding_bwd(dy, ids, vocab: int, scale: float = 1.0, dtype=None, accumulat
     if workspace is None:
         # freed right after the launches: the allocator hands the block to
         # later work on the same stream only, which runs after these kernels
-        workspace = torch.empty(max(nf_embedding_bwd_workspace_size(tokens, hidden), 16),
+        workspace = torch.empty(max(lib().nf_embedding_bwd_workspace_size(tokens, hidden), 16),
                                 dtype=torch.uint8, device=dy.device)
     else:
         _need_on(dev, workspace, workspace.dtype, "workspace")
-    _check(nf_embedding_bwd(grad.data_ptr(), NF_F32 if kind is torch.float32 else NF_BF16,
-                            int(accumulate is not None), dy.data_ptr(), ids.data_ptr(), id_bytes, tokens,
-                            vocab, hidden, scale, workspace.data_ptr(),
-                            workspace.numel() * workspace.element_size(), _stream_on(dev)),
-           "nf_embedding_bwd")
+    st = lib().nf_embedding_bwd(grad.data_ptr(), NF_F32 if kind is torch.float32 else NF_BF16,
+                                int(accumulate is not None), dy.data_ptr(), ids.data_ptr(), id_bytes,
+                                tokens, vocab, hidden, scale, workspace.data_ptr(),
+                                workspace.numel() * workspace.element_size(), _stream_on(dev))
+    if st:
+        raise NFError(st, "nf_embedding_bwd")
     return grad
 
 
@@ -774,9 +779,11 @@ def token_logprob_fwd(logits, targets, temperature: float = 1.0, top: int = 0, s
         top_logprob = torch.empty((rows, top), dtype=f32, device=device)
         top_ids = torch.empty((rows, top), dtype=torch.int64, device=device)
         lp_ptr, id_ptr = top_logprob.data_ptr(), top_ids.data_ptr()
-    _check(nf_token_logprob_fwd(logprob.data_ptr(), entropy.data_ptr(), stats.data_ptr(), lp_ptr, id_ptr,
-                                logits.data_ptr(), kind, stride, targets.data_ptr(), id_bytes, rows, vocab,
-                                temperature, top, _stream_on(dev)), "nf_token_logprob_fwd")
+    st = lib().nf_token_logprob_fwd(logprob.data_ptr(), entropy.data_ptr(), stats.data_ptr(), lp_ptr, id_ptr,
+                                    logits.data_ptr(), kind, stride, targets.data_ptr(), id_bytes, rows,
+                                    vocab, temperature, top, _stream_on(dev))
+    if st:
+        raise NFError(st, "nf_token_logprob_fwd")
     return logprob, entropy, stats, top_logprob, top_ids
 
 
@@ -814,10 +821,12 @@ def token_logprob_bwd(logits, targets, stats, entropy, d_logprob, d_entropy=None
             raise ValueError("out must have the logits' type and shape")
         _need_on(dev, out, out.dtype, "out", contiguous=False)
         out_stride = _logits_stride(out, "out")
-    _check(nf_token_logprob_bwd(out.data_ptr(), out_stride, logits.data_ptr(), kind, stride,
-                                targets.data_ptr(), id_bytes, stats.data_ptr(), ent_ptr,
-                                d_logprob.data_ptr(), d_ent_ptr, rows, vocab, temperature,
-                                _stream_on(dev)), "nf_token_logprob_bwd")
+    st = lib().nf_token_logprob_bwd(out.data_ptr(), out_stride, logits.data_ptr(), kind, stride,
+                                    targets.data_ptr(), id_bytes, stats.data_ptr(), ent_ptr,
+                                    d_logprob.data_ptr(), d_ent_ptr, rows, vocab, temperature,
+                                    _stream_on(dev))
+    if st:
+        raise NFError(st, "nf_token_logprob_bwd")
     return out
 
 
