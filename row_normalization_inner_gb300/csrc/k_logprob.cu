@@ -721,8 +721,19 @@ cudaError_t launch_token_logprob_fwd(float* logprob, float* entropy, float* stat
     a.inv_t = 1.0f / temperature;
     a.wide = wide;
     const int64_t nv = vocab / (f32 ? 4 : 8) + 1;
-    int threads = 128;
-    while (threads < kFwdMaxThreads && threads * kFwdBatch < nv) threads *= 2;
+    // Few rows: the largest CTA that has a batch per thread.  Where the rows
+    // fill the GPU anyway, smaller CTAs, up to eight batches a thread (32
+    // threads: four), so that more rows are in flight beside the one whose
+    // sums are joined: 4096 x 1000 bf16 7.9 -> 4.7 us, with 5 alternatives
+    // 20.1 -> 9.4 us; 4096 x 10000 25.8 -> 18.9 us; 256 x 32000 with 20
+    // alternatives would go from 8.1 to 10.5 us.
+    int threads = 32;
+    if (rows >= 10 * static_cast<int64_t>(sms)) {
+        while (threads < kFwdMaxThreads && nv > threads * kFwdBatch * (threads == 32 ? 4 : 8)) threads *= 2;
+    } else {
+        threads = 128;
+        while (threads < kFwdMaxThreads && threads * kFwdBatch < nv) threads *= 2;
+    }
     // few rows: more CTAs per row, while each thread still has a batch
     int ctas = 1;
     while (ctas < 8 && rows * ctas * 2 <= 2 * static_cast<int64_t>(sms) && nv >= static_cast<int64_t>(ctas) * 2 * threads)

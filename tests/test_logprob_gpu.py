@@ -143,6 +143,15 @@ def test_forward(rows, vocab, fill, kind):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("fill", FILLS)
+@pytest.mark.parametrize("rows,vocab", [(1600, 7), (1601, 1000), (1533, 4097), (1520, 9001), (1521, 20011)])
+def test_forward_of_many_rows(rows, vocab, fill, kind):
+    logits, targets = make(rows, vocab, kind, fill, rows + vocab, room=3, shift=1)
+    for top, temperature in ((0, 1.0), (32, 0.7)):
+        check_forward(logits, targets, temperature, top)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
 @pytest.mark.parametrize("shift,room", [(1, 0), (3, 5), (0, 13), (8, 8), (7, 9)])
 @pytest.mark.parametrize("rows,vocab", [(3, 5), (9, 1000), (20, 33000), (400, 2049)])
 def test_forward_rows_that_start_anywhere(rows, vocab, shift, room, kind):
