@@ -82,15 +82,22 @@ __device__ __forceinline__ float fma_bf16(uint16_t a, uint16_t b, float c) {
     return d;
 }
 
-// MAXT bounds the CTA size, so that rows of few threads keep a larger register
-// budget.
-constexpr int kQ8MaxStages = 8;
-constexpr int kQ8RingBytes = 200 * 1024;  // of an SM, shared by its CTAs (which need some 1.7 KB each besides)
-// Threads per SM the ring kernels are compiled for, and run with.
-constexpr int kRing256 = 512, kRing384 = 768, kRing1024 = 1024;
-constexpr int q8_ring_threads(int maxt) { return maxt <= 256 ? kRing256 : maxt <= 384 ? kRing384 : kRing1024; }
-constexpr int q8_ring_min_ctas(int maxt) { return q8_ring_threads(maxt) / maxt; }
-constexpr int kQ8MaxCtas = 16;
+// The ring's share of an SM: shared memory (each CTA needs some 1.7 KB
+// besides) and threads, for which its kernels are compiled.  Fewer threads
+// than would fit, since more made it slower (16384 x 4096: 512 threads 34.0
+// us, 768 34.6 us, 1024 43.7 us; 5120: 39.4, 42.0, 56.0 us), except that rows
+// of 193 to 384 threads take 768 (8192: 512 threads 66.8 us, 768 62.7 us; with
+// group scales 66.1 and 73.9 us) and longer ones what 1024 give.  Every row
+// length gets three stages or more.
+constexpr int kRingBytes = 200 * 1024;
+constexpr int kRingMaxStages = 8;
+constexpr int ring_threads(int maxt, bool grouped) {
+    return maxt <= 192 || (maxt <= 256 && grouped) ? 512 : maxt <= 384 ? 768 : 1024;
+}
+constexpr bool three_stages(int ctas, int threads) { return kRingBytes / ctas / (4 * threads * 16) >= 3; }
+static_assert(three_stages(4, 128) && three_stages(3, 160) && three_stages(2, 192) && three_stages(3, 256) &&
+              three_stages(2, 384) && three_stages(2, 512) && three_stages(1, 1024), "stages");
+// Shorter rows stay with the row-per-CTA form (16384 x 1024: 10.3 us; the ring 11.3 us).
 constexpr int kRingMinThreads = 128;
 
 __device__ __forceinline__ void bulk_copy(void* to, const void* from, uint32_t bytes, uint64_t* bar) {
@@ -100,8 +107,10 @@ __device__ __forceinline__ void bulk_copy(void* to, const void* from, uint32_t b
 
 // The row of a thread: vectors k * T + t, k < VPT, so that 16 neighbouring
 // lanes hold a group of 128 columns.
-// RING: the weight's vectors are the caller's (KEEPW) or read here, and the
-// products take the mixed-precision form.
+// RING: the products take the mixed-precision form (with it the ring was
+// faster, 16384 x 8192 71 -> 63 us, and the row-per-CTA form slower, 16384 x
+// 4096 34 -> 38 us), and the weight's vectors are the caller's where KEEPW (a
+// CTA's threads keep them for all their rows) or read here.
 template <int VPT, bool RES, bool INT8, bool GROUPED, bool RING, bool KEEPW>
 struct Q8Row {
     float2 p[VPT][4];    // s * w
@@ -279,21 +288,23 @@ norm_q8_rows(const Q8Args a) {
     }
 }
 
-// Calls of many rows: one wave of CTAs that walk the rows blockIdx.x, +
+// Calls of many rows without the residual: one wave of CTAs that walk the rows blockIdx.x, +
 // gridDim.x, ..., each row brought into a ring of `stages` rows in shared
 // memory by bulk copies that thread 0 issues.  A row's loads, its reduction
 // and its stores take turns in a CTA, and with a row per CTA too few bytes
 // are in flight where only 3 bytes move per element; the ring keeps rows in
-// flight whatever the CTA is doing.  One barrier per row: behind it every
+// flight whatever the CTA is doing (16384 x 5120: 45.8 -> 39.4 us, x 12288: 127
+// -> 93 us; with the residual, 7 bytes per element, the row-per-CTA form runs
+// at the copy rate: 16384 x 8192 133 us, the ring 148 us).  One barrier per row: behind it every
 // thread has read the row's stage, which is then refilled, and the reduction
 // buffers alternate.
 template <int VPT, int MAXT, bool INT8, bool GROUPED>
-__global__ void __launch_bounds__(MAXT, q8_ring_min_ctas(MAXT))
+__global__ void __launch_bounds__(MAXT, ring_threads(MAXT, GROUPED) / MAXT)
 norm_q8_ring(const Q8Args a, int stages) {
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ __align__(16) float red_sum[2][32];
     __shared__ __align__(16) uint32_t red_top[2][32];
-    __shared__ __align__(8) uint64_t full[kQ8MaxStages];
+    __shared__ __align__(8) uint64_t full[kRingMaxStages];
     const int T = blockDim.x, t = threadIdx.x, NV = a.hidden / kVec;
     const uint32_t row_bytes = a.hidden * 2;
     if (t < 32) red_sum[0][t] = red_sum[1][t] = red_top[0][t] = red_top[1][t] = 0;
@@ -314,6 +325,7 @@ norm_q8_ring(const Q8Args a, int stages) {
     };
     if (t == 0)
         for (int s = 0; s < stages; ++s) fetch(s, s);
+    // (at 384 threads with group scales, and above, the registers they take cost more)
     constexpr bool kKeepW = MAXT <= 256 || (MAXT == 384 && !GROUPED);
     uint4 wv[kKeepW ? VPT : 1];
     if constexpr (kKeepW) {
@@ -339,14 +351,9 @@ norm_q8_ring(const Q8Args a, int stages) {
         if (ok) r.products(a, row, xv, none, wv, T, t);
         __syncwarp();
         r.reduce_warp();
-        bool failed;
-        if (T > 32) {
-            r.leave(red_sum[i & 1], red_top[i & 1], t);
-            failed = __syncthreads_or(!ok);
-            r.collect(red_sum[i & 1], red_top[i & 1], T >> 5);
-        } else {
-            failed = __any_sync(0xFFFFFFFFu, !ok);
-        }
+        r.leave(red_sum[i & 1], red_top[i & 1], t);
+        const bool failed = __syncthreads_or(!ok);
+        r.collect(red_sum[i & 1], red_top[i & 1], T >> 5);
         if (failed) {  // a copy did not arrive: say so, give those in flight a last chance, and leave
             if (t == 0) {
                 record_status(a.status, kStatusTimeout);
@@ -367,27 +374,23 @@ norm_q8_ring(const Q8Args a, int stages) {
 template <int VPT, int MAXT, bool RES, bool INT8, bool GROUPED>
 cudaError_t go(const Q8Args& a, int threads, int sms, cudaStream_t st) {
     if constexpr (VPT > 2 && !RES) {
-        // the ring, where every resident CTA has several rows
-        const auto kernel = norm_q8_ring<VPT, MAXT, INT8, GROUPED>;
-        static std::atomic<bool> set[64];
-        int dev = 0;
-        if (cudaError_t e = cudaGetDevice(&dev)) return e;
-        if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-        if (!set[dev].load(std::memory_order_acquire)) {
-            if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kQ8RingBytes))
-                return e;
-            set[dev].store(true, std::memory_order_release);
-        }
-        const int stage_bytes = a.hidden * 2;
-        int ctas = q8_ring_threads(MAXT) / threads;
-        ctas = ctas > kQ8MaxCtas ? kQ8MaxCtas : ctas < 1 ? 1 : ctas;
-        while (ctas > 1 && kQ8RingBytes / ctas / stage_bytes < 2) --ctas;
-        int stages = kQ8RingBytes / ctas / stage_bytes;
-        if (stages > kQ8MaxStages) stages = kQ8MaxStages;
+        const int ctas = ring_threads(MAXT, GROUPED) / threads, stage_bytes = a.hidden * 2;
         const int64_t wave = static_cast<int64_t>(ctas) * sms;
-        if (stages >= 2 && threads >= kRingMinThreads && a.rows >= 2 * wave)
+        if (threads >= kRingMinThreads && a.rows >= 2 * wave) {  // every resident CTA has several rows
+            const auto kernel = norm_q8_ring<VPT, MAXT, INT8, GROUPED>;
+            static std::atomic<bool> set[64];
+            int dev = 0;
+            if (cudaError_t e = cudaGetDevice(&dev)) return e;
+            if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+            if (!set[dev].load(std::memory_order_acquire)) {
+                if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes))
+                    return e;
+                set[dev].store(true, std::memory_order_release);
+            }
+            const int fit = kRingBytes / ctas / stage_bytes, stages = fit < kRingMaxStages ? fit : kRingMaxStages;
             return launch_with_pdl(kernel, dim3(static_cast<unsigned>(wave)), dim3(threads),
                                    static_cast<size_t>(stages) * stage_bytes, st, a, stages);
+        }
     }
     const int rpc = VPT > 2 && threads == 32 ? 4 : 1;
     const int64_t blocks = (a.rows + rpc - 1) / rpc;
@@ -419,7 +422,8 @@ cudaError_t launch_norm_q8(const Q8Args& a, bool int8, bool grouped, int sms, cu
     const int t = threads(4);
     if (t > 384) return go<4, 1024>(a, int8, grouped, t, sms, st);
     if (t > 256) return go<4, 384>(a, int8, grouped, t, sms, st);
-    return go<4, 256>(a, int8, grouped, t, sms, st);
+    if (t > 192) return go<4, 256>(a, int8, grouped, t, sms, st);
+    return go<4, 192>(a, int8, grouped, t, sms, st);
 }
 
 }  // namespace nf
