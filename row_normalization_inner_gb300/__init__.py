@@ -527,89 +527,40 @@ def outer_norm_bwd(dy, x, mean, rstd, gamma, workspace=None, out=None, stream=No
     return dx, dgamma, dbeta
 
 
-# The token-side operators' helpers.  A decode step's call takes 2 us on the
-# GPU, so they spend little on the host: one pass of checks per tensor, the
-# raw stream handle, outputs allocated once the arguments are known to fit.
+# The token-side operators' helpers: the checks, the outputs' allocation and
+# the call are native (csrc/tensors.cpp), because a decode step's call takes
+# 2 us on the GPU and the same steps in Python 13 to 23 us.
 
-def _device(t, name, *dtypes):
-    """Device index of a CUDA tensor of one of the types; it must be the
-    current device, whose context and stream the call uses."""
+_native = None
+
+
+def _helpers():
+    """The native helpers (raises if they have not been built)."""
+    global _native
+    if _native is None:
+        import torch  # noqa: F401  (its libraries first)
+        lib()
+        try:
+            from . import _tensors as native
+        except ImportError as e:
+            raise RuntimeError("row_normalization_inner_gb300/_tensors.so cannot be loaded: build it with "
+                               "`python -m row_normalization_inner_gb300.build` (no fallback exists)") from e
+        _native = native
+    return _native
+
+
+def _result(r, where):
+    """A helper's result, or NFError for the status that stands in its place."""
+    if r.__class__ is int:
+        raise NFError(r, where)
+    return r
+
+
+def _on(stream, helper, *args):
+    """helper(*args) with `stream` as the current stream, which its outputs and workspaces then belong to."""
     import torch
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a tensor")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
-    dev = t.get_device()
-    if dev < 0:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if dev != torch.cuda.current_device():
-        raise ValueError(f"{name} is on cuda:{dev}, which is not the current device")
-    return dev
-
-
-def _need_on(dev, t, dtype, name, contiguous=True):
-    import torch
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a tensor")
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must be a CUDA tensor on cuda:{dev}")
-    if contiguous and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-
-
-def _stream_on(dev):
-    """The current stream's handle (torch.cuda.current_stream() builds a Stream object first, 3 us)."""
-    import torch
-    return torch._C._cuda_getCurrentRawStream(dev)
-
-
-def _rmsnorm_q8(x, residual, weight, eps, fmt, group, out, scale):
-    import torch
-    bf16 = torch.bfloat16
-    dev = _device(x, "x", bf16)
-    if not x.is_contiguous():
-        raise ValueError("x must be contiguous")
-    _need_on(dev, weight, bf16, "weight")
-    shape = x.shape
-    hidden = shape[-1] if shape else 0
-    rows = x.numel() // hidden if hidden else 0
-    if weight.shape != (hidden,):
-        raise ValueError("weight must be of shape [hidden]")
-    if residual is not None:
-        _need_on(dev, residual, bf16, "residual")
-        if residual.shape != shape:
-            raise ValueError("residual must have x's shape")
-    code = Q8_FORMATS.get(fmt)
-    if code is None:
-        raise ValueError(f"fmt must be one of {tuple(Q8_FORMATS)}, got {fmt!r}")
-    if group != 0 and group != Q8_GROUP:
-        raise ValueError(f"group must be 0 (one scale per row) or {Q8_GROUP}, got {group!r}")
-    dtype = torch.float8_e4m3fn if code == NF_Q8_E4M3 else torch.int8
-    if out is not None:
-        _need_on(dev, out, dtype, "out")
-        if out.shape != shape:
-            raise ValueError("out must have x's shape")
-    scale_shape = shape[:-1] + (-(-hidden // group),) if group else shape[:-1]
-    if scale is not None:
-        _need_on(dev, scale, torch.float32, "scale")
-        if scale.shape != scale_shape:
-            raise ValueError(f"scale must be of shape {tuple(scale_shape)}")
-    if out is None:
-        out = torch.empty_like(x, dtype=dtype)
-    if scale is None:
-        scale = torch.empty(scale_shape, dtype=torch.float32, device=x.device)
-    if residual is None:
-        st = lib().nf_rmsnorm_q8(out.data_ptr(), scale.data_ptr(), x.data_ptr(), weight.data_ptr(), rows,
-                                 hidden, eps, code, group, _stream_on(dev))
-    else:
-        st = lib().nf_fused_add_rmsnorm_q8(out.data_ptr(), scale.data_ptr(), x.data_ptr(),
-                                           residual.data_ptr(), weight.data_ptr(), rows, hidden, eps,
-                                           code, group, _stream_on(dev))
-    if st:
-        raise NFError(st, "nf_rmsnorm_q8" if residual is None else "nf_fused_add_rmsnorm_q8")
-    return out, scale
+    with torch.cuda.stream(stream):
+        return helper(*args)
 
 
 def rmsnorm_q8(x, weight, eps: float = 1e-6, fmt: str = "e4m3", group: int = 0, out=None,
@@ -619,10 +570,8 @@ def rmsnorm_q8(x, weight, eps: float = 1e-6, fmt: str = "e4m3", group: int = 0, 
     [..., ceil(hidden / 128)] (group=128); q * scale stands for the
     normalized rows, which are not rounded to bf16 in between."""
     if stream is not None:
-        import torch
-        with torch.cuda.stream(stream):
-            return _rmsnorm_q8(x, None, weight, eps, fmt, group, out, scale)
-    return _rmsnorm_q8(x, None, weight, eps, fmt, group, out, scale)
+        return _on(stream, rmsnorm_q8, x, weight, eps, fmt, group, out, scale)
+    return _result(_helpers().norm_q8(x, None, weight, eps, fmt, group, out, scale), "nf_rmsnorm_q8")
 
 
 def fused_add_rmsnorm_q8(x, residual, weight, eps: float = 1e-6, fmt: str = "e4m3",
@@ -630,52 +579,20 @@ def fused_add_rmsnorm_q8(x, residual, weight, eps: float = 1e-6, fmt: str = "e4m
     """residual += x in place; returns (q, scale) of rmsnorm(residual) * weight
     as rmsnorm_q8 does (from the fp32 sums, as fused_add_rmsnorm).  x is left
     as it was."""
-    import torch
     if residual is None:
         raise TypeError("residual must be a tensor")
     if stream is not None:
-        with torch.cuda.stream(stream):
-            return _rmsnorm_q8(x, residual, weight, eps, fmt, group, out, scale)
-    return _rmsnorm_q8(x, residual, weight, eps, fmt, group, out, scale)
-
-
-def _id_bytes(ids, name):
-    """Bytes per id of an int32 / int64 tensor."""
-    import torch
-    if not isinstance(ids, torch.Tensor):
-        raise TypeError(f"{name} must be a tensor")
-    if ids.dtype is torch.int64:
-        return 8
-    if ids.dtype is torch.int32:
-        return 4
-    raise TypeError(f"{name} must be torch.int32 or torch.int64, got {ids.dtype}")
+        return _on(stream, fused_add_rmsnorm_q8, x, residual, weight, eps, fmt, group, out, scale)
+    return _result(_helpers().norm_q8(x, residual, weight, eps, fmt, group, out, scale),
+                   "nf_fused_add_rmsnorm_q8")
 
 
 def embedding_fwd(ids, table, scale: float = 1.0, out=None, stream=None):
     """scale * table[ids], rounded to bf16: a tensor of shape [*ids.shape, hidden].
     ids int32 or int64; an id outside [0, vocab) gives a row of zeros."""
-    import torch
     if stream is not None:
-        with torch.cuda.stream(stream):
-            return embedding_fwd(ids, table, scale, out)
-    id_bytes = _id_bytes(ids, "ids")
-    dev = _device(table, "table", torch.bfloat16)
-    _need_on(dev, ids, ids.dtype, "ids")
-    if table.dim() != 2 or not table.is_contiguous():
-        raise ValueError("table must be [vocab, hidden] and contiguous")
-    vocab, hidden = table.shape
-    shape = ids.shape + (hidden,)
-    if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=table.device)
-    else:
-        _need_on(dev, out, torch.bfloat16, "out")
-        if out.shape != shape:
-            raise ValueError(f"out must be of shape {tuple(shape)}")
-    st = lib().nf_embedding_fwd(out.data_ptr(), ids.data_ptr(), id_bytes, table.data_ptr(), ids.numel(),
-                                vocab, hidden, scale, _stream_on(dev))
-    if st:
-        raise NFError(st, "nf_embedding_fwd")
-    return out
+        return _on(stream, embedding_fwd, ids, table, scale, out)
+    return _result(_helpers().embedding_fwd(ids, table, scale, out), "nf_embedding_fwd")
 
 
 def embedding_bwd(dy, ids, vocab: int, scale: float = 1.0, dtype=None, accumulate=None, out=None,
@@ -686,64 +603,10 @@ def embedding_bwd(dy, ids, vocab: int, scale: float = 1.0, dtype=None, accumulat
     place.  Equal ids are summed in fp32 in token order: the result is
     deterministic.  The workspace (nf_embedding_bwd_workspace_size bytes) is
     allocated here when not given."""
-    import torch
     if stream is not None:
-        with torch.cuda.stream(stream):
-            return embedding_bwd(dy, ids, vocab, scale, dtype, accumulate, out, workspace)
-    id_bytes = _id_bytes(ids, "ids")
-    dev = _device(dy, "dy", torch.bfloat16)
-    _need_on(dev, ids, ids.dtype, "ids")
-    if dy.dim() < 1 or dy.shape[:-1] != ids.shape or not dy.is_contiguous():
-        raise ValueError("dy must be of shape [*ids.shape, hidden] and contiguous")
-    hidden = dy.shape[-1]
-    if accumulate is not None and out is not None:
-        raise ValueError("accumulate is written in place: out cannot be given too")
-    grad = accumulate if accumulate is not None else out
-    if grad is None:
-        grad = torch.empty((vocab, hidden), dtype=dtype or torch.float32, device=dy.device)
-    elif not isinstance(grad, torch.Tensor):
-        raise TypeError("the gradient must be a tensor")
-    kind = grad.dtype
-    if (kind is not torch.float32 and kind is not torch.bfloat16) or (dtype is not None and kind is not dtype):
-        raise TypeError(f"the gradient must be {dtype or 'torch.float32 or torch.bfloat16'}, got {kind}")
-    _need_on(dev, grad, kind, "the gradient")
-    if grad.shape != (vocab, hidden):
-        raise ValueError(f"the gradient must be of shape {(vocab, hidden)}")
-    tokens = ids.numel()
-    if workspace is None:
-        # freed right after the launches: the allocator hands the block to
-        # later work on the same stream only, which runs after these kernels
-        workspace = torch.empty(max(lib().nf_embedding_bwd_workspace_size(tokens, hidden), 16),
-                                dtype=torch.uint8, device=dy.device)
-    else:
-        _need_on(dev, workspace, workspace.dtype, "workspace")
-    st = lib().nf_embedding_bwd(grad.data_ptr(), NF_F32 if kind is torch.float32 else NF_BF16,
-                                int(accumulate is not None), dy.data_ptr(), ids.data_ptr(), id_bytes,
-                                tokens, vocab, hidden, scale, workspace.data_ptr(),
-                                workspace.numel() * workspace.element_size(), _stream_on(dev))
-    if st:
-        raise NFError(st, "nf_embedding_bwd")
-    return grad
-
-
-def _logits_stride(t, name):
-    """Row stride of a [rows, vocab] tensor whose rows may be apart."""
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be [rows, vocab]")
-    rows, vocab = t.shape
-    row_stride, stride = t.stride()
-    if rows <= 1:
-        row_stride = max(vocab, 1)
-    if (vocab > 1 and stride != 1) or row_stride < vocab:
-        raise ValueError(f"{name}'s rows must be contiguous and apart")
-    return row_stride
-
-
-def _need_rows(dev, t, rows, name):
-    import torch
-    _need_on(dev, t, torch.float32, name)
-    if t.shape != (rows,):
-        raise ValueError(f"{name} must be of shape {(rows,)}")
+        return _on(stream, embedding_bwd, dy, ids, vocab, scale, dtype, accumulate, out, workspace)
+    return _result(_helpers().embedding_bwd(dy, ids, vocab, scale, dtype, accumulate, out, workspace),
+                   "nf_embedding_bwd")
 
 
 def token_logprob_fwd(logits, targets, temperature: float = 1.0, top: int = 0, stream=None):
@@ -756,35 +619,9 @@ def token_logprob_fwd(logits, targets, temperature: float = 1.0, top: int = 0, s
     `top` most probable tokens, [rows, top] fp32 and int64 (None with top 0),
     equal ones by rising id.  Entries of -inf are masked; targets outside
     [0, vocab) give 0."""
-    import torch
     if stream is not None:
-        with torch.cuda.stream(stream):
-            return token_logprob_fwd(logits, targets, temperature, top)
-    dev = _device(logits, "logits", torch.bfloat16, torch.float32)
-    stride = _logits_stride(logits, "logits")
-    id_bytes = _id_bytes(targets, "targets")
-    _need_on(dev, targets, targets.dtype, "targets")
-    kind = NF_F32 if logits.dtype is torch.float32 else NF_BF16
-    rows, vocab = logits.shape
-    if targets.shape != (rows,):
-        raise ValueError(f"targets must be of shape {(rows,)}")
-    if not 0 <= top <= TOP_MAX:
-        raise ValueError(f"top must be 0 to {TOP_MAX}, got {top}")
-    device, f32 = logits.device, torch.float32
-    logprob = torch.empty(rows, dtype=f32, device=device)
-    entropy = torch.empty(rows, dtype=f32, device=device)
-    stats = torch.empty((rows, 2), dtype=f32, device=device)
-    top_logprob = top_ids = lp_ptr = id_ptr = None
-    if top:
-        top_logprob = torch.empty((rows, top), dtype=f32, device=device)
-        top_ids = torch.empty((rows, top), dtype=torch.int64, device=device)
-        lp_ptr, id_ptr = top_logprob.data_ptr(), top_ids.data_ptr()
-    st = lib().nf_token_logprob_fwd(logprob.data_ptr(), entropy.data_ptr(), stats.data_ptr(), lp_ptr, id_ptr,
-                                    logits.data_ptr(), kind, stride, targets.data_ptr(), id_bytes, rows,
-                                    vocab, temperature, top, _stream_on(dev))
-    if st:
-        raise NFError(st, "nf_token_logprob_fwd")
-    return logprob, entropy, stats, top_logprob, top_ids
+        return _on(stream, token_logprob_fwd, logits, targets, temperature, top)
+    return _result(_helpers().token_logprob_fwd(logits, targets, temperature, top), "nf_token_logprob_fwd")
 
 
 def token_logprob_bwd(logits, targets, stats, entropy, d_logprob, d_entropy=None,
@@ -792,42 +629,11 @@ def token_logprob_bwd(logits, targets, stats, entropy, d_logprob, d_entropy=None
     """Gradient of token_logprob_fwd's logprob and entropy for the logits, in
     their type, given the gradients d_logprob and (optionally) d_entropy and
     the forward's stats and entropy.  out may be the logits themselves."""
-    import torch
     if stream is not None:
-        with torch.cuda.stream(stream):
-            return token_logprob_bwd(logits, targets, stats, entropy, d_logprob, d_entropy, temperature, out)
-    dev = _device(logits, "logits", torch.bfloat16, torch.float32)
-    stride = _logits_stride(logits, "logits")
-    id_bytes = _id_bytes(targets, "targets")
-    _need_on(dev, targets, targets.dtype, "targets")
-    kind = NF_F32 if logits.dtype is torch.float32 else NF_BF16
-    rows, vocab = logits.shape
-    if targets.shape != (rows,):
-        raise ValueError(f"targets must be of shape {(rows,)}")
-    _need_on(dev, stats, torch.float32, "stats")
-    if stats.shape != (rows, 2):
-        raise ValueError(f"stats must be of shape {(rows, 2)}")
-    _need_rows(dev, d_logprob, rows, "d_logprob")
-    ent_ptr = d_ent_ptr = None
-    if d_entropy is not None:
-        _need_rows(dev, d_entropy, rows, "d_entropy")
-        _need_rows(dev, entropy, rows, "entropy")
-        ent_ptr, d_ent_ptr = entropy.data_ptr(), d_entropy.data_ptr()
-    if out is None:
-        out = torch.empty((rows, vocab), dtype=logits.dtype, device=logits.device)
-        out_stride = max(vocab, 1)
-    else:
-        if not isinstance(out, torch.Tensor) or out.dtype is not logits.dtype or out.shape != logits.shape:
-            raise ValueError("out must have the logits' type and shape")
-        _need_on(dev, out, out.dtype, "out", contiguous=False)
-        out_stride = _logits_stride(out, "out")
-    st = lib().nf_token_logprob_bwd(out.data_ptr(), out_stride, logits.data_ptr(), kind, stride,
-                                    targets.data_ptr(), id_bytes, stats.data_ptr(), ent_ptr,
-                                    d_logprob.data_ptr(), d_ent_ptr, rows, vocab, temperature,
-                                    _stream_on(dev))
-    if st:
-        raise NFError(st, "nf_token_logprob_bwd")
-    return out
+        return _on(stream, token_logprob_bwd, logits, targets, stats, entropy, d_logprob, d_entropy,
+                   temperature, out)
+    return _result(_helpers().token_logprob_bwd(logits, targets, stats, entropy, d_logprob, d_entropy,
+                                                temperature, out), "nf_token_logprob_bwd")
 
 
 def set_path(path):

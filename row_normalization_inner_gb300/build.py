@@ -1,5 +1,7 @@
 """Build libnf.so in-tree: every csrc/*.cu compiled for sm_103a in parallel,
-then linked into row_normalization_inner_gb300/libnf.so.
+then linked into row_normalization_inner_gb300/libnf.so; and _tensors.so, the
+native part of the token-side operators' tensor helpers (csrc/tensors.cpp,
+against the installed PyTorch and libnf.so).
 
     python -m row_normalization_inner_gb300.build [--force] [--ptxas-table]
 
@@ -21,6 +23,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libnf.so")
+TENSORS_SRC = os.path.join(CSRC, "tensors.cpp")
+TENSORS = os.path.join(PKG, "_tensors.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
@@ -37,14 +41,14 @@ def _sources():
 
 
 def _deps():
-    return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) \
+    return _sources() + [TENSORS_SRC] + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) \
         + glob.glob(os.path.join(INCLUDE, "*.h"))
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(TENSORS):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(TENSORS))
     return any(os.path.getmtime(p) > t for p in _deps())
 
 
@@ -57,23 +61,50 @@ def _compile(src: str) -> tuple[str, str]:
     return obj, r.stderr
 
 
+def _torch_dir() -> str:
+    import importlib.util
+    return os.path.dirname(importlib.util.find_spec("torch").origin)
+
+
+def _compile_tensors() -> str:
+    import sysconfig
+    obj = os.path.join(BUILD, "tensors.o")
+    torch_inc = os.path.join(_torch_dir(), "include")
+    cuda_inc = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-c", TENSORS_SRC, "-o", obj, "-isystem", torch_inc, "-isystem",
+           os.path.join(torch_inc, "torch", "csrc", "api", "include"), "-isystem",
+           sysconfig.get_paths()["include"], "-isystem", cuda_inc]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {TENSORS_SRC}:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link(cmd, out):
+    tmp = out + f".tmp{os.getpid()}"
+    r = subprocess.run(cmd + ["-o", tmp], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, out)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     if not force and not _stale():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     srcs = _sources()
-    with cf.ThreadPoolExecutor(max_workers=min(len(srcs), os.cpu_count() or 4)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
+        tensors = ex.submit(_compile_tensors)
         results = list(ex.map(_compile, srcs))
+        tensors_obj = tensors.result()
     objs = [o for o, _ in results]
     with open(os.path.join(BUILD, "ptxas.log"), "w") as f:
         for (o, log), src in zip(results, srcs):
             f.write(f"==== {os.path.basename(src)}\n{log}\n")
-    tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [_nvcc()] + ARCH + ["-shared", "-o", tmp] + objs
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
+    _link([_nvcc()] + ARCH + ["-shared"] + objs, LIB)
+    torch_lib = os.path.join(_torch_dir(), "lib")
+    _link(["g++", "-shared", tensors_obj, "-L", PKG, "-l:libnf.so", "-Wl,-rpath,$ORIGIN", "-L", torch_lib,
+           f"-Wl,-rpath,{torch_lib}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"], TENSORS)
     if verbose:
         print(f"built {LIB}")
     return LIB
