@@ -289,16 +289,19 @@ __device__ __forceinline__ void push_top(const TopShared& sh, const Row<F32>& r,
 __device__ __forceinline__ void sort_top(uint64_t* cand, int n, int top, uint64_t* best, int* n_kept) {
     const int t = threadIdx.x, T = blockDim.x;
     if (n > 256) {
-        // the top-th largest key bit by bit (the keys are distinct), then only what reaches it
+        // the top-th largest key bit by bit (the keys are distinct), then only
+        // what reaches it
+        __shared__ int part[2][kFwdMaxThreads / 32];
         uint64_t bound = 0;
         for (int b = 63; b >= 0; --b) {
             const uint64_t test = bound | (1ull << b);
             int mine = 0;
             for (int i = t; i < n; i += T) mine += cand[i] >= test;
-            // counts beyond `top` per thread are cut: only >= top matters
+            mine = __reduce_add_sync(0xFFFFFFFFu, mine);
+            if ((t & 31) == 0) part[b & 1][t >> 5] = mine;
+            __syncthreads();
             int total = 0;
-#pragma unroll
-            for (int bit = 0; bit < 6; ++bit) total += __syncthreads_count((min(mine, 63) >> bit) & 1) << bit;
+            for (int w = 0; w < T / 32; ++w) total += part[b & 1][w];
             if (total >= top) bound = test;
         }
         // at most 9 of a thread's: n <= 8 T + kTopMax
