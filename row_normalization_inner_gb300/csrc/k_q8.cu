@@ -59,6 +59,10 @@ __device__ __forceinline__ float scale_of(uint32_t top, float rstd) {
 // rstd stands in y and in the scale alike, so y / scale is s w * (Q / max|s w|):
 // fewer roundings than dividing y has.  Only a maximum so small or so large
 // that the quotient could leave fp32, or a smallest scale, takes y itself.
+// Q / max is divided exactly where a row has one (no time at any size; 15% to
+// 30% fewer values that round to the neighbour of the exact result's) and is an
+// approximate reciprocal where every thread computes its group's: exact there,
+// 16384 x 8192 e4m3 would take 72.1 us for 66.3 and 12% fewer such values.
 __device__ __forceinline__ bool plain_range(float top, float scale) {
     return top >= kScaleMin && top <= 0x1p100f && scale > kScaleMin;
 }
@@ -216,7 +220,7 @@ struct Q8Row {
             const float top_value = __uint_as_float(row_top);
             row_scale = scale_of<INT8>(row_top, rstd);
             range = plain_range(top_value, row_scale);
-            factor = (INT8 ? 127.f : 448.f) * reciprocal(top_value);
+            factor = __fdiv_rn(INT8 ? 127.f : 448.f, top_value);
             if (t == 0) a.scale[row] = row_scale;
         }
 #pragma unroll
