@@ -355,8 +355,9 @@ typedef enum { NF_Q8_E4M3 = 0, NF_Q8_INT8 = 1 } nf_q8_format;
  * so q * scale stands for y.  group = 0: one scale per row, scale is [rows]
  * fp32.  group = 128: one scale per 128 columns (the last group may be
  * shorter), scale is [rows, ceil(hidden / 128)] fp32.  y is not rounded to
- * bf16 before it is quantized.  A scale whose largest |y| is not finite is
- * not finite either, and its q are 0; a row whose sum of squares is not
+ * bf16 before it is quantized.  A scale whose largest |y| is not finite, or
+ * whose largest |s_j * weight[j]| is not finite in fp32 (max |y| is found as
+ * that maximum times the rsqrt), is not finite either, and its q are 0; a row whose sum of squares is not
  * finite in fp32 (a NaN, an infinity, magnitudes beyond about 1e19) has NaN
  * for every scale.  x is only read; nothing may overlap.  q: [rows, hidden]
  * bytes, 8-byte aligned; scale 4-byte aligned.  hidden: a multiple of 8 up
@@ -387,11 +388,12 @@ nf_status nf_embedding_fwd(void* y, const void* ids, int32_t id_bytes, const voi
  *     touched).  Ids outside [0, vocab) contribute nothing.
  * dtable: [vocab, hidden], NF_F32 or NF_BF16; a bf16 element is rounded
  * once, at the end.  Sums added to fp32 elements are added in L2, where a
- * result below 2^-126 becomes 0.  The tokens are sorted by id in the workspace (16-byte aligned,
- * at least nf_embedding_bwd_workspace_size(tokens, hidden) bytes on the
- * device that runs the call, contents irrelevant) and equal ids are summed
- * in a fixed order, so results are deterministic; how many ids coincide
- * changes neither the launches nor the workspace.  Sizes as for the lookup.
+ * result below 2^-126 becomes 0.  The tokens are sorted by id in the
+ * workspace (16-byte aligned, at least nf_embedding_bwd_workspace_size(tokens,
+ * hidden) bytes on the device that runs the call, contents irrelevant) and
+ * equal ids are summed in a fixed order, so results are deterministic; how
+ * many ids coincide changes neither the launches nor the workspace.  Sizes as
+ * for the lookup.
  * Nothing may overlap.  tokens == 0 reads nothing (dy, ids and workspace may
  * be NULL) and, with accumulate 0, writes zeros. */
 size_t nf_embedding_bwd_workspace_size(int64_t tokens, int64_t hidden);
@@ -436,7 +438,8 @@ nf_status nf_token_logprob_fwd(float* logprob, float* entropy, float* stats, flo
  * vocab are left as they are.  A row with every entry masked gets zeros.
  * entropy is the forward's, and may be NULL where d_entropy is.  dlogits may
  * be the logits themselves (same pointer and stride); nothing else may
- * overlap it.  Sizes as for the forward. */
+ * overlap it, from its first element to its last (rows of one matrix between
+ * the rows of the other count as an overlap).  Sizes as for the forward. */
 nf_status nf_token_logprob_bwd(void* dlogits, int64_t dstride, const void* logits, nf_dtype type,
                                int64_t stride, const void* targets, int32_t id_bytes, const float* stats,
                                const float* entropy, const float* d_logprob, const float* d_entropy,

@@ -11,7 +11,8 @@
 //   1. the sort: up to kSortRank tokens by counting, up to kSortCluster radix
 //      passes in the shared memory of one cluster of CTAs, above that two
 //      launches per radix pass (digit counts of each tile, then a stable
-//      scatter whose CTAs each add up the counts of the tiles before theirs);
+//      scatter whose CTAs each add up the counts of the tiles before theirs),
+//      and from kOffsetTiles tiles on a third between them for those sums;
 //   2. the sums: the sorted tokens are cut into chunks of equal length, a CTA
 //      per chunk and slice of columns.  A run inside one chunk is written at
 //      once; the pieces of a run that crosses chunks go to the workspace.
@@ -332,12 +333,18 @@ sort_cluster(const void* __restrict__ ids, bool wide, int n, int64_t vocab, int 
     }
 }
 
-// Tiles of many-CTA sorts: 2048 tokens.  Tiles of 4096 were faster from half a
-// million tokens on, where the sums take milliseconds, and slower below
-// (65536 tokens and 8 columns, the whole call: 40.4 against 32.6 us).
+// Tiles of many-CTA sorts: 2048 tokens.  Tiles of 4096 were slower (65536
+// tokens and 8 columns, the whole call: 43 against 33 us; 16 million: 2154
+// against 1795 us).
 constexpr int kTileThreads = 512;
 constexpr int kTileItems = 4;
 constexpr int kTile = kTileThreads * kTileItems;
+// From this many tiles on a launch of its own adds up the tiles' counts; below,
+// every CTA of the scatter adds up those of the tiles before its own, which
+// saves a launch but grows with the square of the tiles (8 columns, the whole
+// call, with the launch and without: 65536 tokens 34.5 and 32.8 us, 131072
+// 45.7 and 47.5 us, a million 153 and 317 us, 16 million 1.8 and 36.9 ms).
+constexpr int kOffsetTiles = 64;
 
 __global__ void __launch_bounds__(kTileThreads)
 sort_count(const void* __restrict__ ids, bool wide, const uint32_t* __restrict__ keys_in, int64_t n,
@@ -362,10 +369,46 @@ sort_count(const void* __restrict__ ids, bool wide, const uint32_t* __restrict__
         hist[(static_cast<int64_t>(blockIdx.x) << bits) + d] = bins[d];
 }
 
+// The counts of each digit in the tiles before each tile, in place of the
+// tiles' own, and behind them the counts of all tiles.  A CTA takes 32 digits,
+// its warps each a stretch of the tiles.
+constexpr int kOffsetWarps = 32;
+__global__ void __launch_bounds__(kOffsetWarps * 32)
+sort_offsets(uint32_t* __restrict__ hist, int bins, int tiles) {
+    __shared__ uint32_t sums[kOffsetWarps][32];
+    grid_dep_wait();
+    grid_dep_release();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, d = blockIdx.x * 32 + lane;
+    const int per = (tiles + kOffsetWarps - 1) / kOffsetWarps;
+    const int i0 = min(warp * per, tiles), i1 = min(i0 + per, tiles);
+    uint32_t sum = 0;
+    if (d < bins) {
+#pragma unroll 16
+        for (int i = i0; i < i1; ++i) sum += hist[static_cast<int64_t>(i) * bins + d];
+    }
+    sums[warp][lane] = sum;
+    __syncthreads();
+    uint32_t run = 0;
+    for (int w = 0; w < warp; ++w) run += sums[w][lane];
+    if (d >= bins) return;
+    if (warp == kOffsetWarps - 1) hist[static_cast<int64_t>(tiles) * bins + d] = run + sum;
+    constexpr int kBatch = 16;  // in flight
+    for (int i = i0; i < i1; i += kBatch) {
+        uint32_t c[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) c[k] = i + k < i1 ? hist[static_cast<int64_t>(i + k) * bins + d] : 0;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            if (i + k < i1) hist[static_cast<int64_t>(i + k) * bins + d] = run;
+            run += c[k];
+        }
+    }
+}
+
 __global__ void __launch_bounds__(kTileThreads)
 sort_scatter(const void* __restrict__ ids, bool wide, const uint32_t* __restrict__ keys_in,
              const uint32_t* __restrict__ at_in, int64_t n, int64_t vocab, int shift, int bits, int tiles,
-             const uint32_t* __restrict__ hist, uint32_t* __restrict__ keys_out,
+             bool offsets, const uint32_t* __restrict__ hist, uint32_t* __restrict__ keys_out,
              uint32_t* __restrict__ at_out) {
     __shared__ __align__(4) uint16_t counts[kTileThreads / 32 * kBins];
     __shared__ uint32_t total[kBins], first[kBins], warp_sums[32];
@@ -389,11 +432,16 @@ sort_scatter(const void* __restrict__ ids, bool wide, const uint32_t* __restrict
     // all tiles' items of a digit, and those of the tiles before this one
     for (int d = threadIdx.x; d < bins; d += kTileThreads) {
         uint32_t all = 0, before = 0;
+        if (offsets) {
+            all = hist[static_cast<int64_t>(tiles) * bins + d];
+            before = hist[static_cast<int64_t>(blockIdx.x) * bins + d];
+        } else {
 #pragma unroll 16
-        for (int i = 0; i < tiles; ++i) {
-            const uint32_t c = hist[static_cast<int64_t>(i) * bins + d];
-            all += c;
-            if (i < static_cast<int>(blockIdx.x)) before += c;
+            for (int i = 0; i < tiles; ++i) {
+                const uint32_t c = hist[static_cast<int64_t>(i) * bins + d];
+                all += c;
+                if (i < static_cast<int>(blockIdx.x)) before += c;
+            }
         }
         total[d] = all;
         first[d] = before;
@@ -666,7 +714,7 @@ Layout layout(int64_t tokens, int64_t hidden, int sms) {
     l.at = take(tokens * 4);
     l.keys2 = take(l.tiles ? tokens * 4 : 0);
     l.at2 = take(l.tiles ? tokens * 4 : 0);
-    l.hist = take(l.tiles * kBins * 4);
+    l.hist = take(l.tiles ? (l.tiles + 1) * kBins * 4 : 0);
     l.crossings = take((4 + l.chunks) * 4);
     l.pieces = take(l.chunks * 2 * hidden * 4);
     l.bytes = at;
@@ -764,12 +812,19 @@ cudaError_t launch_embedding_bwd(void* dtable, bool f32, bool add, const void* d
         uint32_t *to_keys = u32(l.keys), *to_at = u32(l.at), *other_keys = u32(l.keys2), *other_at = u32(l.at2);
         const uint32_t *from_keys = nullptr, *from_at = nullptr;
         const dim3 grid(static_cast<unsigned>(l.tiles));
+        const bool offsets = l.tiles >= kOffsetTiles;
         for (int p = 0; p < passes; ++p) {
             if (cudaError_t e = launch_with_pdl(sort_count, grid, dim3(kTileThreads), 0, st, ids, wide, from_keys,
                                                 tokens, vocab, p * bits, bits, u32(l.hist), u32(l.crossings)))
                 return e;
+            if (offsets) {
+                const dim3 digits(((1 << bits) + 31) / 32);
+                if (cudaError_t e = launch_with_pdl(sort_offsets, digits, dim3(kOffsetWarps * 32), 0, st, u32(l.hist),
+                                                    1 << bits, static_cast<int>(l.tiles)))
+                    return e;
+            }
             if (cudaError_t e = launch_with_pdl(sort_scatter, grid, dim3(kTileThreads), 0, st, ids, wide, from_keys,
-                                                from_at, tokens, vocab, p * bits, bits, static_cast<int>(l.tiles),
+                                                from_at, tokens, vocab, p * bits, bits, static_cast<int>(l.tiles), offsets,
                                                 static_cast<const uint32_t*>(u32(l.hist)), to_keys, to_at))
                 return e;
             from_keys = keys = to_keys;

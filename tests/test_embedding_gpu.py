@@ -151,6 +151,16 @@ def test_gradient_at_the_borders_of_the_sorts(tokens, kind):
     check_grad(nf.embedding_bwd(dy, ids, vocab, 1.0), dy, ids, vocab, 1.0, None)
 
 
+@pytest.mark.parametrize("kind", ["uniform", "words", "one", "none"])
+@pytest.mark.parametrize("tokens,vocab", [(98305, 5), (131072, 70000), (131073, 1 << 21), (400001, 40000)])
+def test_gradient_of_many_tiles(tokens, vocab, kind):
+    # counts of the digits summed over the tiles by a launch of their own
+    hidden = 8
+    ids = make_ids(kind, tokens, vocab, tokens)
+    dy = torch.randn(tokens, hidden, generator=gen(tokens), device="cuda").bfloat16()
+    check_grad(nf.embedding_bwd(dy, ids, vocab, 0.5), dy, ids, vocab, 0.5, None)
+
+
 @pytest.mark.parametrize("tokens", [3000, 30000])
 def test_gradient_is_deterministic_and_in_token_order(tokens):
     vocab, hidden = 500, 520
