@@ -66,8 +66,9 @@ nf_status logprob_checks(nf_dtype type, int32_t id_bytes, int64_t rows, int64_t 
                          float temperature) {
     if ((type != NF_BF16 && type != NF_F32) || (id_bytes != 4 && id_bytes != 8)) return NF_ERR_INVALID_ARG;
     if (rows < 0 || vocab < 1 || vocab > kLogprobMaxVocab || stride < vocab) return NF_ERR_INVALID_ARG;
-    // a row's last element stays addressable, and rows times CTAs per row countable
-    if (stride > INT64_MAX / 32 || rows > (INT64_MAX / 32) / stride) return NF_ERR_INVALID_ARG;
+    // every size in bytes stays in 64 bits (the alternatives of a row take 8 * kLogprobMaxTop)
+    constexpr int64_t kMost = INT64_MAX / (8 * kLogprobMaxTop);
+    if (stride > kMost || rows > kMost / stride) return NF_ERR_INVALID_ARG;
     if (!(temperature >= 0x1p-64f && temperature <= 0x1p64f)) return NF_ERR_INVALID_ARG;
     return NF_OK;
 }

@@ -97,6 +97,16 @@ PyObject* pack(std::initializer_list<PyObject*> items) {
     return tuple;
 }
 
+// The interpreter runs on while a helper allocates and launches: neither
+// needs it, and both can wait (for memory, for room in the launch queue).
+struct WithoutInterpreter {
+    PyThreadState* state = PyEval_SaveThread();
+    WithoutInterpreter() = default;
+    WithoutInterpreter(const WithoutInterpreter&) = delete;
+    WithoutInterpreter& operator=(const WithoutInterpreter&) = delete;
+    ~WithoutInterpreter() { PyEval_RestoreThread(state); }
+};
+
 void count(Py_ssize_t n, Py_ssize_t want) { TORCH_CHECK_TYPE(n == want, "expected ", want, " arguments, got ", n); }
 
 // (x, residual or None, weight, eps, fmt, group, out or None, scale or None) -> (q, scale)
@@ -142,14 +152,18 @@ PyObject* norm_q8(PyObject*, PyObject* const* a, Py_ssize_t n) {
         TORCH_CHECK_VALUE(scale.sizes() == at::IntArrayRef(shape), "scale must be of shape ", at::IntArrayRef(shape));
     }
     const float eps = static_cast<float>(number(a[3]));
-    if (!out.defined()) out = empty(x.sizes(), type, dev);
-    if (!scale.defined()) scale = empty(shape, at::kFloat, dev);
-    const nf_q8_format format = int8 ? NF_Q8_INT8 : NF_Q8_E4M3;
-    float* s = static_cast<float*>(scale.data_ptr());
-    const nf_status st =
-        fused ? nf_fused_add_rmsnorm_q8(out.data_ptr(), s, x.const_data_ptr(), THPVariable_Unpack(a[1]).data_ptr(), weight.const_data_ptr(),
-                                        rows, hidden, eps, format, group, stream_of(dev))
-              : nf_rmsnorm_q8(out.data_ptr(), s, x.const_data_ptr(), weight.const_data_ptr(), rows, hidden, eps, format, group, stream_of(dev));
+    nf_status st;
+    {
+        const WithoutInterpreter w;
+        if (!out.defined()) out = empty(x.sizes(), type, dev);
+        if (!scale.defined()) scale = empty(shape, at::kFloat, dev);
+        const nf_q8_format format = int8 ? NF_Q8_INT8 : NF_Q8_E4M3;
+        float* s = static_cast<float*>(scale.data_ptr());
+        st =
+            fused ? nf_fused_add_rmsnorm_q8(out.data_ptr(), s, x.const_data_ptr(), THPVariable_Unpack(a[1]).data_ptr(), weight.const_data_ptr(),
+                                            rows, hidden, eps, format, group, stream_of(dev))
+                  : nf_rmsnorm_q8(out.data_ptr(), s, x.const_data_ptr(), weight.const_data_ptr(), rows, hidden, eps, format, group, stream_of(dev));
+    }
     if (st != NF_OK) return status(st);
     return pack({object(a[6], out), object(a[7], scale)});
     END_HANDLE_TH_ERRORS
@@ -176,9 +190,13 @@ PyObject* embedding_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
         TORCH_CHECK_VALUE(out.sizes() == at::IntArrayRef(shape), "out must be of shape ", at::IntArrayRef(shape));
     }
     const float scale = static_cast<float>(number(a[2]));
-    if (!out.defined()) out = empty(shape, at::kBFloat16, dev);
-    const nf_status st = nf_embedding_fwd(out.data_ptr(), ids.const_data_ptr(), bytes, table.const_data_ptr(), ids.numel(), table.size(0),
-                                          table.size(1), scale, stream_of(dev));
+    nf_status st;
+    {
+        const WithoutInterpreter w;
+        if (!out.defined()) out = empty(shape, at::kBFloat16, dev);
+        st = nf_embedding_fwd(out.data_ptr(), ids.const_data_ptr(), bytes, table.const_data_ptr(), ids.numel(), table.size(0),
+                                              table.size(1), scale, stream_of(dev));
+    }
     return st != NF_OK ? status(st) : object(a[3], out);
     END_HANDLE_TH_ERRORS
 }
@@ -218,19 +236,21 @@ PyObject* embedding_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
         need_on(ws, "workspace", dev);
     }
     const float scale = static_cast<float>(number(a[3]));
-    if (!grad.defined()) {
-        TORCH_CHECK_VALUE(vocab >= 0, "vocab must not be negative");
-        grad = empty(shape, want, dev);
+    TORCH_CHECK_VALUE(vocab >= 0, "vocab must not be negative");
+    nf_status st;
+    {
+        const WithoutInterpreter w;
+        if (!grad.defined()) grad = empty(shape, want, dev);
+        if (!ws.defined()) {
+            // freed right after the launches: the allocator hands the block to
+            // later work on the same stream only, which runs after these kernels
+            const int64_t need = static_cast<int64_t>(nf_embedding_bwd_workspace_size(tokens, hidden));
+            ws = empty({need > 16 ? need : 16}, at::kByte, dev);
+        }
+        st = nf_embedding_bwd(grad.data_ptr(), grad.scalar_type() == at::kFloat ? NF_F32 : NF_BF16, add, dy.const_data_ptr(),
+                                              ids.const_data_ptr(), bytes, tokens, vocab, hidden, scale, ws.data_ptr(), ws.nbytes(),
+                                              stream_of(dev));
     }
-    if (!ws.defined()) {
-        // freed right after the launches: the allocator hands the block to
-        // later work on the same stream only, which runs after these kernels
-        const int64_t need = static_cast<int64_t>(nf_embedding_bwd_workspace_size(tokens, hidden));
-        ws = empty({need > 16 ? need : 16}, at::kByte, dev);
-    }
-    const nf_status st = nf_embedding_bwd(grad.data_ptr(), grad.scalar_type() == at::kFloat ? NF_F32 : NF_BF16, add, dy.const_data_ptr(),
-                                          ids.const_data_ptr(), bytes, tokens, vocab, hidden, scale, ws.data_ptr(), ws.nbytes(),
-                                          stream_of(dev));
     return st != NF_OK ? status(st) : object(place, grad);
     END_HANDLE_TH_ERRORS
 }
@@ -271,18 +291,23 @@ PyObject* token_logprob_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t top = integer(a[3]);
     TORCH_CHECK_VALUE(top >= 0 && top <= NF_TOP_MAX, "top must be 0 to ", NF_TOP_MAX, ", got ", top);
     const float temperature = static_cast<float>(number(a[2]));
-    const Tensor logprob = empty({rows}, at::kFloat, dev), entropy = empty({rows}, at::kFloat, dev);
-    const Tensor stats = empty({rows, 2}, at::kFloat, dev);
-    Tensor top_logprob, top_ids;
-    if (top) {
-        top_logprob = empty({rows, top}, at::kFloat, dev);
-        top_ids = empty({rows, top}, at::kLong, dev);
+    Tensor logprob, entropy, stats, top_logprob, top_ids;
+    nf_status st;
+    {
+        const WithoutInterpreter w;
+        logprob = empty({rows}, at::kFloat, dev);
+        entropy = empty({rows}, at::kFloat, dev);
+        stats = empty({rows, 2}, at::kFloat, dev);
+        if (top) {
+            top_logprob = empty({rows, top}, at::kFloat, dev);
+            top_ids = empty({rows, top}, at::kLong, dev);
+        }
+        const auto f32 = [](const Tensor& t) { return static_cast<float*>(t.data_ptr()); };
+        st = nf_token_logprob_fwd(f32(logprob), f32(entropy), f32(stats), top ? f32(top_logprob) : nullptr,
+                                                  top ? static_cast<int64_t*>(top_ids.data_ptr()) : nullptr, logits.const_data_ptr(),
+                                                  type_of(logits), stride, targets.const_data_ptr(), bytes, rows, vocab, temperature,
+                                                  static_cast<int32_t>(top), stream_of(dev));
     }
-    const auto f32 = [](const Tensor& t) { return static_cast<float*>(t.data_ptr()); };
-    const nf_status st = nf_token_logprob_fwd(f32(logprob), f32(entropy), f32(stats), top ? f32(top_logprob) : nullptr,
-                                              top ? static_cast<int64_t*>(top_ids.data_ptr()) : nullptr, logits.const_data_ptr(),
-                                              type_of(logits), stride, targets.const_data_ptr(), bytes, rows, vocab, temperature,
-                                              static_cast<int32_t>(top), stream_of(dev));
     if (st != NF_OK) return status(st);
     const auto wrap = [](const Tensor& t) {
         if (t.defined()) return THPVariable_Wrap(t);
@@ -330,11 +355,15 @@ PyObject* token_logprob_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
         out_stride = row_stride(out, "out");
     }
     const float temperature = static_cast<float>(number(a[6]));
-    if (!out.defined()) out = empty({rows, vocab}, logits.scalar_type(), dev);
-    const nf_status st = nf_token_logprob_bwd(out.data_ptr(), out_stride, logits.const_data_ptr(), type_of(logits), stride, targets.const_data_ptr(),
-                                              bytes, static_cast<const float*>(stats.const_data_ptr()), ent,
-                                              static_cast<const float*>(d_logprob.const_data_ptr()), d_ent, rows, vocab, temperature,
-                                              stream_of(dev));
+    nf_status st;
+    {
+        const WithoutInterpreter w;
+        if (!out.defined()) out = empty({rows, vocab}, logits.scalar_type(), dev);
+        st = nf_token_logprob_bwd(out.data_ptr(), out_stride, logits.const_data_ptr(), type_of(logits), stride, targets.const_data_ptr(),
+                                                  bytes, static_cast<const float*>(stats.const_data_ptr()), ent,
+                                                  static_cast<const float*>(d_logprob.const_data_ptr()), d_ent, rows, vocab, temperature,
+                                                  stream_of(dev));
+    }
     return st != NF_OK ? status(st) : object(a[7], out);
     END_HANDLE_TH_ERRORS
 }
