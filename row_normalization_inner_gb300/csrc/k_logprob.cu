@@ -270,17 +270,21 @@ __device__ __forceinline__ void push_top(const TopShared& sh, const Row<F32>& r,
     float2 f[E::N / 2];
     E::unpack(raw, f);
     const int j0 = v * E::N - r.lead;
+    const auto key_of = [&](int q) {
+        return (static_cast<uint64_t>(order_of(q & 1 ? f[q / 2].y : f[q / 2].x)) << 32) | ~static_cast<uint32_t>(j0 + q);
+    };
+    // one addition for the vector: those of a row of equal elements come one after the other
+    uint32_t reach = 0;
+#pragma unroll
+    for (int q = 0; q < E::N; ++q)
+        reach |= static_cast<uint32_t>((q & 1 ? f[q / 2].y : f[q / 2].x) > -INFINITY && key_of(q) >= low) << q;
+    if (reach == 0) return;
+    int at = atomicAdd(sh.n_cand, __popc(reach));
 #pragma unroll
     for (int q = 0; q < E::N; ++q) {
-        const float x = q & 1 ? f[q / 2].y : f[q / 2].x;
-        const uint32_t ord = order_of(x);
-        if (x > -INFINITY && ord >= static_cast<uint32_t>(low >> 32)) {
-            const uint64_t key = (static_cast<uint64_t>(ord) << 32) | ~static_cast<uint32_t>(j0 + q);
-            if (key >= low) {
-                const int at = atomicAdd(sh.n_cand, 1);
-                if (at < sh.capacity) sh.cand[at] = key;
-            }
-        }
+        if (!((reach >> q) & 1)) continue;
+        if (at < sh.capacity) sh.cand[at] = key_of(q);
+        ++at;
     }
 }
 
@@ -289,20 +293,30 @@ __device__ __forceinline__ void push_top(const TopShared& sh, const Row<F32>& r,
 __device__ __forceinline__ void sort_top(uint64_t* cand, int n, int top, uint64_t* best, int* n_kept) {
     const int t = threadIdx.x, T = blockDim.x;
     if (n > 256) {
-        // the top-th largest key bit by bit (the keys are distinct), then only
-        // what reaches it
+        // the top-th largest key (they are distinct) bit by bit below the bits
+        // that all share, then only what reaches it
         __shared__ int part[2][kFwdMaxThreads / 32];
-        uint64_t bound = 0;
-        for (int b = 63; b >= 0; --b) {
+        __shared__ uint2 differ[kFwdMaxThreads / 32];
+        const int lane = t & 31, warp = t >> 5, warps = T >> 5;
+        const uint64_t one = cand[0];
+        uint64_t d = 0;
+        for (int i = t; i < n; i += T) d |= cand[i] ^ one;
+        const uint32_t hi = __reduce_or_sync(0xFFFFFFFFu, static_cast<uint32_t>(d >> 32));
+        const uint32_t lo = __reduce_or_sync(0xFFFFFFFFu, static_cast<uint32_t>(d));
+        if (lane == 0) differ[warp] = make_uint2(hi, lo);
+        __syncthreads();
+        const uint2 mine_d = lane < warps ? differ[lane] : make_uint2(0, 0);
+        d = static_cast<uint64_t>(__reduce_or_sync(0xFFFFFFFFu, mine_d.x)) << 32 | __reduce_or_sync(0xFFFFFFFFu, mine_d.y);
+        const int first = 63 - __clzll(static_cast<long long>(d));
+        uint64_t bound = first == 63 ? 0 : one >> (first + 1) << (first + 1);
+        for (int b = first; b >= 0; --b) {
             const uint64_t test = bound | (1ull << b);
             int mine = 0;
             for (int i = t; i < n; i += T) mine += cand[i] >= test;
             mine = __reduce_add_sync(0xFFFFFFFFu, mine);
-            if ((t & 31) == 0) part[b & 1][t >> 5] = mine;
+            if (lane == 0) part[b & 1][warp] = mine;
             __syncthreads();
-            int total = 0;
-            for (int w = 0; w < T / 32; ++w) total += part[b & 1][w];
-            if (total >= top) bound = test;
+            if (static_cast<int>(__reduce_add_sync(0xFFFFFFFFu, lane < warps ? part[b & 1][lane] : 0)) >= top) bound = test;
         }
         // at most 9 of a thread's: n <= 8 T + kTopMax
         constexpr int kEach = 9;
@@ -475,9 +489,13 @@ token_logprob_rows(const LogprobFwd a) {
             }
             __syncthreads();
             const uint32_t bound = *sh.bound;
-            if (ord >= bound)
+            if (ord >= bound) {
+                int reach = 0;
+                for (int i = 0; i < slots; ++i) reach += order_of(sh.slot[i * T + t]) >= bound;
+                int at = reach ? atomicAdd(sh.n_list, reach) : 0;
                 for (int i = 0; i < slots; ++i)
-                    if (order_of(sh.slot[i * T + t]) >= bound) sh.list[atomicAdd(sh.n_list, 1)] = static_cast<uint16_t>(i * T + t);
+                    if (order_of(sh.slot[i * T + t]) >= bound) sh.list[at++] = static_cast<uint16_t>(i * T + t);
+            }
             __syncthreads();
             // read these stretches again, and the partial vectors
             const int edges = short_row ? 0 : (v0 < f0) + (f1 < v1);
@@ -494,6 +512,7 @@ token_logprob_rows(const LogprobFwd a) {
                 return v < (short_row ? v1 : f1) ? v : v1;
             };
             for (int i0 = t; i0 < items; i0 += T) {
+                if (*const_cast<volatile int*>(sh.n_cand) > sh.capacity) break;  // the rounds below will do it
                 const int v = vector_of(i0);
                 if (v < v1) push_top<F32>(sh, r, v, r.load(v), low);
             }
