@@ -104,7 +104,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     _link([_nvcc()] + ARCH + ["-shared"] + objs, LIB)
     torch_lib = os.path.join(_torch_dir(), "lib")
     _link(["g++", "-shared", tensors_obj, "-L", PKG, "-l:libnf.so", "-Wl,-rpath,$ORIGIN", "-L", torch_lib,
-           f"-Wl,-rpath,{torch_lib}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"], TENSORS)
+           f"-Wl,-rpath,{torch_lib}", "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"], TENSORS)
     if verbose:
         print(f"built {LIB}")
     return LIB
