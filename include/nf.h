@@ -388,8 +388,8 @@ nf_status nf_embedding_fwd(void* y, const void* ids, int32_t id_bytes, const voi
  *     touched).  Ids outside [0, vocab) contribute nothing.
  * dtable: [vocab, hidden], NF_F32 or NF_BF16; a bf16 element is rounded
  * once, at the end.  Sums added to fp32 elements are added in L2, where a
- * result below 2^-126 becomes 0.  The tokens are sorted by id in the
- * workspace (16-byte aligned, at least nf_embedding_bwd_workspace_size(tokens,
+ * result below 2^-126 becomes 0.  All but small calls sort the tokens by id in
+ * the workspace (16-byte aligned, at least nf_embedding_bwd_workspace_size(tokens,
  * hidden) bytes on the device that runs the call, contents irrelevant) and
  * equal ids are summed in a fixed order, so results are deterministic; how
  * many ids coincide changes neither the launches nor the workspace.  Sizes as

@@ -7,7 +7,8 @@
 // Backward: dtable[v] (+)= scale * sum over { i : ids[i] = v } of dy[i].  The
 // tokens are sorted by id, stably, so that equal ids become a run in token
 // order; every run is summed in fp32 in that order, which makes the result
-// deterministic where atomics on the table would not be.  Launches:
+// deterministic where atomics on the table would not be.  Up to kDirect
+// tokens need no sort (embedding_direct).  The launches of the others:
 //   1. the sort: up to kSortRank tokens by counting, up to kSortCluster radix
 //      passes in the shared memory of one cluster of CTAs, above that two
 //      launches per radix pass (digit counts of each tile, then a stable
@@ -21,7 +22,10 @@
 //   3. the join: the pieces of each crossing run are added in order.
 // A chunk rather than a run per CTA, because word frequencies are uneven:
 // one id can hold several percent of a batch.  Bound by memory: dy read
-// once, the rows with tokens (or all rows) written once.
+// once, the rows with tokens (or all rows) written once.  One GB300: lookup
+// of 32768 x 8192 118 us (6.2 TB/s), gradient of 16384 x 4096 written to
+// 131072 fp32 rows 337 us (6.8 TB/s), of 65536 x 4096 added to them 247 us
+// (4.8 TB/s, latency of the rows in the sums).
 #include <cooperative_groups.h>
 
 #include <atomic>
@@ -682,6 +686,171 @@ embedding_join(const EmbedBwd a) {
     }
 }
 
+// ---- few tokens: one launch, no sort ------------------------------------------------
+// Up to kDirect tokens a warp takes a token and 512 columns, and looks for the
+// token's id among all of them, which lie in shared memory: where it stands
+// earlier too, another warp has the run; else the warp adds up the id's rows in
+// token order.  A run of more than kDirectRun rows is left to the whole CTA: its
+// warps each add a stretch, and the stretches are joined in order.  A CTA's
+// tokens are far apart, because the first tokens of a batch begin its longest
+// runs.  Bound by latency: one launch against three.  The search grows with the
+// square of the tokens and with the columns, hence the limit (2048 columns
+// added to bf16, against the sort: 16 tokens 2.6 and 6.0 us, 200 4.5 and 9.7,
+// 512 7.1 and 10.7, 1000 8.6 and 12.0, 2000 16.5 and 14.3; 8192 columns: 512
+// 11.7 and 12.3, 1000 19.1 and 16.4).  Runs of 16 rows for a warp were slower
+// (16 equal ids 4.6 for 3.0 us), of 4 too (64 words 4.1 for 3.6 us).
+constexpr int kDirect = 512;
+constexpr int kDirectThreads = 256, kDirectCtas = 3;
+constexpr int kDirectWarps = kDirectThreads / 32;
+constexpr int kDirectRun = 8;
+constexpr int kDirectVectors = 64;  // of a warp's columns, two per lane
+constexpr int kDirectBatch = 4;     // rows in flight
+
+// Rows at[0, n) of dy added to acc, in order.
+__device__ __forceinline__ void add_rows(const EmbedBwd& a, const uint16_t* at, int n, int v, int nv, float2 (&acc)[2][4]) {
+    for (int i = 0; i < n; i += kDirectBatch) {
+        uint4 d[kDirectBatch][2];
+#pragma unroll
+        for (int k = 0; k < kDirectBatch; ++k)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                if (i + k < n && v + 32 * h < nv)
+                    d[k][h] = ld_stream(a.dy + (static_cast<int64_t>(at[i + k]) * nv + v + 32 * h) * kVec);
+#pragma unroll
+        for (int k = 0; k < kDirectBatch; ++k)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (i + k >= n || v + 32 * h >= nv) continue;
+                float2 f[4];
+                unpack8x2(d[k][h], f);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) acc[h][q] = __fadd2_rn(acc[h][q], f[q]);
+            }
+    }
+}
+
+// CTAs [0, blocks * slices): the sums.  CTAs above: zeros, as in embedding_sums.
+template <bool F32, bool ADD>
+__global__ void __launch_bounds__(kDirectThreads, kDirectCtas)
+embedding_direct(const EmbedBwd a, const void* __restrict__ ids, bool wide, int blocks) {
+    __shared__ __align__(16) uint32_t keys[kDirect];
+    __shared__ float2 sums[kDirectWarps][2][4][32];
+    __shared__ uint16_t list[kDirect];                       // a long run's tokens
+    __shared__ uint16_t short_list[kDirectWarps][kDirectRun];
+    __shared__ uint16_t queue[kDirect / kDirectRun];         // the first tokens of this CTA's long runs
+    __shared__ int queued, counts[kDirectWarps];
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5, n = static_cast<int>(a.tokens), nv = a.hidden / kVec;
+    grid_dep_wait();
+    grid_dep_release();
+    if (!ADD && blockIdx.x >= static_cast<unsigned>(blocks * a.slices)) {
+        const int64_t r0 = static_cast<int64_t>(blockIdx.x - blocks * a.slices) * kZeroRows;
+        const int64_t r1 = r0 + kZeroRows < a.vocab ? r0 + kZeroRows : a.vocab;
+        if (t < kZeroRows) list[t] = 0;
+        __syncthreads();
+        for (int i = t; i < n; i += kDirectThreads) {
+            const uint32_t key = key_of(ids, wide, i, a.vocab);
+            if (key >= r0 && key < r1) list[key - r0] = 1;
+        }
+        __syncthreads();
+        const int per = F32 ? nv * 2 : nv;  // 16-byte vectors of a row
+        for (int r = 0; r < r1 - r0; ++r) {
+            if (list[r]) continue;
+            uint4* p = static_cast<uint4*>(a.dtable) + (r0 + r) * per;
+            for (int v = t; v < per; v += kDirectThreads) __stcs(p + v, make_uint4(0, 0, 0, 0));
+        }
+        return;
+    }
+    const uint32_t none = static_cast<uint32_t>(a.vocab);
+    const int whole = (n + kDirectThreads - 1) / kDirectThreads * kDirectThreads;  // keys, with some that no token has
+    for (int i = t; i < whole; i += kDirectThreads) keys[i] = i < n ? key_of(ids, wide, i, a.vocab) : 0xFFFFFFFFu;
+    if (t == 0) queued = 0;
+    __syncthreads();
+    const int slice = blockIdx.x % a.slices, block = blockIdx.x / a.slices;
+    const int v = slice * kDirectVectors + lane;
+    const uint4* four = reinterpret_cast<const uint4*>(keys);
+    for (int i = block + warp * blocks; i < n; i += kDirectWarps * blocks) {
+        const uint32_t key = keys[i];
+        if (key == none) continue;
+        int before = 0, after = 0;
+        for (int p = lane; p < whole / 4; p += 32) {
+            const uint4 k = four[p];
+            const int same = (k.x == key) + (k.y == key) + (k.z == key) + (k.w == key);
+            if (p < i / 4) before += same;
+            else if (p > i / 4) after += same;
+            else {
+                before += (i % 4 > 0 && k.x == key) + (i % 4 > 1 && k.y == key) + (i % 4 > 2 && k.z == key);
+                after += (i % 4 < 1 && k.y == key) + (i % 4 < 2 && k.z == key) + (i % 4 < 3 && k.w == key);
+            }
+        }
+        if (__any_sync(0xFFFFFFFFu, before > 0)) continue;
+        const int rows = 1 + __reduce_add_sync(0xFFFFFFFFu, after);
+        if (rows > kDirectRun) {
+            if (lane == 0) queue[atomicAdd(&queued, 1)] = static_cast<uint16_t>(i);
+            continue;
+        }
+        uint16_t* mine = short_list[warp];
+        if (lane == 0) mine[0] = static_cast<uint16_t>(i);
+        for (int found = 1, p = (i + 1) / 32 * 32; found < rows; p += 32) {
+            const bool is = p + lane > i && keys[p + lane] == key;
+            const uint32_t which = __ballot_sync(0xFFFFFFFFu, is);
+            if (is) mine[found + __popc(which & ((1u << lane) - 1))] = static_cast<uint16_t>(p + lane);
+            found += __popc(which);
+        }
+        __syncwarp();
+        Old<F32, ADD> old[2];
+        float2 acc[2][4] = {};
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            if (v + 32 * h < nv) old[h].load(a, key, v + 32 * h);
+        add_rows(a, mine, rows, v, nv, acc);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            if (v + 32 * h < nv) old[h].put(a, key, v + 32 * h, acc[h]);
+        __syncwarp();  // the list has been read
+    }
+    __syncthreads();
+    for (int k = 0; k < queued; ++k) {
+        const uint32_t key = keys[queue[k]];
+        const int per = whole / kDirectWarps, p0 = warp * per;  // a multiple of 32
+        int found = 0;
+        for (int p = p0; p < p0 + per; p += 32) found += __popc(__ballot_sync(0xFFFFFFFFu, keys[p + lane] == key));
+        if (lane == 0) counts[warp] = found;
+        __syncthreads();
+        int at = 0, rows = 0;
+        for (int w = 0; w < kDirectWarps; ++w) {
+            if (w == warp) at = rows;
+            rows += counts[w];
+        }
+        for (int p = p0; p < p0 + per; p += 32) {
+            const bool is = keys[p + lane] == key;
+            const uint32_t which = __ballot_sync(0xFFFFFFFFu, is);
+            if (is) list[at + __popc(which & ((1u << lane) - 1))] = static_cast<uint16_t>(p + lane);
+            at += __popc(which);
+        }
+        __syncthreads();
+        const int share = (rows + kDirectWarps - 1) / kDirectWarps, first = min(warp * share, rows);
+        float2 acc[2][4] = {};
+        add_rows(a, list + first, min(share, rows - first), v, nv, acc);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) sums[warp][h][q][lane] = acc[h][q];
+        __syncthreads();
+        if (warp < 2 && v + 32 * warp < nv) {
+            Old<F32, ADD> old;
+            old.load(a, key, v + 32 * warp);
+            float2 sum[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                sum[q] = sums[0][warp][q][lane];
+                for (int w = 1; w < kDirectWarps; ++w) sum[q] = __fadd2_rn(sum[q], sums[w][warp][q][lane]);
+            }
+            old.put(a, key, v + 32 * warp, sum);
+        }
+        __syncthreads();  // counts, list and sums are used again
+    }
+}
+
 int64_t round16(int64_t b) { return (b + 15) / 16 * 16; }
 
 constexpr int kChunksPerSm = 4;
@@ -769,6 +938,18 @@ cudaError_t sums(const EmbedBwd& e, int sms, cudaStream_t st) {
                            dim3(kJoinWarps * 32), 0, st, e);
 }
 
+template <bool F32, bool ADD>
+cudaError_t direct(EmbedBwd e, const void* ids, bool wide, int sms, cudaStream_t st) {
+    e.slices = (e.hidden / kVec + kDirectVectors - 1) / kDirectVectors;
+    // a token per warp, in one wave of CTAs where more would not all fit
+    const int64_t most = kDirectCtas * static_cast<int64_t>(sms) / e.slices;
+    int64_t blocks = (e.tokens + kDirectWarps - 1) / kDirectWarps;
+    if (blocks > most) blocks = most > 0 ? most : 1;
+    const int64_t zero = ADD ? 0 : (e.vocab + kZeroRows - 1) / kZeroRows;
+    return launch_with_pdl(embedding_direct<F32, ADD>, dim3(static_cast<unsigned>(blocks * e.slices + zero)),
+                           dim3(kDirectThreads), 0, st, e, ids, wide, static_cast<int>(blocks));
+}
+
 }  // namespace
 
 cudaError_t launch_embedding_fwd(void* y, const void* ids, bool wide, const void* table, int64_t tokens,
@@ -790,6 +971,17 @@ size_t embedding_bwd_workspace(int64_t tokens, int64_t hidden, int sms) {
 cudaError_t launch_embedding_bwd(void* dtable, bool f32, bool add, const void* dy, const void* ids, bool wide,
                                  int64_t tokens, int64_t vocab, int64_t hidden, float scale, void* workspace,
                                  int sms, cudaStream_t st) {
+    EmbedBwd e{};
+    e.dtable = dtable;
+    e.dy = static_cast<const uint16_t*>(dy);
+    e.tokens = tokens;
+    e.vocab = vocab;
+    e.hidden = static_cast<int>(hidden);
+    e.scale = scale;
+    if (tokens > 0 && tokens <= kDirect) {
+        if (f32) return add ? direct<true, true>(e, ids, wide, sms, st) : direct<true, false>(e, ids, wide, sms, st);
+        return add ? direct<false, true>(e, ids, wide, sms, st) : direct<false, false>(e, ids, wide, sms, st);
+    }
     const Layout l = layout(tokens, hidden, sms);
     char* ws = static_cast<char*>(workspace);
     const auto u32 = [ws](int64_t o) { return reinterpret_cast<uint32_t*>(ws + o); };
@@ -836,20 +1028,13 @@ cudaError_t launch_embedding_bwd(void* dtable, bool f32, bool add, const void* d
             other_at = a;
         }
     }
-    EmbedBwd e{};
-    e.dtable = dtable;
-    e.dy = static_cast<const uint16_t*>(dy);
     e.keys = keys;
     e.at = at;
     e.pieces = reinterpret_cast<float*>(ws + l.pieces);
     e.crossings = u32(l.crossings);
-    e.tokens = tokens;
-    e.vocab = vocab;
-    e.hidden = static_cast<int>(hidden);
     e.chunk = l.chunk;
     e.slices = l.slices;
     e.chunks = l.chunks;
-    e.scale = scale;
     if (f32) return add ? sums<true, true>(e, sms, st) : sums<true, false>(e, sms, st);
     return add ? sums<false, true>(e, sms, st) : sums<false, false>(e, sms, st);
 }

@@ -11,7 +11,8 @@
 // the difference first and the product after, so that its error is relative
 // to d itself and a probability near 1 keeps its logarithm.
 //
-// Bound by memory: the logits are read once.  A row belongs to a CTA, or,
+// Bound by memory: the logits are read once (8192 x 131072 bf16 on a GB300
+// 303 us, 7.1 TB/s; 16 x 131072 4.5 us, with 5 alternatives 7.5 us: latency).  A row belongs to a CTA, or,
 // where there are few rows, to a cluster of 2, 4 or 8 CTAs that join their
 // sums through distributed shared memory.
 //

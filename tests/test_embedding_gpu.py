@@ -151,6 +151,23 @@ def test_gradient_at_the_borders_of_the_sorts(tokens, kind):
     check_grad(nf.embedding_bwd(dy, ids, vocab, 1.0), dy, ids, vocab, 1.0, None)
 
 
+@pytest.mark.parametrize("dtype,add", [(torch.float32, False), (torch.bfloat16, True)])
+@pytest.mark.parametrize("kind", ["uniform", "words", "one", "falling"])
+@pytest.mark.parametrize("tokens,vocab,hidden", [
+    (2, 1, 512), (8, 3, 520), (9, 40, 4104), (17, 2, 1032), (127, 8, 8), (255, 30, 16392), (256, 2000, 248),
+    (511, 60, 1000), (512, 32003, 2056), (512, 3, 504), (513, 60, 1000)])
+def test_gradient_of_few_tokens(tokens, vocab, hidden, kind, dtype, add):
+    # one launch up to 512 tokens; runs of a warp (8 rows) and of the whole CTA
+    ids = make_ids(kind, tokens, vocab, tokens + hidden)
+    g = gen(tokens)
+    dy = torch.randn(tokens, hidden, generator=g, device="cuda").bfloat16()
+    old = torch.randn(vocab, hidden, generator=g, device="cuda").to(dtype) if add else None
+    got = nf.embedding_bwd(dy, ids, vocab, 1.7, dtype=dtype, accumulate=None if old is None else old.clone())
+    check_grad(got, dy, ids, vocab, 1.7, old)
+    again = nf.embedding_bwd(dy, ids, vocab, 1.7, dtype=dtype, accumulate=None if old is None else old.clone())
+    assert torch.equal(got, again)
+
+
 @pytest.mark.parametrize("kind", ["uniform", "words", "one", "none"])
 @pytest.mark.parametrize("tokens,vocab", [(98305, 5), (131072, 70000), (131073, 1 << 21), (400001, 40000)])
 def test_gradient_of_many_tiles(tokens, vocab, kind):
