@@ -571,7 +571,7 @@ def rmsnorm_q8(x, weight, eps: float = 1e-6, fmt: str = "e4m3", group: int = 0, 
     normalized rows, which are not rounded to bf16 in between."""
     if stream is not None:
         return _on(stream, rmsnorm_q8, x, weight, eps, fmt, group, out, scale)
-    return _result(_helpers().norm_q8(x, None, weight, eps, fmt, group, out, scale), "nf_rmsnorm_q8")
+    return _result((_native or _helpers()).norm_q8(x, None, weight, eps, fmt, group, out, scale), "nf_rmsnorm_q8")
 
 
 def fused_add_rmsnorm_q8(x, residual, weight, eps: float = 1e-6, fmt: str = "e4m3",
@@ -583,7 +583,7 @@ def fused_add_rmsnorm_q8(x, residual, weight, eps: float = 1e-6, fmt: str = "e4m
         raise TypeError("residual must be a tensor")
     if stream is not None:
         return _on(stream, fused_add_rmsnorm_q8, x, residual, weight, eps, fmt, group, out, scale)
-    return _result(_helpers().norm_q8(x, residual, weight, eps, fmt, group, out, scale),
+    return _result((_native or _helpers()).norm_q8(x, residual, weight, eps, fmt, group, out, scale),
                    "nf_fused_add_rmsnorm_q8")
 
 
@@ -592,7 +592,7 @@ def embedding_fwd(ids, table, scale: float = 1.0, out=None, stream=None):
     ids int32 or int64; an id outside [0, vocab) gives a row of zeros."""
     if stream is not None:
         return _on(stream, embedding_fwd, ids, table, scale, out)
-    return _result(_helpers().embedding_fwd(ids, table, scale, out), "nf_embedding_fwd")
+    return _result((_native or _helpers()).embedding_fwd(ids, table, scale, out), "nf_embedding_fwd")
 
 
 def embedding_bwd(dy, ids, vocab: int, scale: float = 1.0, dtype=None, accumulate=None, out=None,
@@ -605,7 +605,7 @@ def embedding_bwd(dy, ids, vocab: int, scale: float = 1.0, dtype=None, accumulat
     allocated here when not given."""
     if stream is not None:
         return _on(stream, embedding_bwd, dy, ids, vocab, scale, dtype, accumulate, out, workspace)
-    return _result(_helpers().embedding_bwd(dy, ids, vocab, scale, dtype, accumulate, out, workspace),
+    return _result((_native or _helpers()).embedding_bwd(dy, ids, vocab, scale, dtype, accumulate, out, workspace),
                    "nf_embedding_bwd")
 
 
@@ -621,7 +621,7 @@ def token_logprob_fwd(logits, targets, temperature: float = 1.0, top: int = 0, s
     [0, vocab) give 0."""
     if stream is not None:
         return _on(stream, token_logprob_fwd, logits, targets, temperature, top)
-    return _result(_helpers().token_logprob_fwd(logits, targets, temperature, top), "nf_token_logprob_fwd")
+    return _result((_native or _helpers()).token_logprob_fwd(logits, targets, temperature, top), "nf_token_logprob_fwd")
 
 
 def token_logprob_bwd(logits, targets, stats, entropy, d_logprob, d_entropy=None,
@@ -632,7 +632,7 @@ def token_logprob_bwd(logits, targets, stats, entropy, d_logprob, d_entropy=None
     if stream is not None:
         return _on(stream, token_logprob_bwd, logits, targets, stats, entropy, d_logprob, d_entropy,
                    temperature, out)
-    return _result(_helpers().token_logprob_bwd(logits, targets, stats, entropy, d_logprob, d_entropy,
+    return _result((_native or _helpers()).token_logprob_bwd(logits, targets, stats, entropy, d_logprob, d_entropy,
                                                 temperature, out), "nf_token_logprob_bwd")
 
 

@@ -24,7 +24,7 @@
 // one id can hold several percent of a batch.  Bound by memory: dy read
 // once, the rows with tokens (or all rows) written once.  One GB300: lookup
 // of 32768 x 8192 118 us (6.2 TB/s), gradient of 16384 x 4096 written to
-// 131072 fp32 rows 337 us (6.8 TB/s), of 65536 x 4096 added to them 247 us
+// 131072 fp32 rows 321 us (7.1 TB/s), of 65536 x 4096 added to them 247 us
 // (4.8 TB/s, latency of the rows in the sums).
 #include <cooperative_groups.h>
 
@@ -466,7 +466,13 @@ sort_scatter(const void* __restrict__ ids, bool wide, const uint32_t* __restrict
 constexpr int kSumThreads = 128;   // threads of a column slice, 8 columns each
 constexpr int kSumBatch = 4;       // rows of dy in flight per thread
 constexpr int kSumPart = 256;      // tokens whose ids and numbers are staged at once
-constexpr int kZeroRows = 16;      // rows per CTA that writes zeros
+// A CTA that writes zeros takes rows of kZeroBytes together, and never more
+// than kZeroRows (the gradient of 16384 x 4096 written to 131072 fp32 rows with
+// 128, 32 and 16 KB: 333, 320 and 318 us; of 300 x 4096: 279, 276 and 354 us;
+// 16 rows whatever their length took 49 us where 126725 rows of 192 bytes take
+// 5.5).
+constexpr int kZeroBytes = 32 * 1024;
+constexpr int kZeroRows = 1024;
 
 struct EmbedBwd {
     void* dtable;
@@ -477,6 +483,7 @@ struct EmbedBwd {
     uint32_t* crossings;  // how many chunks a crossing run begins in, then (4 further on) which
     int64_t tokens, vocab;
     int hidden, chunk, slices;
+    int zero_rows;        // per CTA that writes zeros
     int64_t chunks;
     float scale;
 };
@@ -544,12 +551,31 @@ __device__ __forceinline__ int64_t lower_bound_warp(const uint32_t* keys, int64_
     return lo;
 }
 
+// Zeros into the table's rows [r0, r1) that have no tokens, by the whole CTA:
+// touched[r - r0] says which have (only looked at where `any` does).
+template <bool F32>
+__device__ __forceinline__ void zero_rows(const EmbedBwd& a, int64_t r0, int64_t r1, const uint8_t* touched, bool any) {
+    const int per = a.hidden / kVec * (F32 ? 2 : 1), total = static_cast<int>(r1 - r0) * per;  // 16-byte vectors
+    uint4* p = static_cast<uint4*>(a.dtable) + r0 * per;
+    const int T = blockDim.x, down = T / per, along = T % per;
+    int row = threadIdx.x / per, col = threadIdx.x % per;
+    for (int i = threadIdx.x; i < total; i += T) {
+        if (!any || !touched[row]) __stcs(p + i, make_uint4(0, 0, 0, 0));
+        row += down;
+        col += along;
+        if (col >= per) {
+            col -= per;
+            ++row;
+        }
+    }
+}
+
 // CTAs [0, chunks * slices): the sums.  CTAs above: zeros for the table's
-// rows without tokens, kZeroRows each.
+// rows without tokens, zero_rows each.
 template <bool F32, bool ADD>
 __global__ void __launch_bounds__(kSumThreads)
 embedding_sums(const EmbedBwd a) {
-    __shared__ uint32_t touched[kZeroRows];
+    __shared__ uint8_t touched[kZeroRows];
     __shared__ uint32_t keys[kSumPart + kSumBatch], at[kSumPart];  // keys: one more than the part's
     __shared__ int64_t range[2];
     grid_dep_wait();
@@ -557,9 +583,9 @@ embedding_sums(const EmbedBwd a) {
     const int nv = a.hidden / kVec;
     const int64_t work = a.chunks * a.slices;
     if (!ADD && static_cast<int64_t>(blockIdx.x) >= work) {
-        const int64_t r0 = (static_cast<int64_t>(blockIdx.x) - work) * kZeroRows;
-        const int64_t r1 = r0 + kZeroRows < a.vocab ? r0 + kZeroRows : a.vocab;
-        if (threadIdx.x < kZeroRows) touched[threadIdx.x] = 0;
+        const int64_t r0 = (static_cast<int64_t>(blockIdx.x) - work) * a.zero_rows;
+        const int64_t r1 = r0 + a.zero_rows < a.vocab ? r0 + a.zero_rows : a.vocab;
+        for (int r = threadIdx.x; r < a.zero_rows; r += kSumThreads) touched[r] = 0;
         if (threadIdx.x < 64) {
             const int64_t b = lower_bound_warp(a.keys, 0, a.tokens, static_cast<uint32_t>(threadIdx.x < 32 ? r0 : r1));
             if ((threadIdx.x & 31) == 0) range[threadIdx.x >> 5] = b;
@@ -567,12 +593,7 @@ embedding_sums(const EmbedBwd a) {
         __syncthreads();
         for (int64_t i = range[0] + threadIdx.x; i < range[1]; i += kSumThreads) touched[a.keys[i] - r0] = 1;
         __syncthreads();
-        const int per = F32 ? nv * 2 : nv;  // 16-byte vectors of a row
-        for (int r = 0; r < r1 - r0; ++r) {
-            if (touched[r]) continue;
-            uint4* p = static_cast<uint4*>(a.dtable) + (r0 + r) * per;
-            for (int v = threadIdx.x; v < per; v += kSumThreads) __stcs(p + v, make_uint4(0, 0, 0, 0));
-        }
+        zero_rows<F32>(a, r0, r1, touched, range[0] < range[1]);
         return;
     }
     const int64_t c = static_cast<int64_t>(blockIdx.x) / a.slices;
@@ -743,21 +764,22 @@ embedding_direct(const EmbedBwd a, const void* __restrict__ ids, bool wide, int 
     grid_dep_wait();
     grid_dep_release();
     if (!ADD && blockIdx.x >= static_cast<unsigned>(blocks * a.slices)) {
-        const int64_t r0 = static_cast<int64_t>(blockIdx.x - blocks * a.slices) * kZeroRows;
-        const int64_t r1 = r0 + kZeroRows < a.vocab ? r0 + kZeroRows : a.vocab;
-        if (t < kZeroRows) list[t] = 0;
+        uint8_t* touched = reinterpret_cast<uint8_t*>(sums);
+        static_assert(sizeof(sums) >= kZeroRows, "touched");
+        const int64_t r0 = static_cast<int64_t>(blockIdx.x - blocks * a.slices) * a.zero_rows;
+        const int64_t r1 = r0 + a.zero_rows < a.vocab ? r0 + a.zero_rows : a.vocab;
+        for (int r = t; r < a.zero_rows; r += kDirectThreads) touched[r] = 0;
         __syncthreads();
+        bool any = false;
         for (int i = t; i < n; i += kDirectThreads) {
             const uint32_t key = key_of(ids, wide, i, a.vocab);
-            if (key >= r0 && key < r1) list[key - r0] = 1;
+            if (key >= r0 && key < r1) {
+                touched[key - r0] = 1;
+                any = true;
+            }
         }
-        __syncthreads();
-        const int per = F32 ? nv * 2 : nv;  // 16-byte vectors of a row
-        for (int r = 0; r < r1 - r0; ++r) {
-            if (list[r]) continue;
-            uint4* p = static_cast<uint4*>(a.dtable) + (r0 + r) * per;
-            for (int v = t; v < per; v += kDirectThreads) __stcs(p + v, make_uint4(0, 0, 0, 0));
-        }
+        any = __syncthreads_or(any);
+        zero_rows<F32>(a, r0, r1, touched, any);
         return;
     }
     const uint32_t none = static_cast<uint32_t>(a.vocab);
@@ -927,7 +949,7 @@ cudaError_t sort_in_cluster(const void* ids, bool wide, int n, int64_t vocab, in
 template <bool F32, bool ADD>
 cudaError_t sums(const EmbedBwd& e, int sms, cudaStream_t st) {
     const int64_t work = e.chunks * e.slices;
-    const int64_t zero = ADD ? 0 : (e.vocab + kZeroRows - 1) / kZeroRows;
+    const int64_t zero = ADD ? 0 : (e.vocab + e.zero_rows - 1) / e.zero_rows;
     if (cudaError_t err = launch_with_pdl(embedding_sums<F32, ADD>, dim3(static_cast<unsigned>(work + zero)),
                                           dim3(kSumThreads), 0, st, e))
         return err;
@@ -945,7 +967,7 @@ cudaError_t direct(EmbedBwd e, const void* ids, bool wide, int sms, cudaStream_t
     const int64_t most = kDirectCtas * static_cast<int64_t>(sms) / e.slices;
     int64_t blocks = (e.tokens + kDirectWarps - 1) / kDirectWarps;
     if (blocks > most) blocks = most > 0 ? most : 1;
-    const int64_t zero = ADD ? 0 : (e.vocab + kZeroRows - 1) / kZeroRows;
+    const int64_t zero = ADD ? 0 : (e.vocab + e.zero_rows - 1) / e.zero_rows;
     return launch_with_pdl(embedding_direct<F32, ADD>, dim3(static_cast<unsigned>(blocks * e.slices + zero)),
                            dim3(kDirectThreads), 0, st, e, ids, wide, static_cast<int>(blocks));
 }
@@ -978,6 +1000,8 @@ cudaError_t launch_embedding_bwd(void* dtable, bool f32, bool add, const void* d
     e.vocab = vocab;
     e.hidden = static_cast<int>(hidden);
     e.scale = scale;
+    const int64_t fit = kZeroBytes / (hidden * (f32 ? 4 : 2));
+    e.zero_rows = static_cast<int>(fit < 1 ? 1 : fit > kZeroRows ? kZeroRows : fit);
     if (tokens > 0 && tokens <= kDirect) {
         if (f32) return add ? direct<true, true>(e, ids, wide, sms, st) : direct<true, false>(e, ids, wide, sms, st);
         return add ? direct<false, true>(e, ids, wide, sms, st) : direct<false, false>(e, ids, wide, sms, st);

@@ -151,6 +151,17 @@ def test_gradient_at_the_borders_of_the_sorts(tokens, kind):
     check_grad(nf.embedding_bwd(dy, ids, vocab, 1.0), dy, ids, vocab, 1.0, None)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("tokens,vocab,hidden", [(40, 5000, 8), (600, 5001, 24), (40, 2049, 96), (600, 130, 4104),
+                                                 (40, 7, 32768), (600, 1025, 16), (5, 1 << 20, 8)])
+def test_zeros_of_rows_without_tokens(tokens, vocab, hidden, dtype):
+    # rows of many lengths, many or one to a CTA; every element of the table was something else before
+    ids = make_ids("words", tokens, vocab, tokens)
+    dy = torch.randn(tokens, hidden, generator=gen(tokens), device="cuda").bfloat16()
+    out = torch.full((vocab, hidden), float("nan"), dtype=dtype, device="cuda")
+    check_grad(nf.embedding_bwd(dy, ids, vocab, dtype=dtype, out=out), dy, ids, vocab, 1.0, None)
+
+
 @pytest.mark.parametrize("dtype,add", [(torch.float32, False), (torch.bfloat16, True)])
 @pytest.mark.parametrize("kind", ["uniform", "words", "one", "falling"])
 @pytest.mark.parametrize("tokens,vocab,hidden", [
