@@ -240,3 +240,36 @@ def test_calls_at_once_on_two_streams():
         torch.cuda.synchronize()
         for a, b in zip(got, want):
             assert all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(a, b))
+
+
+def test_calls_from_several_threads():
+    # the helpers let the interpreter go while they allocate and launch
+    from concurrent.futures import ThreadPoolExecutor
+    vocab, hidden, tokens, rows = 3000, 256, 900, 7
+
+    def inputs(seed):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        r = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+        ids = torch.randint(-1, vocab, (tokens,), generator=g, device="cuda")
+        return r(tokens, hidden).bfloat16(), ids, r(rows, vocab).bfloat16(), ids[:rows].contiguous(), r(hidden).bfloat16()
+
+    def calls(dy, ids, logits, targets, w):
+        return [nf.embedding_bwd(dy, ids, vocab), *nf.rmsnorm_q8(dy, w, group=128),
+                *nf.token_logprob_fwd(logits, targets, top=4)]
+
+    given = [inputs(s) for s in range(4)]
+    want = [calls(*x) for x in given]
+    torch.cuda.synchronize()
+
+    def work(x):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(50):
+                got = calls(*x)
+            torch.cuda.current_stream().synchronize()
+        return got
+
+    with ThreadPoolExecutor(4) as pool:
+        for got, ref in zip(pool.map(work, given), want):
+            for a, b in zip(got, ref):
+                assert torch.equal(a.view(torch.uint8) if a.dtype == torch.float8_e4m3fn else a,
+                                   b.view(torch.uint8) if b.dtype == torch.float8_e4m3fn else b)
