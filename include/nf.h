@@ -413,7 +413,8 @@ nf_status nf_embedding_bwd(void* dtable, nf_dtype dtable_type, int32_t accumulat
  *     entropy    = log S - sum_j exp(d_j) d_j / S
  *     stats[r]   = (m, log S), what the gradient needs
  *     top_*[r]   = the `top` most probable tokens, the most probable first and
- *                  the lower id first among equals: their log probability and id
+ *                  the lower id first among equals (0 and -0 are equal):
+ *                  their log probability and id
  * Entries of -infinity are masked: probability 0, never an alternative; where
  * fewer than `top` entries are left the rest hold (-infinity, -1).  A row with
  * every entry masked has stats (-inf, -inf), entropy 0, logprob -inf (0 where

@@ -150,9 +150,11 @@ constexpr int fwd_min_ctas(bool f32, bool top) { return f32 || top ? 4 : 5; }
 constexpr int kFwdBatch = 4;   // vectors in flight per thread
 constexpr int kTopMax = kLogprobMaxTop;
 
-// An order-preserving integer of a float, and back.
+// An order-preserving integer of a float, and back.  Zeros of both signs are
+// equal logits (and the running maximum, a comparison of values, keeps
+// whichever came first), so both stand as +0, which adding +0 makes of them.
 __device__ __forceinline__ uint32_t order_of(float f) {
-    const uint32_t b = __float_as_uint(f);
+    const uint32_t b = __float_as_uint(f + 0.f);
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 __device__ __forceinline__ float float_of(uint32_t o) {

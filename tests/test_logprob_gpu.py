@@ -169,6 +169,46 @@ def test_top_of_rows_whose_best_share_a_thread():
         check_forward(logits, targets, 1.0, 32)
 
 
+def zeros_of_both_signs(rows, vocab, kind, layout):
+    """Logits whose largest entries are zeros of both signs, everything else below -1."""
+    g = gen(vocab + len(layout))
+    l = -1 - torch.rand(rows, vocab, generator=g, device="cuda") * 5
+    sign = torch.where(torch.rand(rows, vocab, generator=g, device="cuda") < 0.5, -1.0, 1.0)
+    col = torch.arange(vocab, device="cuda")
+    if layout == "few":          # about 40 a row: the border of 32 alternatives lies among them
+        l = torch.where(torch.rand(rows, vocab, generator=g, device="cuda") < 40 / vocab, 0.0 * sign, l)
+    elif layout == "all":
+        l = 0.0 * sign
+    elif layout == "rising":     # -0 at the lower ids: a thread's first batches, the first CTAs of a cluster
+        l = torch.where(col % 3 == 0, torch.where(col < vocab // 2, -0.0, 0.0), l)
+    elif layout == "falling":
+        l = torch.where(col % 3 == 0, torch.where(col < vocab // 2, 0.0, -0.0), l)
+    elif layout == "one of +0":  # -0 wherever a thread looks, one +0 behind
+        l = torch.where(col % 2 == 0, -0.0, l)
+        l[:, vocab - 1 - vocab // 5] = 0.0
+    return l.to(TYPES[kind])
+
+
+# one batch per thread, several, a cluster per row, and small CTAs of many rows
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("layout", ["few", "all", "rising", "falling", "one of +0"])
+@pytest.mark.parametrize("rows,vocab", [(3, 2), (4, 39), (5, 1000), (16, 4097), (2, 131072), (310, 32003), (400, 32003),
+                                        (1601, 1000), (1533, 9001)])
+def test_zeros_of_both_signs_are_equal(rows, vocab, layout, kind):
+    logits = zeros_of_both_signs(rows, vocab, kind, layout)
+    targets = torch.zeros(rows, dtype=torch.int64, device="cuda")
+    values = logits.double() + 0.0  # -0 becomes +0: ties by id alone
+    best, order = torch.sort(values, dim=1, descending=True, stable=True)
+    for top in (1, 5, 32):
+        _, _, stats, top_lp, top_ids = nf.token_logprob_fwd(logits, targets, 1.0, top=top)
+        k = min(top, vocab)
+        assert torch.equal(top_ids[:, :k], order[:, :k])
+        assert torch.all(top_ids[:, k:] == -1)
+        # equal logits have equal log probabilities, whatever the zero's sign: m - m - log S
+        zero = best[:, :k] == 0
+        assert torch.equal(top_lp[:, :k][zero], (-stats[:, 1:]).expand(rows, k)[zero])
+
+
 @pytest.mark.parametrize("rows", [2, 400])
 @pytest.mark.parametrize("kind", ["bf16", "f32"])
 def test_rows_with_nan_and_infinity(kind, rows):
