@@ -1,7 +1,9 @@
 """Build libnf.so in-tree: every csrc/*.cu compiled for sm_103a in parallel,
 then linked into row_normalization_inner_gb300/libnf.so; and _tensors.so, the
 native part of the token-side operators' tensor helpers (csrc/tensors.cpp,
-against the installed PyTorch and libnf.so).
+against the installed Python, PyTorch and libnf.so).  libnf.so needs neither
+Python nor PyTorch and is linked first; without PyTorch it is all that is
+built.
 
     python -m row_normalization_inner_gb300.build [--force] [--ptxas-table]
 
@@ -13,6 +15,8 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.metadata
+import importlib.util
 import os
 import subprocess
 import sys
@@ -40,16 +44,37 @@ def _sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
-def _deps():
-    return _sources() + [TENSORS_SRC] + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) \
-        + glob.glob(os.path.join(INCLUDE, "*.h"))
+def _headers():
+    return glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(INCLUDE, "*.h"))
 
 
-def _stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(TENSORS):
+def _older(out, deps) -> bool:
+    return not os.path.exists(out) or any(os.path.getmtime(p) > os.path.getmtime(out) for p in deps)
+
+
+def _lib_stale() -> bool:
+    return _older(LIB, _sources() + _headers())
+
+
+def _abi() -> str:
+    """What the helpers are compiled against, beside their sources: an upgrade
+    of Python or PyTorch changes no file of this tree."""
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        version = ""
+    return f"{sys.implementation.cache_tag} torch {version} {_torch_dir()}"
+
+
+def _abi_file() -> str:
+    return os.path.join(BUILD, "tensors.abi")
+
+
+def _tensors_stale() -> bool:
+    if _older(TENSORS, [TENSORS_SRC] + _headers()) or not os.path.exists(_abi_file()):
         return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(TENSORS))
-    return any(os.path.getmtime(p) > t for p in _deps())
+    with open(_abi_file()) as f:
+        return f.read() != _abi()
 
 
 def _compile(src: str) -> tuple[str, str]:
@@ -61,9 +86,9 @@ def _compile(src: str) -> tuple[str, str]:
     return obj, r.stderr
 
 
-def _torch_dir() -> str:
-    import importlib.util
-    return os.path.dirname(importlib.util.find_spec("torch").origin)
+def _torch_dir() -> str | None:
+    spec = importlib.util.find_spec("torch")
+    return os.path.dirname(spec.origin) if spec and spec.origin else None
 
 
 def _compile_tensors() -> str:
@@ -88,23 +113,37 @@ def _link(cmd, out):
     os.replace(tmp, out)
 
 
+def _link_lib(results):
+    with open(os.path.join(BUILD, "ptxas.log"), "w") as f:
+        for (_, log), src in zip(results, _sources()):
+            f.write(f"==== {os.path.basename(src)}\n{log}\n")
+    _link([_nvcc()] + ARCH + ["-shared"] + [o for o, _ in results], LIB)
+
+
+def _link_tensors(obj):
+    torch_lib = os.path.join(_torch_dir(), "lib")
+    _link(["g++", "-shared", obj, "-L", PKG, "-l:libnf.so", "-Wl,-rpath,$ORIGIN", "-L", torch_lib,
+           f"-Wl,-rpath,{torch_lib}", "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"], TENSORS)
+    with open(_abi_file(), "w") as f:
+        f.write(_abi())
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and not _stale():
+    have_torch = _torch_dir() is not None
+    if not have_torch and verbose:
+        print("PyTorch is not installed: libnf.so alone is built, without the tensor helpers", file=sys.stderr)
+    lib, tensors = force or _lib_stale(), have_torch and (force or _tensors_stale())
+    if not lib and not tensors:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
-    srcs = _sources()
+    srcs = _sources() if lib else []
     with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
-        tensors = ex.submit(_compile_tensors)
+        obj = ex.submit(_compile_tensors) if tensors else None
         results = list(ex.map(_compile, srcs))
-        tensors_obj = tensors.result()
-    objs = [o for o, _ in results]
-    with open(os.path.join(BUILD, "ptxas.log"), "w") as f:
-        for (o, log), src in zip(results, srcs):
-            f.write(f"==== {os.path.basename(src)}\n{log}\n")
-    _link([_nvcc()] + ARCH + ["-shared"] + objs, LIB)
-    torch_lib = os.path.join(_torch_dir(), "lib")
-    _link(["g++", "-shared", tensors_obj, "-L", PKG, "-l:libnf.so", "-Wl,-rpath,$ORIGIN", "-L", torch_lib,
-           f"-Wl,-rpath,{torch_lib}", "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"], TENSORS)
+        if lib:
+            _link_lib(results)
+        if tensors:
+            _link_tensors(obj.result())
     if verbose:
         print(f"built {LIB}")
     return LIB
