@@ -382,16 +382,19 @@ nf_status nf_embedding_fwd(void* y, const void* ids, int32_t id_bytes, const voi
                            int64_t vocab, int64_t hidden, float scale, nf_stream stream);
 
 /* Gradient of the lookup, by sorted tokens:
- *     g[v][j] = scale * sum over { i : ids[i] = v } of dy[i][j]          (fp32, in token order)
+ *     g[v][j] = scale * sum over { i : ids[i] = v } of dy[i][j]          (fp32)
  *     dtable = g (accumulate 0: every row is written, those without tokens
  *     with zeros), or dtable += g (accumulate 1: only rows with tokens are
  *     touched).  Ids outside [0, vocab) contribute nothing.
  * dtable: [vocab, hidden], NF_F32 or NF_BF16; a bf16 element is rounded
  * once, at the end.  Sums added to fp32 elements are added in L2, where a
- * result below 2^-126 becomes 0.  All but small calls sort the tokens by id in
- * the workspace (16-byte aligned, at least nf_embedding_bwd_workspace_size(tokens,
- * hidden) bytes on the device that runs the call, contents irrelevant) and
- * equal ids are summed in a fixed order, so results are deterministic; how
+ * result below 2^-126 becomes 0.  The order of every sum is fixed: an id's
+ * tokens are cut into pieces, each piece is summed in token order, and the
+ * pieces' sums are added in a fixed grouping.  So results are deterministic;
+ * where the cuts fall depends on all ids, the sizes and the device's SM count.
+ * All but small calls sort the tokens by id in the workspace (16-byte aligned,
+ * at least nf_embedding_bwd_workspace_size(tokens, hidden) bytes on the device
+ * that runs the call, asked for in small calls too; contents irrelevant).  How
  * many ids coincide changes neither the launches nor the workspace.  Sizes as
  * for the lookup.
  * Nothing may overlap.  tokens == 0 reads nothing (dy, ids and workspace may

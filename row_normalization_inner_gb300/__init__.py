@@ -600,8 +600,8 @@ def embedding_bwd(dy, ids, vocab: int, scale: float = 1.0, dtype=None, accumulat
     """Gradient of embedding_fwd for its table: [vocab, hidden], fp32 or bf16
     (dtype, fp32 unless given), the rows without tokens zero; or, with
     accumulate (a gradient of that shape), that tensor with the sums added in
-    place.  Equal ids are summed in fp32 in token order: the result is
-    deterministic.  The workspace (nf_embedding_bwd_workspace_size bytes) is
+    place.  Equal ids are summed in fp32, in pieces in token order that are
+    joined in a fixed grouping: the result is deterministic.  The workspace (nf_embedding_bwd_workspace_size bytes) is
     allocated here when not given."""
     if stream is not None:
         return _on(stream, embedding_bwd, dy, ids, vocab, scale, dtype, accumulate, out, workspace)

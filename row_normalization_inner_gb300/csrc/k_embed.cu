@@ -6,8 +6,10 @@
 //
 // Backward: dtable[v] (+)= scale * sum over { i : ids[i] = v } of dy[i].  The
 // tokens are sorted by id, stably, so that equal ids become a run in token
-// order; every run is summed in fp32 in that order, which makes the result
-// deterministic where atomics on the table would not be.  Up to kDirect
+// order; every run is summed in fp32, its pieces in that order and the pieces'
+// sums in a fixed grouping, which makes the result deterministic where atomics
+// on the table would not be (bits depend on where the pieces end, and so on the
+// SM count).  Up to kDirect
 // tokens need no sort (embedding_direct).  The launches of the others:
 //   1. the sort: up to kSortRank tokens by counting, up to kSortCluster radix
 //      passes in the shared memory of one cluster of CTAs, above that two

@@ -242,6 +242,29 @@ def test_gradient_is_deterministic_and_in_token_order(tokens):
     assert torch.equal(got[ids], dy.float())
 
 
+@pytest.mark.parametrize("runs", [60, 500, 2500, 10000])
+def test_runs_within_a_piece_are_summed_in_token_order(runs):
+    # every id eight times: a run of one warp (480 tokens), or inside one chunk, whose lengths are powers of two
+    # from 8 on.  Magnitudes from 2^-12 to 2^12 round differently in another order.
+    each, hidden = 8, 72
+    tokens = runs * each
+    ids = torch.arange(runs, device="cuda").repeat(each)[torch.randperm(tokens, generator=gen(1), device="cuda")]
+    dy = torch.randn(tokens, hidden, generator=gen(2), device="cuda")
+    dy = (dy * torch.exp2(torch.randint(-12, 13, dy.shape, generator=gen(3), device="cuda").float())).bfloat16()
+    rows = dy[torch.sort(ids, stable=True).indices].float().view(runs, each, hidden)
+
+    def in_order(which):
+        total = torch.zeros(runs, hidden, device="cuda")
+        for k in which:
+            total = total + rows[:, k]
+        return total
+    want = in_order(range(each))
+    assert not torch.equal(in_order(reversed(range(each))), want)
+    assert torch.equal(nf.embedding_bwd(dy, ids, runs), want)
+    assert torch.equal(nf.embedding_bwd(dy, ids, runs, accumulate=torch.zeros(runs, hidden, device="cuda")), want)
+    assert torch.equal(nf.embedding_bwd(dy, ids, runs, dtype=torch.bfloat16), want.bfloat16())
+
+
 def test_gradient_far_rows():
     vocab, hidden = (1 << 19) + 3, 4104  # offsets beyond 2^31 elements
     ids = torch.tensor([vocab - 1, 5, vocab - 1, vocab], device="cuda")
