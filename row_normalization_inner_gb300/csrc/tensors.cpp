@@ -3,8 +3,8 @@
 //
 // A decode step's call takes 2 us on the GPU.  Checking its tensors,
 // allocating its outputs through the interpreter and converting its
-// arguments one by one took 13 to 23 us on the host; here it is a third of
-// that.  Python keeps the signatures and the documentation
+// arguments one by one took 9 to 19 us on the host; here it is a third to a half
+// of that.  Python keeps the signatures and the documentation
 // (row_normalization_inner_gb300/__init__.py); PyTorch provides device memory
 // and streams only, and every step of the computation runs in libnf.so.
 //
