@@ -25,7 +25,11 @@
  * row stream that the norms work on, and its 8-bit form: the norms with an
  * 8-bit output (nf_rmsnorm_q8, nf_fused_add_rmsnorm_q8), the embedding lookup
  * and its gradient (nf_embedding_*), and log probabilities of given tokens
- * with their gradient (nf_token_logprob_*).  They follow the conventions
+ * with their gradient (nf_token_logprob_*).  Between a block's norm and its
+ * attention stand the operators on heads, short rows that a projection's
+ * output is cut into: their rotation by position (nf_rope_*), their RMSNorm
+ * with that rotation (nf_qk_rmsnorm_rope_*) and the step that appends keys and
+ * values to a paged cache (nf_kv_append).  All of these follow the conventions
  * below except where they say otherwise; nf_set_path does not concern them.
  *
  * Conventions shared by every entry point
@@ -448,6 +452,160 @@ nf_status nf_token_logprob_bwd(void* dlogits, int64_t dstride, const void* logit
                                int64_t stride, const void* targets, int32_t id_bytes, const float* stats,
                                const float* entropy, const float* d_logprob, const float* d_entropy,
                                int64_t rows, int64_t vocab, float temperature, nf_stream stream);
+
+/* ---- Operators on attention heads ----------------------------------------
+ * A row is one head of one token: head_dim elements (1 to NF_HEAD_MAX_DIM,
+ * else NF_ERR_UNSUPPORTED_HIDDEN), contiguous.  A set of heads (queries, keys
+ * or values of a batch) is described by its first element and its strides, so
+ * that views of a projection's output, and orders other than [batch, tokens,
+ * heads, head_dim], need no copy.  Pointers need the alignment of an element.
+ * Rows whose pointers and strides are multiples of 16 bytes, of at most 64
+ * 16-byte vectors and, in the half layout, with whole 16-byte vectors in each
+ * rotated half run on vector kernels; others run element by element on a
+ * slower one.  Strides are not negative.  The rows of an output are apart: in
+ * the order of its strides, each dimension steps over the ones inside it.  An
+ * output overlaps nothing but where it says so; sets whose rows lie between
+ * one another's (the queries and keys of one projection) do not overlap.
+ * batch * tokens * heads, over all sets of a call, is below 2^31.  Types:
+ * NF_BF16 and NF_F32, one for a call, its weights included.                   */
+#define NF_HEAD_MAX_DIM 512
+
+typedef struct {
+    void* data;           /* batch 0, token 0, head 0, element 0; inputs are only read */
+    int64_t batch_stride; /* in elements */
+    int64_t token_stride;
+    int64_t head_stride;
+    int32_t heads;        /* 1 or more */
+} nf_heads;
+
+/* Which elements of a head are a pair i, i < dim / 2. */
+typedef enum {
+    NF_ROPE_HALF = 0,        /* i and i + dim / 2 */
+    NF_ROPE_INTERLEAVED = 1  /* 2i and 2i + 1     */
+} nf_rope_layout;
+
+/* The rotation of a call.  The first `dim` elements of a head (even, 0 to
+ * head_dim; 0: none) are pairs (a, b), which a token at position p turns by
+ * t_i = p * f_i:
+ *     a' = magnitude * (a cos t_i - b sin t_i)
+ *     b' = magnitude * (b cos t_i + a sin t_i)
+ * The elements behind are left as they are.  The frequencies f_i come as
+ * rates: the share of a turn per position, f_i / (2 pi), modulo 1 and in units
+ * of 2^-64 (nf_rope_rates makes them).  The 64-bit product rate * p is then the
+ * angle modulo a turn with no reduction of large angles: it is off by p * 2^-65
+ * turns at most, beside what the rates' own rounding is off.  Positions are
+ * any integers, negative ones too. */
+typedef struct {
+    const uint64_t* rates;  /* device, [dim / 2] */
+    int32_t dim;
+    nf_rope_layout layout;
+    float magnitude;        /* finite; 1 unless the context's scaling asks for another */
+    const void* positions;  /* device, of token t of batch b: [b * position_stride + t] */
+    int32_t position_bytes; /* 4 (int32) or 8 (int64) */
+    int64_t position_stride;/* 0: every batch has the same positions */
+} nf_rope;
+
+/* Scalings of the frequencies f_i = base^(-2i / dim) for contexts longer than
+ * those of training by `factor` (>= 1):
+ *   NF_ROPE_PLAIN   none (factor and the rest are ignored)
+ *   NF_ROPE_LINEAR  f_i / factor (position interpolation)
+ *   NF_ROPE_NTK     the base is base * factor^(dim / (dim - 2)), so that the
+ *                   slowest pair alone is slowed by the factor (dim >= 4)
+ *   NF_ROPE_PARTS   pairs that turn `high` times or more within `length`
+ *                   positions (the context of training) keep f_i, those that
+ *                   turn `low` times or less take f_i / factor, and those
+ *                   between a mixture linear in their number of turns
+ *                   ("YaRN", section 3.2; it suggests the magnitude
+ *                   0.1 ln(factor) + 1) */
+typedef enum { NF_ROPE_PLAIN = 0, NF_ROPE_LINEAR = 1, NF_ROPE_NTK = 2, NF_ROPE_PARTS = 3 } nf_rope_scaling;
+
+/* Host only: writes dim / 2 rates to host memory.  dim even, 2 to
+ * NF_HEAD_MAX_DIM; base > 1, factor >= 1, length > 0, 0 <= low < high, all
+ * finite (those that the scaling uses). */
+nf_status nf_rope_rates(uint64_t* rates, int32_t dim, double base, nf_rope_scaling scaling, double factor,
+                        double length, double low, double high);
+/* The same from given frequencies, in radians per position (finite, below
+ * 2^20 in magnitude; negative ones turn the other way). */
+nf_status nf_rope_rates_of(uint64_t* rates, const double* frequencies, int32_t count);
+
+/* Queries and keys turned by their tokens' positions (k_out and k may both be
+ * NULL).  nf_rope_bwd is the gradient for q and k, given that of the turned
+ * ones: the same pairs turned back, times the magnitude.  An output may be its
+ * own input (same pointer and strides).  Computed in fp32, rounded once. */
+nf_status nf_rope_fwd(const nf_heads* q_out, const nf_heads* q, const nf_heads* k_out, const nf_heads* k,
+                      nf_dtype type, int64_t batch, int64_t tokens, int64_t head_dim, const nf_rope* rope,
+                      nf_stream stream);
+nf_status nf_rope_bwd(const nf_heads* dq, const nf_heads* dq_out, const nf_heads* dk, const nf_heads* dk_out,
+                      nf_dtype type, int64_t batch, int64_t tokens, int64_t head_dim, const nf_rope* rope,
+                      nf_stream stream);
+
+/* RMSNorm of each query and key head, with the rotation in the same pass:
+ *     n   = x * rsqrt(mean(x^2) + eps) * weight
+ *     out = the pairs of n turned, the rest of n
+ * computed in fp32, rounded once.  The weights are [head_dim], one for all
+ * query heads and one for all key heads.  rope may be NULL (no rotation), and
+ * so may k_out, k and k_weight.  An output may be its own input. */
+nf_status nf_qk_rmsnorm_rope_fwd(const nf_heads* q_out, const nf_heads* q, const void* q_weight,
+                                 const nf_heads* k_out, const nf_heads* k, const void* k_weight, nf_dtype type,
+                                 int64_t batch, int64_t tokens, int64_t head_dim, float eps,
+                                 const nf_rope* rope, nf_stream stream);
+
+/* Its gradient.  dq_out and dk_out are the gradients of the outputs.  With g
+ * the pairs of dq_out turned back, xhat = x * rsqrt(mean(x^2) + eps):
+ *     dq       = rstd * (g * weight - xhat * mean(g * weight * xhat))
+ *     dq_weight = sum over batch, tokens and heads of g * xhat   ([head_dim] fp32)
+ * and so for the keys.  dq may be dq_out or q itself (same pointer and
+ * strides), dk likewise.  workspace: 4-byte aligned, at least
+ * nf_qk_rmsnorm_rope_bwd_workspace_size(head_dim) bytes on the device that
+ * runs the call; contents irrelevant.  The order of every sum is fixed.  With
+ * batch * tokens == 0 the weights' gradients are written with zeros. */
+size_t nf_qk_rmsnorm_rope_bwd_workspace_size(int64_t head_dim);
+nf_status nf_qk_rmsnorm_rope_bwd(const nf_heads* dq, float* dq_weight, const nf_heads* dq_out, const nf_heads* q,
+                                 const void* q_weight, const nf_heads* dk, float* dk_weight,
+                                 const nf_heads* dk_out, const nf_heads* k, const void* k_weight, nf_dtype type,
+                                 int64_t batch, int64_t tokens, int64_t head_dim, float eps, const nf_rope* rope,
+                                 void* workspace, size_t workspace_bytes, nf_stream stream);
+
+/* A paged cache of keys or values: `pages` pages of `page_size` slots, a slot
+ * with a row for each head.  In the rows' own type, or in 8 bits with a scale
+ * (fp32) for each row: q * scale stands for the row. */
+typedef enum { NF_CACHE_SAME = 0, NF_CACHE_E4M3 = 1, NF_CACHE_INT8 = 2 } nf_cache_type;
+typedef struct {
+    void* data;
+    int64_t page_stride, slot_stride, head_stride;  /* in elements */
+    float* scale;                                   /* 8-bit caches; else ignored */
+    int64_t scale_page_stride, scale_slot_stride, scale_head_stride;
+} nf_pages;
+
+/* Appends the keys and values of new tokens to a paged cache; the queries of
+ * the same tokens may be prepared in the same launch.  For each token i of
+ * `tokens`:
+ *   - its sequence s: with starts ([seqs + 1] int32, rising from 0), the one
+ *     with starts[s] <= i < starts[s + 1] (sequences without new tokens have
+ *     starts[s] == starts[s + 1]); with starts NULL, one token per sequence, s = i
+ *   - its place p = past[s] + i - starts[s], past ([seqs] int32) the tokens
+ *     that the sequence has in the cache before the call
+ *   - its page table[s * table_stride + p / page_size], its slot p % page_size
+ * k (normalized with k_weight and eps unless that is NULL, then turned by the
+ * token's angles) goes to k_cache, v, as it is, to v_cache; q (likewise, with
+ * q_weight) to q_out, which may be q itself.  The position that turns a token
+ * is rope->positions[i], or p where that is NULL.  A token of no sequence (i
+ * behind starts[seqs] or, without starts, behind seqs), or of one with past <
+ * 0, is padding: nothing of it is written.  A token whose place lies behind
+ * max_pages pages, or whose page is outside [0, pages), is not stored; its q is
+ * written all the same.  Nothing else in the caches is touched.  Where two
+ * tokens of a call share a slot (tables that share a page to be written), what
+ * that slot holds is not defined.
+ * 8-bit rows: scale = max(max|y| / Q, 2^-100), Q = 448 (E4M3) or 127 (INT8),
+ * q = y / scale rounded to nearest, ties to even; y is not rounded to the rows'
+ * type before.  A row with a NaN or an infinity has scale NaN and q 0.
+ * q_out and q may both be NULL.  table is [seqs, max_pages] int32. */
+nf_status nf_kv_append(const nf_pages* k_cache, const nf_pages* v_cache, nf_cache_type cache_type, int64_t pages,
+                       int32_t page_size, const nf_heads* k, const nf_heads* v, const void* k_weight,
+                       const nf_heads* q_out, const nf_heads* q, const void* q_weight, nf_dtype type,
+                       int64_t tokens, int64_t seqs, int64_t head_dim, const int32_t* starts,
+                       const int32_t* past, const int32_t* table, int64_t table_stride, int32_t max_pages,
+                       float eps, const nf_rope* rope, nf_stream stream);
 
 /* Outer normalization: the statistics run down the columns, over the rows
  * (batch normalization of a [rows, hidden] matrix in training mode; the

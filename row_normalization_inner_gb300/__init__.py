@@ -58,6 +58,13 @@ Q8_GROUP = 128                # columns per scale of the grouped 8-bit output
 
 NF_BF16, NF_F32 = 0, 1        # nf_dtype
 
+HEAD_MAX_DIM = 512            # NF_HEAD_MAX_DIM: elements of an attention head
+NF_ROPE_HALF, NF_ROPE_INTERLEAVED = 0, 1
+ROPE_LAYOUTS = {"half": NF_ROPE_HALF, "interleaved": NF_ROPE_INTERLEAVED}
+NF_ROPE_PLAIN, NF_ROPE_LINEAR, NF_ROPE_NTK, NF_ROPE_PARTS = 0, 1, 2, 3
+ROPE_SCALINGS = {"plain": NF_ROPE_PLAIN, "linear": NF_ROPE_LINEAR, "ntk": NF_ROPE_NTK, "parts": NF_ROPE_PARTS}
+NF_CACHE_SAME, NF_CACHE_E4M3, NF_CACHE_INT8 = 0, 1, 2
+
 # Every symbol include/nf.h declares.
 EXPORTS = (
     "nf_fused_add_rmsnorm", "nf_rmsnorm_fwd", "nf_layernorm_fwd",
@@ -69,6 +76,9 @@ EXPORTS = (
     "nf_rmsnorm_q8", "nf_fused_add_rmsnorm_q8",
     "nf_embedding_fwd", "nf_embedding_bwd_workspace_size", "nf_embedding_bwd",
     "nf_token_logprob_fwd", "nf_token_logprob_bwd",
+    "nf_rope_rates", "nf_rope_rates_of", "nf_rope_fwd", "nf_rope_bwd",
+    "nf_qk_rmsnorm_rope_fwd", "nf_qk_rmsnorm_rope_bwd_workspace_size", "nf_qk_rmsnorm_rope_bwd",
+    "nf_kv_append",
     "nf_set_path", "nf_plan_query", "nf_plan_compute", "nf_get_device_status",
     "nf_selftest_wait_timeout", "nf_selftest_grid_timeout", "nf_selftest_floor", "nf_status_string",
     "nf_version",
@@ -93,6 +103,28 @@ class Plan(ctypes.Structure):
         return d
 
 
+class Heads(ctypes.Structure):
+    """nf_heads: a set of heads by its first element and its strides (in elements)."""
+    _fields_ = [("data", ctypes.c_void_p), ("batch_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("heads", ctypes.c_int32)]
+
+
+class Rope(ctypes.Structure):
+    """nf_rope: the rotation of a call."""
+    _fields_ = [("rates", ctypes.c_void_p), ("dim", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("magnitude", ctypes.c_float), ("positions", ctypes.c_void_p),
+                ("position_bytes", ctypes.c_int32), ("position_stride", ctypes.c_int64)]
+
+
+class Pages(ctypes.Structure):
+    """nf_pages: a paged cache of keys or values."""
+    _fields_ = [("data", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
+                ("slot_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("scale", ctypes.c_void_p), ("scale_page_stride", ctypes.c_int64),
+                ("scale_slot_stride", ctypes.c_int64), ("scale_head_stride", ctypes.c_int64)]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -100,6 +132,12 @@ _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _F = ctypes.c_float
 _S = ctypes.c_int
+_D = ctypes.c_double
+_Z = ctypes.c_size_t
+_I32 = ctypes.c_int32
+_H = ctypes.POINTER(Heads)
+_R = ctypes.POINTER(Rope)
+_C = ctypes.POINTER(Pages)
 
 
 def _bind(lib):
@@ -127,6 +165,16 @@ def _bind(lib):
         "nf_embedding_bwd": (_S, [_P, _S, _S, _P, _P, _S, _I64, _I64, _I64, _F, _P, ctypes.c_size_t, _P]),
         "nf_token_logprob_fwd": (_S, [_P, _P, _P, _P, _P, _P, _S, _I64, _P, _S, _I64, _I64, _F, _S, _P]),
         "nf_token_logprob_bwd": (_S, [_P, _I64, _P, _S, _I64, _P, _S, _P, _P, _P, _P, _I64, _I64, _F, _P]),
+        "nf_rope_rates": (_S, [_P, _I32, _D, _S, _D, _D, _D, _D]),
+        "nf_rope_rates_of": (_S, [_P, _P, _I32]),
+        "nf_rope_fwd": (_S, [_H, _H, _H, _H, _S, _I64, _I64, _I64, _R, _P]),
+        "nf_rope_bwd": (_S, [_H, _H, _H, _H, _S, _I64, _I64, _I64, _R, _P]),
+        "nf_qk_rmsnorm_rope_fwd": (_S, [_H, _H, _P, _H, _H, _P, _S, _I64, _I64, _I64, _F, _R, _P]),
+        "nf_qk_rmsnorm_rope_bwd_workspace_size": (_Z, [_I64]),
+        "nf_qk_rmsnorm_rope_bwd": (_S, [_H, _P, _H, _H, _P, _H, _P, _H, _H, _P, _S, _I64, _I64, _I64, _F, _R, _P,
+                                        _Z, _P]),
+        "nf_kv_append": (_S, [_C, _C, _S, _I64, _I32, _H, _H, _P, _H, _H, _P, _S, _I64, _I64, _I64, _P, _P, _P, _I64,
+                              _I32, _F, _R, _P]),
         "nf_set_path": (_S, [_S]),
         "nf_plan_query": (_S, [_S, _I64, _I64, ctypes.POINTER(Plan)]),
         "nf_plan_compute": (_S, [_S, _I64, _I64, ctypes.c_int32, _S, ctypes.POINTER(Plan)]),
@@ -287,6 +335,47 @@ def nf_token_logprob_bwd(dlogits, dstride, logits, type, stride, targets, id_byt
                          d_logprob, d_entropy, rows, vocab, temperature, stream) -> int:
     return lib().nf_token_logprob_bwd(dlogits, dstride, logits, type, stride, targets, id_bytes, stats,
                                       entropy, d_logprob, d_entropy, rows, vocab, temperature, stream)
+
+
+def nf_rope_rates(rates, dim, base, scaling, factor, length, low, high) -> int:
+    return lib().nf_rope_rates(rates, dim, base, scaling, factor, length, low, high)
+
+
+def nf_rope_rates_of(rates, frequencies, count) -> int:
+    return lib().nf_rope_rates_of(rates, frequencies, count)
+
+
+# The entry points on heads take Heads, Rope and Pages structures (None for a null pointer).
+
+def nf_rope_fwd(q_out, q, k_out, k, type, batch, tokens, head_dim, rope, stream) -> int:
+    return lib().nf_rope_fwd(q_out, q, k_out, k, type, batch, tokens, head_dim, rope, stream)
+
+
+def nf_rope_bwd(dq, dq_out, dk, dk_out, type, batch, tokens, head_dim, rope, stream) -> int:
+    return lib().nf_rope_bwd(dq, dq_out, dk, dk_out, type, batch, tokens, head_dim, rope, stream)
+
+
+def nf_qk_rmsnorm_rope_fwd(q_out, q, q_weight, k_out, k, k_weight, type, batch, tokens, head_dim, eps, rope,
+                           stream) -> int:
+    return lib().nf_qk_rmsnorm_rope_fwd(q_out, q, q_weight, k_out, k, k_weight, type, batch, tokens, head_dim, eps,
+                                        rope, stream)
+
+
+def nf_qk_rmsnorm_rope_bwd_workspace_size(head_dim) -> int:
+    return lib().nf_qk_rmsnorm_rope_bwd_workspace_size(head_dim)
+
+
+def nf_qk_rmsnorm_rope_bwd(dq, dq_weight, dq_out, q, q_weight, dk, dk_weight, dk_out, k, k_weight, type, batch,
+                           tokens, head_dim, eps, rope, workspace, workspace_bytes, stream) -> int:
+    return lib().nf_qk_rmsnorm_rope_bwd(dq, dq_weight, dq_out, q, q_weight, dk, dk_weight, dk_out, k, k_weight, type,
+                                        batch, tokens, head_dim, eps, rope, workspace, workspace_bytes, stream)
+
+
+def nf_kv_append(k_cache, v_cache, cache_type, pages, page_size, k, v, k_weight, q_out, q, q_weight, type, tokens,
+                 seqs, head_dim, starts, past, table, table_stride, max_pages, eps, rope, stream) -> int:
+    return lib().nf_kv_append(k_cache, v_cache, cache_type, pages, page_size, k, v, k_weight, q_out, q, q_weight,
+                              type, tokens, seqs, head_dim, starts, past, table, table_stride, max_pages, eps, rope,
+                              stream)
 
 
 def nf_set_path(path) -> int:
@@ -527,7 +616,7 @@ def outer_norm_bwd(dy, x, mean, rstd, gamma, workspace=None, out=None, stream=No
     return dx, dgamma, dbeta
 
 
-# The token-side operators' helpers: the checks, the outputs' allocation and
+# The helpers of the token-side operators and of those on heads: the checks, the outputs' allocation and
 # the call are native (csrc/tensors.cpp), because a decode step's call takes
 # 2 us on the GPU and the same steps in Python took 9 to 19 us on the host.
 
@@ -637,6 +726,112 @@ def token_logprob_bwd(logits, targets, stats, entropy, d_logprob, d_entropy=None
                    temperature, out)
     return _result((_native or _helpers()).token_logprob_bwd(logits, targets, stats, entropy, d_logprob, d_entropy,
                                                 temperature, out), "nf_token_logprob_bwd")
+
+
+def rope_rates(dim: int, base: float = 10000.0, scaling: str = "plain", factor: float = 1.0,
+               length: float = 8192.0, low: float = 1.0, high: float = 32.0, frequencies=None, device="cuda"):
+    """What the operators on heads rotate by: an int64 tensor [dim / 2] on the
+    device, each pair's share of a turn per position in units of 2^-64.
+
+    The frequencies are base^(-2i / dim) radians per position, for contexts
+    longer by `factor` than those of training scaled as `scaling` says: "plain"
+    (not at all), "linear", "ntk" or "parts" (length: the context of training;
+    pairs that turn `high` times or more in it keep their frequency, those that
+    turn `low` times or less are slowed by the factor).  Or they are given:
+    `frequencies`, [dim / 2] numbers.  Made once, on the host."""
+    import torch
+    if dim < 2 or dim % 2 or dim > HEAD_MAX_DIM:
+        raise ValueError(f"dim must be even, 2 to {HEAD_MAX_DIM}, got {dim}")
+    rates = torch.empty(dim // 2, dtype=torch.int64)
+    if frequencies is not None:
+        f = torch.as_tensor(frequencies, dtype=torch.float64, device="cpu").contiguous()
+        if f.shape != (dim // 2,):
+            raise ValueError("frequencies must be of shape [dim / 2]")
+        _check(nf_rope_rates_of(rates.data_ptr(), f.data_ptr(), dim // 2), "nf_rope_rates_of")
+    else:
+        if scaling not in ROPE_SCALINGS:
+            raise ValueError(f"scaling must be one of {', '.join(ROPE_SCALINGS)}, got {scaling!r}")
+        _check(nf_rope_rates(rates.data_ptr(), dim, base, ROPE_SCALINGS[scaling], factor, length, low, high),
+               "nf_rope_rates")
+    return rates.to(device)
+
+
+def rope_fwd(q, k, positions, rates, layout: str = "half", magnitude: float = 1.0, q_out=None, k_out=None,
+             stream=None):
+    """Queries and keys turned by their tokens' positions: (q_out, k_out).
+
+    q, k: [batch, tokens, heads, head_dim] or [tokens, heads, head_dim], bf16 or
+    fp32, in any order with contiguous heads (views of one projection's output
+    need no copy); k may be None.  positions: int32 or int64, [batch, tokens] or
+    [tokens].  rates: rope_rates' (2 * len(rates) elements of a head are
+    turned, the rest left as they are).  layout: a pair is elements i and
+    i + len(rates) ("half") or 2i and 2i + 1 ("interleaved").  q_out may be q."""
+    if stream is not None:
+        return _on(stream, rope_fwd, q, k, positions, rates, layout, magnitude, q_out, k_out)
+    return _result((_native or _helpers()).rope(q, k, positions, rates, layout, magnitude, q_out, k_out, False),
+                   "nf_rope_fwd")
+
+
+def rope_bwd(dq_out, dk_out, positions, rates, layout: str = "half", magnitude: float = 1.0, dq=None, dk=None,
+             stream=None):
+    """Gradient of rope_fwd for q and k: (dq, dk), given that of its outputs.  dq may be dq_out."""
+    if stream is not None:
+        return _on(stream, rope_bwd, dq_out, dk_out, positions, rates, layout, magnitude, dq, dk)
+    return _result((_native or _helpers()).rope(dq_out, dk_out, positions, rates, layout, magnitude, dq, dk, True),
+                   "nf_rope_bwd")
+
+
+def qk_rmsnorm_rope_fwd(q, k, q_weight, k_weight, positions=None, rates=None, eps: float = 1e-6,
+                        layout: str = "half", magnitude: float = 1.0, q_out=None, k_out=None, stream=None):
+    """RMSNorm of each query and key head (weights [head_dim], one for all
+    heads of a kind), turned by the tokens' positions in the same pass (rates
+    None: not turned).  Returns (q_out, k_out).  Tensors as for rope_fwd, the
+    weights of their type; k and k_weight may be None; q_out may be q."""
+    if stream is not None:
+        return _on(stream, qk_rmsnorm_rope_fwd, q, k, q_weight, k_weight, positions, rates, eps, layout, magnitude,
+                   q_out, k_out)
+    return _result((_native or _helpers()).qk_rmsnorm_rope_fwd(q, k, q_weight, k_weight, positions, rates, eps, layout,
+                                                               magnitude, q_out, k_out), "nf_qk_rmsnorm_rope_fwd")
+
+
+def qk_rmsnorm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, positions=None, rates=None, eps: float = 1e-6,
+                        layout: str = "half", magnitude: float = 1.0, dq=None, dk=None, workspace=None,
+                        stream=None):
+    """Gradient of qk_rmsnorm_rope_fwd, given that of its outputs and its
+    inputs: (dq, dk, dq_weight, dk_weight), the weights' in fp32.  dq may be
+    dq_out or q.  The workspace (nf_qk_rmsnorm_rope_bwd_workspace_size bytes)
+    is allocated here when not given."""
+    if stream is not None:
+        return _on(stream, qk_rmsnorm_rope_bwd, dq_out, dk_out, q, k, q_weight, k_weight, positions, rates, eps, layout,
+                   magnitude, dq, dk, workspace)
+    return _result((_native or _helpers()).qk_rmsnorm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, positions,
+                                                               rates, eps, layout, magnitude, dq, dk, workspace),
+                   "nf_qk_rmsnorm_rope_bwd")
+
+
+def kv_append(k, v, k_cache, v_cache, table, past, starts=None, rates=None, positions=None, q=None, q_weight=None,
+              k_weight=None, eps: float = 1e-6, layout: str = "half", magnitude: float = 1.0, k_scale=None,
+              v_scale=None, q_out=None, stream=None):
+    """Appends new tokens' keys and values to a paged cache, in place; returns
+    the queries, prepared in the same launch, or None without q.
+
+    k, v (and q): [tokens, heads, head_dim], as for rope_fwd.  Caches: [pages,
+    page_size, heads, head_dim] in any order with contiguous heads, of k's type,
+    or float8_e4m3fn or int8 with scales k_scale, v_scale, fp32 [pages,
+    page_size, heads]: q * scale stands for a row.  table: int32 [seqs,
+    max_pages], each sequence's pages; past: int32 [seqs], its tokens in the
+    cache before the call (negative: padding, nothing is written); starts: int32
+    [seqs + 1], where its new tokens begin (None: one token per sequence).
+    Tokens behind starts[seqs] are padding; a token without a page in the cache
+    is not stored.  k (and q) are normalized where their weight is given and
+    turned where rates are, by the token's place in its sequence unless
+    positions [tokens] are given."""
+    if stream is not None:
+        return _on(stream, kv_append, k, v, k_cache, v_cache, table, past, starts, rates, positions, q, q_weight,
+                   k_weight, eps, layout, magnitude, k_scale, v_scale, q_out)
+    return _result((_native or _helpers()).kv_append(k, v, k_cache, v_cache, table, past, starts, rates, positions, q,
+                                                     q_weight, k_weight, eps, layout, magnitude, k_scale, v_scale,
+                                                     q_out), "nf_kv_append")
 
 
 def set_path(path):

@@ -1,0 +1,308 @@
+// Attention heads: rotation by position, RMSNorm of each head, and the append
+// of keys and values to a paged cache, in one pass over the heads of a token.
+//
+//   n = x * rsqrt(mean(x^2) + eps) * w       (a segment with a weight; else n = x)
+//   y = the pairs of n turned by the token's angles, the rest of n
+//   out = y rounded once, in the heads' type; or, for an 8-bit cache,
+//   scale = max(max|y| / Q, 2^-100), q = y / scale rounded to nearest
+//
+// Bound by memory: each element is read once and written once.  A warp takes a
+// token and up to `passes` times 32 / G of its heads (heads.cuh), so that the
+// token's angles -- two sines and cosines a lane at 64 pairs -- are computed
+// once for all of them and wait in shared memory; a group of G lanes holds a
+// row, and the row's sums stay in the warp.
+#include "heads.cuh"
+
+namespace nf {
+namespace {
+
+constexpr int kWarps = 4;  // per CTA
+constexpr float kScaleMin = 0x1p-100f;
+
+__device__ __forceinline__ bool finite_bits(uint32_t b) { return (b & 0x7F800000u) != 0x7F800000u; }
+
+// The scale of a row whose largest |y| has the bits `top`; NaN where that is not finite.
+__device__ __forceinline__ float row_scale(uint32_t top, bool int8) {
+    return finite_bits(top) ? fmaxf(__fdiv_rn(__uint_as_float(top), int8 ? 127.f : 448.f), kScaleMin) : __uint_as_float(0x7FC00000u);
+}
+
+// y / scale as one byte: the quotient is rounded to fp32 first, as a division in fp32 is.
+__device__ __forceinline__ uint32_t quant2(float y0, float y1, float scale, bool fine, bool int8) {
+    const float a = fine ? __fdiv_rn(y0, scale) : 0.f, b = fine ? __fdiv_rn(y1, scale) : 0.f;
+    if (int8) return (static_cast<uint32_t>(__float2int_rn(a)) & 0xFF) | ((static_cast<uint32_t>(__float2int_rn(b)) & 0xFF) << 8);
+    uint16_t v;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(v) : "f"(b), "f"(a));
+    return v;
+}
+
+template <int W>
+__device__ __forceinline__ void store_quantized(uint8_t* p, const float (&y)[W], float scale, bool fine, bool int8) {
+    uint32_t q[W / 4];
+#pragma unroll
+    for (int i = 0; i < W / 4; ++i)
+        q[i] = quant2(y[4 * i], y[4 * i + 1], scale, fine, int8) | (quant2(y[4 * i + 2], y[4 * i + 3], scale, fine, int8) << 16);
+    if constexpr (W == 8) *reinterpret_cast<uint2*>(p) = make_uint2(q[0], q[1]);
+    else *reinterpret_cast<uint32_t*>(p) = q[0];
+}
+
+// Where a token of an append stands.
+struct Place {
+    bool used;      // the token belongs to a sequence
+    bool stored;    // and has a page
+    int64_t position, page;
+    int slot;
+};
+
+// All lanes of a warp call this.  The sequence of a token is the last one that
+// starts at or before it; the starts are searched 32 ways at a time, so that
+// the step costs one load's latency for each factor of 32 of their number.
+__device__ __forceinline__ Place find_place(const HeadsArgs& a, uint32_t token, int lane) {
+    Place p{};
+    int seq = static_cast<int>(token), first = static_cast<int>(token);
+    if (a.starts) {
+        int lo = 0, n = a.seqs;  // the answer is in [lo, lo + n): starts[lo] <= token is assumed, and checked at the end
+        while (n > 1) {
+            const int step = (n + 31) / 32;
+            const int at = lo + lane * step;
+            const bool le = lane * step < n && a.starts[at] <= static_cast<int64_t>(token);
+            const uint32_t votes = __ballot_sync(0xFFFFFFFFu, le) | 1u;
+            const int k = 31 - __clz(votes);
+            lo += k * step;
+            n = min(step, n - k * step);
+        }
+        seq = lo;
+        first = a.starts[seq];
+        p.used = first >= 0 && first <= static_cast<int64_t>(token) && static_cast<int64_t>(token) < a.starts[a.seqs];
+    } else {
+        p.used = seq < a.seqs;
+    }
+    if (!p.used) return p;
+    const int past = a.past[seq];
+    p.used = past >= 0;
+    if (!p.used) return p;
+    p.position = static_cast<int64_t>(past) + (static_cast<int64_t>(token) - first);
+    const uint32_t place = static_cast<uint32_t>(p.position);  // below 2^32: both terms are below 2^31
+    const uint32_t column = place / static_cast<uint32_t>(a.page_size);
+    p.slot = static_cast<int>(place - column * static_cast<uint32_t>(a.page_size));
+    if (column < static_cast<uint32_t>(a.max_pages)) {
+        p.page = a.table[seq * a.table_stride + column];
+        p.stored = p.page >= 0 && p.page < a.pages;
+    }
+    return p;
+}
+
+// The row of head `h`: input, output and its scale.
+template <typename T>
+__device__ __forceinline__ const T* row_in(const HeadSegment& s, uint32_t batch, uint32_t at, int h) {
+    return static_cast<const T*>(s.in) + batch * s.in_batch + at * s.in_token + h * s.in_head;
+}
+
+template <typename T, bool INTER, bool APPEND>
+__global__ void __launch_bounds__(kWarps * 32) heads_rows(const __grid_constant__ HeadsArgs a, int G) {
+    constexpr int W = Elem<T>::W;
+    extern __shared__ float2 turns[];
+    grid_dep_wait();
+    grid_dep_release();
+    const int lane = threadIdx.x & 31;
+    const uint32_t unit = blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const uint32_t token = unit / a.chunks;
+    if (token >= a.total) return;
+    int chunk = static_cast<int>(unit - token * a.chunks), si = 0;
+    while (chunk >= a.seg[si].chunks) chunk -= a.seg[si++].chunks;
+    const HeadSegment& s = a.seg[si];
+    const int rows = 32 / G, j = lane & (G - 1);
+    const uint32_t batch = token / a.tokens, at = token - batch * a.tokens;
+    Place place{};
+    if constexpr (APPEND) {
+        place = find_place(a, token, lane);
+        if (!place.used || (s.cache && !place.stored)) return;
+    }
+    const int pairs = s.rotate ? a.rope.pairs : 0;
+    const LaneVectors<W, INTER> v(j, a.dim, pairs);
+    float2* table = turns + (threadIdx.x >> 5) * a.rope.pairs;
+    LaneTurns<W, INTER> t;
+    if (pairs) {
+        const int64_t position = APPEND && !a.rope.positions ? place.position : position_at(a.rope, token, a.tokens);
+        for (int p = lane; p < pairs; p += 32) table[p] = turn_of(a.rope.rates[p], position, a.rope.magnitude, a.rope.direction);
+        __syncwarp();
+        t.read(table, v);
+    }
+    const bool norm = s.weight != nullptr;
+    uint4 wa = make_uint4(0, 0, 0, 0), wb = wa;
+    if (norm) {
+        if (v.has_a) wa = ld_param(static_cast<const T*>(s.weight) + v.a);
+        if (v.has_b) wb = ld_param(static_cast<const T*>(s.weight) + v.b);
+    }
+    int head = chunk * a.passes * rows + lane / G;
+    for (int p = 0; p < a.passes; ++p, head += rows) {
+        const bool here = head < s.heads;
+        const T* in = row_in<T>(s, batch, at, head);
+        uint4 xa = make_uint4(0, 0, 0, 0), xb = xa;
+        if (here && v.has_a) xa = ld_stream(in + v.a);
+        if (here && v.has_b) xb = ld_stream(in + v.b);
+        float fa[W], fb[W];
+        Elem<T>::unpack(xa, fa);
+        Elem<T>::unpack(xb, fb);
+        if (norm) {
+            float ss = 0.f;
+#pragma unroll
+            for (int i = 0; i < W; ++i) ss += fa[i] * fa[i] + fb[i] * fb[i];
+            const float rstd = rsqrtf(sum_lanes(ss, G) / a.dim + a.eps);
+            float ga[W], gb[W];
+            Elem<T>::unpack(wa, ga);
+            Elem<T>::unpack(wb, gb);
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                fa[i] *= rstd * ga[i];
+                fb[i] *= rstd * gb[i];
+            }
+        }
+        if (pairs) t.turn(fa, fb, v);
+        if (APPEND && s.cache) {
+            const int64_t row = place.page * s.out_batch + place.slot * s.out_token + head * s.out_head;
+            if (a.format != kCacheSame) {
+                uint32_t top = 0;
+#pragma unroll
+                for (int i = 0; i < W; ++i) top = max(top, max(__float_as_uint(fabsf(fa[i])), __float_as_uint(fabsf(fb[i]))));
+                for (int off = G >> 1; off > 0; off >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, off));
+                const bool int8 = a.format == kCacheInt8, fine = finite_bits(top);
+                const float scale = row_scale(top, int8);
+                uint8_t* out = static_cast<uint8_t*>(s.out) + row;
+                if (here && v.has_a) store_quantized<W>(out + v.a, fa, scale, fine, int8);
+                if (here && v.has_b) store_quantized<W>(out + v.b, fb, scale, fine, int8);
+                if (here && j == 0) s.scale[place.page * s.scale_page + place.slot * s.scale_slot + head * s.scale_head] = scale;
+            } else {
+                T* out = static_cast<T*>(s.out) + row;
+                if (here && v.has_a) *reinterpret_cast<uint4*>(out + v.a) = norm || pairs ? Elem<T>::pack(fa) : xa;
+                if (here && v.has_b) *reinterpret_cast<uint4*>(out + v.b) = norm || pairs ? Elem<T>::pack(fb) : xb;
+            }
+        } else {
+            T* out = static_cast<T*>(s.out) + batch * s.out_batch + at * s.out_token + head * s.out_head;
+            if (here && v.has_a) st_stream(out + v.a, Elem<T>::pack(fa));
+            if (here && v.has_b) st_stream(out + v.b, Elem<T>::pack(fb));
+        }
+    }
+}
+
+// Any head size, stride and alignment: a warp holds one row in shared memory,
+// element by element, and computes its angles itself.  For rows whose vectors
+// do not fall on 16 bytes, or whose rotated halves are no whole vectors.
+template <typename T, bool APPEND>
+__global__ void __launch_bounds__(kWarps * 32) heads_elements(const __grid_constant__ HeadsArgs a) {
+    extern __shared__ float staged[];
+    grid_dep_wait();
+    grid_dep_release();
+    const int lane = threadIdx.x & 31;
+    const uint32_t unit = blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const uint32_t token = unit / a.chunks;
+    if (token >= a.total) return;
+    int head = static_cast<int>(unit - token * a.chunks), si = 0;
+    while (head >= a.seg[si].heads) head -= a.seg[si++].heads;
+    const HeadSegment& s = a.seg[si];
+    const uint32_t batch = token / a.tokens, at = token - batch * a.tokens;
+    Place place{};
+    if constexpr (APPEND) {
+        place = find_place(a, token, lane);
+        if (!place.used || (s.cache && !place.stored)) return;
+    }
+    const int dim = a.dim, pairs = s.rotate ? a.rope.pairs : 0;
+    float* row = staged + (threadIdx.x >> 5) * dim;
+    const T* in = row_in<T>(s, batch, at, head);
+    float ss = 0.f;
+    for (int i = lane; i < dim; i += 32) {
+        const float x = Elem<T>::load(in + i);
+        row[i] = x;
+        ss += x * x;
+    }
+    if (s.weight) {
+        const float rstd = rsqrtf(sum_lanes(ss, 32) / dim + a.eps);
+        for (int i = lane; i < dim; i += 32) row[i] *= rstd * Elem<T>::load(static_cast<const T*>(s.weight) + i);
+    }
+    __syncwarp();
+    if (pairs) {
+        const int64_t position = APPEND && !a.rope.positions ? place.position : position_at(a.rope, token, a.tokens);
+        for (int p = lane; p < pairs; p += 32) {
+            const float2 t = turn_of(a.rope.rates[p], position, a.rope.magnitude, a.rope.direction);
+            const int ia = a.rope.interleaved ? 2 * p : p, ib = a.rope.interleaved ? 2 * p + 1 : p + pairs;
+            const float x = row[ia], y = row[ib];
+            row[ia] = x * t.x - y * t.y;
+            row[ib] = y * t.x + x * t.y;
+        }
+        __syncwarp();
+    }
+    if (APPEND && s.cache) {
+        const int64_t first = place.page * s.out_batch + place.slot * s.out_token + head * s.out_head;
+        if (a.format != kCacheSame) {
+            uint32_t top = 0;
+            for (int i = lane; i < dim; i += 32) top = max(top, __float_as_uint(fabsf(row[i])));
+            top = __reduce_max_sync(0xFFFFFFFFu, top);
+            const bool int8 = a.format == kCacheInt8, fine = finite_bits(top);
+            const float scale = row_scale(top, int8);
+            uint8_t* out = static_cast<uint8_t*>(s.out) + first;
+            for (int i = lane; i < dim; i += 32) out[i] = static_cast<uint8_t>(quant2(row[i], 0.f, scale, fine, int8));
+            if (lane == 0) s.scale[place.page * s.scale_page + place.slot * s.scale_slot + head * s.scale_head] = scale;
+        } else {
+            T* out = static_cast<T*>(s.out) + first;
+            for (int i = lane; i < dim; i += 32) {
+                if (s.weight || pairs) Elem<T>::store(out + i, row[i]);
+                else out[i] = in[i];
+            }
+        }
+    } else {
+        T* out = static_cast<T*>(s.out) + batch * s.out_batch + at * s.out_token + head * s.out_head;
+        for (int i = lane; i < dim; i += 32) Elem<T>::store(out + i, row[i]);
+    }
+}
+
+bool fits(const void* p, int64_t s0, int64_t s1, int64_t s2, int elements, int bytes) {
+    return (reinterpret_cast<uintptr_t>(p) % bytes) == 0 && s0 % elements == 0 && s1 % elements == 0 && s2 % elements == 0;
+}
+
+// Whether every row falls on whole 16-byte vectors (8-bit rows: on W bytes).
+bool whole_vectors(const HeadsArgs& a, int W) {
+    if (a.dim % W || (a.dim / W + 1) / 2 > 32 || (!a.rope.interleaved && a.rope.pairs % W)) return false;
+    for (int i = 0; i < a.segments; ++i) {
+        const HeadSegment& s = a.seg[i];
+        if (!fits(s.in, s.in_batch, s.in_token, s.in_head, W, 16)) return false;
+        if (!fits(s.out, s.out_batch, s.out_token, s.out_head, W, s.cache && a.format != kCacheSame ? W : 16)) return false;
+        if (reinterpret_cast<uintptr_t>(s.weight) % 16) return false;
+    }
+    return true;
+}
+
+template <typename T, bool APPEND>
+cudaError_t launch(HeadsArgs a, int sms, cudaStream_t st) {
+    constexpr int W = Elem<T>::W;
+    if (!whole_vectors(a, W)) {
+        a.chunks = 0;
+        for (int i = 0; i < a.segments; ++i) a.chunks += a.seg[i].heads;
+        const int64_t units = static_cast<int64_t>(a.total) * a.chunks;
+        return launch_with_pdl(heads_elements<T, APPEND>, dim3(static_cast<unsigned>((units + kWarps - 1) / kWarps)), dim3(kWarps * 32),
+                               kWarps * a.dim * sizeof(float), st, a);
+    }
+    const int G = lanes_for((a.dim / W + 1) / 2), rows = 32 / G;
+    // As many of a token's rows to a warp as leave every SM its warps: each
+    // pass more shares the angles and the weight among more rows.
+    for (a.passes = 8;; a.passes /= 2) {
+        a.chunks = 0;
+        for (int i = 0; i < a.segments; ++i) {
+            a.seg[i].chunks = (a.seg[i].heads + rows * a.passes - 1) / (rows * a.passes);
+            a.chunks += a.seg[i].chunks;
+        }
+        if (a.passes == 1 || static_cast<int64_t>(a.total) * a.chunks >= 64 * sms) break;
+    }
+    const int64_t units = static_cast<int64_t>(a.total) * a.chunks;
+    const dim3 grid(static_cast<unsigned>((units + kWarps - 1) / kWarps));
+    const size_t smem = kWarps * a.rope.pairs * sizeof(float2);
+    return a.rope.interleaved ? launch_with_pdl(heads_rows<T, true, APPEND>, grid, dim3(kWarps * 32), smem, st, a, G)
+                              : launch_with_pdl(heads_rows<T, false, APPEND>, grid, dim3(kWarps * 32), smem, st, a, G);
+}
+
+}  // namespace
+
+cudaError_t launch_heads(const HeadsArgs& a, bool f32, bool append, int sms, cudaStream_t st) {
+    if (f32) return append ? launch<float, true>(a, sms, st) : launch<float, false>(a, sms, st);
+    return append ? launch<uint16_t, true>(a, sms, st) : launch<uint16_t, false>(a, sms, st);
+}
+
+}  // namespace nf

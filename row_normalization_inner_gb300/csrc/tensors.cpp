@@ -1,5 +1,5 @@
-// Tensor helpers of the token-side operators: checks, output allocation and
-// the call, in one native step.
+// Tensor helpers of the token-side operators and of those on attention heads:
+// checks, output allocation and the call, in one native step.
 //
 // A decode step's call takes 2 us on the GPU.  Checking its tensors,
 // allocating its outputs through the interpreter and converting its
@@ -368,10 +368,289 @@ PyObject* token_logprob_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+// ---- attention heads
+
+void need_head_type(const Tensor& t, const char* name) {
+    TORCH_CHECK_TYPE(t.scalar_type() == at::kBFloat16 || t.scalar_type() == at::kFloat, name,
+                     " must be torch.bfloat16 or torch.float32, got ", t.scalar_type());
+}
+
+// A [batch, tokens, heads, head_dim] or [tokens, heads, head_dim] tensor in any order.
+struct Heads {
+    Tensor t;
+    nf_heads h{};
+    int64_t batch = 1, tokens = 0, dim = 0;
+};
+Heads heads_of(const Tensor& t, const char* name, int dev) {
+    need_on(t, name, dev, false);
+    TORCH_CHECK_VALUE(t.dim() == 3 || t.dim() == 4, name, " must be [batch, tokens, heads, head_dim] or [tokens, heads, head_dim]");
+    const int d = static_cast<int>(t.dim());
+    Heads x;
+    x.t = t;
+    x.batch = d == 4 ? t.size(0) : 1;
+    x.tokens = t.size(d - 3);
+    x.dim = t.size(d - 1);
+    TORCH_CHECK_VALUE(x.dim <= 1 || t.stride(d - 1) == 1, name, "'s heads must be contiguous");
+    TORCH_CHECK_VALUE(t.size(d - 2) <= 0x7FFFFFFF, name, " has too many heads");
+    x.h.data = t.numel() ? const_cast<void*>(t.const_data_ptr()) : nullptr;
+    x.h.batch_stride = d == 4 ? t.stride(0) : 0;
+    x.h.token_stride = t.stride(d - 3);
+    x.h.head_stride = t.stride(d - 2);
+    x.h.heads = static_cast<int32_t>(t.size(d - 2));
+    return x;
+}
+// Another tensor of x's batch, tokens and head size, and of its heads too (`alike`).
+Heads heads_like(PyObject* o, const char* name, const Heads& x, const char* x_name, bool alike) {
+    const Tensor& t = tensor(o, name);
+    need_type(t, name, x.t.scalar_type());
+    Heads y = heads_of(t, name, x.t.get_device());
+    TORCH_CHECK_VALUE(t.dim() == x.t.dim() && y.batch == x.batch && y.tokens == x.tokens && y.dim == x.dim && (!alike || y.h.heads == x.h.heads),
+                      name, " of shape ", t.sizes(), " does not go with ", x_name, " of shape ", x.t.sizes());
+    return y;
+}
+Heads empty_heads(const Heads& x) { return heads_of(empty(x.t.sizes(), x.t.scalar_type(), x.t.get_device()), "out", x.t.get_device()); }
+
+const void* head_weight(PyObject* o, const char* name, const Heads& x) {
+    const Tensor& w = tensor(o, name);
+    need_type(w, name, x.t.scalar_type());
+    need_on(w, name, x.t.get_device());
+    TORCH_CHECK_VALUE(w.dim() == 1 && w.size(0) == x.dim, name, " must be of shape [head_dim]");
+    return w.const_data_ptr();
+}
+
+// The rotation of a call, from (positions or None, rates or None, layout, magnitude).
+// The tensors it points to are the caller's.
+nf_rope rope_of(PyObject* positions, PyObject* rates, PyObject* layout, PyObject* magnitude, const Heads& x, bool places) {
+    nf_rope r{};
+    const bool half = PyUnicode_Check(layout) && PyUnicode_CompareWithASCIIString(layout, "half") == 0;
+    const bool inter = PyUnicode_Check(layout) && PyUnicode_CompareWithASCIIString(layout, "interleaved") == 0;
+    TORCH_CHECK_VALUE(half || inter, "layout must be 'half' or 'interleaved'");
+    r.layout = half ? NF_ROPE_HALF : NF_ROPE_INTERLEAVED;
+    r.magnitude = static_cast<float>(number(magnitude));
+    if (!given(rates)) {
+        TORCH_CHECK_VALUE(!given(positions), "positions are given without rates");
+        return r;
+    }
+    const int dev = x.t.get_device();
+    const Tensor& f = tensor(rates, "rates");
+    need_type(f, "rates", at::kLong);
+    need_on(f, "rates", dev);
+    TORCH_CHECK_VALUE(f.dim() == 1 && 2 * f.size(0) <= x.dim, "rates must be of shape [pairs], head_dim / 2 of them at most");
+    r.rates = static_cast<const uint64_t*>(f.const_data_ptr());
+    r.dim = static_cast<int32_t>(2 * f.size(0));
+    TORCH_CHECK_VALUE(given(positions) || places || r.dim == 0, "positions must be given");
+    if (!given(positions)) return r;
+    const Tensor& p = tensor(positions, "positions");
+    r.position_bytes = id_bytes(p, "positions");
+    need_on(p, "positions", dev, false);
+    const bool batched = p.dim() == 2 && x.t.dim() == 4;
+    TORCH_CHECK_VALUE((batched && p.size(0) == x.batch) || p.dim() == 1, "positions must be of shape [batch, tokens] or [tokens]");
+    TORCH_CHECK_VALUE(p.size(-1) == x.tokens && (x.tokens <= 1 || p.stride(-1) == 1),
+                      "positions must be of shape [batch, tokens] or [tokens], contiguous within a batch");
+    r.positions = p.const_data_ptr();
+    r.position_stride = batched && x.batch > 1 ? p.stride(0) : 0;
+    return r;
+}
+
+PyObject* none() {
+    Py_INCREF(Py_None);
+    return Py_None;
+}
+
+// (q, k or None, positions, rates, layout, magnitude, q_out or None, k_out or None, back) -> (q_out, k_out)
+PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    count(n, 9);
+    const Tensor& qt = tensor(a[0], "q");
+    need_head_type(qt, "q");
+    const Heads q = heads_of(qt, "q", device_of(qt, "q"));
+    const bool two = given(a[1]);
+    Heads k, qo, ko;
+    if (two) k = heads_like(a[1], "k", q, "q", false);
+    TORCH_CHECK_VALUE(two || !given(a[7]), "k_out is given without k");
+    TORCH_CHECK_TYPE(given(a[3]), "rates must be a tensor");
+    const nf_rope r = rope_of(a[2], a[3], a[4], a[5], q, false);
+    if (given(a[6])) qo = heads_like(a[6], "q_out", q, "q", true);
+    if (given(a[7])) ko = heads_like(a[7], "k_out", k, "k", true);
+    const bool back = PyObject_IsTrue(a[8]);
+    nf_status st;
+    {
+        const WithoutInterpreter w;
+        if (!qo.t.defined()) qo = empty_heads(q);
+        if (two && !ko.t.defined()) ko = empty_heads(k);
+        st = (back ? nf_rope_bwd : nf_rope_fwd)(&qo.h, &q.h, two ? &ko.h : nullptr, two ? &k.h : nullptr, type_of(q.t), q.batch, q.tokens,
+                                                q.dim, &r, stream_of(q.t.get_device()));
+    }
+    if (st != NF_OK) return status(st);
+    return pack({object(a[6], qo.t), two ? object(a[7], ko.t) : none()});
+    END_HANDLE_TH_ERRORS
+}
+
+// (q, k or None, q_weight, k_weight or None, positions or None, rates or None, eps, layout, magnitude, q_out or None,
+//  k_out or None) -> (q_out, k_out)
+PyObject* qk_rmsnorm_rope_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    count(n, 11);
+    const Tensor& qt = tensor(a[0], "q");
+    need_head_type(qt, "q");
+    const Heads q = heads_of(qt, "q", device_of(qt, "q"));
+    const bool two = given(a[1]);
+    Heads k, qo, ko;
+    if (two) k = heads_like(a[1], "k", q, "q", false);
+    TORCH_CHECK_VALUE(two || (!given(a[3]) && !given(a[10])), "k_weight or k_out is given without k");
+    const void* qw = head_weight(a[2], "q_weight", q);
+    const void* kw = two ? head_weight(a[3], "k_weight", k) : nullptr;
+    const nf_rope r = rope_of(a[4], a[5], a[7], a[8], q, false);
+    if (given(a[9])) qo = heads_like(a[9], "q_out", q, "q", true);
+    if (given(a[10])) ko = heads_like(a[10], "k_out", k, "k", true);
+    const float eps = static_cast<float>(number(a[6]));
+    nf_status st;
+    {
+        const WithoutInterpreter w;
+        if (!qo.t.defined()) qo = empty_heads(q);
+        if (two && !ko.t.defined()) ko = empty_heads(k);
+        st = nf_qk_rmsnorm_rope_fwd(&qo.h, &q.h, qw, two ? &ko.h : nullptr, two ? &k.h : nullptr, kw, type_of(q.t), q.batch, q.tokens, q.dim,
+                                    eps, &r, stream_of(q.t.get_device()));
+    }
+    if (st != NF_OK) return status(st);
+    return pack({object(a[9], qo.t), two ? object(a[10], ko.t) : none()});
+    END_HANDLE_TH_ERRORS
+}
+
+// (dq_out, dk_out or None, q, k or None, q_weight, k_weight or None, positions or None, rates or None, eps, layout,
+//  magnitude, dq or None, dk or None, workspace or None) -> (dq, dk, dq_weight, dk_weight)
+PyObject* qk_rmsnorm_rope_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    count(n, 14);
+    const Tensor& qt = tensor(a[2], "q");
+    need_head_type(qt, "q");
+    const int dev = device_of(qt, "q");
+    const Heads q = heads_of(qt, "q", dev), dqo = heads_like(a[0], "dq_out", q, "q", true);
+    const bool two = given(a[3]);
+    Heads k, dko, dq, dk;
+    if (two) {
+        k = heads_like(a[3], "k", q, "q", false);
+        dko = heads_like(a[1], "dk_out", k, "k", true);
+    }
+    TORCH_CHECK_VALUE(two || (!given(a[1]) && !given(a[5]) && !given(a[12])), "dk_out, k_weight or dk is given without k");
+    const void* qw = head_weight(a[4], "q_weight", q);
+    const void* kw = two ? head_weight(a[5], "k_weight", k) : nullptr;
+    const nf_rope r = rope_of(a[6], a[7], a[9], a[10], q, false);
+    if (given(a[11])) dq = heads_like(a[11], "dq", q, "q", true);
+    if (given(a[12])) dk = heads_like(a[12], "dk", k, "k", true);
+    const float eps = static_cast<float>(number(a[8]));
+    Tensor ws, dqw, dkw;
+    if (given(a[13])) {
+        ws = tensor(a[13], "workspace");
+        need_on(ws, "workspace", dev);
+    }
+    nf_status st;
+    {
+        const WithoutInterpreter w;
+        if (!dq.t.defined()) dq = empty_heads(q);
+        if (two && !dk.t.defined()) dk = empty_heads(k);
+        dqw = empty({q.dim}, at::kFloat, dev);
+        if (two) dkw = empty({q.dim}, at::kFloat, dev);
+        // freed right after the launches, as in embedding_bwd
+        if (!ws.defined()) {
+            const int64_t need = static_cast<int64_t>(nf_qk_rmsnorm_rope_bwd_workspace_size(q.dim));
+            ws = empty({need > 16 ? need : 16}, at::kByte, dev);
+        }
+        st = nf_qk_rmsnorm_rope_bwd(&dq.h, static_cast<float*>(dqw.data_ptr()), &dqo.h, &q.h, qw, two ? &dk.h : nullptr,
+                                    two ? static_cast<float*>(dkw.data_ptr()) : nullptr, two ? &dko.h : nullptr, two ? &k.h : nullptr, kw,
+                                    type_of(q.t), q.batch, q.tokens, q.dim, eps, &r, ws.data_ptr(), ws.nbytes(), stream_of(dev));
+    }
+    if (st != NF_OK) return status(st);
+    return pack({object(a[11], dq.t), two ? object(a[12], dk.t) : none(), THPVariable_Wrap(dqw), two ? THPVariable_Wrap(dkw) : none()});
+    END_HANDLE_TH_ERRORS
+}
+
+const int32_t* int32s(PyObject* o, const char* name, int dev, int64_t size) {
+    const Tensor& t = tensor(o, name);
+    need_type(t, name, at::kInt);
+    need_on(t, name, dev);
+    TORCH_CHECK_VALUE(t.dim() == 1 && t.size(0) == size, name, " must be of shape [", size, "]");
+    return static_cast<const int32_t*>(t.const_data_ptr());
+}
+
+// A cache [pages, page_size, heads, head_dim] in any order, and its scales.
+nf_pages pages_of(PyObject* o, const char* name, PyObject* scale, const char* scale_name, bool scaled, int dev) {
+    const Tensor& t = tensor(o, name);
+    need_on(t, name, dev, false);
+    TORCH_CHECK_VALUE(t.dim() == 4 && (t.size(3) <= 1 || t.stride(3) == 1), name,
+                      " must be [pages, page_size, heads, head_dim] with contiguous heads");
+    nf_pages c{};
+    c.data = t.numel() ? t.data_ptr() : nullptr;
+    c.page_stride = t.stride(0), c.slot_stride = t.stride(1), c.head_stride = t.stride(2);
+    TORCH_CHECK_VALUE(scaled == given(scale), scale_name, scaled ? " must be given for an 8-bit cache" : " is for an 8-bit cache only");
+    if (!scaled) return c;
+    const Tensor& s = tensor(scale, scale_name);
+    need_type(s, scale_name, at::kFloat);
+    need_on(s, scale_name, dev, false);
+    TORCH_CHECK_VALUE(s.sizes() == t.sizes().slice(0, 3), scale_name, " must be [pages, page_size, heads]");
+    c.scale = s.numel() ? static_cast<float*>(s.data_ptr()) : nullptr;
+    c.scale_page_stride = s.stride(0), c.scale_slot_stride = s.stride(1), c.scale_head_stride = s.stride(2);
+    return c;
+}
+
+// (k, v, k_cache, v_cache, table, past, starts or None, rates or None, positions or None, q or None, q_weight or None,
+//  k_weight or None, eps, layout, magnitude, k_scale or None, v_scale or None, q_out or None) -> q_out or None
+PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    count(n, 18);
+    const Tensor& kt = tensor(a[0], "k");
+    need_head_type(kt, "k");
+    const int dev = device_of(kt, "k");
+    TORCH_CHECK_VALUE(kt.dim() == 3, "k must be [tokens, heads, head_dim]");
+    const Heads k = heads_of(kt, "k", dev), v = heads_like(a[1], "v", k, "k", true);
+    const Tensor &kc = tensor(a[2], "k_cache"), &vc = tensor(a[3], "v_cache");
+    const ScalarType cell = kc.scalar_type();
+    const bool scaled = cell == at::kFloat8_e4m3fn || cell == at::kChar;
+    TORCH_CHECK_TYPE(scaled || cell == kt.scalar_type(), "k_cache must be of k's type, torch.float8_e4m3fn or torch.int8, got ", cell);
+    need_type(vc, "v_cache", cell);
+    const nf_pages kp = pages_of(a[2], "k_cache", a[15], "k_scale", scaled, dev), vp = pages_of(a[3], "v_cache", a[16], "v_scale", scaled, dev);
+    TORCH_CHECK_VALUE(kc.sizes() == vc.sizes() && kc.size(2) == k.h.heads && kc.size(3) == k.dim, "caches of shapes ", kc.sizes(), " and ",
+                      vc.sizes(), " do not go with k of shape ", kt.sizes());
+    TORCH_CHECK_VALUE(kc.size(1) >= 1 && kc.size(1) <= 0x7FFFFFFF, "a page must have slots");
+    const Tensor& table = tensor(a[4], "table");
+    need_type(table, "table", at::kInt);
+    need_on(table, "table", dev, false);
+    TORCH_CHECK_VALUE(table.dim() == 2 && (table.size(1) <= 1 || table.stride(1) == 1) && table.size(1) <= 0x7FFFFFFF,
+                      "table must be [seqs, max_pages] with contiguous rows");
+    const int64_t seqs = table.size(0);
+    const int32_t* past = int32s(a[5], "past", dev, seqs);
+    const int32_t* starts = given(a[6]) ? int32s(a[6], "starts", dev, seqs + 1) : nullptr;
+    const nf_rope r = rope_of(a[8], a[7], a[13], a[14], k, true);
+    const bool queries = given(a[9]);
+    Heads q, qo;
+    const void *qw = nullptr, *kw = nullptr;
+    if (queries) {
+        q = heads_like(a[9], "q", k, "k", false);
+        if (given(a[10])) qw = head_weight(a[10], "q_weight", q);
+        if (given(a[17])) qo = heads_like(a[17], "q_out", q, "q", true);
+    }
+    TORCH_CHECK_VALUE(queries || (!given(a[10]) && !given(a[17])), "q_weight or q_out is given without q");
+    if (given(a[11])) kw = head_weight(a[11], "k_weight", k);
+    const float eps = static_cast<float>(number(a[12]));
+    nf_status st;
+    {
+        const WithoutInterpreter w;
+        if (queries && !qo.t.defined()) qo = empty_heads(q);
+        st = nf_kv_append(&kp, &vp, cell == at::kChar ? NF_CACHE_INT8 : scaled ? NF_CACHE_E4M3 : NF_CACHE_SAME, kc.size(0),
+                          static_cast<int32_t>(kc.size(1)), &k.h, &v.h, kw, queries ? &qo.h : nullptr, queries ? &q.h : nullptr, qw, type_of(k.t),
+                          k.tokens, seqs, k.dim, starts, past, static_cast<const int32_t*>(table.const_data_ptr()),
+                          seqs > 1 ? table.stride(0) : table.size(1), static_cast<int32_t>(table.size(1)), eps, &r, stream_of(dev));
+    }
+    if (st != NF_OK) return status(st);
+    return queries ? object(a[17], qo.t) : none();
+    END_HANDLE_TH_ERRORS
+}
+
 #define NF_FUNCTION(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {NF_FUNCTION(norm_q8),           NF_FUNCTION(embedding_fwd),     NF_FUNCTION(embedding_bwd),
-                         NF_FUNCTION(token_logprob_fwd), NF_FUNCTION(token_logprob_bwd), {nullptr, nullptr, 0, nullptr}};
-PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensors", "Tensor helpers of the token-side operators.", -1, methods,
+                         NF_FUNCTION(token_logprob_fwd), NF_FUNCTION(token_logprob_bwd), NF_FUNCTION(rope),
+                         NF_FUNCTION(qk_rmsnorm_rope_fwd), NF_FUNCTION(qk_rmsnorm_rope_bwd), NF_FUNCTION(kv_append), {nullptr, nullptr, 0, nullptr}};
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensors", "Tensor helpers of the token-side operators and of those on attention heads.", -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
