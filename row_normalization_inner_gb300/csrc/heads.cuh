@@ -14,42 +14,49 @@
 // product position * rate IS the angle modulo a turn: exact for every position
 // up to the rate's own rounding (2^-65 turns per position), with no reduction
 // of large angles, no table of angles and no limit to a context.  Its signed
-// value over 2^63 is the angle in half turns, as sincospif takes it.
+// value over 2^63 is the angle in half turns, which sincospif takes.
 #pragma once
 
 #include "common.cuh"
 #include "heads.h"
+#include "pairs.cuh"
 #include "pdl.cuh"
 
 namespace nf {
 
+// A 16-byte vector as W elements in fp32, in pairs for the packed arithmetic.
 template <typename T> struct Elem;
 template <> struct Elem<uint16_t> {  // bf16
     static constexpr int W = 8;
-    static __device__ __forceinline__ void unpack(uint4 v, float (&f)[8]) { unpack8(v, f); }
-    static __device__ __forceinline__ uint4 pack(const float (&f)[8]) { return pack8(f); }
+    static __device__ __forceinline__ void unpack(uint4 v, float2 (&f)[4]) { unpack8x2(v, f); }
+    static __device__ __forceinline__ uint4 pack(const float2 (&f)[4]) { return pack8x2(f); }
     static __device__ __forceinline__ float load(const uint16_t* p) { return bf_lo(*p); }
     static __device__ __forceinline__ void store(uint16_t* p, float f) { *p = static_cast<uint16_t>(pack2(f, 0.f) & 0xFFFF); }
 };
 template <> struct Elem<float> {
     static constexpr int W = 4;
-    static __device__ __forceinline__ void unpack(uint4 v, float (&f)[4]) {
-        f[0] = __uint_as_float(v.x); f[1] = __uint_as_float(v.y);
-        f[2] = __uint_as_float(v.z); f[3] = __uint_as_float(v.w);
+    static __device__ __forceinline__ void unpack(uint4 v, float2 (&f)[2]) {
+        f[0] = make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
+        f[1] = make_float2(__uint_as_float(v.z), __uint_as_float(v.w));
     }
-    static __device__ __forceinline__ uint4 pack(const float (&f)[4]) {
-        return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+    static __device__ __forceinline__ uint4 pack(const float2 (&f)[2]) {
+        return make_uint4(__float_as_uint(f[0].x), __float_as_uint(f[0].y), __float_as_uint(f[1].x), __float_as_uint(f[1].y));
     }
     static __device__ __forceinline__ float load(const float* p) { return *p; }
     static __device__ __forceinline__ void store(float* p, float f) { *p = f; }
 };
 
-// (cos, sin) of a pair at a position, both times `magnitude`.
+// (cos, sin) of a pair at a position, both times `magnitude`.  sincospif takes
+// the angle's upper 24 bits, which fp32 holds exactly; the rest, below 2^-24 half
+// turns, turns its result on to first order (what is left out is below 2^-46).
 __device__ __forceinline__ float2 turn_of(uint64_t rate, int64_t position, float magnitude, float direction) {
-    const int64_t angle = static_cast<int64_t>(rate * static_cast<uint64_t>(position));
+    const uint64_t angle = rate * static_cast<uint64_t>(position);
+    const int64_t upper = static_cast<int64_t>(angle + (1ull << 39)) >> 40;
+    const int64_t rest = static_cast<int64_t>(angle - (static_cast<uint64_t>(upper) << 40));
     float s, c;
-    sincospif(__ll2float_rn(angle) * 0x1p-63f, &s, &c);
-    return make_float2(c * magnitude, s * magnitude * direction);
+    sincospif(static_cast<float>(static_cast<int32_t>(upper)) * 0x1p-23f, &s, &c);
+    const float r = __ll2float_rn(rest) * (3.14159265f * 0x1p-63f);
+    return make_float2((c - s * r) * magnitude, (s + c * r) * magnitude * direction);
 }
 
 __device__ __forceinline__ int64_t position_at(const Rotation& r, uint32_t token, uint32_t tokens) {
@@ -87,50 +94,60 @@ struct LaneVectors {
     }
 };
 
-// A lane's angles, from the warp's table of the token's.
+// The warp's table of a token's angles: `pairs` cosines, then as many sines.
+__device__ __forceinline__ void fill_turns(float* table, const Rotation& r, int pairs, int64_t position, float direction, int lane) {
+    for (int p = lane; p < pairs; p += 32) {
+        const float2 t = turn_of(r.rates[p], position, r.magnitude, direction);
+        table[p] = t.x;
+        table[pairs + p] = t.y;
+    }
+    __syncwarp();
+}
+
+// A lane's angles from that table.  Elements that are not turned are left as
+// they are, whatever stands beside them.
 template <int W, bool INTER>
 struct LaneTurns {
-    float c[W], s[W];  // interleaved: those of a, then those of b
-    __device__ __forceinline__ void read(const float2* table, const LaneVectors<W, INTER>& v) {
-#pragma unroll
-        for (int i = 0; i < W; ++i) {
-            bool on;
-            int p;
-            if constexpr (INTER) {
-                on = i < W / 2 ? i < v.turned_a : i - W / 2 < v.turned_b;
-                p = i < W / 2 ? v.a / 2 + i : v.b / 2 + i - W / 2;
-            } else {
-                on = v.turned_a > 0;
-                p = v.a + i;
-            }
-            const float2 t = on ? table[p] : make_float2(1.f, 0.f);
-            c[i] = t.x;
-            s[i] = t.y;
-        }
-    }
-    // Elements that are not turned are left as they are, whatever stands beside them.
-    __device__ __forceinline__ void turn(float (&a)[W], float (&b)[W], const LaneVectors<W, INTER>& v) const {
+    float2 c[W / 2], s[W / 2];  // of pairs 2i and 2i + 1; interleaved: those of a, then those of b
+    __device__ __forceinline__ void read(const float* table, int pairs, const LaneVectors<W, INTER>& v) {
         if constexpr (INTER) {
-#pragma unroll
-            for (int i = 0; i < W / 2; ++i) {
-                const float x = a[2 * i], y = a[2 * i + 1];
-                if (i < v.turned_a) {
-                    a[2 * i] = x * c[i] - y * s[i];
-                    a[2 * i + 1] = y * c[i] + x * s[i];
-                }
-                const float z = b[2 * i], w = b[2 * i + 1];
-                if (i < v.turned_b) {
-                    b[2 * i] = z * c[W / 2 + i] - w * s[W / 2 + i];
-                    b[2 * i + 1] = w * c[W / 2 + i] + z * s[W / 2 + i];
-                }
-            }
-        } else {
-            const bool on = v.turned_a > 0;
+            float* cf = reinterpret_cast<float*>(c);
+            float* sf = reinterpret_cast<float*>(s);
 #pragma unroll
             for (int i = 0; i < W; ++i) {
-                const float x = a[i], y = b[i];
-                a[i] = on ? x * c[i] - y * s[i] : x;
-                b[i] = on ? y * c[i] + x * s[i] : y;
+                const bool on = i < W / 2 ? i < v.turned_a : i - W / 2 < v.turned_b;
+                const int p = i < W / 2 ? v.a / 2 + i : v.b / 2 + i - W / 2;
+                cf[i] = on ? table[p] : 1.f;
+                sf[i] = on ? table[pairs + p] : 0.f;
+            }
+        } else if (v.turned_a) {  // pairs is a multiple of W here, and so is a
+#pragma unroll
+            for (int i = 0; i < W / 4; ++i) {
+                const float4 cc = *reinterpret_cast<const float4*>(table + v.a + 4 * i);
+                const float4 ss = *reinterpret_cast<const float4*>(table + pairs + v.a + 4 * i);
+                c[2 * i] = make_float2(cc.x, cc.y);
+                c[2 * i + 1] = make_float2(cc.z, cc.w);
+                s[2 * i] = make_float2(ss.x, ss.y);
+                s[2 * i + 1] = make_float2(ss.z, ss.w);
+            }
+        }
+    }
+    static __device__ __forceinline__ float2 turned(float2 v, float c, float s) { return make_float2(v.x * c - v.y * s, v.y * c + v.x * s); }
+    __device__ __forceinline__ void turn(float2 (&a)[W / 2], float2 (&b)[W / 2], const LaneVectors<W, INTER>& v) const {
+        if constexpr (INTER) {
+            const float* cf = reinterpret_cast<const float*>(c);
+            const float* sf = reinterpret_cast<const float*>(s);
+#pragma unroll
+            for (int i = 0; i < W / 2; ++i) {
+                if (i < v.turned_a) a[i] = turned(a[i], cf[i], sf[i]);
+                if (i < v.turned_b) b[i] = turned(b[i], cf[W / 2 + i], sf[W / 2 + i]);
+            }
+        } else if (v.turned_a) {
+#pragma unroll
+            for (int i = 0; i < W / 2; ++i) {
+                const float2 x = a[i], y = b[i], t = __fmul2_rn(y, s[i]);
+                a[i] = __ffma2_rn(x, c[i], make_float2(-t.x, -t.y));
+                b[i] = __ffma2_rn(y, c[i], __fmul2_rn(x, s[i]));
             }
         }
     }

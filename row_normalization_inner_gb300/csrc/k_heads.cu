@@ -26,9 +26,19 @@ __device__ __forceinline__ float row_scale(uint32_t top, bool int8) {
     return finite_bits(top) ? fmaxf(__fdiv_rn(__uint_as_float(top), int8 ? 127.f : 448.f), kScaleMin) : __uint_as_float(0x7FC00000u);
 }
 
-// y / scale as one byte: the quotient is rounded to fp32 first, as a division in fp32 is.
-__device__ __forceinline__ uint32_t quant2(float y0, float y1, float scale, bool fine, bool int8) {
-    const float a = fine ? __fdiv_rn(y0, scale) : 0.f, b = fine ? __fdiv_rn(y1, scale) : 0.f;
+// y / scale in fp32, rounded once, without a division for each element: the
+// product with 1 / scale, corrected by its own remainder (P. Markstein,
+// "Computation of elementary functions on the IBM RISC System/6000 processor",
+// 1990).  Rows of 16-bit values often have quotients that lie exactly between
+// two 8-bit values; a product alone would miss these.  An infinite or NaN
+// `inverse` never gets here: such rows are stored as zeros.
+__device__ __forceinline__ float quotient(float y, float scale, float inverse) {
+    const float q = y * inverse;
+    return fmaf(fmaf(-q, scale, y), inverse, q);
+}
+
+__device__ __forceinline__ uint32_t quant2(float y0, float y1, float scale, float inverse, bool fine, bool int8) {
+    const float a = fine ? quotient(y0, scale, inverse) : 0.f, b = fine ? quotient(y1, scale, inverse) : 0.f;
     if (int8) return (static_cast<uint32_t>(__float2int_rn(a)) & 0xFF) | ((static_cast<uint32_t>(__float2int_rn(b)) & 0xFF) << 8);
     uint16_t v;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(v) : "f"(b), "f"(a));
@@ -36,13 +46,18 @@ __device__ __forceinline__ uint32_t quant2(float y0, float y1, float scale, bool
 }
 
 template <int W>
-__device__ __forceinline__ void store_quantized(uint8_t* p, const float (&y)[W], float scale, bool fine, bool int8) {
+__device__ __forceinline__ void store_quantized(uint8_t* p, const float2 (&y)[W / 2], float scale, float inverse, bool fine, bool int8) {
     uint32_t q[W / 4];
 #pragma unroll
     for (int i = 0; i < W / 4; ++i)
-        q[i] = quant2(y[4 * i], y[4 * i + 1], scale, fine, int8) | (quant2(y[4 * i + 2], y[4 * i + 3], scale, fine, int8) << 16);
+        q[i] = quant2(y[2 * i].x, y[2 * i].y, scale, inverse, fine, int8) |
+               (quant2(y[2 * i + 1].x, y[2 * i + 1].y, scale, inverse, fine, int8) << 16);
     if constexpr (W == 8) *reinterpret_cast<uint2*>(p) = make_uint2(q[0], q[1]);
     else *reinterpret_cast<uint32_t*>(p) = q[0];
+}
+
+__device__ __forceinline__ uint32_t top_of(uint32_t top, float2 v) {
+    return max(top, max(__float_as_uint(fabsf(v.x)), __float_as_uint(fabsf(v.y))));
 }
 
 // Where a token of an append stands.
@@ -54,31 +69,37 @@ struct Place {
 };
 
 // All lanes of a warp call this.  The sequence of a token is the last one that
-// starts at or before it; the starts are searched 32 ways at a time, so that
-// the step costs one load's latency for each factor of 32 of their number.
+// starts at or before it; the starts are searched 32 ways at a time, and the
+// last 32 candidates' lengths come with them, so that the step costs one load's
+// latency for each factor of 32 of the sequences and one for the page.
 __device__ __forceinline__ Place find_place(const HeadsArgs& a, uint32_t token, int lane) {
     Place p{};
-    int seq = static_cast<int>(token), first = static_cast<int>(token);
+    int seq, first, past;
     if (a.starts) {
-        int lo = 0, n = a.seqs;  // the answer is in [lo, lo + n): starts[lo] <= token is assumed, and checked at the end
-        while (n > 1) {
+        const int behind = a.starts[a.seqs];
+        int lo = 0, n = a.seqs;  // the answer is in [lo, lo + n)
+        for (;;) {
             const int step = (n + 31) / 32;
+            const bool in = lane * step < n;
             const int at = lo + lane * step;
-            const bool le = lane * step < n && a.starts[at] <= static_cast<int64_t>(token);
-            const uint32_t votes = __ballot_sync(0xFFFFFFFFu, le) | 1u;
+            const int start = in ? a.starts[at] : 0;
+            const int held = in && step == 1 ? a.past[at] : 0;
+            const uint32_t votes = __ballot_sync(0xFFFFFFFFu, in && start <= static_cast<int64_t>(token)) | 1u;
             const int k = 31 - __clz(votes);
             lo += k * step;
             n = min(step, n - k * step);
+            first = __shfl_sync(0xFFFFFFFFu, start, k);
+            past = __shfl_sync(0xFFFFFFFFu, held, k);
+            if (step == 1) break;
         }
         seq = lo;
-        first = a.starts[seq];
-        p.used = first >= 0 && first <= static_cast<int64_t>(token) && static_cast<int64_t>(token) < a.starts[a.seqs];
+        p.used = first >= 0 && first <= static_cast<int64_t>(token) && static_cast<int64_t>(token) < behind;
     } else {
+        seq = first = static_cast<int>(token);
         p.used = seq < a.seqs;
+        past = p.used ? a.past[seq] : 0;
     }
-    if (!p.used) return p;
-    const int past = a.past[seq];
-    p.used = past >= 0;
+    p.used = p.used && past >= 0;
     if (!p.used) return p;
     p.position = static_cast<int64_t>(past) + (static_cast<int64_t>(token) - first);
     const uint32_t place = static_cast<uint32_t>(p.position);  // below 2^32: both terms are below 2^31
@@ -97,10 +118,12 @@ __device__ __forceinline__ const T* row_in(const HeadSegment& s, uint32_t batch,
     return static_cast<const T*>(s.in) + batch * s.in_batch + at * s.in_token + h * s.in_head;
 }
 
+constexpr int kPasses = 4;  // most passes of a warp: so many rows of a group are in flight
+
 template <typename T, bool INTER, bool APPEND>
 __global__ void __launch_bounds__(kWarps * 32) heads_rows(const __grid_constant__ HeadsArgs a, int G) {
     constexpr int W = Elem<T>::W;
-    extern __shared__ float2 turns[];
+    extern __shared__ float4 turns[];
     grid_dep_wait();
     grid_dep_release();
     const int lane = threadIdx.x & 31;
@@ -111,21 +134,34 @@ __global__ void __launch_bounds__(kWarps * 32) heads_rows(const __grid_constant_
     while (chunk >= a.seg[si].chunks) chunk -= a.seg[si++].chunks;
     const HeadSegment& s = a.seg[si];
     const int rows = 32 / G, j = lane & (G - 1);
-    const uint32_t batch = token / a.tokens, at = token - batch * a.tokens;
+    const uint32_t batch = APPEND ? 0 : token / a.tokens, at = token - batch * a.tokens;
+    const int pairs = s.rotate ? a.rope.pairs : 0;
+    const LaneVectors<W, INTER> v(j, a.dim, pairs);
+    const int head0 = chunk * a.passes * rows, head = head0 + lane / G;
+    const int passes = min(a.passes, (s.heads - head0 + rows - 1) / rows);
+
+    uint4 xa[kPasses], xb[kPasses];
+    const T* in = row_in<T>(s, batch, at, head);
+#pragma unroll
+    for (int p = 0; p < kPasses; ++p) {
+        xa[p] = xb[p] = make_uint4(0, 0, 0, 0);
+        if (p < passes && head + p * rows < s.heads) {
+            const T* row = in + p * rows * s.in_head;
+            if (v.has_a) xa[p] = ld_stream(row + v.a);
+            if (v.has_b) xb[p] = ld_stream(row + v.b);
+        }
+    }
     Place place{};
     if constexpr (APPEND) {
         place = find_place(a, token, lane);
         if (!place.used || (s.cache && !place.stored)) return;
     }
-    const int pairs = s.rotate ? a.rope.pairs : 0;
-    const LaneVectors<W, INTER> v(j, a.dim, pairs);
-    float2* table = turns + (threadIdx.x >> 5) * a.rope.pairs;
     LaneTurns<W, INTER> t;
     if (pairs) {
+        float* table = reinterpret_cast<float*>(turns) + (threadIdx.x >> 5) * 2 * a.rope.pairs;
         const int64_t position = APPEND && !a.rope.positions ? place.position : position_at(a.rope, token, a.tokens);
-        for (int p = lane; p < pairs; p += 32) table[p] = turn_of(a.rope.rates[p], position, a.rope.magnitude, a.rope.direction);
-        __syncwarp();
-        t.read(table, v);
+        fill_turns(table, a.rope, pairs, position, a.rope.direction, lane);
+        t.read(table, pairs, v);
     }
     const bool norm = s.weight != nullptr;
     uint4 wa = make_uint4(0, 0, 0, 0), wb = wa;
@@ -133,51 +169,53 @@ __global__ void __launch_bounds__(kWarps * 32) heads_rows(const __grid_constant_
         if (v.has_a) wa = ld_param(static_cast<const T*>(s.weight) + v.a);
         if (v.has_b) wb = ld_param(static_cast<const T*>(s.weight) + v.b);
     }
-    int head = chunk * a.passes * rows + lane / G;
-    for (int p = 0; p < a.passes; ++p, head += rows) {
-        const bool here = head < s.heads;
-        const T* in = row_in<T>(s, batch, at, head);
-        uint4 xa = make_uint4(0, 0, 0, 0), xb = xa;
-        if (here && v.has_a) xa = ld_stream(in + v.a);
-        if (here && v.has_b) xb = ld_stream(in + v.b);
-        float fa[W], fb[W];
-        Elem<T>::unpack(xa, fa);
-        Elem<T>::unpack(xb, fb);
-        if (norm) {
-            float ss = 0.f;
+    const float mean_of = 1.f / a.dim;
 #pragma unroll
-            for (int i = 0; i < W; ++i) ss += fa[i] * fa[i] + fb[i] * fb[i];
-            const float rstd = rsqrtf(sum_lanes(ss, G) / a.dim + a.eps);
-            float ga[W], gb[W];
+    for (int p = 0; p < kPasses; ++p) {
+        if (p >= passes) break;
+        const bool here = head + p * rows < s.heads;
+        float2 fa[W / 2], fb[W / 2];
+        Elem<T>::unpack(xa[p], fa);
+        Elem<T>::unpack(xb[p], fb);
+        if (norm) {
+            float2 ss = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < W / 2; ++i) {
+                ss = __ffma2_rn(fa[i], fa[i], ss);
+                ss = __ffma2_rn(fb[i], fb[i], ss);
+            }
+            const float r = rsqrtf(sum_lanes(ss.x + ss.y, G) * mean_of + a.eps);
+            const float2 rstd = make_float2(r, r);
+            float2 ga[W / 2], gb[W / 2];
             Elem<T>::unpack(wa, ga);
             Elem<T>::unpack(wb, gb);
 #pragma unroll
-            for (int i = 0; i < W; ++i) {
-                fa[i] *= rstd * ga[i];
-                fb[i] *= rstd * gb[i];
+            for (int i = 0; i < W / 2; ++i) {
+                fa[i] = __fmul2_rn(__fmul2_rn(fa[i], rstd), ga[i]);
+                fb[i] = __fmul2_rn(__fmul2_rn(fb[i], rstd), gb[i]);
             }
         }
         if (pairs) t.turn(fa, fb, v);
         if (APPEND && s.cache) {
-            const int64_t row = place.page * s.out_batch + place.slot * s.out_token + head * s.out_head;
+            const int64_t row = place.page * s.out_batch + place.slot * s.out_token + (head + p * rows) * s.out_head;
             if (a.format != kCacheSame) {
                 uint32_t top = 0;
 #pragma unroll
-                for (int i = 0; i < W; ++i) top = max(top, max(__float_as_uint(fabsf(fa[i])), __float_as_uint(fabsf(fb[i]))));
+                for (int i = 0; i < W / 2; ++i) top = top_of(top_of(top, fa[i]), fb[i]);
                 for (int off = G >> 1; off > 0; off >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, off));
                 const bool int8 = a.format == kCacheInt8, fine = finite_bits(top);
-                const float scale = row_scale(top, int8);
+                const float scale = row_scale(top, int8), inverse = __fdiv_rn(1.f, scale);
                 uint8_t* out = static_cast<uint8_t*>(s.out) + row;
-                if (here && v.has_a) store_quantized<W>(out + v.a, fa, scale, fine, int8);
-                if (here && v.has_b) store_quantized<W>(out + v.b, fb, scale, fine, int8);
-                if (here && j == 0) s.scale[place.page * s.scale_page + place.slot * s.scale_slot + head * s.scale_head] = scale;
+                if (here && v.has_a) store_quantized<W>(out + v.a, fa, scale, inverse, fine, int8);
+                if (here && v.has_b) store_quantized<W>(out + v.b, fb, scale, inverse, fine, int8);
+                if (here && j == 0) s.scale[place.page * s.scale_page + place.slot * s.scale_slot + (head + p * rows) * s.scale_head] = scale;
             } else {
                 T* out = static_cast<T*>(s.out) + row;
-                if (here && v.has_a) *reinterpret_cast<uint4*>(out + v.a) = norm || pairs ? Elem<T>::pack(fa) : xa;
-                if (here && v.has_b) *reinterpret_cast<uint4*>(out + v.b) = norm || pairs ? Elem<T>::pack(fb) : xb;
+                if (here && v.has_a) *reinterpret_cast<uint4*>(out + v.a) = norm || pairs ? Elem<T>::pack(fa) : xa[p];
+                if (here && v.has_b) *reinterpret_cast<uint4*>(out + v.b) = norm || pairs ? Elem<T>::pack(fb) : xb[p];
             }
         } else {
-            T* out = static_cast<T*>(s.out) + batch * s.out_batch + at * s.out_token + head * s.out_head;
+            T* out = static_cast<T*>(s.out) + batch * s.out_batch + at * s.out_token + (head + p * rows) * s.out_head;
             if (here && v.has_a) st_stream(out + v.a, Elem<T>::pack(fa));
             if (here && v.has_b) st_stream(out + v.b, Elem<T>::pack(fb));
         }
@@ -215,7 +253,7 @@ __global__ void __launch_bounds__(kWarps * 32) heads_elements(const __grid_const
         ss += x * x;
     }
     if (s.weight) {
-        const float rstd = rsqrtf(sum_lanes(ss, 32) / dim + a.eps);
+        const float rstd = rsqrtf(sum_lanes(ss, 32) * (1.f / dim) + a.eps);
         for (int i = lane; i < dim; i += 32) row[i] *= rstd * Elem<T>::load(static_cast<const T*>(s.weight) + i);
     }
     __syncwarp();
@@ -237,9 +275,9 @@ __global__ void __launch_bounds__(kWarps * 32) heads_elements(const __grid_const
             for (int i = lane; i < dim; i += 32) top = max(top, __float_as_uint(fabsf(row[i])));
             top = __reduce_max_sync(0xFFFFFFFFu, top);
             const bool int8 = a.format == kCacheInt8, fine = finite_bits(top);
-            const float scale = row_scale(top, int8);
+            const float scale = row_scale(top, int8), inverse = __fdiv_rn(1.f, scale);
             uint8_t* out = static_cast<uint8_t*>(s.out) + first;
-            for (int i = lane; i < dim; i += 32) out[i] = static_cast<uint8_t>(quant2(row[i], 0.f, scale, fine, int8));
+            for (int i = lane; i < dim; i += 32) out[i] = static_cast<uint8_t>(quant2(row[i], 0.f, scale, inverse, fine, int8));
             if (lane == 0) s.scale[place.page * s.scale_page + place.slot * s.scale_slot + head * s.scale_head] = scale;
         } else {
             T* out = static_cast<T*>(s.out) + first;
@@ -283,7 +321,7 @@ cudaError_t launch(HeadsArgs a, int sms, cudaStream_t st) {
     const int G = lanes_for((a.dim / W + 1) / 2), rows = 32 / G;
     // As many of a token's rows to a warp as leave every SM its warps: each
     // pass more shares the angles and the weight among more rows.
-    for (a.passes = 8;; a.passes /= 2) {
+    for (a.passes = kPasses;; a.passes /= 2) {
         a.chunks = 0;
         for (int i = 0; i < a.segments; ++i) {
             a.seg[i].chunks = (a.seg[i].heads + rows * a.passes - 1) / (rows * a.passes);

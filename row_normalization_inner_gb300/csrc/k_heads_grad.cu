@@ -9,9 +9,10 @@
 // Bound by memory: dy and x are read once, dx written once.  A fixed number of
 // CTAs walk the rows, each warp a stretch of its own in token order (so that a
 // token's angles serve all its heads that the warp meets) and each lane with
-// its columns' sums of g n in registers; the next rows are loaded while these
-// are computed.  A CTA's sums go to the workspace, and a second launch adds
-// them up: every sum has a fixed order.
+// its columns' sums of g n in registers.  The rows ahead come through a ring in
+// shared memory, each lane copying what it will read itself, so that no barrier
+// stands between a copy and its use.  A CTA's sums go to the workspace, and a
+// second launch adds them up: every sum has a fixed order.
 #include <algorithm>
 
 #include "heads.cuh"
@@ -21,6 +22,14 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kCtasPerSm = 4;
+constexpr int kStages = 4;
+
+// 16 bytes to shared memory, or zeros.
+__device__ __forceinline__ void copy16(uint4* to, const void* from, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(to)), "l"(from), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 // What a warp walks: passes [first, end) of its segment, `per_token` to a token.
 struct Stretch {
@@ -44,7 +53,7 @@ __device__ __forceinline__ void leave_partials(const float* sums, float* out, in
 template <typename T, bool INTER>
 __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) heads_grad_rows(const __grid_constant__ HeadsGradArgs a, int G) {
     constexpr int W = Elem<T>::W;
-    extern __shared__ float2 turns[];
+    extern __shared__ uint4 ring[];  // [kStages][4][threads], then the turns
     grid_dep_wait();
     grid_dep_release();
     const int lane = threadIdx.x & 31, warp_in = threadIdx.x >> 5;
@@ -55,104 +64,122 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) heads_grad_rows(const
     const Stretch r = stretch_of(static_cast<int64_t>(a.total) * per_token, cta * kWarps + warp_in, s.ctas * kWarps);
     const int pairs = a.rope.pairs;
     const LaneVectors<W, INTER> v(j, a.dim, pairs);
-    float2* table = turns + warp_in * pairs;
-    float* sums = reinterpret_cast<float*>(turns + kWarps * pairs);
+    float* table = reinterpret_cast<float*>(ring + kStages * 4 * kWarps * 32) + warp_in * 2 * pairs;
 
     uint4 wa = make_uint4(0, 0, 0, 0), wb = wa;
     if (v.has_a) wa = ld_param(static_cast<const T*>(s.weight) + v.a);
     if (v.has_b) wb = ld_param(static_cast<const T*>(s.weight) + v.b);
-    float da[W], db[W];
+    float2 da[W / 2], db[W / 2];
 #pragma unroll
-    for (int i = 0; i < W; ++i) da[i] = db[i] = 0.f;
-
-    struct Loaded {
-        uint4 ya, yb, xa, xb;
-    };
-    const auto load = [&](uint32_t token, int head) {
-        Loaded l{make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-        if (head < s.heads) {
-            const uint32_t batch = token / a.tokens, at = token - batch * a.tokens;
-            const T* y = static_cast<const T*>(s.dy) + batch * s.dy_batch + at * s.dy_token + head * s.dy_head;
-            const T* x = static_cast<const T*>(s.x) + batch * s.x_batch + at * s.x_token + head * s.x_head;
-            if (v.has_a) l.ya = ld_stream(y + v.a), l.xa = ld_stream(x + v.a);
-            if (v.has_b) l.yb = ld_stream(y + v.b), l.xb = ld_stream(x + v.b);
-        }
-        return l;
-    };
+    for (int i = 0; i < W / 2; ++i) da[i] = db[i] = make_float2(0.f, 0.f);
 
     if (r.first < r.end) {
+        const float mean_of = 1.f / a.dim;
         uint32_t token = static_cast<uint32_t>(r.first / per_token);
-        int at_pass = static_cast<int>(r.first - static_cast<int64_t>(token) * per_token);
+        int pass = static_cast<int>(r.first - static_cast<int64_t>(token) * per_token);
+        // the pass that is copied next
+        uint32_t next_token = token;
+        int next_pass = pass;
+        int64_t left = r.end - r.first;
+        const auto copy = [&](int stage) {
+            if (left > 0) {
+                const uint32_t batch = next_token / a.tokens, at = next_token - batch * a.tokens;
+                const int head = next_pass * rows + lane / G;
+                const bool here = head < s.heads;
+                const T* y = static_cast<const T*>(s.dy) + batch * s.dy_batch + at * s.dy_token + (here ? head * s.dy_head : 0);
+                const T* x = static_cast<const T*>(s.x) + batch * s.x_batch + at * s.x_token + (here ? head * s.x_head : 0);
+                uint4* to = ring + stage * 4 * kWarps * 32 + threadIdx.x;
+                const bool ha = here && v.has_a, hb = here && v.has_b;
+                copy16(to, y + (ha ? v.a : 0), ha);
+                copy16(to + kWarps * 32, y + (hb ? v.b : 0), hb);
+                copy16(to + 2 * kWarps * 32, x + (ha ? v.a : 0), ha);
+                copy16(to + 3 * kWarps * 32, x + (hb ? v.b : 0), hb);
+                if (++next_pass == per_token) next_pass = 0, ++next_token;
+                --left;
+            }
+            copies_commit();  // a group for every stage, empty ones behind the last pass
+        };
+#pragma unroll
+        for (int i = 0; i < kStages - 1; ++i) copy(i);
         int64_t position = pairs ? position_at(a.rope, token, a.tokens) : 0;
-        Loaded now = load(token, at_pass * rows + lane / G);
         bool fresh = true;
         LaneTurns<W, INTER> t;
+        int stage = 0;
         for (int64_t p = r.first; p < r.end; ++p) {
             if (fresh && pairs) {
                 __syncwarp();
-                for (int i = lane; i < pairs; i += 32) table[i] = turn_of(a.rope.rates[i], position, a.rope.magnitude, -1.f);
-                __syncwarp();
-                t.read(table, v);
+                fill_turns(table, a.rope, pairs, position, -1.f, lane);
+                t.read(table, pairs, v);
             }
-            const uint32_t this_token = token;
-            const int head = at_pass * rows + lane / G;
-            fresh = ++at_pass == per_token;
-            if (fresh) at_pass = 0, ++token;
-            Loaded next{};
-            if (p + 1 < r.end) {
-                next = load(token, at_pass * rows + lane / G);
-                if (fresh && pairs) position = position_at(a.rope, token, a.tokens);
+            const uint32_t batch = token / a.tokens, at = token - batch * a.tokens;
+            const int head = pass * rows + lane / G;
+            fresh = ++pass == per_token;
+            if (fresh) {
+                pass = 0, ++token;
+                if (pairs && p + 1 < r.end) position = position_at(a.rope, token, a.tokens);
             }
-            float ga[W], gb[W], xa[W], xb[W], fa[W], fb[W];
-            Elem<T>::unpack(now.ya, ga);
-            Elem<T>::unpack(now.yb, gb);
-            Elem<T>::unpack(now.xa, xa);
-            Elem<T>::unpack(now.xb, xb);
+            copies_wait<kStages - 2>();
+            const uint4* from = ring + stage * 4 * kWarps * 32 + threadIdx.x;
+            float2 ga[W / 2], gb[W / 2], xa[W / 2], xb[W / 2], fa[W / 2], fb[W / 2];
+            Elem<T>::unpack(from[0], ga);
+            Elem<T>::unpack(from[kWarps * 32], gb);
+            Elem<T>::unpack(from[2 * kWarps * 32], xa);
+            Elem<T>::unpack(from[3 * kWarps * 32], xb);
+            // into the stage before, whose rows are done with
+            copy(stage ? stage - 1 : kStages - 1);
+            stage = stage == kStages - 1 ? 0 : stage + 1;
             if (pairs) t.turn(ga, gb, v);
             Elem<T>::unpack(wa, fa);
             Elem<T>::unpack(wb, fb);
-            float ss = 0.f, dot = 0.f;
+            float2 ss2 = make_float2(0.f, 0.f), dot2 = ss2;
 #pragma unroll
-            for (int i = 0; i < W; ++i) {
-                ss += xa[i] * xa[i] + xb[i] * xb[i];
-                fa[i] *= ga[i];
-                fb[i] *= gb[i];
-                dot += fa[i] * xa[i] + fb[i] * xb[i];
+            for (int i = 0; i < W / 2; ++i) {
+                ss2 = __ffma2_rn(xa[i], xa[i], ss2);
+                ss2 = __ffma2_rn(xb[i], xb[i], ss2);
+                fa[i] = __fmul2_rn(fa[i], ga[i]);
+                fb[i] = __fmul2_rn(fb[i], gb[i]);
+                dot2 = __ffma2_rn(fa[i], xa[i], dot2);
+                dot2 = __ffma2_rn(fb[i], xb[i], dot2);
             }
+            float ss = ss2.x + ss2.y, dot = dot2.x + dot2.y;
             for (int off = G >> 1; off > 0; off >>= 1) {
                 ss += __shfl_xor_sync(0xFFFFFFFFu, ss, off);
                 dot += __shfl_xor_sync(0xFFFFFFFFu, dot, off);
             }
-            const float rstd = rsqrtf(ss / a.dim + a.eps), mean = dot * rstd / a.dim;
+            const float rs = rsqrtf(ss * mean_of + a.eps), m = -dot * rs * mean_of;
+            const float2 rstd = make_float2(rs, rs), mean = make_float2(m, m);
 #pragma unroll
-            for (int i = 0; i < W; ++i) {
-                const float na = xa[i] * rstd, nb = xb[i] * rstd;
-                da[i] += ga[i] * na;
-                db[i] += gb[i] * nb;
-                fa[i] = rstd * (fa[i] - na * mean);
-                fb[i] = rstd * (fb[i] - nb * mean);
+            for (int i = 0; i < W / 2; ++i) {
+                const float2 na = __fmul2_rn(xa[i], rstd), nb = __fmul2_rn(xb[i], rstd);
+                da[i] = __ffma2_rn(ga[i], na, da[i]);
+                db[i] = __ffma2_rn(gb[i], nb, db[i]);
+                fa[i] = __fmul2_rn(rstd, __ffma2_rn(na, mean, fa[i]));
+                fb[i] = __fmul2_rn(rstd, __ffma2_rn(nb, mean, fb[i]));
             }
             if (head < s.heads) {
-                const uint32_t batch = this_token / a.tokens, at = this_token - batch * a.tokens;
                 T* dx = static_cast<T*>(s.dx) + batch * s.dx_batch + at * s.dx_token + head * s.dx_head;
                 if (v.has_a) st_stream(dx + v.a, Elem<T>::pack(fa));
                 if (v.has_b) st_stream(dx + v.b, Elem<T>::pack(fb));
             }
-            now = next;
         }
+        copies_wait<0>();
     }
     for (int off = G; off < 32; off <<= 1) {
 #pragma unroll
-        for (int i = 0; i < W; ++i) {
-            da[i] += __shfl_xor_sync(0xFFFFFFFFu, da[i], off);
-            db[i] += __shfl_xor_sync(0xFFFFFFFFu, db[i], off);
+        for (int i = 0; i < W / 2; ++i) {
+            da[i].x += __shfl_xor_sync(0xFFFFFFFFu, da[i].x, off);
+            da[i].y += __shfl_xor_sync(0xFFFFFFFFu, da[i].y, off);
+            db[i].x += __shfl_xor_sync(0xFFFFFFFFu, db[i].x, off);
+            db[i].y += __shfl_xor_sync(0xFFFFFFFFu, db[i].y, off);
         }
     }
+    __syncthreads();  // the ring is done with: the sums take its place
+    float* sums = reinterpret_cast<float*>(ring);
     if (lane < G) {
 #pragma unroll
-        for (int i = 0; i < W; ++i) {
-            if (v.has_a) sums[warp_in * a.dim + v.a + i] = da[i];
-            if (v.has_b) sums[warp_in * a.dim + v.b + i] = db[i];
+        for (int i = 0; i < W / 2; ++i) {
+            if (v.has_a) *reinterpret_cast<float2*>(sums + warp_in * a.dim + v.a + 2 * i) = da[i];
+            if (v.has_b) *reinterpret_cast<float2*>(sums + warp_in * a.dim + v.b + 2 * i) = db[i];
         }
     }
     leave_partials(sums, a.partials + static_cast<int64_t>(blockIdx.x) * a.dim, a.dim);
@@ -277,7 +304,7 @@ cudaError_t launch(HeadsGradArgs a, int sms, cudaStream_t st) {
     if (!vectors) {
         e = launch_with_pdl(heads_grad_elements<T>, grid, block, kWarps * a.dim * sizeof(float), st, a);
     } else {
-        const size_t smem = kWarps * (a.rope.pairs * sizeof(float2) + a.dim * sizeof(float));
+        const size_t smem = kStages * 4 * kWarps * 32 * sizeof(uint4) + kWarps * a.rope.pairs * sizeof(float2);
         e = a.rope.interleaved ? launch_with_pdl(heads_grad_rows<T, true>, grid, block, smem, st, a, G)
                                : launch_with_pdl(heads_grad_rows<T, false>, grid, block, smem, st, a, G);
     }
