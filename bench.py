@@ -814,7 +814,10 @@ def run_profile_case(spec: str, reps: int):
     token-side operator (rmsnorm_q8, fused_add_rmsnorm_q8 and the same with
     _128 for group scales; embedding_fwd, embedding_bwd, embedding_bwd_add,
     TOKENSxHIDDEN on a table of 131072 rows; token_logprob_fwd,
-    token_logprob_fwd_top, token_logprob_bwd, ROWSxVOCAB); an
+    token_logprob_fwd_top, token_logprob_bwd, ROWSxVOCAB); or one on attention
+    heads (rope_fwd, rope_bwd, qk_rmsnorm_rope_fwd, qk_rmsnorm_rope_bwd,
+    kv_append, kv_append_e4m3: TOKENSxHIDDEN, query heads of 128 and 8 key
+    heads, views of one projection's output); an
     optional @FAMILY suffix (e.g. @split) forces that kernel family for the
     timed calls (inputs are prepared under the automatic choice)."""
     import row_normalization_inner_gb300 as nf
@@ -891,6 +894,24 @@ def run_profile_case(spec: str, reps: int):
         else:
             top = 20 if op.endswith("_top") else 0
             fn = lambda: nf.token_logprob_fwd(logits, targets, top=top)  # noqa: E731
+    elif op.startswith(("rope_", "qk_rmsnorm_rope_", "kv_append")):
+        q, k, v, qw, kw, positions = workloads.heads_inputs(rows, hidden // 128, 8, 128, device=dev)
+        rates = nf.rope_rates(128)
+        if op.startswith("kv_append"):
+            cell = torch.float8_e4m3fn if op.endswith("e4m3") else torch.bfloat16
+            caches = [torch.zeros(-(-rows // 64), 64, 8, 128, dtype=cell, device=dev) for _ in range(2)]
+            scales = [torch.zeros(c.shape[:3], device=dev) if op.endswith("e4m3") else None for c in caches]
+            table = torch.arange(len(caches[0]), dtype=torch.int32, device=dev)[None]
+            starts = torch.tensor([0, rows], dtype=torch.int32, device=dev)
+            fn = lambda: nf.kv_append(k, v, *caches, table, starts[:1], starts, rates, q=q, q_weight=qw, k_weight=kw,  # noqa: E731
+                                      k_scale=scales[0], v_scale=scales[1])
+        elif op in ("rope_fwd", "rope_bwd"):
+            fn = lambda: getattr(nf, op)(q, k, positions, rates)  # noqa: E731
+        elif op == "qk_rmsnorm_rope_fwd":
+            fn = lambda: nf.qk_rmsnorm_rope_fwd(q, k, qw, kw, positions, rates)  # noqa: E731
+        else:
+            dq, dk = q.clone(), k.clone()
+            fn = lambda: nf.qk_rmsnorm_rope_bwd(dq, dk, q, k, qw, kw, positions, rates)  # noqa: E731
     else:
         raise SystemExit(f"unknown op {op}")
     nf.set_path(family or "auto")
@@ -898,7 +919,7 @@ def run_profile_case(spec: str, reps: int):
         for _ in range(reps):
             fn()
         torch.cuda.synchronize()
-        plan = op.split("_")[0] if op.startswith(("outer", "embedding", "token")) or "_q8" in op else nf.nf_plan_query(
+        plan = op.split("_")[0] if op.startswith(("outer", "embedding", "token", "rope", "qk", "kv")) or "_q8" in op else nf.nf_plan_query(
             "rmsnorm_bwd" if op == "fused_add_rmsnorm_bwd" else op, rows, hidden)
     finally:
         nf.set_path("auto")

@@ -59,9 +59,8 @@ __device__ __forceinline__ float2 turn_of(uint64_t rate, int64_t position, float
     return make_float2((c - s * r) * magnitude, (s + c * r) * magnitude * direction);
 }
 
-__device__ __forceinline__ int64_t position_at(const Rotation& r, uint32_t token, uint32_t tokens) {
-    const uint32_t batch = token / tokens;
-    const int64_t at = batch * r.position_batch + (token - batch * tokens);
+__device__ __forceinline__ int64_t position_at(const Rotation& r, uint32_t batch, uint32_t token) {
+    const int64_t at = batch * r.position_batch + token;
     return r.wide ? static_cast<const int64_t*>(r.positions)[at] : static_cast<const int32_t*>(r.positions)[at];
 }
 
@@ -94,14 +93,14 @@ struct LaneVectors {
     }
 };
 
-// The warp's table of a token's angles: `pairs` cosines, then as many sines.
-__device__ __forceinline__ void fill_turns(float* table, const Rotation& r, int pairs, int64_t position, float direction, int lane) {
-    for (int p = lane; p < pairs; p += 32) {
-        const float2 t = turn_of(r.rates[p], position, r.magnitude, direction);
-        table[p] = t.x;
-        table[pairs + p] = t.y;
+// A token's angles in shared memory: `pairs` cosines, then as many sines, by
+// `threads` threads of which this is number `t`.
+__device__ __forceinline__ void fill_turns(float* table, const Rotation& r, int pairs, int64_t position, float direction, int t, int threads) {
+    for (int p = t; p < pairs; p += threads) {
+        const float2 cs = turn_of(r.rates[p], position, r.magnitude, direction);
+        table[p] = cs.x;
+        table[pairs + p] = cs.y;
     }
-    __syncwarp();
 }
 
 // A lane's angles from that table.  Elements that are not turned are left as
@@ -155,9 +154,17 @@ struct LaneTurns {
 
 // Sum over the G lanes of a group; every lane gets the same value.
 __device__ __forceinline__ float sum_lanes(float v, int G) {
+#pragma unroll
     for (int off = G >> 1; off > 0; off >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, off);
     return v;
 }
+
+// 16 bytes to shared memory, or zeros.
+__device__ __forceinline__ void copy16(uint4* to, const void* from, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(to)), "l"(from), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 inline int lanes_for(int items) {
     int g = 1;

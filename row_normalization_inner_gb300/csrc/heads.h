@@ -22,7 +22,7 @@ struct HeadSegment {
     float* scale;                            // an 8-bit cache: per row
     int64_t scale_page, scale_slot, scale_head;
     int heads;
-    int chunks;   // warps per token (set by the launcher)
+    int chunks;   // of a token (set by the launcher)
     bool rotate;
     bool cache;   // out is a paged cache
 };
@@ -61,8 +61,10 @@ struct HeadsArgs {
     int dim;
     int tokens;      // per batch
     uint32_t total;  // batch * tokens
-    int chunks;      // warps per token (set by the launcher)
-    int passes;      // (set by the launcher)
+    int chunks;      // warps' shares of a token (set by the launcher, and the three below)
+    int passes;      // rows of a group in a share
+    int per_cta;     // tokens
+    int turns;       // CTAs of a token (1 where per_cta is more)
     float eps;
     // an append
     const int32_t* starts;  // null: one token per sequence

@@ -11,6 +11,8 @@
 // token's angles -- two sines and cosines a lane at 64 pairs -- are computed
 // once for all of them and wait in shared memory; a group of G lanes holds a
 // row, and the row's sums stay in the warp.
+#include <algorithm>
+
 #include "heads.cuh"
 
 namespace nf {
@@ -68,12 +70,29 @@ struct Place {
     int slot;
 };
 
+// The place of a token of sequence `seq`, which begins at token `first` and has
+// `past` tokens before it (negative: the token is padding).
+__device__ __forceinline__ Place place_in(const HeadsArgs& a, uint32_t token, int seq, int first, int past) {
+    Place p{};
+    p.used = past >= 0;
+    if (!p.used) return p;
+    p.position = static_cast<int64_t>(past) + (static_cast<int64_t>(token) - first);
+    const uint32_t place = static_cast<uint32_t>(p.position);  // below 2^32: both terms are below 2^31
+    const uint32_t column = place / static_cast<uint32_t>(a.page_size);
+    p.slot = static_cast<int>(place - column * static_cast<uint32_t>(a.page_size));
+    if (column < static_cast<uint32_t>(a.max_pages)) {
+        p.page = a.table[seq * a.table_stride + column];
+        p.stored = p.page >= 0 && p.page < a.pages;
+    }
+    return p;
+}
+
 // All lanes of a warp call this.  The sequence of a token is the last one that
 // starts at or before it; the starts are searched 32 ways at a time, and the
 // last 32 candidates' lengths come with them, so that the step costs one load's
 // latency for each factor of 32 of the sequences and one for the page.
 __device__ __forceinline__ Place find_place(const HeadsArgs& a, uint32_t token, int lane) {
-    Place p{};
+    bool used;
     int seq, first, past;
     if (a.starts) {
         const int behind = a.starts[a.seqs];
@@ -93,23 +112,13 @@ __device__ __forceinline__ Place find_place(const HeadsArgs& a, uint32_t token, 
             if (step == 1) break;
         }
         seq = lo;
-        p.used = first >= 0 && first <= static_cast<int64_t>(token) && static_cast<int64_t>(token) < behind;
+        used = first >= 0 && first <= static_cast<int64_t>(token) && static_cast<int64_t>(token) < behind;
     } else {
         seq = first = static_cast<int>(token);
-        p.used = seq < a.seqs;
-        past = p.used ? a.past[seq] : 0;
+        used = seq < a.seqs;
+        past = used ? a.past[seq] : 0;
     }
-    p.used = p.used && past >= 0;
-    if (!p.used) return p;
-    p.position = static_cast<int64_t>(past) + (static_cast<int64_t>(token) - first);
-    const uint32_t place = static_cast<uint32_t>(p.position);  // below 2^32: both terms are below 2^31
-    const uint32_t column = place / static_cast<uint32_t>(a.page_size);
-    p.slot = static_cast<int>(place - column * static_cast<uint32_t>(a.page_size));
-    if (column < static_cast<uint32_t>(a.max_pages)) {
-        p.page = a.table[seq * a.table_stride + column];
-        p.stored = p.page >= 0 && p.page < a.pages;
-    }
-    return p;
+    return place_in(a, token, seq, first, used ? past : -1);
 }
 
 // The row of head `h`: input, output and its scale.
@@ -118,51 +127,59 @@ __device__ __forceinline__ const T* row_in(const HeadSegment& s, uint32_t batch,
     return static_cast<const T*>(s.in) + batch * s.in_batch + at * s.in_token + h * s.in_head;
 }
 
-constexpr int kPasses = 4;  // most passes of a warp: so many rows of a group are in flight
+constexpr int kPasses = 4;     // most rows of a group in a share: so many are in flight
+constexpr int kMaxWarps = 5;  // per CTA
 
-template <typename T, bool INTER, bool APPEND>
-__global__ void __launch_bounds__(kWarps * 32) heads_rows(const __grid_constant__ HeadsArgs a, int G) {
-    constexpr int W = Elem<T>::W;
-    extern __shared__ float4 turns[];
+// A CTA takes `per_cta` tokens, its warps their shares: so many rows of queries,
+// keys or values.  The angles of a token are computed once, by all the warps
+// that need them, while the rows are on their way.
+template <typename T, bool INTER, bool APPEND, int GT>
+__global__ void __launch_bounds__(kMaxWarps * 32, 4) heads_rows(const __grid_constant__ HeadsArgs a, int lanes) {
+    constexpr int W = Elem<T>::W, P = W / 2;
+    const int G = GT ? GT : lanes;
+    extern __shared__ float4 tables[];  // [per_cta][2][pairs]
     grid_dep_wait();
     grid_dep_release();
-    const int lane = threadIdx.x & 31;
-    const uint32_t unit = blockIdx.x * kWarps + (threadIdx.x >> 5);
-    const uint32_t token = unit / a.chunks;
-    if (token >= a.total) return;
-    int chunk = static_cast<int>(unit - token * a.chunks), si = 0;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = (blockDim.x >> 5) / a.per_cta;
+    const int nth = warp / warps, share = warp - nth * warps;  // the warp's token in the CTA
+    const uint32_t group = a.turns == 1 ? blockIdx.x : blockIdx.x / a.turns;
+    const uint32_t token = group * a.per_cta + nth;
+    const int rows = 32 / G, j = lane & (G - 1), lane_row = lane / G;
+    const uint32_t batch = APPEND ? 0 : token / a.tokens, at = token - batch * a.tokens;
+    // the warp's share: queries, keys or values, and which rows of them
+    int chunk = static_cast<int>(blockIdx.x - group * a.turns) * warps + share, si = 0;
+    const bool real = token < a.total && chunk < a.chunks;
+    if (!real) chunk = 0;
     while (chunk >= a.seg[si].chunks) chunk -= a.seg[si++].chunks;
     const HeadSegment& s = a.seg[si];
-    const int rows = 32 / G, j = lane & (G - 1);
-    const uint32_t batch = APPEND ? 0 : token / a.tokens, at = token - batch * a.tokens;
     const int pairs = s.rotate ? a.rope.pairs : 0;
     const LaneVectors<W, INTER> v(j, a.dim, pairs);
-    const int head0 = chunk * a.passes * rows, head = head0 + lane / G;
-    const int passes = min(a.passes, (s.heads - head0 + rows - 1) / rows);
-
+    const int head = chunk * a.passes * rows + lane_row;
+    const int passes = min(a.passes, (s.heads - chunk * a.passes * rows + rows - 1) / rows);
     uint4 xa[kPasses], xb[kPasses];
     const T* in = row_in<T>(s, batch, at, head);
 #pragma unroll
     for (int p = 0; p < kPasses; ++p) {
         xa[p] = xb[p] = make_uint4(0, 0, 0, 0);
-        if (p < passes && head + p * rows < s.heads) {
+        if (real && p < passes && head + p * rows < s.heads) {
             const T* row = in + p * rows * s.in_head;
             if (v.has_a) xa[p] = ld_stream(row + v.a);
             if (v.has_b) xb[p] = ld_stream(row + v.b);
         }
     }
     Place place{};
-    if constexpr (APPEND) {
-        place = find_place(a, token, lane);
-        if (!place.used || (s.cache && !place.stored)) return;
+    if (APPEND && token < a.total) place = find_place(a, token, lane);
+    float* table = reinterpret_cast<float*>(tables) + nth * 2 * a.rope.pairs;
+    if (a.rope.pairs) {
+        if (token < a.total) {
+            const int64_t position = APPEND && !a.rope.positions ? place.position : position_at(a.rope, batch, at);
+            fill_turns(table, a.rope, a.rope.pairs, position, a.rope.direction, share * 32 + lane, warps * 32);
+        }
+        __syncthreads();
     }
+    if (!real || (APPEND && (!place.used || (s.cache && !place.stored)))) return;
     LaneTurns<W, INTER> t;
-    if (pairs) {
-        float* table = reinterpret_cast<float*>(turns) + (threadIdx.x >> 5) * 2 * a.rope.pairs;
-        const int64_t position = APPEND && !a.rope.positions ? place.position : position_at(a.rope, token, a.tokens);
-        fill_turns(table, a.rope, pairs, position, a.rope.direction, lane);
-        t.read(table, pairs, v);
-    }
+    if (pairs) t.read(table, pairs, v);
     const bool norm = s.weight != nullptr;
     uint4 wa = make_uint4(0, 0, 0, 0), wb = wa;
     if (norm) {
@@ -174,23 +191,23 @@ __global__ void __launch_bounds__(kWarps * 32) heads_rows(const __grid_constant_
     for (int p = 0; p < kPasses; ++p) {
         if (p >= passes) break;
         const bool here = head + p * rows < s.heads;
-        float2 fa[W / 2], fb[W / 2];
+        float2 fa[P], fb[P];
         Elem<T>::unpack(xa[p], fa);
         Elem<T>::unpack(xb[p], fb);
         if (norm) {
             float2 ss = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int i = 0; i < W / 2; ++i) {
+            for (int i = 0; i < P; ++i) {
                 ss = __ffma2_rn(fa[i], fa[i], ss);
                 ss = __ffma2_rn(fb[i], fb[i], ss);
             }
             const float r = rsqrtf(sum_lanes(ss.x + ss.y, G) * mean_of + a.eps);
             const float2 rstd = make_float2(r, r);
-            float2 ga[W / 2], gb[W / 2];
+            float2 ga[P], gb[P];
             Elem<T>::unpack(wa, ga);
             Elem<T>::unpack(wb, gb);
 #pragma unroll
-            for (int i = 0; i < W / 2; ++i) {
+            for (int i = 0; i < P; ++i) {
                 fa[i] = __fmul2_rn(__fmul2_rn(fa[i], rstd), ga[i]);
                 fb[i] = __fmul2_rn(__fmul2_rn(fb[i], rstd), gb[i]);
             }
@@ -201,7 +218,8 @@ __global__ void __launch_bounds__(kWarps * 32) heads_rows(const __grid_constant_
             if (a.format != kCacheSame) {
                 uint32_t top = 0;
 #pragma unroll
-                for (int i = 0; i < W / 2; ++i) top = top_of(top_of(top, fa[i]), fb[i]);
+                for (int i = 0; i < P; ++i) top = top_of(top_of(top, fa[i]), fb[i]);
+#pragma unroll
                 for (int off = G >> 1; off > 0; off >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, off));
                 const bool int8 = a.format == kCacheInt8, fine = finite_bits(top);
                 const float scale = row_scale(top, int8), inverse = __fdiv_rn(1.f, scale);
@@ -258,7 +276,7 @@ __global__ void __launch_bounds__(kWarps * 32) heads_elements(const __grid_const
     }
     __syncwarp();
     if (pairs) {
-        const int64_t position = APPEND && !a.rope.positions ? place.position : position_at(a.rope, token, a.tokens);
+        const int64_t position = APPEND && !a.rope.positions ? place.position : position_at(a.rope, batch, at);
         for (int p = lane; p < pairs; p += 32) {
             const float2 t = turn_of(a.rope.rates[p], position, a.rope.magnitude, a.rope.direction);
             const int ia = a.rope.interleaved ? 2 * p : p, ib = a.rope.interleaved ? 2 * p + 1 : p + pairs;
@@ -308,6 +326,15 @@ bool whole_vectors(const HeadsArgs& a, int W) {
     return true;
 }
 
+template <typename T, bool INTER, bool APPEND>
+cudaError_t launch_lanes(const HeadsArgs& a, int G, dim3 grid, dim3 block, size_t smem, cudaStream_t st) {
+    switch (G) {  // the common heads: 128 elements, 256 (bf16) and 64 (fp32)
+        case 8: return launch_with_pdl(heads_rows<T, INTER, APPEND, 8>, grid, block, smem, st, a, G);
+        case 16: return launch_with_pdl(heads_rows<T, INTER, APPEND, 16>, grid, block, smem, st, a, G);
+        default: return launch_with_pdl(heads_rows<T, INTER, APPEND, 0>, grid, block, smem, st, a, G);
+    }
+}
+
 template <typename T, bool APPEND>
 cudaError_t launch(HeadsArgs a, int sms, cudaStream_t st) {
     constexpr int W = Elem<T>::W;
@@ -319,8 +346,8 @@ cudaError_t launch(HeadsArgs a, int sms, cudaStream_t st) {
                                kWarps * a.dim * sizeof(float), st, a);
     }
     const int G = lanes_for((a.dim / W + 1) / 2), rows = 32 / G;
-    // As many of a token's rows to a warp as leave every SM its warps: each
-    // pass more shares the angles and the weight among more rows.
+    // As many rows to a share as leave every SM its warps: each pass more
+    // spreads what a warp does before its rows over more of them.
     for (a.passes = kPasses;; a.passes /= 2) {
         a.chunks = 0;
         for (int i = 0; i < a.segments; ++i) {
@@ -329,11 +356,13 @@ cudaError_t launch(HeadsArgs a, int sms, cudaStream_t st) {
         }
         if (a.passes == 1 || static_cast<int64_t>(a.total) * a.chunks >= 64 * sms) break;
     }
-    const int64_t units = static_cast<int64_t>(a.total) * a.chunks;
-    const dim3 grid(static_cast<unsigned>((units + kWarps - 1) / kWarps));
-    const size_t smem = kWarps * a.rope.pairs * sizeof(float2);
-    return a.rope.interleaved ? launch_with_pdl(heads_rows<T, true, APPEND>, grid, dim3(kWarps * 32), smem, st, a, G)
-                              : launch_with_pdl(heads_rows<T, false, APPEND>, grid, dim3(kWarps * 32), smem, st, a, G);
+    // a warp to each share, in several CTAs where a token has many; tokens of few shares side by side in a CTA of four warps or more
+    a.turns = (a.chunks + kMaxWarps - 1) / kMaxWarps;
+    const int warps = (a.chunks + a.turns - 1) / a.turns;
+    a.per_cta = warps >= 4 ? 1 : 4 / warps;
+    const dim3 grid((a.total + a.per_cta - 1) / a.per_cta * a.turns), block(warps * a.per_cta * 32);
+    const size_t smem = a.per_cta * a.rope.pairs * sizeof(float2);
+    return a.rope.interleaved ? launch_lanes<T, true, APPEND>(a, G, grid, block, smem, st) : launch_lanes<T, false, APPEND>(a, G, grid, block, smem, st);
 }
 
 }  // namespace

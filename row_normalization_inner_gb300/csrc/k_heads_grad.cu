@@ -24,13 +24,6 @@ constexpr int kWarps = 4;
 constexpr int kCtasPerSm = 4;
 constexpr int kStages = 4;
 
-// 16 bytes to shared memory, or zeros.
-__device__ __forceinline__ void copy16(uint4* to, const void* from, bool there) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(to)), "l"(from), "r"(there ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
 // What a warp walks: passes [first, end) of its segment, `per_token` to a token.
 struct Stretch {
     int64_t first, end;
@@ -101,14 +94,15 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) heads_grad_rows(const
         };
 #pragma unroll
         for (int i = 0; i < kStages - 1; ++i) copy(i);
-        int64_t position = pairs ? position_at(a.rope, token, a.tokens) : 0;
+        int64_t position = pairs ? position_at(a.rope, token / a.tokens, token % a.tokens) : 0;
         bool fresh = true;
         LaneTurns<W, INTER> t;
         int stage = 0;
         for (int64_t p = r.first; p < r.end; ++p) {
             if (fresh && pairs) {
                 __syncwarp();
-                fill_turns(table, a.rope, pairs, position, -1.f, lane);
+                fill_turns(table, a.rope, pairs, position, -1.f, lane, 32);
+                __syncwarp();
                 t.read(table, pairs, v);
             }
             const uint32_t batch = token / a.tokens, at = token - batch * a.tokens;
@@ -116,7 +110,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) heads_grad_rows(const
             fresh = ++pass == per_token;
             if (fresh) {
                 pass = 0, ++token;
-                if (pairs && p + 1 < r.end) position = position_at(a.rope, token, a.tokens);
+                if (pairs && p + 1 < r.end) position = position_at(a.rope, token / a.tokens, token % a.tokens);
             }
             copies_wait<kStages - 2>();
             const uint4* from = ring + stage * 4 * kWarps * 32 + threadIdx.x;
@@ -212,7 +206,7 @@ __global__ void __launch_bounds__(kWarps * 32) heads_grad_elements(const __grid_
         for (int i = lane; i < dim; i += 32) g[i] = Elem<T>::load(y + i);
         __syncwarp();
         if (pairs) {
-            const int64_t position = position_at(a.rope, token, a.tokens);
+            const int64_t position = position_at(a.rope, token / a.tokens, token % a.tokens);
             for (int q = lane; q < pairs; q += 32) {
                 const float2 t = turn_of(a.rope.rates[q], position, a.rope.magnitude, -1.f);
                 const int ia = a.rope.interleaved ? 2 * q : q, ib = a.rope.interleaved ? 2 * q + 1 : q + pairs;

@@ -130,6 +130,18 @@ def logprob_inputs(rows: int, vocab: int, seed: int = 0, device="cpu"):
     return logits, targets, d_logprob, d_entropy
 
 
+def heads_inputs(tokens: int, q_heads: int, k_heads: int, dim: int, seed: int = 0, device="cpu"):
+    """Queries, keys and values ~ N(0, 1) as views of one projection's output
+    [tokens, heads, dim], weights ~ N(1, 0.1), bf16, and positions 0 to tokens - 1.
+    Returns (q, k, v, q_weight, k_weight, positions int64)."""
+    g = _gen(seed, device)
+    whole = _draw(g, (tokens, q_heads + 2 * k_heads, dim), 0.0, 1.0, device)
+    q, k, v = torch.split(whole, [q_heads, k_heads, k_heads], 1)
+    q_weight = _draw(g, (dim,), 1.0, 0.1, device)
+    k_weight = _draw(g, (dim,), 1.0, 0.1, device)
+    return q, k, v, q_weight, k_weight, torch.arange(tokens, device=device)
+
+
 @dataclass(frozen=True)
 class Workload:
     name: str
