@@ -8,6 +8,9 @@
 //     for lane j below pairs / W, then the elements behind the rotated ones,
 //     two vectors to a lane;
 //   interleaved (pairs 2i, 2i + 1): a and b are any two vectors.
+// Either way a lane has W pairs (x, y): in the half layout x from a and y from
+// b, interleaved the even elements of a and b and the odd ones.  A vector's
+// pairs are all turned, or none.
 //
 // Angles.  A pair turns by position * frequency.  `rates` holds frequencies as
 // the share of a turn per position, in units of 2^-64, so that the 64-bit
@@ -24,27 +27,63 @@
 
 namespace nf {
 
-// A 16-byte vector as W elements in fp32, in pairs for the packed arithmetic.
-template <typename T> struct Elem;
-template <> struct Elem<uint16_t> {  // bf16
+__device__ __forceinline__ uint32_t divide(uint32_t n, const Divider& d) {
+    return d.m ? static_cast<uint32_t>(__umul64hi(n, d.m)) : n;
+}
+
+// A lane's two vectors as pairs (x, y) in fp32, two pairs to a register pair for
+// the packed arithmetic.
+template <typename T, bool INTER> struct Elem;
+template <bool INTER> struct Elem<uint16_t, INTER> {  // bf16
     static constexpr int W = 8;
-    static __device__ __forceinline__ void unpack(uint4 v, float2 (&f)[4]) { unpack8x2(v, f); }
-    static __device__ __forceinline__ uint4 pack(const float2 (&f)[4]) { return pack8x2(f); }
-    static __device__ __forceinline__ float load(const uint16_t* p) { return bf_lo(*p); }
-    static __device__ __forceinline__ void store(uint16_t* p, float f) { *p = static_cast<uint16_t>(pack2(f, 0.f) & 0xFFFF); }
+    static __device__ __forceinline__ void unpack(uint4 a, uint4 b, float2 (&x)[4], float2 (&y)[4]) {
+        if constexpr (INTER) {
+            x[0] = make_float2(bf_lo(a.x), bf_lo(a.y)), y[0] = make_float2(bf_hi(a.x), bf_hi(a.y));
+            x[1] = make_float2(bf_lo(a.z), bf_lo(a.w)), y[1] = make_float2(bf_hi(a.z), bf_hi(a.w));
+            x[2] = make_float2(bf_lo(b.x), bf_lo(b.y)), y[2] = make_float2(bf_hi(b.x), bf_hi(b.y));
+            x[3] = make_float2(bf_lo(b.z), bf_lo(b.w)), y[3] = make_float2(bf_hi(b.z), bf_hi(b.w));
+        } else {
+            unpack8x2(a, x);
+            unpack8x2(b, y);
+        }
+    }
+    static __device__ __forceinline__ void pack(const float2 (&x)[4], const float2 (&y)[4], uint4& a, uint4& b) {
+        if constexpr (INTER) {
+            a = make_uint4(pack2(x[0].x, y[0].x), pack2(x[0].y, y[0].y), pack2(x[1].x, y[1].x), pack2(x[1].y, y[1].y));
+            b = make_uint4(pack2(x[2].x, y[2].x), pack2(x[2].y, y[2].y), pack2(x[3].x, y[3].x), pack2(x[3].y, y[3].y));
+        } else {
+            a = pack8x2(x);
+            b = pack8x2(y);
+        }
+    }
 };
-template <> struct Elem<float> {
+template <bool INTER> struct Elem<float, INTER> {
     static constexpr int W = 4;
-    static __device__ __forceinline__ void unpack(uint4 v, float2 (&f)[2]) {
-        f[0] = make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
-        f[1] = make_float2(__uint_as_float(v.z), __uint_as_float(v.w));
+    static __device__ __forceinline__ float f(uint32_t u) { return __uint_as_float(u); }
+    static __device__ __forceinline__ uint32_t u(float v) { return __float_as_uint(v); }
+    static __device__ __forceinline__ void unpack(uint4 a, uint4 b, float2 (&x)[2], float2 (&y)[2]) {
+        if constexpr (INTER) {
+            x[0] = make_float2(f(a.x), f(a.z)), y[0] = make_float2(f(a.y), f(a.w));
+            x[1] = make_float2(f(b.x), f(b.z)), y[1] = make_float2(f(b.y), f(b.w));
+        } else {
+            x[0] = make_float2(f(a.x), f(a.y)), x[1] = make_float2(f(a.z), f(a.w));
+            y[0] = make_float2(f(b.x), f(b.y)), y[1] = make_float2(f(b.z), f(b.w));
+        }
     }
-    static __device__ __forceinline__ uint4 pack(const float2 (&f)[2]) {
-        return make_uint4(__float_as_uint(f[0].x), __float_as_uint(f[0].y), __float_as_uint(f[1].x), __float_as_uint(f[1].y));
+    static __device__ __forceinline__ void pack(const float2 (&x)[2], const float2 (&y)[2], uint4& a, uint4& b) {
+        if constexpr (INTER) {
+            a = make_uint4(u(x[0].x), u(y[0].x), u(x[0].y), u(y[0].y));
+            b = make_uint4(u(x[1].x), u(y[1].x), u(x[1].y), u(y[1].y));
+        } else {
+            a = make_uint4(u(x[0].x), u(x[0].y), u(x[1].x), u(x[1].y));
+            b = make_uint4(u(y[0].x), u(y[0].y), u(y[1].x), u(y[1].y));
+        }
     }
-    static __device__ __forceinline__ float load(const float* p) { return *p; }
-    static __device__ __forceinline__ void store(float* p, float f) { *p = f; }
 };
+__device__ __forceinline__ float load_element(const uint16_t* p) { return bf_lo(*p); }
+__device__ __forceinline__ float load_element(const float* p) { return *p; }
+__device__ __forceinline__ void store_element(uint16_t* p, float f) { *p = static_cast<uint16_t>(pack2(f, 0.f) & 0xFFFF); }
+__device__ __forceinline__ void store_element(float* p, float f) { *p = f; }
 
 // (cos, sin) of a pair at a position, both times `magnitude`.  sincospif takes
 // the angle's upper 24 bits, which fp32 holds exactly; the rest, below 2^-24 half
@@ -64,33 +103,33 @@ __device__ __forceinline__ int64_t position_at(const Rotation& r, uint32_t batch
     return r.wide ? static_cast<const int64_t*>(r.positions)[at] : static_cast<const int32_t*>(r.positions)[at];
 }
 
-// Lane j's two vectors: where they start, whether they are there, and how many
-// pairs of each are turned (half layout: W of a, with b, or none).
-template <int W, bool INTER>
+// Lane j's two vectors: where they start, whether they are there, and whether
+// their pairs are turned.  FULL: every lane of a group has both.
+template <int W, bool INTER, bool FULL>
 struct LaneVectors {
     int a, b;
-    bool has_a, has_b;
-    int turned_a, turned_b;
+    bool in_a, in_b;
+    bool turn_a, turn_b;  // of the first and the second half of the lane's pairs
     __device__ __forceinline__ LaneVectors(int j, int dim, int pairs) {
         const int vectors = dim / W, items = (vectors + 1) / 2;
         if constexpr (INTER) {
             a = j * W;
             b = (items + j) * W;
-            has_a = j < items;
-            has_b = has_a && items + j < vectors;
-            turned_a = has_a ? max(0, min(W / 2, pairs - a / 2)) : 0;
-            turned_b = has_b ? max(0, min(W / 2, pairs - b / 2)) : 0;
+            in_a = j < items;
+            in_b = in_a && items + j < vectors;
+            turn_a = in_a && a < 2 * pairs;
+            turn_b = in_b && b < 2 * pairs;
         } else {
             const int turned = pairs / W, rest = vectors - 2 * turned, rest_items = (rest + 1) / 2;
-            const bool t = j < turned;
-            a = t ? j * W : (turned + j) * W;
-            b = t ? (turned + j) * W : (turned + rest_items + j) * W;
-            has_a = j < turned + rest_items;
-            has_b = has_a && (t || turned + rest_items + j < vectors);
-            turned_a = t ? W : 0;
-            turned_b = 0;
+            turn_a = turn_b = j < turned;
+            a = turn_a ? j * W : (turned + j) * W;
+            b = turn_a ? (turned + j) * W : (turned + rest_items + j) * W;
+            in_a = j < turned + rest_items;
+            in_b = in_a && (turn_a || turned + rest_items + j < vectors);
         }
     }
+    __device__ __forceinline__ bool has_a() const { return FULL || in_a; }
+    __device__ __forceinline__ bool has_b() const { return FULL || in_b; }
 };
 
 // A token's angles in shared memory: `pairs` cosines, then as many sines, by
@@ -103,54 +142,92 @@ __device__ __forceinline__ void fill_turns(float* table, const Rotation& r, int 
     }
 }
 
-// A lane's angles from that table.  Elements that are not turned are left as
-// they are, whatever stands beside them.
-template <int W, bool INTER>
-struct LaneTurns {
-    float2 c[W / 2], s[W / 2];  // of pairs 2i and 2i + 1; interleaved: those of a, then those of b
-    __device__ __forceinline__ void read(const float* table, int pairs, const LaneVectors<W, INTER>& v) {
-        if constexpr (INTER) {
-            float* cf = reinterpret_cast<float*>(c);
-            float* sf = reinterpret_cast<float*>(s);
+// The lane's cosines and sines from that table (pairs and the vectors' first
+// pairs are whole multiples of what is read at once).  Pairs that are not turned
+// get (1, 0).
+template <int W, bool INTER, bool FULL>
+__device__ __forceinline__ void read_turns(const float* table, int pairs, const LaneVectors<W, INTER, FULL>& v, float2 (&c)[W / 2], float2 (&s)[W / 2]) {
 #pragma unroll
-            for (int i = 0; i < W; ++i) {
-                const bool on = i < W / 2 ? i < v.turned_a : i - W / 2 < v.turned_b;
-                const int p = i < W / 2 ? v.a / 2 + i : v.b / 2 + i - W / 2;
-                cf[i] = on ? table[p] : 1.f;
-                sf[i] = on ? table[pairs + p] : 0.f;
-            }
-        } else if (v.turned_a) {  // pairs is a multiple of W here, and so is a
-#pragma unroll
-            for (int i = 0; i < W / 4; ++i) {
-                const float4 cc = *reinterpret_cast<const float4*>(table + v.a + 4 * i);
-                const float4 ss = *reinterpret_cast<const float4*>(table + pairs + v.a + 4 * i);
-                c[2 * i] = make_float2(cc.x, cc.y);
-                c[2 * i + 1] = make_float2(cc.z, cc.w);
-                s[2 * i] = make_float2(ss.x, ss.y);
-                s[2 * i + 1] = make_float2(ss.z, ss.w);
-            }
+    for (int h = 0; h < 2; ++h) {  // the first and the second half of the lane's pairs
+        const bool on = h ? v.turn_b : v.turn_a;
+        const float* from = table + (!INTER ? v.a + h * (W / 2) : (h ? v.b : v.a) / 2);
+        if constexpr (W == 8) {
+            const float4 cc = on ? *reinterpret_cast<const float4*>(from) : make_float4(1.f, 1.f, 1.f, 1.f);
+            const float4 ss = on ? *reinterpret_cast<const float4*>(from + pairs) : make_float4(0.f, 0.f, 0.f, 0.f);
+            c[2 * h] = make_float2(cc.x, cc.y), c[2 * h + 1] = make_float2(cc.z, cc.w);
+            s[2 * h] = make_float2(ss.x, ss.y), s[2 * h + 1] = make_float2(ss.z, ss.w);
+        } else {
+            c[h] = on ? *reinterpret_cast<const float2*>(from) : make_float2(1.f, 1.f);
+            s[h] = on ? *reinterpret_cast<const float2*>(from + pairs) : make_float2(0.f, 0.f);
         }
     }
-    static __device__ __forceinline__ float2 turned(float2 v, float c, float s) { return make_float2(v.x * c - v.y * s, v.y * c + v.x * s); }
-    __device__ __forceinline__ void turn(float2 (&a)[W / 2], float2 (&b)[W / 2], const LaneVectors<W, INTER>& v) const {
-        if constexpr (INTER) {
-            const float* cf = reinterpret_cast<const float*>(c);
-            const float* sf = reinterpret_cast<const float*>(s);
+}
+
+// A lane's factors at a token, the weights folded into the angles:
+//   x' = x xc + y ys,   y' = y yc + x xs
+// which takes a product per element out of every row.  A pair that is not
+// turned takes xc and yc alone, whatever stands in its other element.
+template <int W, bool INTER, bool FULL>
+struct LaneFactors {
+    static constexpr int P = W / 2;
+    float2 xc[P], ys[P], yc[P], xs[P];
+    bool turn_a, turn_b;
+    template <typename T>
+    __device__ __forceinline__ void read(const T* weight, const float* table, int pairs, const LaneVectors<W, INTER, FULL>& v) {
+        float2 c[P], s[P];
+        turn_a = v.turn_a, turn_b = v.turn_b;
+        if (pairs) {
+            read_turns<W, INTER, FULL>(table, pairs, v, c, s);
+        } else {
 #pragma unroll
-            for (int i = 0; i < W / 2; ++i) {
-                if (i < v.turned_a) a[i] = turned(a[i], cf[i], sf[i]);
-                if (i < v.turned_b) b[i] = turned(b[i], cf[W / 2 + i], sf[W / 2 + i]);
+            for (int i = 0; i < P; ++i) c[i] = make_float2(1.f, 1.f), s[i] = make_float2(0.f, 0.f);
+        }
+        if (weight) {
+            uint4 ua = make_uint4(0, 0, 0, 0), ub = ua;
+            if (v.has_a()) ua = ld_param(weight + v.a);
+            if (v.has_b()) ub = ld_param(weight + v.b);
+            float2 x[P], y[P];
+            Elem<T, INTER>::unpack(ua, ub, x, y);
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                xc[i] = __fmul2_rn(x[i], c[i]);
+                yc[i] = __fmul2_rn(y[i], c[i]);
+                xs[i] = __fmul2_rn(x[i], s[i]);
+                ys[i] = __fmul2_rn(y[i], make_float2(-s[i].x, -s[i].y));
             }
-        } else if (v.turned_a) {
+        } else {
 #pragma unroll
-            for (int i = 0; i < W / 2; ++i) {
-                const float2 x = a[i], y = b[i], t = __fmul2_rn(y, s[i]);
-                a[i] = __ffma2_rn(x, c[i], make_float2(-t.x, -t.y));
-                b[i] = __ffma2_rn(y, c[i], __fmul2_rn(x, s[i]));
+            for (int i = 0; i < P; ++i) xc[i] = yc[i] = c[i], xs[i] = s[i], ys[i] = make_float2(-s[i].x, -s[i].y);
+        }
+    }
+    __device__ __forceinline__ void apply(float2 (&x)[P], float2 (&y)[P]) const {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (h ? turn_b : turn_a) {
+#pragma unroll
+                for (int i = h * P / 2; i < (h + 1) * P / 2; ++i) {
+                    const float2 u = x[i];
+                    x[i] = __ffma2_rn(y[i], ys[i], __fmul2_rn(u, xc[i]));
+                    y[i] = __ffma2_rn(u, xs[i], __fmul2_rn(y[i], yc[i]));
+                }
+            } else {
+#pragma unroll
+                for (int i = h * P / 2; i < (h + 1) * P / 2; ++i) x[i] = __fmul2_rn(x[i], xc[i]), y[i] = __fmul2_rn(y[i], yc[i]);
             }
         }
     }
 };
+
+// The elements of vectors a and b in their order.
+template <int W, bool INTER>
+__device__ __forceinline__ void in_order(const float2 (&x)[W / 2], const float2 (&y)[W / 2], float (&a)[W], float (&b)[W]) {
+    const float *xf = reinterpret_cast<const float*>(x), *yf = reinterpret_cast<const float*>(y);
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+        a[i] = !INTER ? xf[i] : i % 2 ? yf[i / 2] : xf[i / 2];
+        b[i] = !INTER ? yf[i] : i % 2 ? yf[W / 2 + i / 2] : xf[W / 2 + i / 2];
+    }
+}
 
 // Sum over the G lanes of a group; every lane gets the same value.
 __device__ __forceinline__ float sum_lanes(float v, int G) {

@@ -12,6 +12,15 @@ namespace nf {
 constexpr int kHeadMaxDim = 512;
 constexpr int kMaxSegments = 3;
 
+// n / d for 32-bit n by a product (set up on the host): with M = ceil(2^64 / d)
+// the upper half of n * M is the quotient, as n (M d - 2^64) < 2^64.
+struct Divider {
+    uint64_t m;  // 0: d is 1
+    uint32_t d;
+    Divider() = default;
+    explicit Divider(uint32_t by) : m(by > 1 ? ~0ull / by + 1 : 0), d(by) {}
+};
+
 // One set of heads of a call: queries, keys or values.  Strides in elements.
 struct HeadSegment {
     const void* in;
@@ -62,9 +71,9 @@ struct HeadsArgs {
     int tokens;      // per batch
     uint32_t total;  // batch * tokens
     int chunks;      // warps' shares of a token (set by the launcher, and the three below)
-    int passes;      // rows of a group in a share
     int per_cta;     // tokens
     int turns;       // CTAs of a token (1 where per_cta is more)
+    Divider by_tokens, by_turns, by_page;
     float eps;
     // an append
     const int32_t* starts;  // null: one token per sequence
@@ -85,6 +94,7 @@ struct HeadsGradArgs {
     int dim;
     int tokens;
     uint32_t total;
+    Divider by_tokens;  // set by the launcher
     float eps;
     float* partials;  // [CTAs][dim]
 };

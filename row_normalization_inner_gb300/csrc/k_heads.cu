@@ -48,12 +48,11 @@ __device__ __forceinline__ uint32_t quant2(float y0, float y1, float scale, floa
 }
 
 template <int W>
-__device__ __forceinline__ void store_quantized(uint8_t* p, const float2 (&y)[W / 2], float scale, float inverse, bool fine, bool int8) {
+__device__ __forceinline__ void store_quantized(uint8_t* p, const float (&v)[W], float scale, float inverse, bool fine, bool int8) {
     uint32_t q[W / 4];
 #pragma unroll
     for (int i = 0; i < W / 4; ++i)
-        q[i] = quant2(y[2 * i].x, y[2 * i].y, scale, inverse, fine, int8) |
-               (quant2(y[2 * i + 1].x, y[2 * i + 1].y, scale, inverse, fine, int8) << 16);
+        q[i] = quant2(v[4 * i], v[4 * i + 1], scale, inverse, fine, int8) | (quant2(v[4 * i + 2], v[4 * i + 3], scale, inverse, fine, int8) << 16);
     if constexpr (W == 8) *reinterpret_cast<uint2*>(p) = make_uint2(q[0], q[1]);
     else *reinterpret_cast<uint32_t*>(p) = q[0];
 }
@@ -78,7 +77,7 @@ __device__ __forceinline__ Place place_in(const HeadsArgs& a, uint32_t token, in
     if (!p.used) return p;
     p.position = static_cast<int64_t>(past) + (static_cast<int64_t>(token) - first);
     const uint32_t place = static_cast<uint32_t>(p.position);  // below 2^32: both terms are below 2^31
-    const uint32_t column = place / static_cast<uint32_t>(a.page_size);
+    const uint32_t column = divide(place, a.by_page);
     p.slot = static_cast<int>(place - column * static_cast<uint32_t>(a.page_size));
     if (column < static_cast<uint32_t>(a.max_pages)) {
         p.page = a.table[seq * a.table_stride + column];
@@ -121,31 +120,67 @@ __device__ __forceinline__ Place find_place(const HeadsArgs& a, uint32_t token, 
     return place_in(a, token, seq, first, used ? past : -1);
 }
 
-// The row of head `h`: input, output and its scale.
-template <typename T>
-__device__ __forceinline__ const T* row_in(const HeadSegment& s, uint32_t batch, uint32_t at, int h) {
-    return static_cast<const T*>(s.in) + batch * s.in_batch + at * s.in_token + h * s.in_head;
+constexpr int kMaxWarps = 5;  // per CTA
+constexpr int64_t kManyShares = 64;  // per SM
+
+// 1 over a row's root mean square.
+template <typename T, bool INTER>
+__device__ __forceinline__ float rstd_of(uint4 a, uint4 b, int G, float mean_of, float eps) {
+    constexpr int P = Elem<T, INTER>::W / 2;
+    float2 x[P], y[P];
+    Elem<T, false>::unpack(a, b, x, y);
+    float2 ss = __fmul2_rn(x[0], x[0]);
+    ss = __ffma2_rn(y[0], y[0], ss);
+#pragma unroll
+    for (int i = 1; i < P; ++i) ss = __ffma2_rn(y[i], y[i], __ffma2_rn(x[i], x[i], ss));
+    return rsqrtf(sum_lanes(ss.x + ss.y, G) * mean_of + eps);
 }
 
-constexpr int kPasses = 4;     // most rows of a group in a share: so many are in flight
-constexpr int kMaxWarps = 5;  // per CTA
+// A row of a lane's group: over its root mean square, weighted and turned.
+template <typename T, bool INTER, bool FULL, bool NORM, int P>
+__device__ __forceinline__ void turn_row(uint4 a, uint4 b, float rstd, const LaneFactors<2 * P, INTER, FULL>& f, float2 (&x)[P], float2 (&y)[P]) {
+    Elem<T, INTER>::unpack(a, b, x, y);
+    if constexpr (NORM) {
+        const float2 r = make_float2(rstd, rstd);
+#pragma unroll
+        for (int i = 0; i < P; ++i) x[i] = __fmul2_rn(x[i], r), y[i] = __fmul2_rn(y[i], r);
+    }
+    f.apply(x, y);
+}
+
+// N such rows, rounded to vectors again.  Without a branch between them, so that
+// one is waited for under another's arithmetic.
+template <typename T, bool INTER, bool FULL, bool NORM, int N, int M>
+__device__ __forceinline__ void turn_rows(uint4 (&a)[M], uint4 (&b)[M], const float (&rstd)[M], const LaneFactors<Elem<T, INTER>::W, INTER, FULL>& f,
+                                          int G, float mean_of, float eps) {
+    constexpr int P = Elem<T, INTER>::W / 2;
+#pragma unroll
+    for (int p = 0; p < N; ++p) {
+        float2 x[P], y[P];
+        const float r = NORM && M > 1 ? rstd_of<T, INTER>(a[p], b[p], G, mean_of, eps) : rstd[p];
+        turn_row<T, INTER, FULL, NORM, P>(a[p], b[p], r, f, x, y);
+        Elem<T, INTER>::pack(x, y, a[p], b[p]);
+    }
+}
 
 // A CTA takes `per_cta` tokens, its warps their shares: so many rows of queries,
 // keys or values.  The angles of a token are computed once, by all the warps
-// that need them, while the rows are on their way.
-template <typename T, bool INTER, bool APPEND, int GT>
+// that need them, while the rows are on their way.  N: the rows of a group in a
+// share.  GT: lanes of a group, each with both its vectors; 0: any.
+template <typename T, bool INTER, bool APPEND, int GT, int N>
 __global__ void __launch_bounds__(kMaxWarps * 32, 4) heads_rows(const __grid_constant__ HeadsArgs a, int lanes) {
-    constexpr int W = Elem<T>::W, P = W / 2;
-    const int G = GT ? GT : lanes;
+    constexpr int W = Elem<T, INTER>::W, P = W / 2;
+    constexpr bool FULL = GT != 0;
+    const int G = FULL ? GT : lanes;
     extern __shared__ float4 tables[];  // [per_cta][2][pairs]
     grid_dep_wait();
     grid_dep_release();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = (blockDim.x >> 5) / a.per_cta;
-    const int nth = warp / warps, share = warp - nth * warps;  // the warp's token in the CTA
-    const uint32_t group = a.turns == 1 ? blockIdx.x : blockIdx.x / a.turns;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = a.per_cta == 1 ? blockDim.x >> 5 : (blockDim.x >> 5) / a.per_cta;
+    const int nth = a.per_cta == 1 ? 0 : warp / warps, share = warp - nth * warps;  // the warp's token in the CTA
+    const uint32_t group = divide(blockIdx.x, a.by_turns);
     const uint32_t token = group * a.per_cta + nth;
     const int rows = 32 / G, j = lane & (G - 1), lane_row = lane / G;
-    const uint32_t batch = APPEND ? 0 : token / a.tokens, at = token - batch * a.tokens;
+    const uint32_t batch = APPEND ? 0 : divide(token, a.by_tokens), at = token - batch * a.tokens;
     // the warp's share: queries, keys or values, and which rows of them
     int chunk = static_cast<int>(blockIdx.x - group * a.turns) * warps + share, si = 0;
     const bool real = token < a.total && chunk < a.chunks;
@@ -153,89 +188,106 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 4) heads_rows(const __grid_con
     while (chunk >= a.seg[si].chunks) chunk -= a.seg[si++].chunks;
     const HeadSegment& s = a.seg[si];
     const int pairs = s.rotate ? a.rope.pairs : 0;
-    const LaneVectors<W, INTER> v(j, a.dim, pairs);
-    const int head = chunk * a.passes * rows + lane_row;
-    const int passes = min(a.passes, (s.heads - chunk * a.passes * rows + rows - 1) / rows);
-    uint4 xa[kPasses], xb[kPasses];
-    const T* in = row_in<T>(s, batch, at, head);
+    const LaneVectors<W, INTER, FULL> v(j, FULL ? 2 * W * GT : a.dim, pairs);
+    const int first = chunk * N * rows, head = first + lane_row;
+    // what the angles need is asked for first: it is waited for before the rows are
+    const int mine = share * 32 + lane;
+    int64_t position = 0;
+    uint64_t rate = 0;
+    if (a.rope.pairs && token < a.total) {
+        if (a.rope.positions) position = position_at(a.rope, batch, at);
+        if (mine < a.rope.pairs) rate = a.rope.rates[mine];
+    }
+    uint4 xa[N], xb[N];
+    {
+        const T* in = static_cast<const T*>(s.in) + batch * s.in_batch + at * s.in_token;
 #pragma unroll
-    for (int p = 0; p < kPasses; ++p) {
-        xa[p] = xb[p] = make_uint4(0, 0, 0, 0);
-        if (real && p < passes && head + p * rows < s.heads) {
-            const T* row = in + p * rows * s.in_head;
-            if (v.has_a) xa[p] = ld_stream(row + v.a);
-            if (v.has_b) xb[p] = ld_stream(row + v.b);
+        for (int p = 0; p < N; ++p) {
+            xa[p] = xb[p] = make_uint4(0, 0, 0, 0);
+            if (real && first + p * rows < s.heads) {  // the same for all lanes; a row behind the last is the last
+                const T* row = in + min(head + p * rows, s.heads - 1) * s.in_head;
+                if (v.has_a()) xa[p] = ld_stream(row + v.a);
+                if (v.has_b()) xb[p] = ld_stream(row + v.b);
+            }
         }
     }
+    const T* weight = static_cast<const T*>(s.weight);
     Place place{};
     if (APPEND && token < a.total) place = find_place(a, token, lane);
+    if (APPEND && !a.rope.positions) position = place.position;
     float* table = reinterpret_cast<float*>(tables) + nth * 2 * a.rope.pairs;
-    if (a.rope.pairs) {
-        if (token < a.total) {
-            const int64_t position = APPEND && !a.rope.positions ? place.position : position_at(a.rope, batch, at);
-            fill_turns(table, a.rope, a.rope.pairs, position, a.rope.direction, share * 32 + lane, warps * 32);
+    if (token < a.total) {
+        for (int p = mine; p < a.rope.pairs; p += warps * 32) {
+            if (p != mine) rate = a.rope.rates[p];
+            const float2 cs = turn_of(rate, position, a.rope.magnitude, a.rope.direction);
+            table[p] = cs.x;
+            table[a.rope.pairs + p] = cs.y;
         }
-        __syncthreads();
     }
+    const float mean_of = 1.f / (FULL ? 2 * W * GT : a.dim);
+    // A single row's norm does not wait for the angles (2% of a decode step); of
+    // four rows it would be computed from values that are unpacked once more (4%
+    // slower at 16384 tokens of 72 heads).
+    float rstd[N] = {};
+    const auto norms = [&] {
+#pragma unroll
+        for (int p = 0; p < N; ++p) rstd[p] = rstd_of<T, INTER>(xa[p], xb[p], G, mean_of, a.eps);
+    };
+    if (N == 1 && weight) norms();
+    if (a.rope.pairs) __syncthreads();
     if (!real || (APPEND && (!place.used || (s.cache && !place.stored)))) return;
-    LaneTurns<W, INTER> t;
-    if (pairs) t.read(table, pairs, v);
-    const bool norm = s.weight != nullptr;
-    uint4 wa = make_uint4(0, 0, 0, 0), wb = wa;
-    if (norm) {
-        if (v.has_a) wa = ld_param(static_cast<const T*>(s.weight) + v.a);
-        if (v.has_b) wb = ld_param(static_cast<const T*>(s.weight) + v.b);
-    }
-    const float mean_of = 1.f / a.dim;
+    const bool half = N > 2 && first + 2 * rows >= s.heads;  // of the share's rows at most
+    T* out = static_cast<T*>(s.out);
+    if (APPEND && s.cache) {
+        const int64_t cell = place.page * s.out_batch + place.slot * s.out_token;
+        if (a.format != kCacheSame) {
+            LaneFactors<W, INTER, FULL> f;
+            f.read(weight, table, pairs, v);
+            if (N > 1 && weight) norms();
+            const bool int8 = a.format == kCacheInt8;
+            const int64_t scales = place.page * s.scale_page + place.slot * s.scale_slot;
 #pragma unroll
-    for (int p = 0; p < kPasses; ++p) {
-        if (p >= passes) break;
-        const bool here = head + p * rows < s.heads;
-        float2 fa[P], fb[P];
-        Elem<T>::unpack(xa[p], fa);
-        Elem<T>::unpack(xb[p], fb);
-        if (norm) {
-            float2 ss = make_float2(0.f, 0.f);
-#pragma unroll
-            for (int i = 0; i < P; ++i) {
-                ss = __ffma2_rn(fa[i], fa[i], ss);
-                ss = __ffma2_rn(fb[i], fb[i], ss);
-            }
-            const float r = rsqrtf(sum_lanes(ss.x + ss.y, G) * mean_of + a.eps);
-            const float2 rstd = make_float2(r, r);
-            float2 ga[P], gb[P];
-            Elem<T>::unpack(wa, ga);
-            Elem<T>::unpack(wb, gb);
-#pragma unroll
-            for (int i = 0; i < P; ++i) {
-                fa[i] = __fmul2_rn(__fmul2_rn(fa[i], rstd), ga[i]);
-                fb[i] = __fmul2_rn(__fmul2_rn(fb[i], rstd), gb[i]);
-            }
-        }
-        if (pairs) t.turn(fa, fb, v);
-        if (APPEND && s.cache) {
-            const int64_t row = place.page * s.out_batch + place.slot * s.out_token + (head + p * rows) * s.out_head;
-            if (a.format != kCacheSame) {
+            for (int p = 0; p < N; ++p) {
+                if (first + p * rows >= s.heads) break;
+                float2 x[P], y[P];
+                if (weight) turn_row<T, INTER, FULL, true, P>(xa[p], xb[p], rstd[p], f, x, y);
+                else turn_row<T, INTER, FULL, false, P>(xa[p], xb[p], rstd[p], f, x, y);
                 uint32_t top = 0;
 #pragma unroll
-                for (int i = 0; i < P; ++i) top = top_of(top_of(top, fa[i]), fb[i]);
+                for (int i = 0; i < P; ++i) top = top_of(top_of(top, x[i]), y[i]);
 #pragma unroll
                 for (int off = G >> 1; off > 0; off >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, off));
-                const bool int8 = a.format == kCacheInt8, fine = finite_bits(top);
+                const bool fine = finite_bits(top), here = head + p * rows < s.heads;
                 const float scale = row_scale(top, int8), inverse = __fdiv_rn(1.f, scale);
-                uint8_t* out = static_cast<uint8_t*>(s.out) + row;
-                if (here && v.has_a) store_quantized<W>(out + v.a, fa, scale, inverse, fine, int8);
-                if (here && v.has_b) store_quantized<W>(out + v.b, fb, scale, inverse, fine, int8);
-                if (here && j == 0) s.scale[place.page * s.scale_page + place.slot * s.scale_slot + (head + p * rows) * s.scale_head] = scale;
-            } else {
-                T* out = static_cast<T*>(s.out) + row;
-                if (here && v.has_a) *reinterpret_cast<uint4*>(out + v.a) = norm || pairs ? Elem<T>::pack(fa) : xa[p];
-                if (here && v.has_b) *reinterpret_cast<uint4*>(out + v.b) = norm || pairs ? Elem<T>::pack(fb) : xb[p];
+                float fa[W], fb[W];
+                in_order<W, INTER>(x, y, fa, fb);
+                uint8_t* q = static_cast<uint8_t*>(s.out) + cell + (head + p * rows) * s.out_head;
+                if (here && v.has_a()) store_quantized<W>(q + v.a, fa, scale, inverse, fine, int8);
+                if (here && v.has_b()) store_quantized<W>(q + v.b, fb, scale, inverse, fine, int8);
+                if (here && j == 0) s.scale[scales + (head + p * rows) * s.scale_head] = scale;
             }
+            return;
+        }
+        out += cell;
+    } else {
+        out += batch * s.out_batch + at * s.out_token;
+    }
+    if (weight || pairs) {  // else the rows go as they are
+        LaneFactors<W, INTER, FULL> f;
+        f.read(weight, table, pairs, v);
+        if (weight) {
+            if (half) turn_rows<T, INTER, FULL, true, (N + 1) / 2>(xa, xb, rstd, f, G, mean_of, a.eps);
+            else turn_rows<T, INTER, FULL, true, N>(xa, xb, rstd, f, G, mean_of, a.eps);
         } else {
-            T* out = static_cast<T*>(s.out) + batch * s.out_batch + at * s.out_token + (head + p * rows) * s.out_head;
-            if (here && v.has_a) st_stream(out + v.a, Elem<T>::pack(fa));
-            if (here && v.has_b) st_stream(out + v.b, Elem<T>::pack(fb));
+            turn_rows<T, INTER, FULL, false, N>(xa, xb, rstd, f, G, mean_of, a.eps);
+        }
+    }
+#pragma unroll
+    for (int p = 0; p < N; ++p) {
+        if (head + p * rows < s.heads) {
+            T* row = out + (head + p * rows) * s.out_head;
+            if (v.has_a()) st_stream(row + v.a, xa[p]);
+            if (v.has_b()) st_stream(row + v.b, xb[p]);
         }
     }
 }
@@ -263,16 +315,16 @@ __global__ void __launch_bounds__(kWarps * 32) heads_elements(const __grid_const
     }
     const int dim = a.dim, pairs = s.rotate ? a.rope.pairs : 0;
     float* row = staged + (threadIdx.x >> 5) * dim;
-    const T* in = row_in<T>(s, batch, at, head);
+    const T* in = static_cast<const T*>(s.in) + batch * s.in_batch + at * s.in_token + head * s.in_head;
     float ss = 0.f;
     for (int i = lane; i < dim; i += 32) {
-        const float x = Elem<T>::load(in + i);
+        const float x = load_element(in + i);
         row[i] = x;
         ss += x * x;
     }
     if (s.weight) {
         const float rstd = rsqrtf(sum_lanes(ss, 32) * (1.f / dim) + a.eps);
-        for (int i = lane; i < dim; i += 32) row[i] *= rstd * Elem<T>::load(static_cast<const T*>(s.weight) + i);
+        for (int i = lane; i < dim; i += 32) row[i] *= rstd * load_element(static_cast<const T*>(s.weight) + i);
     }
     __syncwarp();
     if (pairs) {
@@ -281,8 +333,8 @@ __global__ void __launch_bounds__(kWarps * 32) heads_elements(const __grid_const
             const float2 t = turn_of(a.rope.rates[p], position, a.rope.magnitude, a.rope.direction);
             const int ia = a.rope.interleaved ? 2 * p : p, ib = a.rope.interleaved ? 2 * p + 1 : p + pairs;
             const float x = row[ia], y = row[ib];
-            row[ia] = x * t.x - y * t.y;
-            row[ib] = y * t.x + x * t.y;
+            row[ia] = fmaf(y, -t.y, __fmul_rn(x, t.x));  // rounded as in the vector kernel
+            row[ib] = fmaf(x, t.y, __fmul_rn(y, t.x));
         }
         __syncwarp();
     }
@@ -300,13 +352,13 @@ __global__ void __launch_bounds__(kWarps * 32) heads_elements(const __grid_const
         } else {
             T* out = static_cast<T*>(s.out) + first;
             for (int i = lane; i < dim; i += 32) {
-                if (s.weight || pairs) Elem<T>::store(out + i, row[i]);
+                if (s.weight || pairs) store_element(out + i, row[i]);
                 else out[i] = in[i];
             }
         }
     } else {
         T* out = static_cast<T*>(s.out) + batch * s.out_batch + at * s.out_token + head * s.out_head;
-        for (int i = lane; i < dim; i += 32) Elem<T>::store(out + i, row[i]);
+        for (int i = lane; i < dim; i += 32) store_element(out + i, row[i]);
     }
 }
 
@@ -314,9 +366,10 @@ bool fits(const void* p, int64_t s0, int64_t s1, int64_t s2, int elements, int b
     return (reinterpret_cast<uintptr_t>(p) % bytes) == 0 && s0 % elements == 0 && s1 % elements == 0 && s2 % elements == 0;
 }
 
-// Whether every row falls on whole 16-byte vectors (8-bit rows: on W bytes).
+// Whether every row falls on whole 16-byte vectors (8-bit rows: on W bytes), each
+// with all its pairs turned or none.
 bool whole_vectors(const HeadsArgs& a, int W) {
-    if (a.dim % W || (a.dim / W + 1) / 2 > 32 || (!a.rope.interleaved && a.rope.pairs % W)) return false;
+    if (a.dim % W || (a.dim / W + 1) / 2 > 32 || a.rope.pairs % (a.rope.interleaved ? W / 2 : W)) return false;
     for (int i = 0; i < a.segments; ++i) {
         const HeadSegment& s = a.seg[i];
         if (!fits(s.in, s.in_batch, s.in_token, s.in_head, W, 16)) return false;
@@ -326,18 +379,24 @@ bool whole_vectors(const HeadsArgs& a, int W) {
     return true;
 }
 
+template <typename T, bool INTER, bool APPEND, int GT>
+cudaError_t launch_rows(const HeadsArgs& a, int passes, int G, dim3 grid, dim3 block, size_t smem, cudaStream_t st) {
+    return passes == 1 ? launch_with_pdl(heads_rows<T, INTER, APPEND, GT, 1>, grid, block, smem, st, a, G)
+                       : launch_with_pdl(heads_rows<T, INTER, APPEND, GT, 4>, grid, block, smem, st, a, G);
+}
+
 template <typename T, bool INTER, bool APPEND>
-cudaError_t launch_lanes(const HeadsArgs& a, int G, dim3 grid, dim3 block, size_t smem, cudaStream_t st) {
-    switch (G) {  // the common heads: 128 elements, 256 (bf16) and 64 (fp32)
-        case 8: return launch_with_pdl(heads_rows<T, INTER, APPEND, 8>, grid, block, smem, st, a, G);
-        case 16: return launch_with_pdl(heads_rows<T, INTER, APPEND, 16>, grid, block, smem, st, a, G);
-        default: return launch_with_pdl(heads_rows<T, INTER, APPEND, 0>, grid, block, smem, st, a, G);
-    }
+cudaError_t launch_lanes(const HeadsArgs& a, int passes, int G, dim3 grid, dim3 block, size_t smem, cudaStream_t st) {
+    const bool full = a.dim == 2 * Elem<T, INTER>::W * G;
+    if (full && G == 8) return launch_rows<T, INTER, APPEND, 8>(a, passes, G, grid, block, smem, st);
+    if (full && G == 16) return launch_rows<T, INTER, APPEND, 16>(a, passes, G, grid, block, smem, st);
+    return launch_rows<T, INTER, APPEND, 0>(a, passes, G, grid, block, smem, st);
 }
 
 template <typename T, bool APPEND>
 cudaError_t launch(HeadsArgs a, int sms, cudaStream_t st) {
-    constexpr int W = Elem<T>::W;
+    constexpr int W = Elem<T, false>::W;
+    if (APPEND) a.by_page = Divider(a.page_size);
     if (!whole_vectors(a, W)) {
         a.chunks = 0;
         for (int i = 0; i < a.segments; ++i) a.chunks += a.seg[i].heads;
@@ -346,23 +405,27 @@ cudaError_t launch(HeadsArgs a, int sms, cudaStream_t st) {
                                kWarps * a.dim * sizeof(float), st, a);
     }
     const int G = lanes_for((a.dim / W + 1) / 2), rows = 32 / G;
-    // As many rows to a share as leave every SM its warps: each pass more
-    // spreads what a warp does before its rows over more of them.
-    for (a.passes = kPasses;; a.passes /= 2) {
+    // Four rows of a group to a share where that leaves every SM its warps: they
+    // are in flight together and spread what a warp does before them.
+    int passes = 4;
+    for (;; passes = 1) {
         a.chunks = 0;
         for (int i = 0; i < a.segments; ++i) {
-            a.seg[i].chunks = (a.seg[i].heads + rows * a.passes - 1) / (rows * a.passes);
+            a.seg[i].chunks = (a.seg[i].heads + rows * passes - 1) / (rows * passes);
             a.chunks += a.seg[i].chunks;
         }
-        if (a.passes == 1 || static_cast<int64_t>(a.total) * a.chunks >= 64 * sms) break;
+        if (passes == 1 || static_cast<int64_t>(a.total) * a.chunks >= kManyShares * sms) break;
     }
     // a warp to each share, in several CTAs where a token has many; tokens of few shares side by side in a CTA of four warps or more
     a.turns = (a.chunks + kMaxWarps - 1) / kMaxWarps;
     const int warps = (a.chunks + a.turns - 1) / a.turns;
-    a.per_cta = warps >= 4 ? 1 : 4 / warps;
+    a.per_cta = warps >= 4 || a.turns > 1 ? 1 : 4 / warps;
+    a.by_turns = Divider(a.turns);
+    a.by_tokens = Divider(a.tokens);
     const dim3 grid((a.total + a.per_cta - 1) / a.per_cta * a.turns), block(warps * a.per_cta * 32);
     const size_t smem = a.per_cta * a.rope.pairs * sizeof(float2);
-    return a.rope.interleaved ? launch_lanes<T, true, APPEND>(a, G, grid, block, smem, st) : launch_lanes<T, false, APPEND>(a, G, grid, block, smem, st);
+    return a.rope.interleaved ? launch_lanes<T, true, APPEND>(a, passes, G, grid, block, smem, st)
+                              : launch_lanes<T, false, APPEND>(a, passes, G, grid, block, smem, st);
 }
 
 }  // namespace

@@ -14,6 +14,7 @@
 // stands between a copy and its use.  A CTA's sums go to the workspace, and a
 // second launch adds them up: every sum has a fixed order.
 #include <algorithm>
+#include <cstdlib>
 
 #include "heads.cuh"
 
@@ -43,137 +44,178 @@ __device__ __forceinline__ void leave_partials(const float* sums, float* out, in
     }
 }
 
-template <typename T, bool INTER>
-__global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) heads_grad_rows(const __grid_constant__ HeadsGradArgs a, int G) {
-    constexpr int W = Elem<T>::W;
-    extern __shared__ uint4 ring[];  // [kStages][4][threads], then the turns
+// A row of one of the walk's tensors, for the lane that holds it: `step` further
+// with every pass of a token.
+template <typename T>
+struct RowPointer {
+    T* p;
+    int64_t step, next;  // to the next pass, and from behind a token's last pass to the next token's first
+    __device__ __forceinline__ RowPointer(void* base, int64_t batch_stride, int64_t token_stride, int64_t head_stride, uint32_t batch, uint32_t token,
+                                          int pass, int rows, int lane_row, int per_token)
+        : step(rows * head_stride), next(token_stride - per_token * step) {
+        p = static_cast<T*>(base) + batch * batch_stride + token * token_stride + (pass * rows + lane_row) * head_stride;
+    }
+};
+
+template <typename T, bool INTER, int GT>
+__global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) heads_grad_rows(const __grid_constant__ HeadsGradArgs a, int lanes) {
+    constexpr int W = Elem<T, INTER>::W, P = W / 2;
+    constexpr bool FULL = GT != 0;
+    const int G = FULL ? GT : lanes;
+    constexpr int kSlot = 4 * kWarps * 32;  // vectors of a stage
+    extern __shared__ uint4 ring[];         // [kStages][4][threads], then the turns
     grid_dep_wait();
     grid_dep_release();
     const int lane = threadIdx.x & 31, warp_in = threadIdx.x >> 5;
     int cta = blockIdx.x, si = 0;
     if (cta >= a.seg[0].ctas) cta -= a.seg[0].ctas, si = 1;
     const HeadGradSegment& s = a.seg[si];
-    const int rows = 32 / G, j = lane & (G - 1), per_token = (s.heads + rows - 1) / rows;
+    const int rows = 32 / G, j = lane & (G - 1), lane_row = lane / G, per_token = (s.heads + rows - 1) / rows;
     const Stretch r = stretch_of(static_cast<int64_t>(a.total) * per_token, cta * kWarps + warp_in, s.ctas * kWarps);
     const int pairs = a.rope.pairs;
-    const LaneVectors<W, INTER> v(j, a.dim, pairs);
-    float* table = reinterpret_cast<float*>(ring + kStages * 4 * kWarps * 32) + warp_in * 2 * pairs;
+    const LaneVectors<W, INTER, FULL> v(j, FULL ? 2 * W * GT : a.dim, pairs);
+    float* table = reinterpret_cast<float*>(ring + kStages * kSlot) + warp_in * 2 * pairs;
 
     uint4 wa = make_uint4(0, 0, 0, 0), wb = wa;
-    if (v.has_a) wa = ld_param(static_cast<const T*>(s.weight) + v.a);
-    if (v.has_b) wb = ld_param(static_cast<const T*>(s.weight) + v.b);
-    float2 da[W / 2], db[W / 2];
+    if (v.has_a()) wa = ld_param(static_cast<const T*>(s.weight) + v.a);
+    if (v.has_b()) wb = ld_param(static_cast<const T*>(s.weight) + v.b);
+    float2 dwx[P], dwy[P];
 #pragma unroll
-    for (int i = 0; i < W / 2; ++i) da[i] = db[i] = make_float2(0.f, 0.f);
+    for (int i = 0; i < P; ++i) dwx[i] = dwy[i] = make_float2(0.f, 0.f);
 
     if (r.first < r.end) {
-        const float mean_of = 1.f / a.dim;
+        const float mean_of = 1.f / (FULL ? 2 * W * GT : a.dim);
         uint32_t token = static_cast<uint32_t>(r.first / per_token);
-        int pass = static_cast<int>(r.first - static_cast<int64_t>(token) * per_token);
-        // the pass that is copied next
-        uint32_t next_token = token;
-        int next_pass = pass;
-        int64_t left = r.end - r.first;
+        int pass = static_cast<int>(r.first - static_cast<int64_t>(token) * per_token), left = static_cast<int>(r.end - r.first);
+        uint32_t batch = divide(token, a.by_tokens), at = token - batch * a.tokens;
+        // the rows that are copied next, kStages - 1 passes ahead
+        RowPointer<const T> y(const_cast<void*>(s.dy), s.dy_batch, s.dy_token, s.dy_head, batch, at, pass, rows, lane_row, per_token);
+        RowPointer<const T> x(const_cast<void*>(s.x), s.x_batch, s.x_token, s.x_head, batch, at, pass, rows, lane_row, per_token);
+        int ahead_head = pass * rows + lane_row, ahead_pass = pass, ahead_left = left;
+        uint32_t ahead_at = at;
         const auto copy = [&](int stage) {
-            if (left > 0) {
-                const uint32_t batch = next_token / a.tokens, at = next_token - batch * a.tokens;
-                const int head = next_pass * rows + lane / G;
-                const bool here = head < s.heads;
-                const T* y = static_cast<const T*>(s.dy) + batch * s.dy_batch + at * s.dy_token + (here ? head * s.dy_head : 0);
-                const T* x = static_cast<const T*>(s.x) + batch * s.x_batch + at * s.x_token + (here ? head * s.x_head : 0);
-                uint4* to = ring + stage * 4 * kWarps * 32 + threadIdx.x;
-                const bool ha = here && v.has_a, hb = here && v.has_b;
-                copy16(to, y + (ha ? v.a : 0), ha);
-                copy16(to + kWarps * 32, y + (hb ? v.b : 0), hb);
-                copy16(to + 2 * kWarps * 32, x + (ha ? v.a : 0), ha);
-                copy16(to + 3 * kWarps * 32, x + (hb ? v.b : 0), hb);
-                if (++next_pass == per_token) next_pass = 0, ++next_token;
-                --left;
+            if (ahead_left > 0) {
+                const bool here = ahead_head < s.heads;
+                uint4* to = ring + stage * kSlot + threadIdx.x;
+                const T* yp = here ? y.p : static_cast<const T*>(s.dy);
+                const T* xp = here ? x.p : static_cast<const T*>(s.x);
+                const bool ha = here && v.has_a(), hb = here && v.has_b();
+                copy16(to, yp + (ha ? v.a : 0), ha);
+                copy16(to + kWarps * 32, yp + (hb ? v.b : 0), hb);
+                copy16(to + 2 * kWarps * 32, xp + (ha ? v.a : 0), ha);
+                copy16(to + 3 * kWarps * 32, xp + (hb ? v.b : 0), hb);
+                y.p += y.step, x.p += x.step, ahead_head += rows;
+                if (++ahead_pass == per_token) {
+                    ahead_pass = 0, ahead_head = lane_row;
+                    y.p += y.next, x.p += x.next;
+                    if (++ahead_at == static_cast<uint32_t>(a.tokens)) {
+                        ahead_at = 0;
+                        y.p += s.dy_batch - a.tokens * s.dy_token, x.p += s.x_batch - a.tokens * s.x_token;
+                    }
+                }
+                --ahead_left;
             }
             copies_commit();  // a group for every stage, empty ones behind the last pass
         };
 #pragma unroll
         for (int i = 0; i < kStages - 1; ++i) copy(i);
-        int64_t position = pairs ? position_at(a.rope, token / a.tokens, token % a.tokens) : 0;
-        bool fresh = true;
-        LaneTurns<W, INTER> t;
+        RowPointer<T> dx(s.dx, s.dx_batch, s.dx_token, s.dx_head, batch, at, pass, rows, lane_row, per_token);
+        int64_t position = pairs ? position_at(a.rope, batch, at) : 0;
         int stage = 0;
-        for (int64_t p = r.first; p < r.end; ++p) {
-            if (fresh && pairs) {
+        while (left > 0) {  // a token
+            float2 c[P], sn[P];
+            if (pairs) {
                 __syncwarp();
-                fill_turns(table, a.rope, pairs, position, -1.f, lane, 32);
+                fill_turns(table, a.rope, pairs, position, 1.f, lane, 32);
                 __syncwarp();
-                t.read(table, pairs, v);
+                read_turns<W, INTER, FULL>(table, pairs, v, c, sn);
             }
-            const uint32_t batch = token / a.tokens, at = token - batch * a.tokens;
-            const int head = pass * rows + lane / G;
-            fresh = ++pass == per_token;
-            if (fresh) {
-                pass = 0, ++token;
-                if (pairs && p + 1 < r.end) position = position_at(a.rope, token / a.tokens, token % a.tokens);
-            }
-            copies_wait<kStages - 2>();
-            const uint4* from = ring + stage * 4 * kWarps * 32 + threadIdx.x;
-            float2 ga[W / 2], gb[W / 2], xa[W / 2], xb[W / 2], fa[W / 2], fb[W / 2];
-            Elem<T>::unpack(from[0], ga);
-            Elem<T>::unpack(from[kWarps * 32], gb);
-            Elem<T>::unpack(from[2 * kWarps * 32], xa);
-            Elem<T>::unpack(from[3 * kWarps * 32], xb);
-            // into the stage before, whose rows are done with
-            copy(stage ? stage - 1 : kStages - 1);
-            stage = stage == kStages - 1 ? 0 : stage + 1;
-            if (pairs) t.turn(ga, gb, v);
-            Elem<T>::unpack(wa, fa);
-            Elem<T>::unpack(wb, fb);
-            float2 ss2 = make_float2(0.f, 0.f), dot2 = ss2;
+            const int passes = min(left, per_token - pass);
+            left -= passes;
+            int head = pass * rows + lane_row;
+            if (++at == static_cast<uint32_t>(a.tokens)) at = 0, ++batch;
+            if (pairs && left > 0) position = position_at(a.rope, batch, at);  // the next token's, on its way meanwhile
+            for (int p = 0; p < passes; ++p) {
+                copies_wait<kStages - 2>();
+                const uint4* from = ring + stage * kSlot + threadIdx.x;
+                float2 gx[P], gy[P], xx[P], xy[P], fx[P], fy[P];
+                Elem<T, INTER>::unpack(from[0], from[kWarps * 32], gx, gy);
+                Elem<T, INTER>::unpack(from[2 * kWarps * 32], from[3 * kWarps * 32], xx, xy);
+                // into the stage before, whose rows are done with
+                copy(stage ? stage - 1 : kStages - 1);
+                stage = stage == kStages - 1 ? 0 : stage + 1;
+                if (pairs) {  // turned back
 #pragma unroll
-            for (int i = 0; i < W / 2; ++i) {
-                ss2 = __ffma2_rn(xa[i], xa[i], ss2);
-                ss2 = __ffma2_rn(xb[i], xb[i], ss2);
-                fa[i] = __fmul2_rn(fa[i], ga[i]);
-                fb[i] = __fmul2_rn(fb[i], gb[i]);
-                dot2 = __ffma2_rn(fa[i], xa[i], dot2);
-                dot2 = __ffma2_rn(fb[i], xb[i], dot2);
-            }
-            float ss = ss2.x + ss2.y, dot = dot2.x + dot2.y;
-            for (int off = G >> 1; off > 0; off >>= 1) {
-                ss += __shfl_xor_sync(0xFFFFFFFFu, ss, off);
-                dot += __shfl_xor_sync(0xFFFFFFFFu, dot, off);
-            }
-            const float rs = rsqrtf(ss * mean_of + a.eps), m = -dot * rs * mean_of;
-            const float2 rstd = make_float2(rs, rs), mean = make_float2(m, m);
+                    for (int h = 0; h < 2; ++h) {
+                        if (h ? v.turn_b : v.turn_a) {
 #pragma unroll
-            for (int i = 0; i < W / 2; ++i) {
-                const float2 na = __fmul2_rn(xa[i], rstd), nb = __fmul2_rn(xb[i], rstd);
-                da[i] = __ffma2_rn(ga[i], na, da[i]);
-                db[i] = __ffma2_rn(gb[i], nb, db[i]);
-                fa[i] = __fmul2_rn(rstd, __ffma2_rn(na, mean, fa[i]));
-                fb[i] = __fmul2_rn(rstd, __ffma2_rn(nb, mean, fb[i]));
+                            for (int i = h * P / 2; i < (h + 1) * P / 2; ++i) {
+                                const float2 u = gx[i], t = __fmul2_rn(u, sn[i]);
+                                gx[i] = __ffma2_rn(gy[i], sn[i], __fmul2_rn(u, c[i]));
+                                gy[i] = __ffma2_rn(gy[i], c[i], make_float2(-t.x, -t.y));
+                            }
+                        }
+                    }
+                }
+                Elem<T, INTER>::unpack(wa, wb, fx, fy);
+                float2 ss2 = make_float2(0.f, 0.f), dot2 = ss2;
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    ss2 = __ffma2_rn(xx[i], xx[i], ss2);
+                    ss2 = __ffma2_rn(xy[i], xy[i], ss2);
+                    fx[i] = __fmul2_rn(fx[i], gx[i]);
+                    fy[i] = __fmul2_rn(fy[i], gy[i]);
+                    dot2 = __ffma2_rn(fx[i], xx[i], dot2);
+                    dot2 = __ffma2_rn(fy[i], xy[i], dot2);
+                }
+                float ss = ss2.x + ss2.y, dot = dot2.x + dot2.y;
+#pragma unroll
+                for (int off = G >> 1; off > 0; off >>= 1) {
+                    ss += __shfl_xor_sync(0xFFFFFFFFu, ss, off);
+                    dot += __shfl_xor_sync(0xFFFFFFFFu, dot, off);
+                }
+                const float rs = rsqrtf(ss * mean_of + a.eps), m = -dot * rs * mean_of;
+                const float2 rstd = make_float2(rs, rs), mean = make_float2(m, m);
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    const float2 nx = __fmul2_rn(xx[i], rstd), ny = __fmul2_rn(xy[i], rstd);
+                    dwx[i] = __ffma2_rn(gx[i], nx, dwx[i]);
+                    dwy[i] = __ffma2_rn(gy[i], ny, dwy[i]);
+                    fx[i] = __fmul2_rn(rstd, __ffma2_rn(nx, mean, fx[i]));
+                    fy[i] = __fmul2_rn(rstd, __ffma2_rn(ny, mean, fy[i]));
+                }
+                if (head < s.heads) {
+                    uint4 oa, ob;
+                    Elem<T, INTER>::pack(fx, fy, oa, ob);
+                    if (v.has_a()) st_stream(dx.p + v.a, oa);
+                    if (v.has_b()) st_stream(dx.p + v.b, ob);
+                }
+                dx.p += dx.step, head += rows;
             }
-            if (head < s.heads) {
-                T* dx = static_cast<T*>(s.dx) + batch * s.dx_batch + at * s.dx_token + head * s.dx_head;
-                if (v.has_a) st_stream(dx + v.a, Elem<T>::pack(fa));
-                if (v.has_b) st_stream(dx + v.b, Elem<T>::pack(fb));
-            }
+            pass = 0;
+            dx.p += dx.next;
+            if (at == 0) dx.p += s.dx_batch - a.tokens * s.dx_token;
         }
         copies_wait<0>();
     }
     for (int off = G; off < 32; off <<= 1) {
 #pragma unroll
-        for (int i = 0; i < W / 2; ++i) {
-            da[i].x += __shfl_xor_sync(0xFFFFFFFFu, da[i].x, off);
-            da[i].y += __shfl_xor_sync(0xFFFFFFFFu, da[i].y, off);
-            db[i].x += __shfl_xor_sync(0xFFFFFFFFu, db[i].x, off);
-            db[i].y += __shfl_xor_sync(0xFFFFFFFFu, db[i].y, off);
+        for (int i = 0; i < P; ++i) {
+            dwx[i].x += __shfl_xor_sync(0xFFFFFFFFu, dwx[i].x, off);
+            dwx[i].y += __shfl_xor_sync(0xFFFFFFFFu, dwx[i].y, off);
+            dwy[i].x += __shfl_xor_sync(0xFFFFFFFFu, dwy[i].x, off);
+            dwy[i].y += __shfl_xor_sync(0xFFFFFFFFu, dwy[i].y, off);
         }
     }
     __syncthreads();  // the ring is done with: the sums take its place
     float* sums = reinterpret_cast<float*>(ring);
     if (lane < G) {
+        float da[W], db[W];
+        in_order<W, INTER>(dwx, dwy, da, db);
 #pragma unroll
-        for (int i = 0; i < W / 2; ++i) {
-            if (v.has_a) *reinterpret_cast<float2*>(sums + warp_in * a.dim + v.a + 2 * i) = da[i];
-            if (v.has_b) *reinterpret_cast<float2*>(sums + warp_in * a.dim + v.b + 2 * i) = db[i];
+        for (int i = 0; i < W; ++i) {
+            if (v.has_a()) sums[warp_in * a.dim + v.a + i] = da[i];
+            if (v.has_b()) sums[warp_in * a.dim + v.b + i] = db[i];
         }
     }
     leave_partials(sums, a.partials + static_cast<int64_t>(blockIdx.x) * a.dim, a.dim);
@@ -197,16 +239,16 @@ __global__ void __launch_bounds__(kWarps * 32) heads_grad_elements(const __grid_
 #pragma unroll
     for (int i = 0; i < kPerLane; ++i) dw[i] = 0.f;
     for (int64_t p = r.first; p < r.end; ++p) {
-        const uint32_t token = static_cast<uint32_t>(p / s.heads), batch = token / a.tokens, at = token - batch * a.tokens;
+        const uint32_t token = static_cast<uint32_t>(p / s.heads), batch = divide(token, a.by_tokens), at = token - batch * a.tokens;
         const int head = static_cast<int>(p - static_cast<int64_t>(token) * s.heads);
         const T* y = static_cast<const T*>(s.dy) + batch * s.dy_batch + at * s.dy_token + head * s.dy_head;
         const T* x = static_cast<const T*>(s.x) + batch * s.x_batch + at * s.x_token + head * s.x_head;
         T* dx = static_cast<T*>(s.dx) + batch * s.dx_batch + at * s.dx_token + head * s.dx_head;
         __syncwarp();
-        for (int i = lane; i < dim; i += 32) g[i] = Elem<T>::load(y + i);
+        for (int i = lane; i < dim; i += 32) g[i] = load_element(y + i);
         __syncwarp();
         if (pairs) {
-            const int64_t position = position_at(a.rope, token / a.tokens, token % a.tokens);
+            const int64_t position = position_at(a.rope, batch, at);
             for (int q = lane; q < pairs; q += 32) {
                 const float2 t = turn_of(a.rope.rates[q], position, a.rope.magnitude, -1.f);
                 const int ia = a.rope.interleaved ? 2 * q : q, ib = a.rope.interleaved ? 2 * q + 1 : q + pairs;
@@ -218,9 +260,9 @@ __global__ void __launch_bounds__(kWarps * 32) heads_grad_elements(const __grid_
         }
         float ss = 0.f, dot = 0.f;
         for (int i = lane; i < dim; i += 32) {
-            const float xi = Elem<T>::load(x + i);
+            const float xi = load_element(x + i);
             ss += xi * xi;
-            dot += g[i] * Elem<T>::load(static_cast<const T*>(s.weight) + i) * xi;
+            dot += g[i] * load_element(static_cast<const T*>(s.weight) + i) * xi;
         }
         ss = sum_lanes(ss, 32);
         dot = sum_lanes(dot, 32);
@@ -229,9 +271,9 @@ __global__ void __launch_bounds__(kWarps * 32) heads_grad_elements(const __grid_
         for (int k = 0; k < kPerLane; ++k) {
             const int i = lane + 32 * k;
             if (i < dim) {
-                const float n = Elem<T>::load(x + i) * rstd;
+                const float n = load_element(x + i) * rstd;
                 dw[k] += g[i] * n;
-                Elem<T>::store(dx + i, rstd * (g[i] * Elem<T>::load(static_cast<const T*>(s.weight) + i) - n * mean));
+                store_element(dx + i, rstd * (g[i] * load_element(static_cast<const T*>(s.weight) + i) - n * mean));
             }
         }
     }
@@ -242,24 +284,42 @@ __global__ void __launch_bounds__(kWarps * 32) heads_grad_elements(const __grid_
     leave_partials(staged, a.partials + static_cast<int64_t>(blockIdx.x) * dim, dim);
 }
 
-// dweight[i] = sum of its segment's partials: 32 columns to a CTA, 32 warps
-// over the partials, then over the warps, in a fixed order.
-__global__ void __launch_bounds__(1024) heads_grad_sum(const __grid_constant__ HeadsGradArgs a) {
-    __shared__ float part[32][33];
+// dweight: the sum of a segment's partials, V columns to a CTA.  A thread adds up
+// every 256th partial, all of them on their way at once (at most three with
+// four CTAs to each of 192 SMs), then the warp its lanes' and the CTA its
+// warps', in a fixed order.  With 32 columns to a CTA of 32 warps the 608
+// partials of 128 columns took 9.6 us.
+constexpr int kSumThreads = 256;
+template <int V>
+__global__ void __launch_bounds__(kSumThreads) heads_grad_sum(const __grid_constant__ HeadsGradArgs a) {
+    __shared__ float part[kSumThreads / 32][V];
     grid_dep_wait();
     grid_dep_release();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, column = blockIdx.x * 32 + lane;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, column = blockIdx.x * V;
     const HeadGradSegment& s = a.seg[blockIdx.y];
     const float* from = a.partials + static_cast<int64_t>(blockIdx.y ? a.seg[0].ctas : 0) * a.dim + column;
-    float sum = 0.f;
-    if (column < a.dim) {
-#pragma unroll 8
-        for (int p = warp; p < s.ctas; p += 32) sum += __ldcg(from + static_cast<int64_t>(p) * a.dim);
+    float sum[V] = {};
+#pragma unroll 4
+    for (int p = threadIdx.x; p < s.ctas; p += kSumThreads) {
+        if constexpr (V == 4) {
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(from + static_cast<int64_t>(p) * a.dim));
+            sum[0] += v.x, sum[1] += v.y, sum[2] += v.z, sum[3] += v.w;
+        } else {
+            sum[0] += __ldcg(from + static_cast<int64_t>(p) * a.dim);
+        }
     }
-    part[warp][lane] = sum;
+    warp_sum<V>(sum);
+    if (lane == 0) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) part[warp][i] = sum[i];
+    }
     __syncthreads();
-    sum = sum_lanes(part[lane][warp], 32);
-    if (lane == 0 && blockIdx.x * 32 + warp < a.dim) s.dweight[blockIdx.x * 32 + warp] = sum;
+    if (threadIdx.x < V) {
+        float t = part[0][threadIdx.x];
+#pragma unroll
+        for (int w = 1; w < kSumThreads / 32; ++w) t += part[w][threadIdx.x];
+        s.dweight[column + threadIdx.x] = t;
+    }
 }
 
 bool fits(const void* p, int64_t s0, int64_t s1, int64_t s2, int W) {
@@ -267,7 +327,7 @@ bool fits(const void* p, int64_t s0, int64_t s1, int64_t s2, int W) {
 }
 
 bool whole_vectors(const HeadsGradArgs& a, int W) {
-    if (a.dim % W || (a.dim / W + 1) / 2 > 32 || (!a.rope.interleaved && a.rope.pairs % W)) return false;
+    if (a.dim % W || (a.dim / W + 1) / 2 > 32 || a.rope.pairs % (a.rope.interleaved ? W / 2 : W)) return false;
     for (int i = 0; i < a.segments; ++i) {
         const HeadGradSegment& s = a.seg[i];
         if (!fits(s.dx, s.dx_batch, s.dx_token, s.dx_head, W) || !fits(s.dy, s.dy_batch, s.dy_token, s.dy_head, W) ||
@@ -277,33 +337,49 @@ bool whole_vectors(const HeadsGradArgs& a, int W) {
     return true;
 }
 
+template <typename T, bool INTER>
+cudaError_t launch_lanes(const HeadsGradArgs& a, int G, dim3 grid, cudaStream_t st) {
+    const size_t smem = kStages * 4 * kWarps * 32 * sizeof(uint4) + kWarps * a.rope.pairs * sizeof(float2);
+    const bool full = a.dim == 2 * Elem<T, INTER>::W * G;
+    if (full && G == 8) return launch_with_pdl(heads_grad_rows<T, INTER, 8>, grid, dim3(kWarps * 32), smem, st, a, G);
+    if (full && G == 16) return launch_with_pdl(heads_grad_rows<T, INTER, 16>, grid, dim3(kWarps * 32), smem, st, a, G);
+    return launch_with_pdl(heads_grad_rows<T, INTER, 0>, grid, dim3(kWarps * 32), smem, st, a, G);
+}
+
 template <typename T>
 cudaError_t launch(HeadsGradArgs a, int sms, cudaStream_t st) {
-    constexpr int W = Elem<T>::W;
+    constexpr int W = Elem<T, false>::W;
     const bool vectors = whole_vectors(a, W);
     const int G = vectors ? lanes_for((a.dim / W + 1) / 2) : 32, rows = 32 / G;
-    // CTAs in proportion to the segments' passes, two passes to a warp at least
-    int64_t passes[2] = {0, 0};
-    for (int i = 0; i < a.segments; ++i) passes[i] = static_cast<int64_t>(a.total) * ((a.seg[i].heads + rows - 1) / rows);
-    const int64_t all = passes[0] + passes[1], most = static_cast<int64_t>(sms) * kCtasPerSm;
-    const int64_t ctas = std::max<int64_t>(a.segments, std::min(most, (all + 2 * kWarps - 1) / (2 * kWarps)));
+    a.by_tokens = Divider(a.tokens);
+    // CTAs in proportion to the segments' work, two passes to a warp at least.  A
+    // token's angles take as long as some passes.
+    const int setup = getenv("SETUP") ? atoi(getenv("SETUP")) : 2;
+    int64_t work[2] = {0, 0}, passes = 0;
+    for (int i = 0; i < a.segments; ++i) {
+        const int64_t per_token = (a.seg[i].heads + rows - 1) / rows;
+        passes += a.total * per_token;
+        work[i] = a.total * (per_token + (vectors && a.rope.pairs ? setup : 0));
+    }
+    const int64_t all = work[0] + work[1], most = static_cast<int64_t>(sms) * kCtasPerSm;
+    const int64_t ctas = std::max<int64_t>(a.segments, std::min(most, (passes + 2 * kWarps - 1) / (2 * kWarps)));
     a.seg[0].ctas = static_cast<int>(ctas);
     if (a.segments == 2) {
-        const int64_t share = all ? (ctas * passes[1] + all / 2) / all : 1;
+        const int64_t share = all ? (ctas * work[1] + all / 2) / all : 1;
         a.seg[1].ctas = static_cast<int>(std::max<int64_t>(1, std::min(ctas - 1, share)));
         a.seg[0].ctas -= a.seg[1].ctas;
     }
-    const dim3 grid(static_cast<unsigned>(ctas)), block(kWarps * 32);
+    const dim3 grid(static_cast<unsigned>(ctas));
     cudaError_t e;
     if (!vectors) {
-        e = launch_with_pdl(heads_grad_elements<T>, grid, block, kWarps * a.dim * sizeof(float), st, a);
+        e = launch_with_pdl(heads_grad_elements<T>, grid, dim3(kWarps * 32), kWarps * a.dim * sizeof(float), st, a);
     } else {
-        const size_t smem = kStages * 4 * kWarps * 32 * sizeof(uint4) + kWarps * a.rope.pairs * sizeof(float2);
-        e = a.rope.interleaved ? launch_with_pdl(heads_grad_rows<T, true>, grid, block, smem, st, a, G)
-                               : launch_with_pdl(heads_grad_rows<T, false>, grid, block, smem, st, a, G);
+        e = a.rope.interleaved ? launch_lanes<T, true>(a, G, grid, st) : launch_lanes<T, false>(a, G, grid, st);
     }
     if (e != cudaSuccess) return e;
-    return launch_with_pdl(heads_grad_sum, dim3((a.dim + 31) / 32, a.segments), dim3(1024), 0, st, a);
+    return a.dim % 4 || reinterpret_cast<uintptr_t>(a.partials) % 16
+               ? launch_with_pdl(heads_grad_sum<1>, dim3(a.dim, a.segments), dim3(kSumThreads), 0, st, a)
+               : launch_with_pdl(heads_grad_sum<4>, dim3(a.dim / 4, a.segments), dim3(kSumThreads), 0, st, a);
 }
 
 }  // namespace
