@@ -23,42 +23,77 @@ constexpr float kScaleMin = 0x1p-100f;
 
 __device__ __forceinline__ bool finite_bits(uint32_t b) { return (b & 0x7F800000u) != 0x7F800000u; }
 
-// The scale of a row whose largest |y| has the bits `top`; NaN where that is not finite.
-__device__ __forceinline__ float row_scale(uint32_t top, bool int8) {
-    return finite_bits(top) ? fmaxf(__fdiv_rn(__uint_as_float(top), int8 ? 127.f : 448.f), kScaleMin) : __uint_as_float(0x7FC00000u);
-}
-
-// y / scale in fp32, rounded once, without a division for each element: the
-// product with 1 / scale, corrected by its own remainder (P. Markstein,
-// "Computation of elementary functions on the IBM RISC System/6000 processor",
-// 1990).  Rows of 16-bit values often have quotients that lie exactly between
-// two 8-bit values; a product alone would miss these.  An infinite or NaN
-// `inverse` never gets here: such rows are stored as zeros.
-__device__ __forceinline__ float quotient(float y, float scale, float inverse) {
+// y / d rounded to fp32 once, given about 1 / d: the product with it, corrected
+// by its own remainder (P. Markstein, "Computation of elementary functions on
+// the IBM RISC System/6000 processor", 1990).  Rows of 16-bit values often have
+// quotients that lie exactly between two 8-bit values; a product alone would
+// miss these.
+__device__ __forceinline__ float quotient(float y, float d, float inverse) {
     const float q = y * inverse;
-    return fmaf(fmaf(-q, scale, y), inverse, q);
+    return fmaf(fmaf(-q, d, y), inverse, q);
+}
+__device__ __forceinline__ float about_inverse(float d) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
+    return r;
 }
 
-__device__ __forceinline__ uint32_t quant2(float y0, float y1, float scale, float inverse, bool fine, bool int8) {
-    const float a = fine ? quotient(y0, scale, inverse) : 0.f, b = fine ? quotient(y1, scale, inverse) : 0.f;
-    if (int8) return (static_cast<uint32_t>(__float2int_rn(a)) & 0xFF) | ((static_cast<uint32_t>(__float2int_rn(b)) & 0xFF) << 8);
+// The scale of a row whose largest |y| has the bits `top`; NaN where that is not finite.
+template <bool INT8>
+__device__ __forceinline__ float row_scale(uint32_t top) {
+    constexpr float most = INT8 ? 127.f : 448.f;
+    return finite_bits(top) ? fmaxf(quotient(__uint_as_float(top), most, 1.f / most), kScaleMin) : __uint_as_float(0x7FC00000u);
+}
+
+template <bool INT8>
+__device__ __forceinline__ uint32_t quant2(float y0, float y1, float scale, float inverse) {
+    const float a = quotient(y0, scale, inverse), b = quotient(y1, scale, inverse);
+    if constexpr (INT8) return (static_cast<uint32_t>(__float2int_rn(a)) & 0xFF) | ((static_cast<uint32_t>(__float2int_rn(b)) & 0xFF) << 8);
     uint16_t v;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(v) : "f"(b), "f"(a));
     return v;
 }
 
-template <int W>
-__device__ __forceinline__ void store_quantized(uint8_t* p, const float (&v)[W], float scale, float inverse, bool fine, bool int8) {
+template <bool INT8, int W>
+__device__ __forceinline__ void store_quantized(uint8_t* p, const float (&v)[W], float scale, float inverse) {
     uint32_t q[W / 4];
 #pragma unroll
     for (int i = 0; i < W / 4; ++i)
-        q[i] = quant2(v[4 * i], v[4 * i + 1], scale, inverse, fine, int8) | (quant2(v[4 * i + 2], v[4 * i + 3], scale, inverse, fine, int8) << 16);
+        q[i] = quant2<INT8>(v[4 * i], v[4 * i + 1], scale, inverse) | (quant2<INT8>(v[4 * i + 2], v[4 * i + 3], scale, inverse) << 16);
     if constexpr (W == 8) *reinterpret_cast<uint2*>(p) = make_uint2(q[0], q[1]);
     else *reinterpret_cast<uint32_t*>(p) = q[0];
 }
 
-__device__ __forceinline__ uint32_t top_of(uint32_t top, float2 v) {
-    return max(top, max(__float_as_uint(fabsf(v.x)), __float_as_uint(fabsf(v.y))));
+// The largest magnitude of three, a NaN standing above every number.
+__device__ __forceinline__ float largest(float a, float b, float c) {
+    float d;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// A row in 8 bits, and its scale.  All lanes of its group call this.
+template <bool INT8, bool INTER, bool FULL, int P>
+__device__ __forceinline__ void store_row_8(uint8_t* to, float* scale_to, float2 (&x)[P], float2 (&y)[P], int G, bool here, bool first_lane,
+                                            const LaneVectors<2 * P, INTER, FULL>& v) {
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < P; ++i) m = largest(largest(m, x[i].x, x[i].y), y[i].x, y[i].y);
+    uint32_t top = __float_as_uint(m) & 0x7FFFFFFFu;  // as integers: a NaN stands above every number here too
+#pragma unroll
+    for (int off = G >> 1; off > 0; off >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, off));
+    const float scale = row_scale<INT8>(top);
+    float inverse = about_inverse(scale);
+    if (!finite_bits(top)) {  // stored as zeros
+        inverse = 0.f;
+#pragma unroll
+        for (int i = 0; i < P; ++i) x[i] = y[i] = make_float2(0.f, 0.f);
+    }
+    float a[2 * P], b[2 * P];
+    in_order<2 * P, INTER>(x, y, a, b);
+    const float divisor = finite_bits(top) ? scale : 1.f;
+    if (here && v.has_a()) store_quantized<INT8>(to + v.a, a, divisor, inverse);
+    if (here && v.has_b()) store_quantized<INT8>(to + v.b, b, divisor, inverse);
+    if (here && first_lane) *scale_to = scale;
 }
 
 // Where a token of an append stands.
@@ -120,7 +155,7 @@ __device__ __forceinline__ Place find_place(const HeadsArgs& a, uint32_t token, 
     return place_in(a, token, seq, first, used ? past : -1);
 }
 
-constexpr int kMaxWarps = 5;  // per CTA
+constexpr int kMaxWarps = 3;  // per CTA
 constexpr int64_t kManyShares = 64;  // per SM
 
 // 1 over a row's root mean square.
@@ -168,7 +203,7 @@ __device__ __forceinline__ void turn_rows(uint4 (&a)[M], uint4 (&b)[M], const fl
 // that need them, while the rows are on their way.  N: the rows of a group in a
 // share.  GT: lanes of a group, each with both its vectors; 0: any.
 template <typename T, bool INTER, bool APPEND, int GT, int N>
-__global__ void __launch_bounds__(kMaxWarps * 32, 4) heads_rows(const __grid_constant__ HeadsArgs a, int lanes) {
+__global__ void __launch_bounds__(kMaxWarps * 32, 7) heads_rows(const __grid_constant__ HeadsArgs a, int lanes) {
     constexpr int W = Elem<T, INTER>::W, P = W / 2;
     constexpr bool FULL = GT != 0;
     const int G = FULL ? GT : lanes;
@@ -190,14 +225,17 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 4) heads_rows(const __grid_con
     const int pairs = s.rotate ? a.rope.pairs : 0;
     const LaneVectors<W, INTER, FULL> v(j, FULL ? 2 * W * GT : a.dim, pairs);
     const int first = chunk * N * rows, head = first + lane_row;
-    // what the angles need is asked for first: it is waited for before the rows are
+    // what the angles need; for a single row it is asked for first, as it is waited for first
     const int mine = share * 32 + lane;
     int64_t position = 0;
     uint64_t rate = 0;
-    if (a.rope.pairs && token < a.total) {
-        if (a.rope.positions) position = position_at(a.rope, batch, at);
-        if (mine < a.rope.pairs) rate = a.rope.rates[mine];
-    }
+    const auto ask = [&] {
+        if (a.rope.pairs && token < a.total) {
+            if (a.rope.positions) position = position_at(a.rope, batch, at);
+            if (mine < a.rope.pairs) rate = a.rope.rates[mine];
+        }
+    };
+    if (N == 1) ask();
     uint4 xa[N], xb[N];
     {
         const T* in = static_cast<const T*>(s.in) + batch * s.in_batch + at * s.in_token;
@@ -211,6 +249,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 4) heads_rows(const __grid_con
             }
         }
     }
+    if (N > 1) ask();
     const T* weight = static_cast<const T*>(s.weight);
     Place place{};
     if (APPEND && token < a.total) place = find_place(a, token, lane);
@@ -244,7 +283,6 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 4) heads_rows(const __grid_con
             LaneFactors<W, INTER, FULL> f;
             f.read(weight, table, pairs, v);
             if (N > 1 && weight) norms();
-            const bool int8 = a.format == kCacheInt8;
             const int64_t scales = place.page * s.scale_page + place.slot * s.scale_slot;
 #pragma unroll
             for (int p = 0; p < N; ++p) {
@@ -252,19 +290,11 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 4) heads_rows(const __grid_con
                 float2 x[P], y[P];
                 if (weight) turn_row<T, INTER, FULL, true, P>(xa[p], xb[p], rstd[p], f, x, y);
                 else turn_row<T, INTER, FULL, false, P>(xa[p], xb[p], rstd[p], f, x, y);
-                uint32_t top = 0;
-#pragma unroll
-                for (int i = 0; i < P; ++i) top = top_of(top_of(top, x[i]), y[i]);
-#pragma unroll
-                for (int off = G >> 1; off > 0; off >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, off));
-                const bool fine = finite_bits(top), here = head + p * rows < s.heads;
-                const float scale = row_scale(top, int8), inverse = __fdiv_rn(1.f, scale);
-                float fa[W], fb[W];
-                in_order<W, INTER>(x, y, fa, fb);
+                const bool here = head + p * rows < s.heads;
                 uint8_t* q = static_cast<uint8_t*>(s.out) + cell + (head + p * rows) * s.out_head;
-                if (here && v.has_a()) store_quantized<W>(q + v.a, fa, scale, inverse, fine, int8);
-                if (here && v.has_b()) store_quantized<W>(q + v.b, fb, scale, inverse, fine, int8);
-                if (here && j == 0) s.scale[scales + (head + p * rows) * s.scale_head] = scale;
+                float* scale = s.scale + scales + (head + p * rows) * s.scale_head;
+                if (a.format == kCacheInt8) store_row_8<true, INTER, FULL, P>(q, scale, x, y, G, here, j == 0, v);
+                else store_row_8<false, INTER, FULL, P>(q, scale, x, y, G, here, j == 0, v);
             }
             return;
         }
@@ -345,9 +375,12 @@ __global__ void __launch_bounds__(kWarps * 32) heads_elements(const __grid_const
             for (int i = lane; i < dim; i += 32) top = max(top, __float_as_uint(fabsf(row[i])));
             top = __reduce_max_sync(0xFFFFFFFFu, top);
             const bool int8 = a.format == kCacheInt8, fine = finite_bits(top);
-            const float scale = row_scale(top, int8), inverse = __fdiv_rn(1.f, scale);
+            const float scale = int8 ? row_scale<true>(top) : row_scale<false>(top), inverse = about_inverse(scale);
             uint8_t* out = static_cast<uint8_t*>(s.out) + first;
-            for (int i = lane; i < dim; i += 32) out[i] = static_cast<uint8_t>(quant2(row[i], 0.f, scale, inverse, fine, int8));
+            for (int i = lane; i < dim; i += 32) {
+                const uint32_t q = int8 ? quant2<true>(row[i], 0.f, scale, inverse) : quant2<false>(row[i], 0.f, scale, inverse);
+                out[i] = fine ? static_cast<uint8_t>(q) : 0;
+            }
             if (lane == 0) s.scale[place.page * s.scale_page + place.slot * s.scale_slot + head * s.scale_head] = scale;
         } else {
             T* out = static_cast<T*>(s.out) + first;
@@ -388,6 +421,7 @@ cudaError_t launch_rows(const HeadsArgs& a, int passes, int G, dim3 grid, dim3 b
 template <typename T, bool INTER, bool APPEND>
 cudaError_t launch_lanes(const HeadsArgs& a, int passes, int G, dim3 grid, dim3 block, size_t smem, cudaStream_t st) {
     const bool full = a.dim == 2 * Elem<T, INTER>::W * G;
+    if (full && G == 4) return launch_rows<T, INTER, APPEND, 4>(a, passes, G, grid, block, smem, st);
     if (full && G == 8) return launch_rows<T, INTER, APPEND, 8>(a, passes, G, grid, block, smem, st);
     if (full && G == 16) return launch_rows<T, INTER, APPEND, 16>(a, passes, G, grid, block, smem, st);
     return launch_rows<T, INTER, APPEND, 0>(a, passes, G, grid, block, smem, st);
@@ -416,10 +450,10 @@ cudaError_t launch(HeadsArgs a, int sms, cudaStream_t st) {
         }
         if (passes == 1 || static_cast<int64_t>(a.total) * a.chunks >= kManyShares * sms) break;
     }
-    // a warp to each share, in several CTAs where a token has many; tokens of few shares side by side in a CTA of four warps or more
+    // a warp to each share, in several CTAs where a token has many; tokens of one share side by side
     a.turns = (a.chunks + kMaxWarps - 1) / kMaxWarps;
     const int warps = (a.chunks + a.turns - 1) / a.turns;
-    a.per_cta = warps >= 4 || a.turns > 1 ? 1 : 4 / warps;
+    a.per_cta = a.turns == 1 ? kMaxWarps / warps : 1;
     a.by_turns = Divider(a.turns);
     a.by_tokens = Divider(a.tokens);
     const dim3 grid((a.total + a.per_cta - 1) / a.per_cta * a.turns), block(warps * a.per_cta * 32);

@@ -14,7 +14,6 @@
 // stands between a copy and its use.  A CTA's sums go to the workspace, and a
 // second launch adds them up: every sum has a fixed order.
 #include <algorithm>
-#include <cstdlib>
 
 #include "heads.cuh"
 
@@ -23,7 +22,13 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kCtasPerSm = 4;
-constexpr int kStages = 4;
+// What a token's angles take, in passes: the CTAs of 8 key heads (2 passes a
+// token) were the last ones where only passes counted (16384 tokens of 64 + 8
+// heads: 181 us, with 1 165, 2 165, 4 160, 6 161).
+constexpr int kTurnPasses = 4;
+// Two passes ahead: with one ahead 16384 tokens of 72 heads of 128 took 165 us for
+// 144, with three 157, with four CTAs to an SM (five: 220 us, its registers spill).
+constexpr int kStages = 3;
 
 // What a warp walks: passes [first, end) of its segment, `per_token` to a token.
 struct Stretch {
@@ -341,6 +346,7 @@ template <typename T, bool INTER>
 cudaError_t launch_lanes(const HeadsGradArgs& a, int G, dim3 grid, cudaStream_t st) {
     const size_t smem = kStages * 4 * kWarps * 32 * sizeof(uint4) + kWarps * a.rope.pairs * sizeof(float2);
     const bool full = a.dim == 2 * Elem<T, INTER>::W * G;
+    if (full && G == 4) return launch_with_pdl(heads_grad_rows<T, INTER, 4>, grid, dim3(kWarps * 32), smem, st, a, G);
     if (full && G == 8) return launch_with_pdl(heads_grad_rows<T, INTER, 8>, grid, dim3(kWarps * 32), smem, st, a, G);
     if (full && G == 16) return launch_with_pdl(heads_grad_rows<T, INTER, 16>, grid, dim3(kWarps * 32), smem, st, a, G);
     return launch_with_pdl(heads_grad_rows<T, INTER, 0>, grid, dim3(kWarps * 32), smem, st, a, G);
@@ -352,14 +358,12 @@ cudaError_t launch(HeadsGradArgs a, int sms, cudaStream_t st) {
     const bool vectors = whole_vectors(a, W);
     const int G = vectors ? lanes_for((a.dim / W + 1) / 2) : 32, rows = 32 / G;
     a.by_tokens = Divider(a.tokens);
-    // CTAs in proportion to the segments' work, two passes to a warp at least.  A
-    // token's angles take as long as some passes.
-    const int setup = getenv("SETUP") ? atoi(getenv("SETUP")) : 2;
+    // CTAs in proportion to the segments' work, two passes to a warp at least.
     int64_t work[2] = {0, 0}, passes = 0;
     for (int i = 0; i < a.segments; ++i) {
         const int64_t per_token = (a.seg[i].heads + rows - 1) / rows;
         passes += a.total * per_token;
-        work[i] = a.total * (per_token + (vectors && a.rope.pairs ? setup : 0));
+        work[i] = a.total * (per_token + (vectors && a.rope.pairs ? kTurnPasses : 0));
     }
     const int64_t all = work[0] + work[1], most = static_cast<int64_t>(sms) * kCtasPerSm;
     const int64_t ctas = std::max<int64_t>(a.segments, std::min(most, (passes + 2 * kWarps - 1) / (2 * kWarps)));

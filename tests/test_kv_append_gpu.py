@@ -102,6 +102,8 @@ STEPS = [  # past, new, page, query heads, key heads, head_dim, rotated
     ([4, 8], [3, 5], 16, 2, 2, 20, 10),
     ([4, 8], [3, 5], 16, 2, 2, 256, 0),
     ([4, 8, 1], [3, 5, 1], 16, 2, 3, 7, 6),
+    ([9, 500, 0], [2000, 1, 3003], 64, 17, 9, 64, 64),  # several rows to a warp
+    ([0, 5], [1500, 1011], 128, 40, 8, 128, 64),
 ]
 
 

@@ -31,7 +31,8 @@ def check(got, x, w, eps, positions, freq, magnitude=1.0, layout="half"):
 
 SHAPES = [(1, 1, 1, 1, 64, 64), (16, 1, 32, 8, 128, 128), (3, 5, 6, 2, 128, 64), (2, 33, 5, 1, 80, 80), (1, 257, 3, 3, 96, 48),
           (1, 40, 9, 3, 256, 256), (1, 3, 2, 2, 512, 512), (1, 19, 3, 1, 80, 20), (2, 11, 2, 1, 36, 30), (1, 9, 3, 2, 7, 6),
-          (1, 5, 2, 2, 8, 2), (1, 5, 2, 2, 8, 0), (1, 7, 3, 2, 1, 0), (2, 50, 4, 2, 64, 0), (1, 1500, 12, 12, 64, 64), (2, 700, 40, 8, 128, 128)]
+          (1, 5, 2, 2, 8, 2), (1, 5, 2, 2, 8, 0), (1, 7, 3, 2, 1, 0), (2, 50, 4, 2, 64, 0), (1, 1500, 12, 12, 64, 64), (2, 700, 40, 8, 128, 128), (1, 10007, 3, 1, 128, 64),
+          (2, 2503, 9, 7, 96, 96), (1, 1201, 72, 8, 128, 128), (5, 601, 33, 1, 256, 256), (1, 3001, 17, 1, 64, 0)]
 
 
 @pytest.mark.parametrize("layout", ["half", "interleaved"])
@@ -59,7 +60,7 @@ def test_forward_and_gradient(batch, tokens, hq, hk, dim, rot, kind, layout):
     # every sum has a fixed order
     assert all(torch.equal(a, b) for a, b in zip(got, nf.qk_rmsnorm_rope_bwd(*args)))
     # one kind of heads alone
-    assert torch.equal(nf.qk_rmsnorm_rope_fwd(q, None, qw, None, positions, rates_of(rot), EPS, layout, magnitude)[0], qo)
+    check(nf.qk_rmsnorm_rope_fwd(q, None, qw, None, positions, rates_of(rot), EPS, layout, magnitude)[0], q, qw, EPS, positions, freq, magnitude, layout)
     alone = nf.qk_rmsnorm_rope_bwd(dko, None, k, None, kw, None, positions, rates_of(rot), EPS, layout, magnitude)
     assert alone[1] is None and alone[3] is None
     assert torch.equal(alone[0], got[1])

@@ -54,6 +54,24 @@ def test_rope(batch, tokens, hq, hk, dim, rot, kind, layout):
         assert torch.equal(qo[..., rot:], q[..., rot:]) and torch.equal(dk[..., rot:], k[..., rot:])
 
 
+# enough rows that a warp takes several, in tokens of one share, of some and of many; the last rows of a share missing or not
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("kind", [BF, F32])
+@pytest.mark.parametrize("batch,tokens,hq,hk,dim,rot", [(3, 3337, 1, 0, 64, 64), (1, 10007, 3, 1, 128, 64), (2, 2503, 9, 7, 96, 96), (1, 4001, 24, 8, 80, 80),
+                                                        (1, 1201, 72, 8, 128, 128), (5, 601, 33, 1, 256, 256), (1, 3001, 17, 1, 64, 32)])
+def test_many_rows(batch, tokens, hq, hk, dim, rot, kind, layout):
+    g = gen(tokens + dim)
+    q = heads(g, batch, tokens, hq, dim, kind=kind)
+    k = heads(g, batch, tokens, hk, dim, kind=kind) if hk else None
+    positions, freq = torch.randint(0, 9000, (batch, tokens), generator=g, device="cuda"), frequencies(rot)
+    qo, ko = nf.rope_fwd(q, k, positions, nf.rope_rates(rot), layout)
+    check(qo, q, positions, freq, layout=layout)
+    if hk:
+        check(ko, k, positions, freq, layout=layout)
+        wq, wk = nf.rope_fwd(q, k, positions, nf.rope_rates(rot), layout, q_out=q, k_out=k)
+        assert torch.equal(wq, qo) and torch.equal(wk, ko)
+
+
 @pytest.mark.parametrize("layout", ["half", "interleaved"])
 def test_gradient_is_the_transpose(layout):
     # <R x, y> = <x, R^T y>, and against differences of the forward pass
