@@ -229,11 +229,32 @@ __device__ __forceinline__ void in_order(const float2 (&x)[W / 2], const float2 
     }
 }
 
-// Sum over the G lanes of a group; every lane gets the same value.
-__device__ __forceinline__ float sum_lanes(float v, int G) {
+// Over the G lanes of a lane's group; all lanes of the warp call this, and every
+// lane of a group gets the same value.  Where G is no power of two the group's
+// first lane gathers it and hands it on.
+template <int GT, typename V, typename Op>
+__device__ __forceinline__ V over_lanes(V v, int G, int lane, Op op) {
+    if constexpr (GT == 0 || (GT & (GT - 1)) == 0) {
 #pragma unroll
-    for (int off = G >> 1; off > 0; off >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, off);
-    return v;
+        for (int off = G >> 1; off > 0; off >>= 1) v = op(v, __shfl_xor_sync(0xFFFFFFFFu, v, off));
+        return v;
+    } else {
+        const int j = lane % GT;
+#pragma unroll
+        for (int off = GT > 8 ? 8 : 4; off > 0; off >>= 1) {
+            const V w = __shfl_down_sync(0xFFFFFFFFu, v, off);
+            if (j + off < GT) v = op(v, w);
+        }
+        return __shfl_sync(0xFFFFFFFFu, v, lane - j);
+    }
+}
+template <int GT>
+__device__ __forceinline__ float sum_lanes(float v, int G, int lane) {
+    return over_lanes<GT>(v, G, lane, [](float a, float b) { return a + b; });
+}
+template <int GT>
+__device__ __forceinline__ uint32_t max_lanes(uint32_t v, int G, int lane) {
+    return over_lanes<GT>(v, G, lane, [](uint32_t a, uint32_t b) { return max(a, b); });
 }
 
 // 16 bytes to shared memory, or zeros.
@@ -243,9 +264,29 @@ __device__ __forceinline__ void copy16(uint4* to, const void* from, bool there) 
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-inline int lanes_for(int items) {
+constexpr int kNoHead = 1 << 30;  // of a lane without a row; far from overflow when passes are added
+
+// Lanes of a group.  Sizes whose lanes all have two whole vectors and that heads
+// come in have kernels compiled for them; 5, 6, 7, 10, 12 or 14 lanes leave a few
+// of a warp's idle (heads of 80 in bf16: six rows of five lanes, where groups of
+// eight held four).  Others take the next power of two.
+#define NF_EACH_LANES_bf16(X) X(4) X(5) X(6) X(7) X(8) X(12) X(16)
+#define NF_EACH_LANES_f32(X) X(8) X(10) X(12) X(14) X(16)
+template <int W>
+inline int own_lanes(int dim) {
+    if (dim % (2 * W)) return 0;
+    const int n = dim / (2 * W);
+    bool own = false;
+#define NF_IS(m) own = own || n == m;
+    if (W == 8) { NF_EACH_LANES_bf16(NF_IS) } else { NF_EACH_LANES_f32(NF_IS) }
+#undef NF_IS
+    return own ? n : 0;
+}
+template <int W>
+inline int lanes_of(int dim) {
+    if (const int own = own_lanes<W>(dim)) return own;
     int g = 1;
-    while (g < items) g *= 2;
+    while (g < (dim / W + 1) / 2) g *= 2;
     return g;
 }
 

@@ -1,0 +1,474 @@
+// Attention heads: rotation by position, RMSNorm of each head, and the append
+// of keys and values to a paged cache, in one pass over the heads of a token.
+//
+//   n = x * rsqrt(mean(x^2) + eps) * w       (a segment with a weight; else n = x)
+//   y = the pairs of n turned by the token's angles, the rest of n
+//   out = y rounded once, in the heads' type; or, for an 8-bit cache,
+//   scale = max(max|y| / Q, 2^-100), q = y / scale rounded to nearest
+//
+// Bound by memory: each element is read once and written once.  A warp takes a
+// token and up to `passes` times 32 / G of its heads (heads.cuh), so that the
+// token's angles -- two sines and cosines a lane at 64 pairs -- are computed
+// once for all of them and wait in shared memory; a group of G lanes holds a
+// row, and the row's sums stay in the warp.
+#pragma once
+
+#include <algorithm>
+
+#include "heads.cuh"
+
+namespace nf {
+namespace {
+
+constexpr int kWarps = 4;  // per CTA
+constexpr float kScaleMin = 0x1p-100f;
+
+__device__ __forceinline__ bool finite_bits(uint32_t b) { return (b & 0x7F800000u) != 0x7F800000u; }
+
+// y / d rounded to fp32 once, given about 1 / d: the product with it, corrected
+// by its own remainder (P. Markstein, "Computation of elementary functions on
+// the IBM RISC System/6000 processor", 1990).  Rows of 16-bit values often have
+// quotients that lie exactly between two 8-bit values; a product alone would
+// miss these.
+__device__ __forceinline__ float quotient(float y, float d, float inverse) {
+    const float q = y * inverse;
+    return fmaf(fmaf(-q, d, y), inverse, q);
+}
+__device__ __forceinline__ float about_inverse(float d) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
+    return r;
+}
+
+// The scale of a row whose largest |y| has the bits `top`; NaN where that is not finite.
+template <bool INT8>
+__device__ __forceinline__ float row_scale(uint32_t top) {
+    constexpr float most = INT8 ? 127.f : 448.f;
+    return finite_bits(top) ? fmaxf(quotient(__uint_as_float(top), most, 1.f / most), kScaleMin) : __uint_as_float(0x7FC00000u);
+}
+
+template <bool INT8>
+__device__ __forceinline__ uint32_t quant2(float y0, float y1, float scale, float inverse) {
+    const float a = quotient(y0, scale, inverse), b = quotient(y1, scale, inverse);
+    if constexpr (INT8) return (static_cast<uint32_t>(__float2int_rn(a)) & 0xFF) | ((static_cast<uint32_t>(__float2int_rn(b)) & 0xFF) << 8);
+    uint16_t v;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(v) : "f"(b), "f"(a));
+    return v;
+}
+
+template <bool INT8, int W>
+__device__ __forceinline__ void store_quantized(uint8_t* p, const float (&v)[W], float scale, float inverse) {
+    uint32_t q[W / 4];
+#pragma unroll
+    for (int i = 0; i < W / 4; ++i)
+        q[i] = quant2<INT8>(v[4 * i], v[4 * i + 1], scale, inverse) | (quant2<INT8>(v[4 * i + 2], v[4 * i + 3], scale, inverse) << 16);
+    if constexpr (W == 8) *reinterpret_cast<uint2*>(p) = make_uint2(q[0], q[1]);
+    else *reinterpret_cast<uint32_t*>(p) = q[0];
+}
+
+// The largest magnitude of three, a NaN standing above every number.
+__device__ __forceinline__ float largest(float a, float b, float c) {
+    float d;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// A row in 8 bits, and its scale.  All lanes of its group call this.
+template <bool INT8, bool INTER, int GT, int P>
+__device__ __forceinline__ void store_row_8(uint8_t* to, float* scale_to, float2 (&x)[P], float2 (&y)[P], int G, int lane, bool here, bool first_lane,
+                                            const LaneVectors<2 * P, INTER, GT != 0>& v) {
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < P; ++i) m = largest(largest(m, x[i].x, x[i].y), y[i].x, y[i].y);
+    uint32_t top = __float_as_uint(m) & 0x7FFFFFFFu;  // as integers: a NaN stands above every number here too
+    top = max_lanes<GT>(top, G, lane);
+    const float scale = row_scale<INT8>(top);
+    float inverse = about_inverse(scale);
+    if (!finite_bits(top)) {  // stored as zeros
+        inverse = 0.f;
+#pragma unroll
+        for (int i = 0; i < P; ++i) x[i] = y[i] = make_float2(0.f, 0.f);
+    }
+    float a[2 * P], b[2 * P];
+    in_order<2 * P, INTER>(x, y, a, b);
+    const float divisor = finite_bits(top) ? scale : 1.f;
+    if (here && v.has_a()) store_quantized<INT8>(to + v.a, a, divisor, inverse);
+    if (here && v.has_b()) store_quantized<INT8>(to + v.b, b, divisor, inverse);
+    if (here && first_lane) *scale_to = scale;
+}
+
+// Where a token of an append stands.
+struct Place {
+    bool used;      // the token belongs to a sequence
+    bool stored;    // and has a page
+    int64_t position, page;
+    int slot;
+};
+
+// The place of a token of sequence `seq`, which begins at token `first` and has
+// `past` tokens before it (negative: the token is padding).
+__device__ __forceinline__ Place place_in(const HeadsArgs& a, uint32_t token, int seq, int first, int past) {
+    Place p{};
+    p.used = past >= 0;
+    if (!p.used) return p;
+    p.position = static_cast<int64_t>(past) + (static_cast<int64_t>(token) - first);
+    const uint32_t place = static_cast<uint32_t>(p.position);  // below 2^32: both terms are below 2^31
+    const uint32_t column = divide(place, a.by_page);
+    p.slot = static_cast<int>(place - column * static_cast<uint32_t>(a.page_size));
+    if (column < static_cast<uint32_t>(a.max_pages)) {
+        p.page = a.table[seq * a.table_stride + column];
+        p.stored = p.page >= 0 && p.page < a.pages;
+    }
+    return p;
+}
+
+// All lanes of a warp call this.  The sequence of a token is the last one that
+// starts at or before it; the starts are searched 32 ways at a time, and the
+// last 32 candidates' lengths come with them, so that the step costs one load's
+// latency for each factor of 32 of the sequences and one for the page.
+__device__ __forceinline__ Place find_place(const HeadsArgs& a, uint32_t token, int lane) {
+    bool used;
+    int seq, first, past;
+    if (a.starts) {
+        const int behind = a.starts[a.seqs];
+        int lo = 0, n = a.seqs;  // the answer is in [lo, lo + n)
+        for (;;) {
+            const int step = (n + 31) / 32;
+            const bool in = lane * step < n;
+            const int at = lo + lane * step;
+            const int start = in ? a.starts[at] : 0;
+            const int held = in && step == 1 ? a.past[at] : 0;
+            const uint32_t votes = __ballot_sync(0xFFFFFFFFu, in && start <= static_cast<int64_t>(token)) | 1u;
+            const int k = 31 - __clz(votes);
+            lo += k * step;
+            n = min(step, n - k * step);
+            first = __shfl_sync(0xFFFFFFFFu, start, k);
+            past = __shfl_sync(0xFFFFFFFFu, held, k);
+            if (step == 1) break;
+        }
+        seq = lo;
+        used = first >= 0 && first <= static_cast<int64_t>(token) && static_cast<int64_t>(token) < behind;
+    } else {
+        seq = first = static_cast<int>(token);
+        used = seq < a.seqs;
+        past = used ? a.past[seq] : 0;
+    }
+    return place_in(a, token, seq, first, used ? past : -1);
+}
+
+constexpr int kMaxWarps = 3;  // per CTA
+constexpr int64_t kManyShares = 64;  // per SM
+
+// 1 over a row's root mean square.
+template <typename T, bool INTER, int GT>
+__device__ __forceinline__ float rstd_of(uint4 a, uint4 b, int G, int lane, float mean_of, float eps) {
+    constexpr int P = Elem<T, INTER>::W / 2;
+    float2 x[P], y[P];
+    Elem<T, false>::unpack(a, b, x, y);
+    float2 ss = __fmul2_rn(x[0], x[0]);
+    ss = __ffma2_rn(y[0], y[0], ss);
+#pragma unroll
+    for (int i = 1; i < P; ++i) ss = __ffma2_rn(y[i], y[i], __ffma2_rn(x[i], x[i], ss));
+    return rsqrtf(sum_lanes<GT>(ss.x + ss.y, G, lane) * mean_of + eps);
+}
+
+// A row of a lane's group: over its root mean square, weighted and turned.
+template <typename T, bool INTER, bool FULL, bool NORM, int P>
+__device__ __forceinline__ void turn_row(uint4 a, uint4 b, float rstd, const LaneFactors<2 * P, INTER, FULL>& f, float2 (&x)[P], float2 (&y)[P]) {
+    Elem<T, INTER>::unpack(a, b, x, y);
+    if constexpr (NORM) {
+        const float2 r = make_float2(rstd, rstd);
+#pragma unroll
+        for (int i = 0; i < P; ++i) x[i] = __fmul2_rn(x[i], r), y[i] = __fmul2_rn(y[i], r);
+    }
+    f.apply(x, y);
+}
+
+// N such rows, rounded to vectors again.  Without a branch between them, so that
+// one is waited for under another's arithmetic.
+template <typename T, bool INTER, int GT, bool NORM, int N, int M>
+__device__ __forceinline__ void turn_rows(uint4 (&a)[M], uint4 (&b)[M], const float (&rstd)[M], const LaneFactors<Elem<T, INTER>::W, INTER, GT != 0>& f,
+                                          int G, int lane, float mean_of, float eps) {
+    constexpr int P = Elem<T, INTER>::W / 2;
+#pragma unroll
+    for (int p = 0; p < N; ++p) {
+        float2 x[P], y[P];
+        const float r = NORM && M > 1 ? rstd_of<T, INTER, GT>(a[p], b[p], G, lane, mean_of, eps) : rstd[p];
+        turn_row<T, INTER, GT != 0, NORM, P>(a[p], b[p], r, f, x, y);
+        Elem<T, INTER>::pack(x, y, a[p], b[p]);
+    }
+}
+
+// A CTA takes `per_cta` tokens, its warps their shares: so many rows of queries,
+// keys or values.  The angles of a token are computed once, by all the warps
+// that need them, while the rows are on their way.  N: the rows of a group in a
+// share.  GT: lanes of a group, each with both its vectors; 0: a power of two that the
+// host gives, some lanes without one or both.
+template <typename T, bool INTER, bool APPEND, int GT, int N>
+__global__ void __launch_bounds__(kMaxWarps * 32, 7) heads_rows(const __grid_constant__ HeadsArgs a, int lanes) {
+    constexpr int W = Elem<T, INTER>::W, P = W / 2;
+    constexpr bool FULL = GT != 0;
+    const int G = FULL ? GT : lanes;
+    extern __shared__ float4 tables[];  // [per_cta][2][pairs]
+    grid_dep_wait();
+    grid_dep_release();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = a.per_cta == 1 ? blockDim.x >> 5 : (blockDim.x >> 5) / a.per_cta;
+    const int nth = a.per_cta == 1 ? 0 : warp / warps, share = warp - nth * warps;  // the warp's token in the CTA
+    const uint32_t group = divide(blockIdx.x, a.by_turns);
+    const uint32_t token = group * a.per_cta + nth;
+    const int rows = 32 / G, lane_row = lane / G, j = lane - lane_row * G;
+    const uint32_t batch = APPEND ? 0 : divide(token, a.by_tokens), at = token - batch * a.tokens;
+    // the warp's share: queries, keys or values, and which rows of them
+    int chunk = static_cast<int>(blockIdx.x - group * a.turns) * warps + share, si = 0;
+    const bool real = token < a.total && chunk < a.chunks;
+    if (!real) chunk = 0;
+    while (chunk >= a.seg[si].chunks) chunk -= a.seg[si++].chunks;
+    const HeadSegment& s = a.seg[si];
+    const int pairs = s.rotate ? a.rope.pairs : 0;
+    const LaneVectors<W, INTER, FULL> v(j, FULL ? 2 * W * GT : a.dim, pairs);
+    const int first = chunk * N * rows, head = lane_row < rows ? first + lane_row : kNoHead;  // lanes behind the last whole group hold none
+    // what the angles need; for a single row it is asked for first, as it is waited for first
+    const int mine = share * 32 + lane;
+    int64_t position = 0;
+    uint64_t rate = 0;
+    const auto ask = [&] {
+        if (a.rope.pairs && token < a.total) {
+            if (a.rope.positions) position = position_at(a.rope, batch, at);
+            if (mine < a.rope.pairs) rate = a.rope.rates[mine];
+        }
+    };
+    if (N == 1) ask();
+    uint4 xa[N], xb[N];
+    {
+        const T* in = static_cast<const T*>(s.in) + batch * s.in_batch + at * s.in_token;
+#pragma unroll
+        for (int p = 0; p < N; ++p) {
+            xa[p] = xb[p] = make_uint4(0, 0, 0, 0);
+            if (real && first + p * rows < s.heads) {  // the same for all lanes; a row behind the last is the last
+                const T* row = in + min(head + p * rows, s.heads - 1) * s.in_head;
+                if (v.has_a()) xa[p] = ld_stream(row + v.a);
+                if (v.has_b()) xb[p] = ld_stream(row + v.b);
+            }
+        }
+    }
+    if (N > 1) ask();
+    const T* weight = static_cast<const T*>(s.weight);
+    Place place{};
+    if (APPEND && token < a.total) place = find_place(a, token, lane);
+    if (APPEND && !a.rope.positions) position = place.position;
+    float* table = reinterpret_cast<float*>(tables) + nth * 2 * a.rope.pairs;
+    if (token < a.total) {
+        for (int p = mine; p < a.rope.pairs; p += warps * 32) {
+            if (p != mine) rate = a.rope.rates[p];
+            const float2 cs = turn_of(rate, position, a.rope.magnitude, a.rope.direction);
+            table[p] = cs.x;
+            table[a.rope.pairs + p] = cs.y;
+        }
+    }
+    const float mean_of = 1.f / (FULL ? 2 * W * GT : a.dim);
+    // A single row's norm does not wait for the angles (2% of a decode step); of
+    // four rows it would be computed from values that are unpacked once more (4%
+    // slower at 16384 tokens of 72 heads).
+    float rstd[N] = {};
+    const auto norms = [&] {
+#pragma unroll
+        for (int p = 0; p < N; ++p) rstd[p] = rstd_of<T, INTER, GT>(xa[p], xb[p], G, lane, mean_of, a.eps);
+    };
+    if (N == 1 && weight) norms();
+    if (a.rope.pairs) __syncthreads();
+    if (!real || (APPEND && (!place.used || (s.cache && !place.stored)))) return;
+    const bool half = N > 2 && first + 2 * rows >= s.heads;  // of the share's rows at most
+    T* out = static_cast<T*>(s.out);
+    if (APPEND && s.cache) {
+        const int64_t cell = place.page * s.out_batch + place.slot * s.out_token;
+        if (a.format != kCacheSame) {
+            LaneFactors<W, INTER, FULL> f;
+            f.read(weight, table, pairs, v);
+            if (N > 1 && weight) norms();
+            const int64_t scales = place.page * s.scale_page + place.slot * s.scale_slot;
+#pragma unroll
+            for (int p = 0; p < N; ++p) {
+                if (first + p * rows >= s.heads) break;
+                float2 x[P], y[P];
+                if (weight) turn_row<T, INTER, FULL, true, P>(xa[p], xb[p], rstd[p], f, x, y);
+                else turn_row<T, INTER, FULL, false, P>(xa[p], xb[p], rstd[p], f, x, y);
+                const bool here = head + p * rows < s.heads;
+                uint8_t* q = static_cast<uint8_t*>(s.out) + cell + (head + p * rows) * s.out_head;
+                float* scale = s.scale + scales + (head + p * rows) * s.scale_head;
+                if (a.format == kCacheInt8) store_row_8<true, INTER, GT, P>(q, scale, x, y, G, lane, here, j == 0, v);
+                else store_row_8<false, INTER, GT, P>(q, scale, x, y, G, lane, here, j == 0, v);
+            }
+            return;
+        }
+        out += cell;
+    } else {
+        out += batch * s.out_batch + at * s.out_token;
+    }
+    if (weight || pairs) {  // else the rows go as they are
+        LaneFactors<W, INTER, FULL> f;
+        f.read(weight, table, pairs, v);
+        if (weight) {
+            if (half) turn_rows<T, INTER, GT, true, (N + 1) / 2>(xa, xb, rstd, f, G, lane, mean_of, a.eps);
+            else turn_rows<T, INTER, GT, true, N>(xa, xb, rstd, f, G, lane, mean_of, a.eps);
+        } else {
+            turn_rows<T, INTER, GT, false, N>(xa, xb, rstd, f, G, lane, mean_of, a.eps);
+        }
+    }
+#pragma unroll
+    for (int p = 0; p < N; ++p) {
+        if (head + p * rows < s.heads) {
+            T* row = out + (head + p * rows) * s.out_head;
+            if (v.has_a()) st_stream(row + v.a, xa[p]);
+            if (v.has_b()) st_stream(row + v.b, xb[p]);
+        }
+    }
+}
+
+// Any head size, stride and alignment: a warp holds one row in shared memory,
+// element by element, and computes its angles itself.  For rows whose vectors
+// do not fall on 16 bytes, or whose rotated halves are no whole vectors.
+template <typename T, bool APPEND>
+__global__ void __launch_bounds__(kWarps * 32) heads_elements(const __grid_constant__ HeadsArgs a) {
+    extern __shared__ float staged[];
+    grid_dep_wait();
+    grid_dep_release();
+    const int lane = threadIdx.x & 31;
+    const uint32_t unit = blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const uint32_t token = unit / a.chunks;
+    if (token >= a.total) return;
+    int head = static_cast<int>(unit - token * a.chunks), si = 0;
+    while (head >= a.seg[si].heads) head -= a.seg[si++].heads;
+    const HeadSegment& s = a.seg[si];
+    const uint32_t batch = token / a.tokens, at = token - batch * a.tokens;
+    Place place{};
+    if constexpr (APPEND) {
+        place = find_place(a, token, lane);
+        if (!place.used || (s.cache && !place.stored)) return;
+    }
+    const int dim = a.dim, pairs = s.rotate ? a.rope.pairs : 0;
+    float* row = staged + (threadIdx.x >> 5) * dim;
+    const T* in = static_cast<const T*>(s.in) + batch * s.in_batch + at * s.in_token + head * s.in_head;
+    float ss = 0.f;
+    for (int i = lane; i < dim; i += 32) {
+        const float x = load_element(in + i);
+        row[i] = x;
+        ss += x * x;
+    }
+    if (s.weight) {
+        const float rstd = rsqrtf(sum_lanes<32>(ss, 32, lane) * (1.f / dim) + a.eps);
+        for (int i = lane; i < dim; i += 32) row[i] *= rstd * load_element(static_cast<const T*>(s.weight) + i);
+    }
+    __syncwarp();
+    if (pairs) {
+        const int64_t position = APPEND && !a.rope.positions ? place.position : position_at(a.rope, batch, at);
+        for (int p = lane; p < pairs; p += 32) {
+            const float2 t = turn_of(a.rope.rates[p], position, a.rope.magnitude, a.rope.direction);
+            const int ia = a.rope.interleaved ? 2 * p : p, ib = a.rope.interleaved ? 2 * p + 1 : p + pairs;
+            const float x = row[ia], y = row[ib];
+            row[ia] = fmaf(y, -t.y, __fmul_rn(x, t.x));  // rounded as in the vector kernel
+            row[ib] = fmaf(x, t.y, __fmul_rn(y, t.x));
+        }
+        __syncwarp();
+    }
+    if (APPEND && s.cache) {
+        const int64_t first = place.page * s.out_batch + place.slot * s.out_token + head * s.out_head;
+        if (a.format != kCacheSame) {
+            uint32_t top = 0;
+            for (int i = lane; i < dim; i += 32) top = max(top, __float_as_uint(fabsf(row[i])));
+            top = __reduce_max_sync(0xFFFFFFFFu, top);
+            const bool int8 = a.format == kCacheInt8, fine = finite_bits(top);
+            const float scale = int8 ? row_scale<true>(top) : row_scale<false>(top), inverse = about_inverse(scale);
+            uint8_t* out = static_cast<uint8_t*>(s.out) + first;
+            for (int i = lane; i < dim; i += 32) {
+                const uint32_t q = int8 ? quant2<true>(row[i], 0.f, scale, inverse) : quant2<false>(row[i], 0.f, scale, inverse);
+                out[i] = fine ? static_cast<uint8_t>(q) : 0;
+            }
+            if (lane == 0) s.scale[place.page * s.scale_page + place.slot * s.scale_slot + head * s.scale_head] = scale;
+        } else {
+            T* out = static_cast<T*>(s.out) + first;
+            for (int i = lane; i < dim; i += 32) {
+                if (s.weight || pairs) store_element(out + i, row[i]);
+                else out[i] = in[i];
+            }
+        }
+    } else {
+        T* out = static_cast<T*>(s.out) + batch * s.out_batch + at * s.out_token + head * s.out_head;
+        for (int i = lane; i < dim; i += 32) store_element(out + i, row[i]);
+    }
+}
+
+bool fits(const void* p, int64_t s0, int64_t s1, int64_t s2, int elements, int bytes) {
+    return (reinterpret_cast<uintptr_t>(p) % bytes) == 0 && s0 % elements == 0 && s1 % elements == 0 && s2 % elements == 0;
+}
+
+// Whether every row falls on whole 16-byte vectors (8-bit rows: on W bytes), each
+// with all its pairs turned or none.
+bool whole_vectors(const HeadsArgs& a, int W) {
+    if (a.dim % W || (a.dim / W + 1) / 2 > 32 || a.rope.pairs % (a.rope.interleaved ? W / 2 : W)) return false;
+    for (int i = 0; i < a.segments; ++i) {
+        const HeadSegment& s = a.seg[i];
+        if (!fits(s.in, s.in_batch, s.in_token, s.in_head, W, 16)) return false;
+        if (!fits(s.out, s.out_batch, s.out_token, s.out_head, W, s.cache && a.format != kCacheSame ? W : 16)) return false;
+        if (reinterpret_cast<uintptr_t>(s.weight) % 16) return false;
+    }
+    return true;
+}
+
+template <typename T, bool INTER, bool APPEND, int GT>
+cudaError_t launch_rows(const HeadsArgs& a, int passes, int G, dim3 grid, dim3 block, size_t smem, cudaStream_t st) {
+    return passes == 1 ? launch_with_pdl(heads_rows<T, INTER, APPEND, GT, 1>, grid, block, smem, st, a, G)
+                       : launch_with_pdl(heads_rows<T, INTER, APPEND, GT, 4>, grid, block, smem, st, a, G);
+}
+
+// The head sizes with kernels of their own: 64, 80, 96, 112, 128, 192 and 256.
+template <typename T, bool INTER, bool APPEND>
+cudaError_t launch_lanes(const HeadsArgs& a, int passes, int lanes, dim3 grid, dim3 block, size_t smem, cudaStream_t st) {
+    const int own = own_lanes<Elem<T, INTER>::W>(a.dim);
+#define NF_LANES(n) \
+    if (own == n) return launch_rows<T, INTER, APPEND, n>(a, passes, n, grid, block, smem, st);
+    if constexpr (sizeof(T) == 2) {
+        NF_EACH_LANES_bf16(NF_LANES)
+    } else {
+        NF_EACH_LANES_f32(NF_LANES)
+    }
+#undef NF_LANES
+    return launch_rows<T, INTER, APPEND, 0>(a, passes, lanes, grid, block, smem, st);
+}
+
+template <typename T, bool APPEND>
+cudaError_t launch_heads_rows(HeadsArgs a, int sms, cudaStream_t st) {
+    constexpr int W = Elem<T, false>::W;
+    if (APPEND) a.by_page = Divider(a.page_size);
+    if (!whole_vectors(a, W)) {
+        a.chunks = 0;
+        for (int i = 0; i < a.segments; ++i) a.chunks += a.seg[i].heads;
+        const int64_t units = static_cast<int64_t>(a.total) * a.chunks;
+        return launch_with_pdl(heads_elements<T, APPEND>, dim3(static_cast<unsigned>((units + kWarps - 1) / kWarps)), dim3(kWarps * 32),
+                               kWarps * a.dim * sizeof(float), st, a);
+    }
+    const int G = lanes_of<W>(a.dim), rows = 32 / G;
+    // Four rows of a group to a share where that leaves every SM its warps: they
+    // are in flight together and spread what a warp does before them.
+    int passes = 4;
+    for (;; passes = 1) {
+        a.chunks = 0;
+        for (int i = 0; i < a.segments; ++i) {
+            a.seg[i].chunks = (a.seg[i].heads + rows * passes - 1) / (rows * passes);
+            a.chunks += a.seg[i].chunks;
+        }
+        if (passes == 1 || static_cast<int64_t>(a.total) * a.chunks >= kManyShares * sms) break;
+    }
+    // a warp to each share, in several CTAs where a token has many; tokens of one share side by side
+    a.turns = (a.chunks + kMaxWarps - 1) / kMaxWarps;
+    const int warps = (a.chunks + a.turns - 1) / a.turns;
+    a.per_cta = a.turns == 1 ? kMaxWarps / warps : 1;
+    a.by_turns = Divider(a.turns);
+    a.by_tokens = Divider(a.tokens);
+    const dim3 grid((a.total + a.per_cta - 1) / a.per_cta * a.turns), block(warps * a.per_cta * 32);
+    const size_t smem = a.per_cta * a.rope.pairs * sizeof(float2);
+    return a.rope.interleaved ? launch_lanes<T, true, APPEND>(a, passes, G, grid, block, smem, st)
+                              : launch_lanes<T, false, APPEND>(a, passes, G, grid, block, smem, st);
+}
+
+}  // namespace
+}  // namespace nf

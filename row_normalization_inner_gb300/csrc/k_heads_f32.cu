@@ -1,0 +1,8 @@
+// Rotation and norm of attention heads in fp32.
+#include "heads_rows.cuh"
+
+namespace nf {
+
+cudaError_t launch_heads_f32(const HeadsArgs& a, int sms, cudaStream_t st) { return launch_heads_rows<float, false>(a, sms, st); }
+
+}  // namespace nf

@@ -1,0 +1,8 @@
+// Appends of bf16 keys and values to a paged cache.
+#include "heads_rows.cuh"
+
+namespace nf {
+
+cudaError_t launch_append_bf16(const HeadsArgs& a, int sms, cudaStream_t st) { return launch_heads_rows<uint16_t, true>(a, sms, st); }
+
+}  // namespace nf
