@@ -99,25 +99,23 @@ __device__ __forceinline__ void store_row_8(uint8_t* to, float* scale_to, float2
 
 // Where a token of an append stands.
 struct Place {
-    bool used;      // the token belongs to a sequence
-    bool stored;    // and has a page
-    int64_t position, page;
-    int slot;
+    int64_t position;  // in its sequence
+    int page;          // -1: not stored
+    int slot;          // -1: the token belongs to no sequence
 };
 
 // The place of a token of sequence `seq`, which begins at token `first` and has
 // `past` tokens before it (negative: the token is padding).
-__device__ __forceinline__ Place place_in(const HeadsArgs& a, uint32_t token, int seq, int first, int past) {
-    Place p{};
-    p.used = past >= 0;
-    if (!p.used) return p;
-    p.position = static_cast<int64_t>(past) + (static_cast<int64_t>(token) - first);
-    const uint32_t place = static_cast<uint32_t>(p.position);  // below 2^32: both terms are below 2^31
+__device__ __forceinline__ Place place_in(const HeadsArgs& a, int token, int seq, int first, int past) {
+    Place p{0, -1, -1};
+    if (past < 0) return p;
+    const uint32_t place = static_cast<uint32_t>(past) + static_cast<uint32_t>(token - first);  // both below 2^31
     const uint32_t column = divide(place, a.by_page);
+    p.position = place;
     p.slot = static_cast<int>(place - column * static_cast<uint32_t>(a.page_size));
     if (column < static_cast<uint32_t>(a.max_pages)) {
-        p.page = a.table[seq * a.table_stride + column];
-        p.stored = p.page >= 0 && p.page < a.pages;
+        const int page = a.table[seq * a.table_stride + column];
+        if (static_cast<uint32_t>(page) < static_cast<uint32_t>(a.pages)) p.page = page;
     }
     return p;
 }
@@ -126,37 +124,33 @@ __device__ __forceinline__ Place place_in(const HeadsArgs& a, uint32_t token, in
 // starts at or before it; the starts are searched 32 ways at a time, and the
 // last 32 candidates' lengths come with them, so that the step costs one load's
 // latency for each factor of 32 of the sequences and one for the page.
-__device__ __forceinline__ Place find_place(const HeadsArgs& a, uint32_t token, int lane) {
-    bool used;
-    int seq, first, past;
-    if (a.starts) {
-        const int behind = a.starts[a.seqs];
-        int lo = 0, n = a.seqs;  // the answer is in [lo, lo + n)
-        for (;;) {
-            const int step = (n + 31) / 32;
-            const bool in = lane * step < n;
-            const int at = lo + lane * step;
-            const int start = in ? a.starts[at] : 0;
-            const int held = in && step == 1 ? a.past[at] : 0;
-            const uint32_t votes = __ballot_sync(0xFFFFFFFFu, in && start <= static_cast<int64_t>(token)) | 1u;
-            const int k = 31 - __clz(votes);
-            lo += k * step;
-            n = min(step, n - k * step);
-            first = __shfl_sync(0xFFFFFFFFu, start, k);
-            past = __shfl_sync(0xFFFFFFFFu, held, k);
-            if (step == 1) break;
-        }
-        seq = lo;
-        used = first >= 0 && first <= static_cast<int64_t>(token) && static_cast<int64_t>(token) < behind;
-    } else {
-        seq = first = static_cast<int>(token);
-        used = seq < a.seqs;
-        past = used ? a.past[seq] : 0;
+__device__ __forceinline__ Place find_place(const HeadsArgs& a, int token, int lane) {
+    if (!a.starts) return place_in(a, token, token, token, token < a.seqs ? a.past[token] : -1);
+    const int behind = a.starts[a.seqs];
+    int lo = 0, n = a.seqs, first, past;  // the answer is in [lo, lo + n)
+    for (;;) {
+        const int step = (n + 31) / 32;
+        const bool in = lane * step < n;
+        const int at = lo + lane * step;
+        const int start = in ? a.starts[at] : 0;
+        const int held = in && step == 1 ? a.past[at] : 0;
+        const uint32_t votes = __ballot_sync(0xFFFFFFFFu, in && start <= token) | 1u;
+        const int k = 31 - __clz(votes);
+        lo += k * step;
+        n = min(step, n - k * step);
+        first = __shfl_sync(0xFFFFFFFFu, start, k);
+        past = __shfl_sync(0xFFFFFFFFu, held, k);
+        if (step == 1) break;
     }
-    return place_in(a, token, seq, first, used ? past : -1);
+    return place_in(a, token, lo, first, first >= 0 && first <= token && token < behind ? past : -1);
 }
 
-constexpr int kMaxWarps = 3;  // per CTA
+// Warps of a CTA at most, and CTAs that the registers of an SM hold (80 a thread).
+// Small ones take turns best: 16384 tokens of 64 + 8 heads with 3, 5 and 10 warps
+// take 103, 102 and 103 us, of 32 + 8 heads 54, 57 and 57, an append to an 8-bit
+// cache (8192 tokens of 64 + 8 + 8) 63, 71 and 69.
+constexpr int kMaxWarps = 3;
+constexpr int kMinCtas = 7;
 constexpr int64_t kManyShares = 64;  // per SM
 
 // 1 over a row's root mean square.
@@ -205,11 +199,12 @@ __device__ __forceinline__ void turn_rows(uint4 (&a)[M], uint4 (&b)[M], const fl
 // share.  GT: lanes of a group, each with both its vectors; 0: a power of two that the
 // host gives, some lanes without one or both.
 template <typename T, bool INTER, bool APPEND, int GT, int N>
-__global__ void __launch_bounds__(kMaxWarps * 32, 7) heads_rows(const __grid_constant__ HeadsArgs a, int lanes) {
+__global__ void __launch_bounds__(kMaxWarps * 32, kMinCtas) heads_rows(const __grid_constant__ HeadsArgs a, int lanes) {
     constexpr int W = Elem<T, INTER>::W, P = W / 2;
     constexpr bool FULL = GT != 0;
     const int G = FULL ? GT : lanes;
     extern __shared__ float4 tables[];  // [per_cta][2][pairs]
+    __shared__ Place places[APPEND ? kMaxWarps : 1];
     grid_dep_wait();
     grid_dep_release();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = a.per_cta == 1 ? blockDim.x >> 5 : (blockDim.x >> 5) / a.per_cta;
@@ -239,23 +234,38 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 7) heads_rows(const __grid_con
     };
     if (N == 1) ask();
     uint4 xa[N], xb[N];
+    const bool whole = real && first + N * rows <= s.heads;  // the share has all its rows
     {
         const T* in = static_cast<const T*>(s.in) + batch * s.in_batch + at * s.in_token;
+        if (FULL && whole) {
+            const T* row = in + (first + (lane_row < rows ? lane_row : 0)) * s.in_head;
+            const int64_t step = rows * s.in_head;
 #pragma unroll
-        for (int p = 0; p < N; ++p) {
-            xa[p] = xb[p] = make_uint4(0, 0, 0, 0);
-            if (real && first + p * rows < s.heads) {  // the same for all lanes; a row behind the last is the last
-                const T* row = in + min(head + p * rows, s.heads - 1) * s.in_head;
-                if (v.has_a()) xa[p] = ld_stream(row + v.a);
-                if (v.has_b()) xb[p] = ld_stream(row + v.b);
+            for (int p = 0; p < N; ++p, row += step) xa[p] = ld_stream(row + v.a), xb[p] = ld_stream(row + v.b);
+        } else {
+#pragma unroll
+            for (int p = 0; p < N; ++p) {
+                xa[p] = xb[p] = make_uint4(0, 0, 0, 0);
+                if (real && first + p * rows < s.heads) {  // the same for all lanes; a row behind the last is the last
+                    const T* row = in + min(head + p * rows, s.heads - 1) * s.in_head;
+                    if (v.has_a()) xa[p] = ld_stream(row + v.a);
+                    if (v.has_b()) xb[p] = ld_stream(row + v.b);
+                }
             }
         }
     }
     if (N > 1) ask();
     const T* weight = static_cast<const T*>(s.weight);
-    Place place{};
-    if (APPEND && token < a.total) place = find_place(a, token, lane);
-    if (APPEND && !a.rope.positions) position = place.position;
+    Place place{0, -1, -1};
+    if constexpr (APPEND) {
+        if (share == 0 && token < a.total) {
+            place = find_place(a, static_cast<int>(token), lane);
+            if (lane == 0) places[nth] = place;
+        }
+        __syncthreads();
+        if (token < a.total) place = places[nth];
+        if (!a.rope.positions) position = place.position;
+    }
     float* table = reinterpret_cast<float*>(tables) + nth * 2 * a.rope.pairs;
     if (token < a.total) {
         for (int p = mine; p < a.rope.pairs; p += warps * 32) {
@@ -270,31 +280,31 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 7) heads_rows(const __grid_con
     // four rows it would be computed from values that are unpacked once more (4%
     // slower at 16384 tokens of 72 heads).
     float rstd[N] = {};
-    const auto norms = [&] {
-#pragma unroll
-        for (int p = 0; p < N; ++p) rstd[p] = rstd_of<T, INTER, GT>(xa[p], xb[p], G, lane, mean_of, a.eps);
-    };
-    if (N == 1 && weight) norms();
+    if (N == 1 && weight) rstd[0] = rstd_of<T, INTER, GT>(xa[0], xb[0], G, lane, mean_of, a.eps);
     if (a.rope.pairs) __syncthreads();
-    if (!real || (APPEND && (!place.used || (s.cache && !place.stored)))) return;
+    if (!real || (APPEND && (place.slot < 0 || (s.cache && place.page < 0)))) return;
     const bool half = N > 2 && first + 2 * rows >= s.heads;  // of the share's rows at most
     T* out = static_cast<T*>(s.out);
     if (APPEND && s.cache) {
         const int64_t cell = place.page * s.out_batch + place.slot * s.out_token;
         if (a.format != kCacheSame) {
             LaneFactors<W, INTER, FULL> f;
-            f.read(weight, table, pairs, v);
-            if (N > 1 && weight) norms();
-            const int64_t scales = place.page * s.scale_page + place.slot * s.scale_slot;
+            if (weight || pairs) f.read(weight, table, pairs, v);
+            uint8_t* q = static_cast<uint8_t*>(s.out) + cell + head * s.out_head;
+            float* scale = s.scale + place.page * s.scale_page + place.slot * s.scale_slot + head * s.scale_head;
 #pragma unroll
-            for (int p = 0; p < N; ++p) {
+            for (int p = 0; p < N; ++p, q += rows * s.out_head, scale += rows * s.scale_head) {
                 if (first + p * rows >= s.heads) break;
                 float2 x[P], y[P];
-                if (weight) turn_row<T, INTER, FULL, true, P>(xa[p], xb[p], rstd[p], f, x, y);
-                else turn_row<T, INTER, FULL, false, P>(xa[p], xb[p], rstd[p], f, x, y);
+                if (weight) {
+                    const float r = N > 1 ? rstd_of<T, INTER, GT>(xa[p], xb[p], G, lane, mean_of, a.eps) : rstd[p];
+                    turn_row<T, INTER, FULL, true, P>(xa[p], xb[p], r, f, x, y);
+                } else if (pairs) {
+                    turn_row<T, INTER, FULL, false, P>(xa[p], xb[p], 1.f, f, x, y);
+                } else {
+                    Elem<T, INTER>::unpack(xa[p], xb[p], x, y);
+                }
                 const bool here = head + p * rows < s.heads;
-                uint8_t* q = static_cast<uint8_t*>(s.out) + cell + (head + p * rows) * s.out_head;
-                float* scale = s.scale + scales + (head + p * rows) * s.scale_head;
                 if (a.format == kCacheInt8) store_row_8<true, INTER, GT, P>(q, scale, x, y, G, lane, here, j == 0, v);
                 else store_row_8<false, INTER, GT, P>(q, scale, x, y, G, lane, here, j == 0, v);
             }
@@ -314,12 +324,21 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 7) heads_rows(const __grid_con
             turn_rows<T, INTER, GT, false, N>(xa, xb, rstd, f, G, lane, mean_of, a.eps);
         }
     }
+    if (FULL && whole) {
+        T* row = out + (first + lane_row) * s.out_head;
+        const int64_t step = rows * s.out_head;
+        if (32 % G == 0 || lane_row < rows) {
 #pragma unroll
-    for (int p = 0; p < N; ++p) {
-        if (head + p * rows < s.heads) {
-            T* row = out + (head + p * rows) * s.out_head;
-            if (v.has_a()) st_stream(row + v.a, xa[p]);
-            if (v.has_b()) st_stream(row + v.b, xb[p]);
+            for (int p = 0; p < N; ++p, row += step) st_stream(row + v.a, xa[p]), st_stream(row + v.b, xb[p]);
+        }
+    } else {
+#pragma unroll
+        for (int p = 0; p < N; ++p) {
+            if (head + p * rows < s.heads) {
+                T* row = out + (head + p * rows) * s.out_head;
+                if (v.has_a()) st_stream(row + v.a, xa[p]);
+                if (v.has_b()) st_stream(row + v.b, xb[p]);
+            }
         }
     }
 }
@@ -340,10 +359,10 @@ __global__ void __launch_bounds__(kWarps * 32) heads_elements(const __grid_const
     while (head >= a.seg[si].heads) head -= a.seg[si++].heads;
     const HeadSegment& s = a.seg[si];
     const uint32_t batch = token / a.tokens, at = token - batch * a.tokens;
-    Place place{};
+    Place place{0, -1, -1};
     if constexpr (APPEND) {
-        place = find_place(a, token, lane);
-        if (!place.used || (s.cache && !place.stored)) return;
+        place = find_place(a, static_cast<int>(token), lane);
+        if (place.slot < 0 || (s.cache && place.page < 0)) return;
     }
     const int dim = a.dim, pairs = s.rotate ? a.rope.pairs : 0;
     float* row = staged + (threadIdx.x >> 5) * dim;
