@@ -103,6 +103,11 @@ __device__ __forceinline__ int64_t position_at(const Rotation& r, uint32_t batch
     return r.wide ? static_cast<const int64_t*>(r.positions)[at] : static_cast<const int32_t*>(r.positions)[at];
 }
 
+__device__ __forceinline__ int64_t position_of(const HeadsArgs& a, uint32_t token) {
+    const uint32_t batch = divide(token, a.by_tokens);
+    return position_at(a.rope, batch, token - batch * a.tokens);
+}
+
 // Lane j's two vectors: where they start, whether they are there, and whether
 // their pairs are turned.  FULL: every lane of a group has both.
 template <int W, bool INTER, bool FULL>

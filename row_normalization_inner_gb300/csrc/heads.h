@@ -31,7 +31,12 @@ struct HeadSegment {
     float* scale;                            // an 8-bit cache: per row
     int64_t scale_page, scale_slot, scale_head;
     int heads;
-    int chunks;   // of a token (set by the launcher)
+    // How a call's launcher shares out the rows (heads_rows.cuh).
+    int shares;           // of a CTA's tokens
+    int per_token;        // shares of a token; 0: a share holds several tokens,
+    int tokens_of_share;  //   so many,
+    int groups_of_token;  //   each on so many groups of lanes
+    int groups_factor;
     bool rotate;
     bool cache;   // out is a paged cache
 };
@@ -70,9 +75,9 @@ struct HeadsArgs {
     int dim;
     int tokens;      // per batch
     uint32_t total;  // batch * tokens
-    int chunks;      // warps' shares of a token (set by the launcher, and the three below)
+    int shares;      // of a CTA's tokens, over all segments (set by the launcher, and the five below)
     int per_cta;     // tokens
-    int turns;       // CTAs of a token (1 where per_cta is more)
+    int turns;       // CTAs that take these shares
     Divider by_tokens, by_turns, by_page;
     float eps;
     // an append

@@ -151,7 +151,11 @@ __device__ __forceinline__ Place find_place(const HeadsArgs& a, int token, int l
 // cache (8192 tokens of 64 + 8 + 8) 63, 71 and 69.
 constexpr int kMaxWarps = 3;
 constexpr int kMinCtas = 7;
-constexpr int64_t kManyShares = 64;  // per SM
+// Shares of four rows per SM from which these are taken rather than single rows
+// (us, four rows / one): 256 tokens of 32 + 8 heads, five to an SM, turned 2.4 /
+// 2.7, normalized too 3.0 / 3.1, 1024 tokens 4.3 / 6.0 and 5.0 / 6.8; appended, 256
+// tokens with 8 + 8 heads, seven to an SM, 3.8 / 3.5, 1024 tokens 8.0 / 8.8.
+constexpr int64_t many_shares(bool append) { return append ? 8 : 4; }
 
 // 1 over a row's root mean square.
 template <typename T, bool INTER, int GT>
@@ -193,61 +197,85 @@ __device__ __forceinline__ void turn_rows(uint4 (&a)[M], uint4 (&b)[M], const fl
     }
 }
 
-// A CTA takes `per_cta` tokens, its warps their shares: so many rows of queries,
-// keys or values.  The angles of a token are computed once, by all the warps
-// that need them, while the rows are on their way.  N: the rows of a group in a
-// share.  GT: lanes of a group, each with both its vectors; 0: a power of two that the
+constexpr int kMaxTokens = 8;  // of a CTA
+
+// A CTA takes `per_cta` tokens (several CTAs take turns where there is more to
+// do), its warps their shares: N rows for each group of lanes, of queries, keys
+// or values.  A share is part of a token, pass after pass of 32 / G heads; or,
+// where a token has fewer heads, several tokens, each on as many groups as it
+// needs, so that a few heads fill a warp too.  The angles are computed once for
+// all the warps that need them, while the rows are on their way.
+// GT: lanes of a group, each with both its vectors; 0: a power of two that the
 // host gives, some lanes without one or both.
-template <typename T, bool INTER, bool APPEND, int GT, int N>
+// SEVERAL: the CTA has several tokens.
+template <typename T, bool INTER, bool APPEND, int GT, int N, bool SEVERAL>
 __global__ void __launch_bounds__(kMaxWarps * 32, kMinCtas) heads_rows(const __grid_constant__ HeadsArgs a, int lanes) {
     constexpr int W = Elem<T, INTER>::W, P = W / 2;
     constexpr bool FULL = GT != 0;
     const int G = FULL ? GT : lanes;
     extern __shared__ float4 tables[];  // [per_cta][2][pairs]
-    __shared__ Place places[APPEND ? kMaxWarps : 1];
-    grid_dep_wait();
-    grid_dep_release();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = a.per_cta == 1 ? blockDim.x >> 5 : (blockDim.x >> 5) / a.per_cta;
-    const int nth = a.per_cta == 1 ? 0 : warp / warps, share = warp - nth * warps;  // the warp's token in the CTA
-    const uint32_t group = divide(blockIdx.x, a.by_turns);
-    const uint32_t token = group * a.per_cta + nth;
-    const int rows = 32 / G, lane_row = lane / G, j = lane - lane_row * G;
-    const uint32_t batch = APPEND ? 0 : divide(token, a.by_tokens), at = token - batch * a.tokens;
-    // the warp's share: queries, keys or values, and which rows of them
-    int chunk = static_cast<int>(blockIdx.x - group * a.turns) * warps + share, si = 0;
-    const bool real = token < a.total && chunk < a.chunks;
-    if (!real) chunk = 0;
-    while (chunk >= a.seg[si].chunks) chunk -= a.seg[si++].chunks;
+    __shared__ Place places[APPEND ? SEVERAL ? kMaxTokens : 1 : 1];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const uint32_t cta_of_tokens = divide(blockIdx.x, a.by_turns), first_token = SEVERAL ? cta_of_tokens * a.per_cta : cta_of_tokens;
+    const int tokens = SEVERAL ? min(a.per_cta, static_cast<int>(a.total - first_token)) : 1;
+    const int rows = 32 / G, group = lane / G, j = lane - group * G;
+    // the warp's share: queries, keys or values, which tokens and which rows of them
+    int share = static_cast<int>(blockIdx.x - cta_of_tokens * a.turns) * warps + warp, si = 0;
+    const bool real = share < a.shares;
+    if (!real) share = 0;
+    while (share >= a.seg[si].shares) share -= a.seg[si++].shares;
     const HeadSegment& s = a.seg[si];
+    int nth = 0, head, step = rows, passes;  // the lane's token in the CTA and its first head; how far the next is; how many there are (of any lane)
+    bool whole;                              // every group has N rows
+    if (!SEVERAL || s.per_token) {
+        if (SEVERAL) nth = share / s.per_token;
+        const int first = (share - (SEVERAL ? nth * s.per_token : 0)) * N * rows;
+        head = group < rows ? first + group : kNoHead;  // lanes behind the last whole group hold none
+        passes = min(N, (s.heads - first + rows - 1) / rows);
+        whole = real && first + N * rows <= s.heads && nth < tokens;
+    } else {
+        const int in_share = (group * s.groups_factor) >> 10, first = share * s.tokens_of_share;  // group / groups_of_token
+        nth = first + in_share;
+        head = in_share < s.tokens_of_share && nth < tokens ? group - in_share * s.groups_of_token : kNoHead;
+        step = s.groups_of_token;
+        passes = (s.heads + step - 1) / step;
+        whole = real && s.heads == N * step && first + s.tokens_of_share <= tokens;
+    }
+    if (SEVERAL && nth >= tokens) head = kNoHead, nth = 0;
+    const uint32_t token = first_token + nth;
+    const uint32_t batch = APPEND ? 0 : divide(token, a.by_tokens), at = token - batch * a.tokens;
     const int pairs = s.rotate ? a.rope.pairs : 0;
     const LaneVectors<W, INTER, FULL> v(j, FULL ? 2 * W * GT : a.dim, pairs);
-    const int first = chunk * N * rows, head = lane_row < rows ? first + lane_row : kNoHead;  // lanes behind the last whole group hold none
+    // Nothing before this touches memory: it runs under the kernel ahead (a decode
+    // step's rotation 1.49 us, with the wait first 1.74).
+    grid_dep_wait();
+    grid_dep_release();
     // what the angles need; for a single row it is asked for first, as it is waited for first
-    const int mine = share * 32 + lane;
+    const int mine = warp * 32 + lane, threads = warps * 32;
     int64_t position = 0;
     uint64_t rate = 0;
     const auto ask = [&] {
-        if (a.rope.pairs && token < a.total) {
-            if (a.rope.positions) position = position_at(a.rope, batch, at);
-            if (mine < a.rope.pairs) rate = a.rope.rates[mine];
+        if (mine < a.rope.pairs * tokens) {  // of the thread's first pair
+            const int t = SEVERAL ? mine / a.rope.pairs : 0;
+            if (a.rope.positions) position = SEVERAL ? position_of(a, first_token + t) : position_at(a.rope, batch, at);
+            rate = a.rope.rates[mine - t * a.rope.pairs];
         }
     };
     if (N == 1) ask();
     uint4 xa[N], xb[N];
-    const bool whole = real && first + N * rows <= s.heads;  // the share has all its rows
     {
         const T* in = static_cast<const T*>(s.in) + batch * s.in_batch + at * s.in_token;
         if (FULL && whole) {
-            const T* row = in + (first + (lane_row < rows ? lane_row : 0)) * s.in_head;
-            const int64_t step = rows * s.in_head;
+            const T* row = in + (head == kNoHead ? 0 : head) * s.in_head;
+            const int64_t further = step * s.in_head;
 #pragma unroll
-            for (int p = 0; p < N; ++p, row += step) xa[p] = ld_stream(row + v.a), xb[p] = ld_stream(row + v.b);
+            for (int p = 0; p < N; ++p, row += further) xa[p] = ld_stream(row + v.a), xb[p] = ld_stream(row + v.b);
         } else {
 #pragma unroll
             for (int p = 0; p < N; ++p) {
                 xa[p] = xb[p] = make_uint4(0, 0, 0, 0);
-                if (real && first + p * rows < s.heads) {  // the same for all lanes; a row behind the last is the last
-                    const T* row = in + min(head + p * rows, s.heads - 1) * s.in_head;
+                if (real && p < passes) {  // the same for all lanes; a row behind the last is the last
+                    const T* row = in + min(head + p * step, s.heads - 1) * s.in_head;
                     if (v.has_a()) xa[p] = ld_stream(row + v.a);
                     if (v.has_b()) xb[p] = ld_stream(row + v.b);
                 }
@@ -258,23 +286,28 @@ __global__ void __launch_bounds__(kMaxWarps * 32, kMinCtas) heads_rows(const __g
     const T* weight = static_cast<const T*>(s.weight);
     Place place{0, -1, -1};
     if constexpr (APPEND) {
-        if (share == 0 && token < a.total) {
-            place = find_place(a, static_cast<int>(token), lane);
-            if (lane == 0) places[nth] = place;
+        for (int t = warp; t < tokens; t += warps) {  // a warp to a token
+            place = find_place(a, static_cast<int>(first_token) + t, lane);
+            if (lane == 0) places[t] = place;
         }
         __syncthreads();
-        if (token < a.total) place = places[nth];
-        if (!a.rope.positions) position = place.position;
+        place = places[nth];
     }
-    float* table = reinterpret_cast<float*>(tables) + nth * 2 * a.rope.pairs;
-    if (token < a.total) {
-        for (int p = mine; p < a.rope.pairs; p += warps * 32) {
-            if (p != mine) rate = a.rope.rates[p];
+    if (a.rope.pairs) {
+        float* table = reinterpret_cast<float*>(tables);
+        for (int i = mine; i < a.rope.pairs * tokens; i += threads) {
+            const int t = SEVERAL ? i / a.rope.pairs : 0, p = i - t * a.rope.pairs;
+            if (i != mine) {
+                if (SEVERAL && a.rope.positions) position = position_of(a, first_token + t);
+                rate = a.rope.rates[p];
+            }
+            if (APPEND && !a.rope.positions) position = places[t].position;
             const float2 cs = turn_of(rate, position, a.rope.magnitude, a.rope.direction);
-            table[p] = cs.x;
-            table[a.rope.pairs + p] = cs.y;
+            table[2 * t * a.rope.pairs + p] = cs.x;
+            table[(2 * t + 1) * a.rope.pairs + p] = cs.y;
         }
     }
+    const float* table = reinterpret_cast<const float*>(tables) + 2 * nth * a.rope.pairs;
     const float mean_of = 1.f / (FULL ? 2 * W * GT : a.dim);
     // A single row's norm does not wait for the angles (2% of a decode step); of
     // four rows it would be computed from values that are unpacked once more (4%
@@ -282,19 +315,24 @@ __global__ void __launch_bounds__(kMaxWarps * 32, kMinCtas) heads_rows(const __g
     float rstd[N] = {};
     if (N == 1 && weight) rstd[0] = rstd_of<T, INTER, GT>(xa[0], xb[0], G, lane, mean_of, a.eps);
     if (a.rope.pairs) __syncthreads();
-    if (!real || (APPEND && (place.slot < 0 || (s.cache && place.page < 0)))) return;
-    const bool half = N > 2 && first + 2 * rows >= s.heads;  // of the share's rows at most
+    if (!real) return;
+    if (APPEND && (place.slot < 0 || (s.cache && place.page < 0))) {  // padding, or no page: nothing is stored
+        if (!SEVERAL || s.per_token) return;                          // the whole warp's token
+        head = kNoHead;
+    }
+    const bool half = N > 2 && passes <= 2;
     T* out = static_cast<T*>(s.out);
     if (APPEND && s.cache) {
         const int64_t cell = place.page * s.out_batch + place.slot * s.out_token;
         if (a.format != kCacheSame) {
             LaneFactors<W, INTER, FULL> f;
             if (weight || pairs) f.read(weight, table, pairs, v);
-            uint8_t* q = static_cast<uint8_t*>(s.out) + cell + head * s.out_head;
-            float* scale = s.scale + place.page * s.scale_page + place.slot * s.scale_slot + head * s.scale_head;
+            const int at_head = head == kNoHead ? 0 : head;
+            uint8_t* q = static_cast<uint8_t*>(s.out) + cell + at_head * s.out_head;
+            float* scale = s.scale + place.page * s.scale_page + place.slot * s.scale_slot + at_head * s.scale_head;
 #pragma unroll
-            for (int p = 0; p < N; ++p, q += rows * s.out_head, scale += rows * s.scale_head) {
-                if (first + p * rows >= s.heads) break;
+            for (int p = 0; p < N; ++p, q += step * s.out_head, scale += step * s.scale_head) {
+                if (p >= passes) break;
                 float2 x[P], y[P];
                 if (weight) {
                     const float r = N > 1 ? rstd_of<T, INTER, GT>(xa[p], xb[p], G, lane, mean_of, a.eps) : rstd[p];
@@ -304,7 +342,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, kMinCtas) heads_rows(const __g
                 } else {
                     Elem<T, INTER>::unpack(xa[p], xb[p], x, y);
                 }
-                const bool here = head + p * rows < s.heads;
+                const bool here = head + p * step < s.heads;
                 if (a.format == kCacheInt8) store_row_8<true, INTER, GT, P>(q, scale, x, y, G, lane, here, j == 0, v);
                 else store_row_8<false, INTER, GT, P>(q, scale, x, y, G, lane, here, j == 0, v);
             }
@@ -325,17 +363,17 @@ __global__ void __launch_bounds__(kMaxWarps * 32, kMinCtas) heads_rows(const __g
         }
     }
     if (FULL && whole) {
-        T* row = out + (first + lane_row) * s.out_head;
-        const int64_t step = rows * s.out_head;
-        if (32 % G == 0 || lane_row < rows) {
+        if (head != kNoHead) {
+            T* row = out + head * s.out_head;
+            const int64_t further = step * s.out_head;
 #pragma unroll
-            for (int p = 0; p < N; ++p, row += step) st_stream(row + v.a, xa[p]), st_stream(row + v.b, xb[p]);
+            for (int p = 0; p < N; ++p, row += further) st_stream(row + v.a, xa[p]), st_stream(row + v.b, xb[p]);
         }
     } else {
 #pragma unroll
         for (int p = 0; p < N; ++p) {
-            if (head + p * rows < s.heads) {
-                T* row = out + (head + p * rows) * s.out_head;
+            if (head + p * step < s.heads) {
+                T* row = out + (head + p * step) * s.out_head;
                 if (v.has_a()) st_stream(row + v.a, xa[p]);
                 if (v.has_b()) st_stream(row + v.b, xb[p]);
             }
@@ -353,9 +391,9 @@ __global__ void __launch_bounds__(kWarps * 32) heads_elements(const __grid_const
     grid_dep_release();
     const int lane = threadIdx.x & 31;
     const uint32_t unit = blockIdx.x * kWarps + (threadIdx.x >> 5);
-    const uint32_t token = unit / a.chunks;
+    const uint32_t token = unit / a.shares;
     if (token >= a.total) return;
-    int head = static_cast<int>(unit - token * a.chunks), si = 0;
+    int head = static_cast<int>(unit - token * a.shares), si = 0;
     while (head >= a.seg[si].heads) head -= a.seg[si++].heads;
     const HeadSegment& s = a.seg[si];
     const uint32_t batch = token / a.tokens, at = token - batch * a.tokens;
@@ -433,10 +471,42 @@ bool whole_vectors(const HeadsArgs& a, int W) {
     return true;
 }
 
+// Shares the rows of `tokens` tokens out among warps.
+inline void share_out_tokens(HeadsArgs& a, int tokens, int passes, int rows) {
+    a.per_cta = tokens;
+    a.shares = 0;
+    for (int i = 0; i < a.segments; ++i) {
+        HeadSegment& s = a.seg[i];
+        s.groups_of_token = (s.heads + passes - 1) / passes;
+        s.groups_factor = 1024 / s.groups_of_token + 1;  // n * this >> 10 is n / groups_of_token for n and that below 32
+        s.tokens_of_share = std::min(tokens, s.groups_of_token <= rows ? rows / s.groups_of_token : 1);
+        const bool several = passes > 1 && s.tokens_of_share > 1;
+        s.per_token = several ? 0 : (s.heads + rows * passes - 1) / (rows * passes);
+        s.shares = several ? (tokens + s.tokens_of_share - 1) / s.tokens_of_share : tokens * s.per_token;
+        a.shares += s.shares;
+    }
+}
+
+// The tokens to a CTA that take the fewest instructions a token: some 300 for a
+// share before its rows, 90 for 32 angles, which every CTA of the tokens computes.
+// Single rows keep to a token.
+inline void share_out(HeadsArgs& a, int passes, int rows) {
+    int best = 1;
+    double least = 0;
+    for (int tokens = 1; tokens <= (passes == 1 ? 1 : kMaxTokens) && tokens * a.rope.pairs <= 1024; ++tokens) {
+        share_out_tokens(a, tokens, passes, rows);
+        const int turns = (a.shares + kMaxWarps - 1) / kMaxWarps;
+        const double cost = (300.0 * a.shares + 90.0 * turns * ((tokens * a.rope.pairs + 31) / 32)) / tokens;
+        if (tokens == 1 || cost < 0.9 * least) best = tokens, least = cost;
+    }
+    share_out_tokens(a, best, passes, rows);
+}
+
 template <typename T, bool INTER, bool APPEND, int GT>
 cudaError_t launch_rows(const HeadsArgs& a, int passes, int G, dim3 grid, dim3 block, size_t smem, cudaStream_t st) {
-    return passes == 1 ? launch_with_pdl(heads_rows<T, INTER, APPEND, GT, 1>, grid, block, smem, st, a, G)
-                       : launch_with_pdl(heads_rows<T, INTER, APPEND, GT, 4>, grid, block, smem, st, a, G);
+    return passes == 1      ? launch_with_pdl(heads_rows<T, INTER, APPEND, GT, 1, false>, grid, block, smem, st, a, G)
+           : a.per_cta == 1 ? launch_with_pdl(heads_rows<T, INTER, APPEND, GT, 4, false>, grid, block, smem, st, a, G)
+                            : launch_with_pdl(heads_rows<T, INTER, APPEND, GT, 4, true>, grid, block, smem, st, a, G);
 }
 
 // The head sizes with kernels of their own: 64, 80, 96, 112, 128, 192 and 256.
@@ -459,9 +529,9 @@ cudaError_t launch_heads_rows(HeadsArgs a, int sms, cudaStream_t st) {
     constexpr int W = Elem<T, false>::W;
     if (APPEND) a.by_page = Divider(a.page_size);
     if (!whole_vectors(a, W)) {
-        a.chunks = 0;
-        for (int i = 0; i < a.segments; ++i) a.chunks += a.seg[i].heads;
-        const int64_t units = static_cast<int64_t>(a.total) * a.chunks;
+        a.shares = 0;
+        for (int i = 0; i < a.segments; ++i) a.shares += a.seg[i].heads;
+        const int64_t units = static_cast<int64_t>(a.total) * a.shares;
         return launch_with_pdl(heads_elements<T, APPEND>, dim3(static_cast<unsigned>((units + kWarps - 1) / kWarps)), dim3(kWarps * 32),
                                kWarps * a.dim * sizeof(float), st, a);
     }
@@ -469,21 +539,13 @@ cudaError_t launch_heads_rows(HeadsArgs a, int sms, cudaStream_t st) {
     // Four rows of a group to a share where that leaves every SM its warps: they
     // are in flight together and spread what a warp does before them.
     int passes = 4;
-    for (;; passes = 1) {
-        a.chunks = 0;
-        for (int i = 0; i < a.segments; ++i) {
-            a.seg[i].chunks = (a.seg[i].heads + rows * passes - 1) / (rows * passes);
-            a.chunks += a.seg[i].chunks;
-        }
-        if (passes == 1 || static_cast<int64_t>(a.total) * a.chunks >= kManyShares * sms) break;
-    }
-    // a warp to each share, in several CTAs where a token has many; tokens of one share side by side
-    a.turns = (a.chunks + kMaxWarps - 1) / kMaxWarps;
-    const int warps = (a.chunks + a.turns - 1) / a.turns;
-    a.per_cta = a.turns == 1 ? kMaxWarps / warps : 1;
+    share_out(a, passes, rows);
+    if ((static_cast<int64_t>(a.total) + a.per_cta - 1) / a.per_cta * a.shares < many_shares(APPEND) * sms) share_out(a, passes = 1, rows);
+    a.turns = (a.shares + kMaxWarps - 1) / kMaxWarps;
+    const int warps = (a.shares + a.turns - 1) / a.turns;
     a.by_turns = Divider(a.turns);
     a.by_tokens = Divider(a.tokens);
-    const dim3 grid((a.total + a.per_cta - 1) / a.per_cta * a.turns), block(warps * a.per_cta * 32);
+    const dim3 grid((a.total + a.per_cta - 1) / a.per_cta * a.turns), block(warps * 32);
     const size_t smem = a.per_cta * a.rope.pairs * sizeof(float2);
     return a.rope.interleaved ? launch_lanes<T, true, APPEND>(a, passes, G, grid, block, smem, st)
                               : launch_lanes<T, false, APPEND>(a, passes, G, grid, block, smem, st);

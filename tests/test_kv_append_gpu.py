@@ -104,6 +104,8 @@ STEPS = [  # past, new, page, query heads, key heads, head_dim, rotated
     ([4, 8, 1], [3, 5, 1], 16, 2, 3, 7, 6),
     ([9, 500, 0], [2000, 1, 3003], 64, 17, 9, 64, 64),  # several rows to a warp
     ([0, 5], [1500, 1011], 128, 40, 8, 128, 64),
+    ([3, 0, 100, 7] * 10, [100, 101, 1, 50] * 10, 16, 8, 2, 128, 128),  # several tokens to a warp
+    ([7] * 40, [101] * 40, 10, 3, 1, 80, 80),
 ]
 
 
@@ -134,6 +136,27 @@ def test_append(past, new, page, hq, hk, dim, rot, kind, cell):
                 t.copy_(old)
         assert s.call(rates=rates_of(rot), layout=layout, magnitude=1.25 if rot else 1.0, **({"k_weight": s.kw} if norm else {})) is None
         assert all(a is None or torch.equal(bits(a), bits(b)) for a, b in zip(after, s.copy()))
+
+
+@pytest.mark.parametrize("cell", ["same", E4M3])
+@pytest.mark.parametrize("dim", [128, 80])
+def test_padding_among_many_tokens(cell, dim):
+    # padded sequences and missing pages beside others in one warp
+    g = gen(27)
+    past = [(-1 if n % 5 == 3 else 3 * n) for n in range(300)]
+    s = Step(g, past, [n % 17 for n in range(300)], 8, 8, 2, dim, BF, None if cell == "same" else cell)
+    gone = torch.arange(0, 300, 7)
+    s.table[gone.cuda(), 1] = s.pages + 5
+    before = s.copy()
+    q_out = torch.full_like(s.q, 9.0)
+    s.call(q=s.q, rates=rates_of(dim), q_out=q_out)
+    used = s.used()
+    stored = used & ~((s.seq % 7 == 0) & (s.place // 8 == 1))
+    assert torch.all(q_out[~used] == 9.0)
+    y, size = turn(s.q, s.place, frequencies(dim))
+    close(q_out[used], y[used], TURN * size[used])
+    y, size = turn(s.k, s.place, frequencies(dim))
+    s.check(before, y, TURN * size, stored)
 
 
 @pytest.mark.parametrize("cell", ["same", E4M3])

@@ -32,7 +32,7 @@ def check(got, x, w, eps, positions, freq, magnitude=1.0, layout="half"):
 SHAPES = [(1, 1, 1, 1, 64, 64), (16, 1, 32, 8, 128, 128), (3, 5, 6, 2, 128, 64), (2, 33, 5, 1, 80, 80), (1, 257, 3, 3, 96, 48),
           (1, 40, 9, 3, 256, 256), (1, 3, 2, 2, 512, 512), (1, 19, 3, 1, 80, 20), (2, 11, 2, 1, 36, 30), (1, 9, 3, 2, 7, 6),
           (1, 5, 2, 2, 8, 2), (1, 5, 2, 2, 8, 0), (1, 7, 3, 2, 1, 0), (2, 50, 4, 2, 64, 0), (1, 1500, 12, 12, 64, 64), (2, 700, 40, 8, 128, 128), (1, 10007, 3, 1, 128, 64),
-          (2, 2503, 9, 7, 96, 96), (1, 1201, 72, 8, 128, 128), (5, 601, 33, 1, 256, 256), (1, 3001, 17, 1, 64, 0)]
+          (2, 2503, 9, 7, 96, 96), (1, 1201, 72, 8, 128, 128), (5, 601, 33, 1, 256, 256), (1, 3001, 17, 1, 64, 0), (1, 5003, 8, 2, 128, 128), (2, 2001, 2, 1, 80, 80), (3, 1111, 16, 3, 64, 64)]
 
 
 @pytest.mark.parametrize("layout", ["half", "interleaved"])

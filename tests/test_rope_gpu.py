@@ -58,7 +58,8 @@ def test_rope(batch, tokens, hq, hk, dim, rot, kind, layout):
 @pytest.mark.parametrize("layout", ["half", "interleaved"])
 @pytest.mark.parametrize("kind", [BF, F32])
 @pytest.mark.parametrize("batch,tokens,hq,hk,dim,rot", [(3, 3337, 1, 0, 64, 64), (1, 10007, 3, 1, 128, 64), (2, 2503, 9, 7, 96, 96), (1, 4001, 24, 8, 80, 80),
-                                                        (1, 1201, 72, 8, 128, 128), (5, 601, 33, 1, 256, 256), (1, 3001, 17, 1, 64, 32)])
+                                                        (1, 1201, 72, 8, 128, 128), (5, 601, 33, 1, 256, 256), (1, 3001, 17, 1, 64, 32), (1, 5003, 8, 2, 128, 128),
+                                                        (2, 2001, 2, 1, 80, 80), (1, 4003, 16, 5, 64, 64), (3, 1111, 4, 1, 192, 64), (1, 2999, 7, 3, 112, 112)])
 def test_many_rows(batch, tokens, hq, hk, dim, rot, kind, layout):
     g = gen(tokens + dim)
     q = heads(g, batch, tokens, hq, dim, kind=kind)
