@@ -23,14 +23,15 @@ namespace nf {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kCtasPerSm = 4;
-// What a token's angles take, in passes: the CTAs of 8 key heads (2 passes a
-// token) were the last ones where only passes counted (16384 tokens of 64 + 8
-// heads: 181 us, with 1 165, 2 165, 4 160, 6 161).
-constexpr int kTurnPasses = 4;
-// Two passes ahead: with one ahead 16384 tokens of 72 heads of 128 took 165 us for
-// 144, with three 157, with four CTAs to an SM (five: 220 us, its registers spill).
+// Three CTAs to an SM and two passes ahead (16384 tokens of 72 heads of 128: 140 us;
+// four CTAs, whose registers spill a little, 144, two 166; with four one pass
+// ahead 165 and three 157, with five CTAs 220).
+constexpr int kCtasPerSm = 3;
 constexpr int kStages = 3;
+// What a token's angles take, in passes: where only passes counted, the CTAs of 8
+// key heads (two passes a token) were the last ones (0: 181 us with four CTAs to
+// an SM, 1 165; with three CTAs 1 140, 2 141, 4 144).
+constexpr int kTurnPasses = 1;
 
 // What a warp walks: passes [first, end) of its segment, `per_token` to a token.
 struct Stretch {
