@@ -261,3 +261,42 @@ def test_binding_constants_match_the_header():
     for name in ("NF_ROPE_HALF", "NF_ROPE_INTERLEAVED", "NF_ROPE_PLAIN", "NF_ROPE_LINEAR", "NF_ROPE_NTK", "NF_ROPE_PARTS", "NF_CACHE_SAME",
                  "NF_CACHE_E4M3", "NF_CACHE_INT8"):
         assert getattr(nf, name) == int(re.search(rf"\b{name} = (\d+)", src).group(1)), name
+
+
+def test_overlaps_are_never_let_through():
+    # random views of one small buffer against the bytes that they cover; calls that are let through end at the short
+    # workspace, so nothing is ever launched
+    import random
+    rng = random.Random(5)
+    late = (nf.NF_ERR_WORKSPACE_TOO_SMALL, nf.NF_ERR_CUDA)
+    dim, let, refused = 4, 0, 0
+
+    def covered(base, n, strides):
+        return [base + 2 * (b * strides[0] + t * strides[1] + h * strides[2] + e) for b in range(n[0]) for t in range(n[1]) for h in range(n[2])
+                for e in range(dim)]
+    for _ in range(4000):
+        n = (rng.choice([1, 2, 3]), rng.choice([1, 2, 4]))
+        views = []
+        for heads in (rng.choice([1, 2, 3]), rng.choice([1, 2])):
+            order = rng.sample(range(3), 3)
+            sizes = (n[0], n[1], heads)
+            strides, step = [0, 0, 0], dim * rng.choice([1, 1, 2, 3])
+            for d in order:
+                strides[d] = step
+                step *= sizes[d] * rng.choice([1, 1, 2])
+            if views and rng.random() < 0.7:  # the same steps as the other
+                strides = views[0][2]
+            views.append((sizes, A + 2 * rng.choice([0, 1, 4, 8, 12, 16, 24, 32, 48, 64, 100]), strides))
+        q, k = (nf.Heads(base, *strides, sizes[2]) for sizes, base, strides in views)
+        far = [nf.Heads(x << 36, 10 ** 6, 10 ** 4, 100, h) for x, h in ((2, q.heads), (3, k.heads), (4, q.heads), (5, k.heads))]
+        bytes_of = [covered(base, sizes, strides) for sizes, base, strides in views]
+        own = any(len(set(b)) < len(b) for b in bytes_of)
+        shared = own or bool(set(bytes_of[0]) & set(bytes_of[1]))
+        # both as outputs; and k as an input beside the output q
+        for dk, dk_in in ((k, far[1]), (far[3], k)):
+            st = nf.nf_qk_rmsnorm_rope_bwd(q, K, far[0], far[2], E, dk, K + 4096, far[1], dk_in, F, nf.NF_BF16, n[0], n[1], dim, 1e-6, None, L, 0, None)
+            bad = shared if dk is k else len(set(bytes_of[0])) < len(bytes_of[0]) or bool(set(bytes_of[0]) & set(bytes_of[1]))
+            assert st == nf.NF_ERR_INVALID_ARG or (st in late and not bad), (views, st)
+            let += st in late
+            refused += bad
+    assert let > 1000 and refused > 1000
