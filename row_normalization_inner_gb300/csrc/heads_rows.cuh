@@ -100,7 +100,7 @@ __device__ __forceinline__ void store_row_8(uint8_t* to, float* scale_to, float2
 // Where a token of an append stands.
 struct Place {
     int64_t position;  // in its sequence
-    int page;          // -1: not stored
+    int64_t entry;     // of the table, for its page; -1: it has none
     int slot;          // -1: the token belongs to no sequence
 };
 
@@ -113,17 +113,21 @@ __device__ __forceinline__ Place place_in(const HeadsArgs& a, int token, int seq
     const uint32_t column = divide(place, a.by_page);
     p.position = place;
     p.slot = static_cast<int>(place - column * static_cast<uint32_t>(a.page_size));
-    if (column < static_cast<uint32_t>(a.max_pages)) {
-        const int page = a.table[seq * a.table_stride + column];
-        if (static_cast<uint32_t>(page) < static_cast<uint32_t>(a.pages)) p.page = page;
-    }
+    if (column < static_cast<uint32_t>(a.max_pages)) p.entry = seq * a.table_stride + column;
     return p;
+}
+
+// Its page, or -1 where the cache has none for it.  Only those ask that store there.
+__device__ __forceinline__ int page_of(const HeadsArgs& a, const Place& p) {
+    if (p.entry < 0) return -1;
+    const int page = a.table[p.entry];
+    return static_cast<uint32_t>(page) < static_cast<uint32_t>(a.pages) ? page : -1;
 }
 
 // All lanes of a warp call this.  The sequence of a token is the last one that
 // starts at or before it; the starts are searched 32 ways at a time, and the
 // last 32 candidates' lengths come with them, so that the step costs one load's
-// latency for each factor of 32 of the sequences and one for the page.
+// latency for each factor of 32 of the sequences.
 __device__ __forceinline__ Place find_place(const HeadsArgs& a, int token, int lane) {
     if (!a.starts) return place_in(a, token, token, token, token < a.seqs ? a.past[token] : -1);
     const int behind = a.starts[a.seqs];
@@ -316,20 +320,21 @@ __global__ void __launch_bounds__(kMaxWarps * 32, kMinCtas) heads_rows(const __g
     if (N == 1 && weight) rstd[0] = rstd_of<T, INTER, GT>(xa[0], xb[0], G, lane, mean_of, a.eps);
     if (a.rope.pairs) __syncthreads();
     if (!real) return;
-    if (APPEND && (place.slot < 0 || (s.cache && place.page < 0))) {  // padding, or no page: nothing is stored
-        if (!SEVERAL || s.per_token) return;                          // the whole warp's token
+    const int page = APPEND && s.cache ? page_of(a, place) : 0;
+    if (APPEND && (place.slot < 0 || page < 0)) {  // padding, or no page: nothing is stored
+        if (!SEVERAL || s.per_token) return;       // the whole warp's token
         head = kNoHead;
     }
     const bool half = N > 2 && passes <= 2;
     T* out = static_cast<T*>(s.out);
     if (APPEND && s.cache) {
-        const int64_t cell = place.page * s.out_batch + place.slot * s.out_token;
+        const int64_t cell = page * s.out_batch + place.slot * s.out_token;
         if (a.format != kCacheSame) {
             LaneFactors<W, INTER, FULL> f;
             if (weight || pairs) f.read(weight, table, pairs, v);
             const int at_head = head == kNoHead ? 0 : head;
             uint8_t* q = static_cast<uint8_t*>(s.out) + cell + at_head * s.out_head;
-            float* scale = s.scale + place.page * s.scale_page + place.slot * s.scale_slot + at_head * s.scale_head;
+            float* scale = s.scale + page * s.scale_page + place.slot * s.scale_slot + at_head * s.scale_head;
 #pragma unroll
             for (int p = 0; p < N; ++p, q += step * s.out_head, scale += step * s.scale_head) {
                 if (p >= passes) break;
@@ -398,9 +403,11 @@ __global__ void __launch_bounds__(kWarps * 32) heads_elements(const __grid_const
     const HeadSegment& s = a.seg[si];
     const uint32_t batch = token / a.tokens, at = token - batch * a.tokens;
     Place place{0, -1, -1};
+    int64_t page = 0;
     if constexpr (APPEND) {
         place = find_place(a, static_cast<int>(token), lane);
-        if (place.slot < 0 || (s.cache && place.page < 0)) return;
+        page = s.cache ? page_of(a, place) : 0;
+        if (place.slot < 0 || page < 0) return;
     }
     const int dim = a.dim, pairs = s.rotate ? a.rope.pairs : 0;
     float* row = staged + (threadIdx.x >> 5) * dim;
@@ -428,7 +435,7 @@ __global__ void __launch_bounds__(kWarps * 32) heads_elements(const __grid_const
         __syncwarp();
     }
     if (APPEND && s.cache) {
-        const int64_t first = place.page * s.out_batch + place.slot * s.out_token + head * s.out_head;
+        const int64_t first = page * s.out_batch + place.slot * s.out_token + head * s.out_head;
         if (a.format != kCacheSame) {
             uint32_t top = 0;
             for (int i = lane; i < dim; i += 32) top = max(top, __float_as_uint(fabsf(row[i])));
@@ -440,7 +447,7 @@ __global__ void __launch_bounds__(kWarps * 32) heads_elements(const __grid_const
                 const uint32_t q = int8 ? quant2<true>(row[i], 0.f, scale, inverse) : quant2<false>(row[i], 0.f, scale, inverse);
                 out[i] = fine ? static_cast<uint8_t>(q) : 0;
             }
-            if (lane == 0) s.scale[place.page * s.scale_page + place.slot * s.scale_slot + head * s.scale_head] = scale;
+            if (lane == 0) s.scale[page * s.scale_page + place.slot * s.scale_slot + head * s.scale_head] = scale;
         } else {
             T* out = static_cast<T*>(s.out) + first;
             for (int i = lane; i < dim; i += 32) {
