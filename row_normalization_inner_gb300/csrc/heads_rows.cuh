@@ -6,11 +6,15 @@
 //   out = y rounded once, in the heads' type; or, for an 8-bit cache,
 //   scale = max(max|y| / Q, 2^-100), q = y / scale rounded to nearest
 //
-// Bound by memory: each element is read once and written once.  A warp takes a
-// token and up to `passes` times 32 / G of its heads (heads.cuh), so that the
-// token's angles -- two sines and cosines a lane at 64 pairs -- are computed
-// once for all of them and wait in shared memory; a group of G lanes holds a
-// row, and the row's sums stay in the warp.
+// Bound by memory: each element is read once and written once (16384 tokens of
+// 64 + 8 heads of 128 in bf16: turned 89.6 us, 6.74 TB/s, a copy's rate; normalized
+// too 97.4 us, 6.2 TB/s).  A group of lanes holds a row (heads.cuh), so that its
+// sums stay in the warp; a warp has four rows of every group in flight.  What it
+// does before them -- its share, addresses, angles, weights -- is a good half of
+// its instructions and the reason for most of what follows: the angles are
+// computed once for a token's warps, the weights are folded into them, and few
+// heads share a warp with other tokens' (16384 tokens of 8 + 2 heads: 16 us, 25
+// with a warp to each).
 #pragma once
 
 #include <algorithm>
@@ -149,10 +153,11 @@ __device__ __forceinline__ Place find_place(const HeadsArgs& a, int token, int l
     return place_in(a, token, lo, first, first >= 0 && first <= token && token < behind ? past : -1);
 }
 
-// Warps of a CTA at most, and CTAs that the registers of an SM hold (80 a thread).
-// Small ones take turns best: 16384 tokens of 64 + 8 heads with 3, 5 and 10 warps
-// take 103, 102 and 103 us, of 32 + 8 heads 54, 57 and 57, an append to an 8-bit
-// cache (8192 tokens of 64 + 8 + 8) 63, 71 and 69.
+// Warps of a CTA at most, and CTAs that the registers of an SM hold (80 a thread,
+// some spilled).  With 3, 5 (of 96 registers) and 9 warps 16384 tokens of 64 + 8
+// heads take 97, 95 and 95 us, of 32 + 8 heads 50, 52 and 52 turned and 54, 57 and
+// 57 normalized too, an append to an 8-bit cache (8192 tokens of 64 + 8 + 8) 62, 70
+// and 67.
 constexpr int kMaxWarps = 3;
 constexpr int kMinCtas = 7;
 // Shares of four rows per SM from which these are taken rather than single rows
@@ -225,27 +230,36 @@ __global__ void __launch_bounds__(kMaxWarps * 32, kMinCtas) heads_rows(const __g
     const int rows = 32 / G, group = lane / G, j = lane - group * G;
     // the warp's share: queries, keys or values, which tokens and which rows of them
     int share = static_cast<int>(blockIdx.x - cta_of_tokens * a.turns) * warps + warp, si = 0;
-    const bool real = share < a.shares;
+    bool real = share < a.shares;
     if (!real) share = 0;
     while (share >= a.seg[si].shares) share -= a.seg[si++].shares;
     const HeadSegment& s = a.seg[si];
-    int nth = 0, head, step = rows, passes;  // the lane's token in the CTA and its first head; how far the next is; how many there are (of any lane)
-    bool whole;                              // every group has N rows
+    // The lane's token in the CTA and its first head, how far its next head is, and
+    // how many heads the share has for a group at most.  Lanes without a row of
+    // their own (behind the last whole group, or the last token) are not `mine`:
+    // they load along with the share's first, and store nothing.
+    int nth = 0, head, step = rows, passes;
+    bool mine, whole;  // whole: every group has N rows
     if (!SEVERAL || s.per_token) {
         if (SEVERAL) nth = share / s.per_token;
         const int first = (share - (SEVERAL ? nth * s.per_token : 0)) * N * rows;
-        head = group < rows ? first + group : kNoHead;  // lanes behind the last whole group hold none
+        if (SEVERAL) real = real && nth < tokens;
+        mine = (FULL && 32 % (GT ? GT : 1) == 0) || group < rows;
+        head = first + (mine ? group : 0);
         passes = min(N, (s.heads - first + rows - 1) / rows);
-        whole = real && first + N * rows <= s.heads && nth < tokens;
+        whole = real && first + N * rows <= s.heads;
     } else {
         const int in_share = (group * s.groups_factor) >> 10, first = share * s.tokens_of_share;  // group / groups_of_token
         nth = first + in_share;
-        head = in_share < s.tokens_of_share && nth < tokens ? group - in_share * s.groups_of_token : kNoHead;
+        real = real && first < tokens;
+        mine = in_share < s.tokens_of_share && nth < tokens;
+        if (!mine) nth = first;
         step = s.groups_of_token;
+        head = mine ? group - in_share * step : 0;
         passes = (s.heads + step - 1) / step;
-        whole = real && s.heads == N * step && first + s.tokens_of_share <= tokens;
+        whole = real && s.heads == N * step;
     }
-    if (SEVERAL && nth >= tokens) head = kNoHead, nth = 0;
+    if (SEVERAL && !real) nth = 0;
     const uint32_t token = first_token + nth;
     const uint32_t batch = APPEND ? 0 : divide(token, a.by_tokens), at = token - batch * a.tokens;
     const int pairs = s.rotate ? a.rope.pairs : 0;
@@ -255,14 +269,14 @@ __global__ void __launch_bounds__(kMaxWarps * 32, kMinCtas) heads_rows(const __g
     grid_dep_wait();
     grid_dep_release();
     // what the angles need; for a single row it is asked for first, as it is waited for first
-    const int mine = warp * 32 + lane, threads = warps * 32;
+    const int thread = threadIdx.x, threads = warps * 32;
     int64_t position = 0;
     uint64_t rate = 0;
     const auto ask = [&] {
-        if (mine < a.rope.pairs * tokens) {  // of the thread's first pair
-            const int t = SEVERAL ? mine / a.rope.pairs : 0;
+        if (thread < a.rope.pairs * tokens) {  // of the thread's first pair
+            const int t = SEVERAL ? thread / a.rope.pairs : 0;
             if (a.rope.positions) position = SEVERAL ? position_of(a, first_token + t) : position_at(a.rope, batch, at);
-            rate = a.rope.rates[mine - t * a.rope.pairs];
+            rate = a.rope.rates[thread - t * a.rope.pairs];
         }
     };
     if (N == 1) ask();
@@ -270,7 +284,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, kMinCtas) heads_rows(const __g
     {
         const T* in = static_cast<const T*>(s.in) + batch * s.in_batch + at * s.in_token;
         if (FULL && whole) {
-            const T* row = in + (head == kNoHead ? 0 : head) * s.in_head;
+            const T* row = in + head * s.in_head;
             const int64_t further = step * s.in_head;
 #pragma unroll
             for (int p = 0; p < N; ++p, row += further) xa[p] = ld_stream(row + v.a), xb[p] = ld_stream(row + v.b);
@@ -278,7 +292,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, kMinCtas) heads_rows(const __g
 #pragma unroll
             for (int p = 0; p < N; ++p) {
                 xa[p] = xb[p] = make_uint4(0, 0, 0, 0);
-                if (real && p < passes) {  // the same for all lanes; a row behind the last is the last
+                if (real && p < passes) {  // the same for all lanes; a head behind the last is the last, which is in the share
                     const T* row = in + min(head + p * step, s.heads - 1) * s.in_head;
                     if (v.has_a()) xa[p] = ld_stream(row + v.a);
                     if (v.has_b()) xb[p] = ld_stream(row + v.b);
@@ -299,9 +313,9 @@ __global__ void __launch_bounds__(kMaxWarps * 32, kMinCtas) heads_rows(const __g
     }
     if (a.rope.pairs) {
         float* table = reinterpret_cast<float*>(tables);
-        for (int i = mine; i < a.rope.pairs * tokens; i += threads) {
+        for (int i = thread; i < a.rope.pairs * tokens; i += threads) {
             const int t = SEVERAL ? i / a.rope.pairs : 0, p = i - t * a.rope.pairs;
-            if (i != mine) {
+            if (i != thread) {
                 if (SEVERAL && a.rope.positions) position = position_of(a, first_token + t);
                 rate = a.rope.rates[p];
             }
@@ -323,7 +337,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, kMinCtas) heads_rows(const __g
     const int page = APPEND && s.cache ? page_of(a, place) : 0;
     if (APPEND && (place.slot < 0 || page < 0)) {  // padding, or no page: nothing is stored
         if (!SEVERAL || s.per_token) return;       // the whole warp's token
-        head = kNoHead;
+        mine = false;
     }
     const bool half = N > 2 && passes <= 2;
     T* out = static_cast<T*>(s.out);
@@ -332,9 +346,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32, kMinCtas) heads_rows(const __g
         if (a.format != kCacheSame) {
             LaneFactors<W, INTER, FULL> f;
             if (weight || pairs) f.read(weight, table, pairs, v);
-            const int at_head = head == kNoHead ? 0 : head;
-            uint8_t* q = static_cast<uint8_t*>(s.out) + cell + at_head * s.out_head;
-            float* scale = s.scale + page * s.scale_page + place.slot * s.scale_slot + at_head * s.scale_head;
+            uint8_t* q = static_cast<uint8_t*>(s.out) + cell + head * s.out_head;
+            float* scale = s.scale + page * s.scale_page + place.slot * s.scale_slot + head * s.scale_head;
 #pragma unroll
             for (int p = 0; p < N; ++p, q += step * s.out_head, scale += step * s.scale_head) {
                 if (p >= passes) break;
@@ -347,7 +360,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, kMinCtas) heads_rows(const __g
                 } else {
                     Elem<T, INTER>::unpack(xa[p], xb[p], x, y);
                 }
-                const bool here = head + p * step < s.heads;
+                const bool here = mine && head + p * step < s.heads;
                 if (a.format == kCacheInt8) store_row_8<true, INTER, GT, P>(q, scale, x, y, G, lane, here, j == 0, v);
                 else store_row_8<false, INTER, GT, P>(q, scale, x, y, G, lane, here, j == 0, v);
             }
@@ -368,7 +381,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, kMinCtas) heads_rows(const __g
         }
     }
     if (FULL && whole) {
-        if (head != kNoHead) {
+        if (mine) {
             T* row = out + head * s.out_head;
             const int64_t further = step * s.out_head;
 #pragma unroll
@@ -377,7 +390,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, kMinCtas) heads_rows(const __g
     } else {
 #pragma unroll
         for (int p = 0; p < N; ++p) {
-            if (head + p * step < s.heads) {
+            if (mine && head + p * step < s.heads) {
                 T* row = out + (head + p * step) * s.out_head;
                 if (v.has_a()) st_stream(row + v.a, xa[p]);
                 if (v.has_b()) st_stream(row + v.b, xb[p]);
