@@ -765,7 +765,8 @@ def rope_fwd(q, k, positions, rates, layout: str = "half", magnitude: float = 1.
     need no copy); k may be None.  positions: int32 or int64, [batch, tokens] or
     [tokens].  rates: rope_rates' (2 * len(rates) elements of a head are
     turned, the rest left as they are).  layout: a pair is elements i and
-    i + len(rates) ("half") or 2i and 2i + 1 ("interleaved").  q_out may be q."""
+    i + len(rates) ("half") or 2i and 2i + 1 ("interleaved").  q_out may be q;
+    outputs made here are parts of one allocation."""
     if stream is not None:
         return _on(stream, rope_fwd, q, k, positions, rates, layout, magnitude, q_out, k_out)
     return _result((_native or _helpers()).rope(q, k, positions, rates, layout, magnitude, q_out, k_out, False),

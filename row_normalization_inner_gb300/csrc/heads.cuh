@@ -269,6 +269,23 @@ __device__ __forceinline__ void copy16(uint4* to, const void* from, bool there) 
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
+// As launch_with_pdl, the arguments (600 bytes) handed to the driver where they are.
+template <typename Args>
+cudaError_t launch_args(void (*kernel)(Args, int), dim3 grid, dim3 block, size_t smem, cudaStream_t st, const Args& args, int lanes) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    void* pointers[] = {const_cast<Args*>(&args), &lanes};
+    return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(kernel), pointers);
+}
+
 constexpr int kNoHead = 1 << 30;  // of a lane without a row; far from overflow when passes are added
 
 // Lanes of a group.  Sizes whose lanes all have two whole vectors and that heads

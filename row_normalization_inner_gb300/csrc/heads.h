@@ -90,12 +90,12 @@ struct HeadsArgs {
     CacheFormat format;
 };
 // `append`: the call has a sequence per token, and segments that go to a cache.
-cudaError_t launch_heads(const HeadsArgs& a, bool f32, bool append, int sms, cudaStream_t st);
+cudaError_t launch_heads(HeadsArgs& a, bool f32, bool append, int sms, cudaStream_t st);
 // By type, each in a file of its own so that they are compiled side by side.
-cudaError_t launch_heads_bf16(const HeadsArgs& a, int sms, cudaStream_t st);
-cudaError_t launch_heads_f32(const HeadsArgs& a, int sms, cudaStream_t st);
-cudaError_t launch_append_bf16(const HeadsArgs& a, int sms, cudaStream_t st);
-cudaError_t launch_append_f32(const HeadsArgs& a, int sms, cudaStream_t st);
+cudaError_t launch_heads_bf16(HeadsArgs& a, int sms, cudaStream_t st);
+cudaError_t launch_heads_f32(HeadsArgs& a, int sms, cudaStream_t st);
+cudaError_t launch_append_bf16(HeadsArgs& a, int sms, cudaStream_t st);
+cudaError_t launch_append_f32(HeadsArgs& a, int sms, cudaStream_t st);
 
 struct HeadsGradArgs {
     HeadGradSegment seg[2];
@@ -109,7 +109,7 @@ struct HeadsGradArgs {
     float* partials;  // [CTAs][dim]
 };
 size_t heads_grad_workspace(int64_t dim, int sms);
-cudaError_t launch_heads_grad(const HeadsGradArgs& a, bool f32, int sms, cudaStream_t st);
+cudaError_t launch_heads_grad(HeadsGradArgs& a, bool f32, int sms, cudaStream_t st);
 // The passes over the rows, by type; a.seg[].ctas partials of each segment are left in a.partials.
 cudaError_t launch_heads_grad_bf16(HeadsGradArgs& a, int sms, cudaStream_t st);
 cudaError_t launch_heads_grad_f32(HeadsGradArgs& a, int sms, cudaStream_t st);

@@ -314,14 +314,14 @@ cudaError_t launch_lanes(const HeadsGradArgs& a, int G, dim3 grid, cudaStream_t 
     const size_t smem = kStages * 4 * kWarps * 32 * sizeof(uint4) + kWarps * a.rope.pairs * sizeof(float2);
     const int own = own_lanes<Elem<T, INTER>::W>(a.dim);
 #define NF_LANES(n) \
-    if (own == n) return launch_with_pdl(heads_grad_rows<T, INTER, n>, grid, dim3(kWarps * 32), smem, st, a, n);
+    if (own == n) return launch_args(heads_grad_rows<T, INTER, n>, grid, dim3(kWarps * 32), smem, st, a, n);
     if constexpr (sizeof(T) == 2) {
         NF_EACH_LANES_bf16(NF_LANES)
     } else {
         NF_EACH_LANES_f32(NF_LANES)
     }
 #undef NF_LANES
-    return launch_with_pdl(heads_grad_rows<T, INTER, 0>, grid, dim3(kWarps * 32), smem, st, a, G);
+    return launch_args(heads_grad_rows<T, INTER, 0>, grid, dim3(kWarps * 32), smem, st, a, G);
 }
 
 template <typename T>

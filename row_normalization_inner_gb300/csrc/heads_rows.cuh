@@ -497,36 +497,49 @@ inline void share_out_tokens(HeadsArgs& a, int tokens, int passes, int rows) {
     a.shares = 0;
     for (int i = 0; i < a.segments; ++i) {
         HeadSegment& s = a.seg[i];
-        s.groups_of_token = (s.heads + passes - 1) / passes;
-        s.groups_factor = 1024 / s.groups_of_token + 1;  // n * this >> 10 is n / groups_of_token for n and that below 32
-        s.tokens_of_share = std::min(tokens, s.groups_of_token <= rows ? rows / s.groups_of_token : 1);
-        const bool several = passes > 1 && s.tokens_of_share > 1;
-        s.per_token = several ? 0 : (s.heads + rows * passes - 1) / (rows * passes);
-        s.shares = several ? (tokens + s.tokens_of_share - 1) / s.tokens_of_share : tokens * s.per_token;
+        s.per_token = (s.heads + rows * passes - 1) / (rows * passes);
+        s.shares = tokens * s.per_token;
+        if (tokens > 1) {
+            s.groups_of_token = (s.heads + passes - 1) / passes;
+            s.groups_factor = 1024 / s.groups_of_token + 1;  // n * this >> 10 is n / groups_of_token for n and that below 32
+            s.tokens_of_share = std::min(tokens, rows / s.groups_of_token);
+            if (s.tokens_of_share > 1) s.per_token = 0, s.shares = (tokens + s.tokens_of_share - 1) / s.tokens_of_share;
+        }
         a.shares += s.shares;
     }
 }
 
-// The tokens to a CTA that take the fewest instructions a token: some 300 for a
-// share before its rows, 90 for 32 angles, which every CTA of the tokens computes.
-// Single rows keep to a token.
-inline void share_out(HeadsArgs& a, int passes, int rows) {
+// Rows of a group to a share, and the tokens to a CTA.  Four rows where that
+// leaves every SM its warps: they are in flight together and spread what a warp
+// does before them.  Then the tokens that take the fewest instructions each (some
+// 300 for a share before its rows, 90 for 32 angles, which every CTA of the tokens
+// computes).
+inline int share_out(HeadsArgs& a, int rows, int64_t many, int sms) {
+    const auto shares = [&] { return (static_cast<int64_t>(a.total) + a.per_cta - 1) / a.per_cta * a.shares; };
+    share_out_tokens(a, 1, 4, rows);
+    if (shares() < many * sms) {
+        share_out_tokens(a, 1, 1, rows);
+        return 1;
+    }
+    const int angles = (a.rope.pairs + 31) / 32;
     int best = 1;
-    double least = 0;
-    for (int tokens = 1; tokens <= (passes == 1 ? 1 : kMaxTokens) && tokens * a.rope.pairs <= 1024; ++tokens) {
-        share_out_tokens(a, tokens, passes, rows);
+    double least = 300.0 * a.shares + 90.0 * ((a.shares + kMaxWarps - 1) / kMaxWarps) * angles;
+    for (int tokens = 2; tokens <= kMaxTokens && tokens * a.rope.pairs <= 1024; ++tokens) {
+        share_out_tokens(a, tokens, 4, rows);
+        if (shares() < many * sms) break;
         const int turns = (a.shares + kMaxWarps - 1) / kMaxWarps;
         const double cost = (300.0 * a.shares + 90.0 * turns * ((tokens * a.rope.pairs + 31) / 32)) / tokens;
-        if (tokens == 1 || cost < 0.9 * least) best = tokens, least = cost;
+        if (cost < 0.9 * least) best = tokens, least = cost;
     }
-    share_out_tokens(a, best, passes, rows);
+    share_out_tokens(a, best, 4, rows);
+    return 4;
 }
 
 template <typename T, bool INTER, bool APPEND, int GT>
 cudaError_t launch_rows(const HeadsArgs& a, int passes, int G, dim3 grid, dim3 block, size_t smem, cudaStream_t st) {
-    return passes == 1      ? launch_with_pdl(heads_rows<T, INTER, APPEND, GT, 1, false>, grid, block, smem, st, a, G)
-           : a.per_cta == 1 ? launch_with_pdl(heads_rows<T, INTER, APPEND, GT, 4, false>, grid, block, smem, st, a, G)
-                            : launch_with_pdl(heads_rows<T, INTER, APPEND, GT, 4, true>, grid, block, smem, st, a, G);
+    return passes == 1      ? launch_args(heads_rows<T, INTER, APPEND, GT, 1, false>, grid, block, smem, st, a, G)
+           : a.per_cta == 1 ? launch_args(heads_rows<T, INTER, APPEND, GT, 4, false>, grid, block, smem, st, a, G)
+                            : launch_args(heads_rows<T, INTER, APPEND, GT, 4, true>, grid, block, smem, st, a, G);
 }
 
 // The head sizes with kernels of their own: 64, 80, 96, 112, 128, 192 and 256.
@@ -545,7 +558,7 @@ cudaError_t launch_lanes(const HeadsArgs& a, int passes, int lanes, dim3 grid, d
 }
 
 template <typename T, bool APPEND>
-cudaError_t launch_heads_rows(HeadsArgs a, int sms, cudaStream_t st) {
+cudaError_t launch_heads_rows(HeadsArgs& a, int sms, cudaStream_t st) {
     constexpr int W = Elem<T, false>::W;
     if (APPEND) a.by_page = Divider(a.page_size);
     if (!whole_vectors(a, W)) {
@@ -556,11 +569,7 @@ cudaError_t launch_heads_rows(HeadsArgs a, int sms, cudaStream_t st) {
                                kWarps * a.dim * sizeof(float), st, a);
     }
     const int G = lanes_of<W>(a.dim), rows = 32 / G;
-    // Four rows of a group to a share where that leaves every SM its warps: they
-    // are in flight together and spread what a warp does before them.
-    int passes = 4;
-    share_out(a, passes, rows);
-    if ((static_cast<int64_t>(a.total) + a.per_cta - 1) / a.per_cta * a.shares < many_shares(APPEND) * sms) share_out(a, passes = 1, rows);
+    const int passes = share_out(a, rows, many_shares(APPEND), sms);
     a.turns = (a.shares + kMaxWarps - 1) / kMaxWarps;
     const int warps = (a.shares + a.turns - 1) / a.turns;
     a.by_turns = Divider(a.turns);

@@ -50,8 +50,7 @@ size_t heads_grad_workspace(int64_t dim, int sms) {
 
 cudaError_t launch_heads_grad_bf16(HeadsGradArgs& a, int sms, cudaStream_t st) { return launch_heads_grad_rows<uint16_t>(a, sms, st); }
 
-cudaError_t launch_heads_grad(const HeadsGradArgs& args, bool f32, int sms, cudaStream_t st) {
-    HeadsGradArgs a = args;
+cudaError_t launch_heads_grad(HeadsGradArgs& a, bool f32, int sms, cudaStream_t st) {
     if (const cudaError_t e = f32 ? launch_heads_grad_f32(a, sms, st) : launch_heads_grad_bf16(a, sms, st)) return e;
     return a.dim % 4 || reinterpret_cast<uintptr_t>(a.partials) % 16
                ? launch_with_pdl(heads_grad_sum<1>, dim3(a.dim, a.segments), dim3(kSumThreads), 0, st, a)

@@ -3,6 +3,6 @@
 
 namespace nf {
 
-cudaError_t launch_append_bf16(const HeadsArgs& a, int sms, cudaStream_t st) { return launch_heads_rows<uint16_t, true>(a, sms, st); }
+cudaError_t launch_append_bf16(HeadsArgs& a, int sms, cudaStream_t st) { return launch_heads_rows<uint16_t, true>(a, sms, st); }
 
 }  // namespace nf
