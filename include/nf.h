@@ -460,9 +460,9 @@ nf_status nf_token_logprob_bwd(void* dlogits, int64_t dstride, const void* logit
  * that views of a projection's output, and orders other than [batch, tokens,
  * heads, head_dim], need no copy.  Pointers need the alignment of an element.
  * Rows whose pointers and strides are multiples of 16 bytes, of at most 64
- * 16-byte vectors and, in the half layout, with whole 16-byte vectors in each
- * rotated half run on vector kernels; others run element by element on a
- * slower one.  Strides are not negative.  The rows of an output are apart: in
+ * 16-byte vectors, and whose rotated part (in the half layout each half of it)
+ * is whole vectors run on vector kernels; others run element by element on
+ * slower ones.  Strides are not negative.  The rows of an output are apart: in
  * the order of its strides, each dimension steps over the ones inside it.  An
  * output overlaps nothing but where it says so; sets whose rows lie between
  * one another's (the queries and keys of one projection) do not overlap.
@@ -557,7 +557,8 @@ nf_status nf_qk_rmsnorm_rope_fwd(const nf_heads* q_out, const nf_heads* q, const
  * and so for the keys.  dq may be dq_out or q itself (same pointer and
  * strides), dk likewise.  workspace: 4-byte aligned, at least
  * nf_qk_rmsnorm_rope_bwd_workspace_size(head_dim) bytes on the device that
- * runs the call; contents irrelevant.  The order of every sum is fixed.  With
+ * runs the call; contents irrelevant, and no call that overlaps this one on the
+ * GPU may use it.  The order of every sum is fixed.  With
  * batch * tokens == 0 the weights' gradients are written with zeros. */
 size_t nf_qk_rmsnorm_rope_bwd_workspace_size(int64_t head_dim);
 nf_status nf_qk_rmsnorm_rope_bwd(const nf_heads* dq, float* dq_weight, const nf_heads* dq_out, const nf_heads* q,
@@ -599,7 +600,8 @@ typedef struct {
  * 8-bit rows: scale = max(max|y| / Q, 2^-100), Q = 448 (E4M3) or 127 (INT8),
  * q = y / scale rounded to nearest, ties to even; y is not rounded to the rows'
  * type before.  A row with a NaN or an infinity has scale NaN and q 0.
- * q_out and q may both be NULL.  table is [seqs, max_pages] int32. */
+ * q_out and q may both be NULL.  table is [seqs, max_pages] int32; seqs up to
+ * 2^30. */
 nf_status nf_kv_append(const nf_pages* k_cache, const nf_pages* v_cache, nf_cache_type cache_type, int64_t pages,
                        int32_t page_size, const nf_heads* k, const nf_heads* v, const void* k_weight,
                        const nf_heads* q_out, const nf_heads* q, const void* q_weight, nf_dtype type,

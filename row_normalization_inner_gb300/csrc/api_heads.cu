@@ -15,6 +15,7 @@ namespace {
 
 constexpr int64_t kMostStride = int64_t{1} << 40;
 constexpr int64_t kMostRows = 0x7FFFFFFF;
+constexpr int64_t kMostSeqs = 1 << 30;
 
 // What a set of rows covers: up to three dimensions over rows of `inner`
 // bytes.  Extents fit 128 bits whatever the arguments.
@@ -164,16 +165,19 @@ Rotation rotation_of(const nf_rope* r, float direction) {
 
 bool eps_ok(float eps) { return std::isfinite(eps) && eps > 0.f; }
 
-HeadSegment segment_of(const nf_heads* out, const nf_heads* in, const void* weight) {
+// A stride that is ever taken: that of a dimension of one may be anything.
+int64_t taken(int64_t stride, int64_t n) { return n > 1 ? stride : 0; }
+
+HeadSegment segment_of(const nf_heads* out, const nf_heads* in, const void* weight, int64_t batch, int64_t tokens) {
     HeadSegment s{};
     s.in = in->data;
-    s.in_batch = in->batch_stride, s.in_token = in->token_stride, s.in_head = in->head_stride;
+    s.in_batch = taken(in->batch_stride, batch), s.in_token = taken(in->token_stride, tokens), s.in_head = taken(in->head_stride, in->heads);
     s.weight = weight;
     s.heads = in->heads;
     s.rotate = true;
     if (out) {
         s.out = out->data;
-        s.out_batch = out->batch_stride, s.out_token = out->token_stride, s.out_head = out->head_stride;
+        s.out_batch = taken(out->batch_stride, batch), s.out_token = taken(out->token_stride, tokens), s.out_head = taken(out->head_stride, in->heads);
     }
     return s;
 }
@@ -213,7 +217,7 @@ nf_status heads_call(const nf_heads* q_out, const nf_heads* q, const void* q_wei
     int sms;
     if (nf_status st = device_sm_count(&sms)) return st;
     HeadsArgs a{};
-    for (int i = 0; i < sets; ++i) a.seg[i] = segment_of(outs[i], ins[i], norm ? weights[i] : nullptr);
+    for (int i = 0; i < sets; ++i) a.seg[i] = segment_of(outs[i], ins[i], norm ? weights[i] : nullptr, batch, tokens);
     a.segments = sets;
     a.rope = rotation_of(rope, direction);
     a.dim = static_cast<int>(head_dim);
@@ -360,10 +364,10 @@ nf_status nf_qk_rmsnorm_rope_bwd(const nf_heads* dq, float* dq_weight, const nf_
         HeadGradSegment& s = a.seg[i];
         s.dx = dxs[i]->data, s.dy = dys[i]->data, s.x = xs[i]->data;
         s.weight = weights[i], s.dweight = dweights[i];
-        s.dx_batch = dxs[i]->batch_stride, s.dx_token = dxs[i]->token_stride, s.dx_head = dxs[i]->head_stride;
-        s.dy_batch = dys[i]->batch_stride, s.dy_token = dys[i]->token_stride, s.dy_head = dys[i]->head_stride;
-        s.x_batch = xs[i]->batch_stride, s.x_token = xs[i]->token_stride, s.x_head = xs[i]->head_stride;
         s.heads = xs[i]->heads;
+        s.dx_batch = taken(dxs[i]->batch_stride, batch), s.dx_token = taken(dxs[i]->token_stride, tokens), s.dx_head = taken(dxs[i]->head_stride, s.heads);
+        s.dy_batch = taken(dys[i]->batch_stride, batch), s.dy_token = taken(dys[i]->token_stride, tokens), s.dy_head = taken(dys[i]->head_stride, s.heads);
+        s.x_batch = taken(xs[i]->batch_stride, batch), s.x_token = taken(xs[i]->token_stride, tokens), s.x_head = taken(xs[i]->head_stride, s.heads);
     }
     a.segments = sets;
     a.rope = rotation_of(rope, -1.f);
@@ -390,7 +394,7 @@ nf_status nf_kv_append(const nf_pages* k_cache, const nf_pages* v_cache, nf_cach
     if (nf_status st = sizes_ok(type, 1, tokens, head_dim, heads)) return st;
     if (nf_status st = rope_ok(rope, head_dim)) return st;
     if ((k_weight || q_weight) && !eps_ok(eps)) return NF_ERR_INVALID_ARG;
-    if (pages < 0 || pages > kMostRows || page_size < 1 || seqs < 0 || seqs > kMostRows - 1 || max_pages < 0 ||
+    if (pages < 0 || pages > kMostRows || page_size < 1 || seqs < 0 || seqs > kMostSeqs || max_pages < 0 ||
         !stride_ok(table_stride) || (seqs > 1 && table_stride < max_pages))
         return NF_ERR_INVALID_ARG;
     if (tokens == 0 || seqs == 0) return NF_OK;
@@ -429,13 +433,13 @@ nf_status nf_kv_append(const nf_pages* k_cache, const nf_pages* v_cache, nf_cach
     int sms;
     if (nf_status st = device_sm_count(&sms)) return st;
     HeadsArgs a{};
-    if (q) a.seg[a.segments++] = segment_of(q_out, q, q_weight);
+    if (q) a.seg[a.segments++] = segment_of(q_out, q, q_weight, 1, tokens);
     for (int i = 0; i < 2; ++i) {
         HeadSegment& s = a.seg[a.segments++];
-        s = segment_of(nullptr, i ? v : k, i ? nullptr : k_weight);
+        s = segment_of(nullptr, i ? v : k, i ? nullptr : k_weight, 1, tokens);
         const nf_pages* c = caches[i];
         s.out = c->data;
-        s.out_batch = c->page_stride, s.out_token = c->slot_stride, s.out_head = c->head_stride;
+        s.out_batch = taken(c->page_stride, pages), s.out_token = taken(c->slot_stride, page_size), s.out_head = taken(c->head_stride, k->heads);
         s.scale = c->scale;
         s.scale_page = c->scale_page_stride, s.scale_slot = c->scale_slot_stride, s.scale_head = c->scale_head_stride;
         s.rotate = i == 0;

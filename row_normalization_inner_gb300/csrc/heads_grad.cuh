@@ -232,59 +232,82 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) heads_grad_rows(const
 }
 
 // Any head size, stride and alignment: a warp's row in shared memory, element
-// by element (as heads_elements).
-template <typename T>
+// by element (as heads_elements), its token's angles beside it; the next row is
+// loaded meanwhile (16384 tokens of 32 heads of 128 from odd addresses: 333 us,
+// 837 without; whole vectors 55).
+template <typename T, int kPerLane>
 __global__ void __launch_bounds__(kWarps * 32) heads_grad_elements(const __grid_constant__ HeadsGradArgs a) {
     extern __shared__ float staged[];
     grid_dep_wait();
     grid_dep_release();
-    constexpr int kPerLane = kHeadMaxDim / 32;
     const int lane = threadIdx.x & 31, warp_in = threadIdx.x >> 5, dim = a.dim, pairs = a.rope.pairs;
     int cta = blockIdx.x, si = 0;
     if (cta >= a.seg[0].ctas) cta -= a.seg[0].ctas, si = 1;
     const HeadGradSegment& s = a.seg[si];
     const Stretch r = stretch_of(static_cast<int64_t>(a.total) * s.heads, cta * kWarps + warp_in, s.ctas * kWarps);
-    float* g = staged + warp_in * dim;
-    float dw[kPerLane];
+    float* const g = staged + warp_in * dim;
+    float* const table = staged + kWarps * dim + warp_in * 2 * pairs;
+    float dw[kPerLane], w[kPerLane], x[kPerLane], y[kPerLane];  // elements lane + 32 k; x and y of the row that is next
 #pragma unroll
-    for (int i = 0; i < kPerLane; ++i) dw[i] = 0.f;
+    for (int k = 0; k < kPerLane; ++k) {
+        dw[k] = 0.f;
+        w[k] = lane + 32 * k < dim ? load_element(static_cast<const T*>(s.weight) + lane + 32 * k) : 0.f;
+    }
+    uint32_t token = static_cast<uint32_t>(r.first / s.heads), batch = divide(token, a.by_tokens), at = token - batch * a.tokens;
+    int head = static_cast<int>(r.first - static_cast<int64_t>(token) * s.heads);
+    const auto load = [&] {
+        const T* yp = static_cast<const T*>(s.dy) + batch * s.dy_batch + at * s.dy_token + head * s.dy_head;
+        const T* xp = static_cast<const T*>(s.x) + batch * s.x_batch + at * s.x_token + head * s.x_head;
+#pragma unroll
+        for (int k = 0; k < kPerLane; ++k) {
+            const int i = lane + 32 * k;
+            x[k] = i < dim ? load_element(xp + i) : 0.f;
+            y[k] = i < dim ? load_element(yp + i) : 0.f;
+        }
+    };
+    if (r.first < r.end) load();
+    bool fresh = true;  // a token's first row
     for (int64_t p = r.first; p < r.end; ++p) {
-        const uint32_t token = static_cast<uint32_t>(p / s.heads), batch = divide(token, a.by_tokens), at = token - batch * a.tokens;
-        const int head = static_cast<int>(p - static_cast<int64_t>(token) * s.heads);
-        const T* y = static_cast<const T*>(s.dy) + batch * s.dy_batch + at * s.dy_token + head * s.dy_head;
-        const T* x = static_cast<const T*>(s.x) + batch * s.x_batch + at * s.x_token + head * s.x_head;
         T* dx = static_cast<T*>(s.dx) + batch * s.dx_batch + at * s.dx_token + head * s.dx_head;
         __syncwarp();
-        for (int i = lane; i < dim; i += 32) g[i] = load_element(y + i);
+        if (fresh && pairs) fill_turns(table, a.rope, pairs, position_at(a.rope, batch, at), -1.f, lane, 32);
+        float now[kPerLane];
+#pragma unroll
+        for (int k = 0; k < kPerLane; ++k) {
+            now[k] = x[k];
+            if (lane + 32 * k < dim) g[lane + 32 * k] = y[k];
+        }
+        fresh = ++head == s.heads;
+        if (fresh) {
+            head = 0;
+            batch = divide(++token, a.by_tokens), at = token - batch * a.tokens;
+        }
+        if (p + 1 < r.end) load();
         __syncwarp();
         if (pairs) {
-            const int64_t position = position_at(a.rope, batch, at);
             for (int q = lane; q < pairs; q += 32) {
-                const float2 t = turn_of(a.rope.rates[q], position, a.rope.magnitude, -1.f);
                 const int ia = a.rope.interleaved ? 2 * q : q, ib = a.rope.interleaved ? 2 * q + 1 : q + pairs;
-                const float u = g[ia], w = g[ib];
-                g[ia] = u * t.x - w * t.y;
-                g[ib] = w * t.x + u * t.y;
+                const float u = g[ia], v = g[ib], c = table[q], t = table[pairs + q];
+                g[ia] = u * c - v * t;
+                g[ib] = v * c + u * t;
             }
             __syncwarp();
         }
-        float ss = 0.f, dot = 0.f;
-        for (int i = lane; i < dim; i += 32) {
-            const float xi = load_element(x + i);
-            ss += xi * xi;
-            dot += g[i] * load_element(static_cast<const T*>(s.weight) + i) * xi;
+        float ss = 0.f, dot = 0.f, gk[kPerLane];
+#pragma unroll
+        for (int k = 0; k < kPerLane; ++k) {
+            gk[k] = lane + 32 * k < dim ? g[lane + 32 * k] : 0.f;
+            ss += now[k] * now[k];
+            dot += gk[k] * w[k] * now[k];
         }
         ss = sum_lanes<32>(ss, 32, lane);
         dot = sum_lanes<32>(dot, 32, lane);
         const float rstd = rsqrtf(ss / dim + a.eps), mean = dot * rstd / dim;
 #pragma unroll
         for (int k = 0; k < kPerLane; ++k) {
-            const int i = lane + 32 * k;
-            if (i < dim) {
-                const float n = load_element(x + i) * rstd;
-                dw[k] += g[i] * n;
-                store_element(dx + i, rstd * (g[i] * load_element(static_cast<const T*>(s.weight) + i) - n * mean));
-            }
+            const float n = now[k] * rstd;
+            dw[k] += gk[k] * n;
+            if (lane + 32 * k < dim) store_element(dx + lane + 32 * k, rstd * (gk[k] * w[k] - n * mean));
         }
     }
     __syncwarp();
@@ -346,7 +369,11 @@ cudaError_t launch_heads_grad_rows(HeadsGradArgs& a, int sms, cudaStream_t st) {
         a.seg[0].ctas -= a.seg[1].ctas;
     }
     const dim3 grid(static_cast<unsigned>(ctas));
-    if (!vectors) return launch_with_pdl(heads_grad_elements<T>, grid, dim3(kWarps * 32), kWarps * a.dim * sizeof(float), st, a);
+    if (!vectors) {
+        const size_t smem = kWarps * (a.dim + 2 * a.rope.pairs) * sizeof(float);
+        return a.dim <= 128 ? launch_with_pdl(heads_grad_elements<T, 4>, grid, dim3(kWarps * 32), smem, st, a)
+                            : launch_with_pdl(heads_grad_elements<T, kHeadMaxDim / 32>, grid, dim3(kWarps * 32), smem, st, a);
+    }
     return a.rope.interleaved ? launch_lanes<T, true>(a, G, grid, st) : launch_lanes<T, false>(a, G, grid, st);
 }
 

@@ -400,77 +400,84 @@ __global__ void __launch_bounds__(kMaxWarps * 32, kMinCtas) heads_rows(const __g
 }
 
 // Any head size, stride and alignment: a warp holds one row in shared memory,
-// element by element, and computes its angles itself.  For rows whose vectors
-// do not fall on 16 bytes, or whose rotated halves are no whole vectors.
+// element by element.  For rows whose vectors do not fall on 16 bytes, or whose
+// rotated halves are no whole vectors.  A CTA takes a token, each of its warps
+// `heads` rows, and the angles are computed once (16384 tokens of 32 heads of 128
+// from odd addresses: 113 us, with angles for every row 196; whole vectors 42).
 template <typename T, bool APPEND>
-__global__ void __launch_bounds__(kWarps * 32) heads_elements(const __grid_constant__ HeadsArgs a) {
-    extern __shared__ float staged[];
+__global__ void __launch_bounds__(kWarps * 32) heads_elements(const __grid_constant__ HeadsArgs a, int heads) {
+    extern __shared__ float staged[];  // [kWarps][dim], then [2][pairs]
     grid_dep_wait();
     grid_dep_release();
-    const int lane = threadIdx.x & 31;
-    const uint32_t unit = blockIdx.x * kWarps + (threadIdx.x >> 5);
-    const uint32_t token = unit / a.shares;
-    if (token >= a.total) return;
-    int head = static_cast<int>(unit - token * a.shares), si = 0;
-    while (head >= a.seg[si].heads) head -= a.seg[si++].heads;
-    const HeadSegment& s = a.seg[si];
-    const uint32_t batch = token / a.tokens, at = token - batch * a.tokens;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, dim = a.dim;
+    const uint32_t token = divide(blockIdx.x, a.by_turns), batch = APPEND ? 0 : divide(token, a.by_tokens), at = token - batch * a.tokens;
     Place place{0, -1, -1};
-    int64_t page = 0;
     if constexpr (APPEND) {
         place = find_place(a, static_cast<int>(token), lane);
-        page = s.cache ? page_of(a, place) : 0;
-        if (place.slot < 0 || page < 0) return;
+        if (place.slot < 0) return;  // the whole CTA's token
     }
-    const int dim = a.dim, pairs = s.rotate ? a.rope.pairs : 0;
-    float* row = staged + (threadIdx.x >> 5) * dim;
-    const T* in = static_cast<const T*>(s.in) + batch * s.in_batch + at * s.in_token + head * s.in_head;
-    float ss = 0.f;
-    for (int i = lane; i < dim; i += 32) {
-        const float x = load_element(in + i);
-        row[i] = x;
-        ss += x * x;
-    }
-    if (s.weight) {
-        const float rstd = rsqrtf(sum_lanes<32>(ss, 32, lane) * (1.f / dim) + a.eps);
-        for (int i = lane; i < dim; i += 32) row[i] *= rstd * load_element(static_cast<const T*>(s.weight) + i);
-    }
-    __syncwarp();
-    if (pairs) {
+    float* const row = staged + warp * dim;
+    float* const table = staged + kWarps * dim;
+    if (a.rope.pairs) {
         const int64_t position = APPEND && !a.rope.positions ? place.position : position_at(a.rope, batch, at);
-        for (int p = lane; p < pairs; p += 32) {
-            const float2 t = turn_of(a.rope.rates[p], position, a.rope.magnitude, a.rope.direction);
-            const int ia = a.rope.interleaved ? 2 * p : p, ib = a.rope.interleaved ? 2 * p + 1 : p + pairs;
-            const float x = row[ia], y = row[ib];
-            row[ia] = fmaf(y, -t.y, __fmul_rn(x, t.x));  // rounded as in the vector kernel
-            row[ib] = fmaf(x, t.y, __fmul_rn(y, t.x));
+        fill_turns(table, a.rope, a.rope.pairs, position, a.rope.direction, threadIdx.x, kWarps * 32);
+        __syncthreads();
+    }
+    int next = static_cast<int>(blockIdx.x - token * a.turns) * kWarps * heads + warp;
+    for (int n = 0; n < heads && next < a.shares; ++n, next += kWarps) {
+        int head = next, si = 0;
+        while (head >= a.seg[si].heads) head -= a.seg[si++].heads;
+        const HeadSegment& s = a.seg[si];
+        const int page = APPEND && s.cache ? page_of(a, place) : 0;
+        if (page < 0) continue;
+        const int pairs = s.rotate ? a.rope.pairs : 0;
+        const T* in = static_cast<const T*>(s.in) + batch * s.in_batch + at * s.in_token + head * s.in_head;
+        float ss = 0.f;
+        for (int i = lane; i < dim; i += 32) {
+            const float x = load_element(in + i);
+            row[i] = x;
+            ss += x * x;
+        }
+        if (s.weight) {
+            const float rstd = rsqrtf(sum_lanes<32>(ss, 32, lane) * (1.f / dim) + a.eps);
+            for (int i = lane; i < dim; i += 32) row[i] *= rstd * load_element(static_cast<const T*>(s.weight) + i);
         }
         __syncwarp();
-    }
-    if (APPEND && s.cache) {
-        const int64_t first = page * s.out_batch + place.slot * s.out_token + head * s.out_head;
-        if (a.format != kCacheSame) {
-            uint32_t top = 0;
-            for (int i = lane; i < dim; i += 32) top = max(top, __float_as_uint(fabsf(row[i])));
-            top = __reduce_max_sync(0xFFFFFFFFu, top);
-            const bool int8 = a.format == kCacheInt8, fine = finite_bits(top);
-            const float scale = int8 ? row_scale<true>(top) : row_scale<false>(top), inverse = about_inverse(scale);
-            uint8_t* out = static_cast<uint8_t*>(s.out) + first;
-            for (int i = lane; i < dim; i += 32) {
-                const uint32_t q = int8 ? quant2<true>(row[i], 0.f, scale, inverse) : quant2<false>(row[i], 0.f, scale, inverse);
-                out[i] = fine ? static_cast<uint8_t>(q) : 0;
+        if (pairs) {
+            for (int p = lane; p < pairs; p += 32) {
+                const int ia = a.rope.interleaved ? 2 * p : p, ib = a.rope.interleaved ? 2 * p + 1 : p + pairs;
+                const float x = row[ia], y = row[ib], c = table[p], t = table[pairs + p];
+                row[ia] = fmaf(y, -t, __fmul_rn(x, c));  // rounded as in the vector kernel
+                row[ib] = fmaf(x, t, __fmul_rn(y, c));
             }
-            if (lane == 0) s.scale[page * s.scale_page + place.slot * s.scale_slot + head * s.scale_head] = scale;
-        } else {
-            T* out = static_cast<T*>(s.out) + first;
-            for (int i = lane; i < dim; i += 32) {
-                if (s.weight || pairs) store_element(out + i, row[i]);
-                else out[i] = in[i];
-            }
+            __syncwarp();
         }
-    } else {
-        T* out = static_cast<T*>(s.out) + batch * s.out_batch + at * s.out_token + head * s.out_head;
-        for (int i = lane; i < dim; i += 32) store_element(out + i, row[i]);
+        if (APPEND && s.cache) {
+            const int64_t first = page * s.out_batch + place.slot * s.out_token + head * s.out_head;
+            if (a.format != kCacheSame) {
+                uint32_t top = 0;
+                for (int i = lane; i < dim; i += 32) top = max(top, __float_as_uint(fabsf(row[i])));
+                top = __reduce_max_sync(0xFFFFFFFFu, top);
+                const bool int8 = a.format == kCacheInt8, fine = finite_bits(top);
+                const float scale = int8 ? row_scale<true>(top) : row_scale<false>(top), inverse = about_inverse(scale);
+                uint8_t* out = static_cast<uint8_t*>(s.out) + first;
+                for (int i = lane; i < dim; i += 32) {
+                    const uint32_t q = int8 ? quant2<true>(row[i], 0.f, scale, inverse) : quant2<false>(row[i], 0.f, scale, inverse);
+                    out[i] = fine ? static_cast<uint8_t>(q) : 0;
+                }
+                if (lane == 0) s.scale[page * s.scale_page + place.slot * s.scale_slot + head * s.scale_head] = scale;
+            } else {
+                T* out = static_cast<T*>(s.out) + first;
+                for (int i = lane; i < dim; i += 32) {
+                    if (s.weight || pairs) store_element(out + i, row[i]);
+                    else out[i] = in[i];
+                }
+            }
+        } else {
+            T* out = static_cast<T*>(s.out) + batch * s.out_batch + at * s.out_token + head * s.out_head;
+            for (int i = lane; i < dim; i += 32) store_element(out + i, row[i]);
+        }
+        __syncwarp();  // before the next row takes its place
     }
 }
 
@@ -561,19 +568,22 @@ template <typename T, bool APPEND>
 cudaError_t launch_heads_rows(HeadsArgs& a, int sms, cudaStream_t st) {
     constexpr int W = Elem<T, false>::W;
     if (APPEND) a.by_page = Divider(a.page_size);
+    a.by_tokens = Divider(a.tokens);
     if (!whole_vectors(a, W)) {
         a.shares = 0;
         for (int i = 0; i < a.segments; ++i) a.shares += a.seg[i].heads;
-        const int64_t units = static_cast<int64_t>(a.total) * a.shares;
-        return launch_with_pdl(heads_elements<T, APPEND>, dim3(static_cast<unsigned>((units + kWarps - 1) / kWarps)), dim3(kWarps * 32),
-                               kWarps * a.dim * sizeof(float), st, a);
+        // eight rows to a warp where every SM has its warps all the same
+        const int heads = static_cast<int64_t>(a.total) * a.shares >= 256 * static_cast<int64_t>(sms) ? 8 : 1;
+        a.turns = (a.shares + kWarps * heads - 1) / (kWarps * heads);
+        a.by_turns = Divider(a.turns);
+        return launch_args(heads_elements<T, APPEND>, dim3(a.total * a.turns), dim3(kWarps * 32),
+                           (kWarps * a.dim + 2 * a.rope.pairs) * sizeof(float), st, a, heads);
     }
     const int G = lanes_of<W>(a.dim), rows = 32 / G;
     const int passes = share_out(a, rows, many_shares(APPEND), sms);
     a.turns = (a.shares + kMaxWarps - 1) / kMaxWarps;
     const int warps = (a.shares + a.turns - 1) / a.turns;
     a.by_turns = Divider(a.turns);
-    a.by_tokens = Divider(a.tokens);
     const dim3 grid((a.total + a.per_cta - 1) / a.per_cta * a.turns), block(warps * 32);
     const size_t smem = a.per_cta * a.rope.pairs * sizeof(float2);
     return a.rope.interleaved ? launch_lanes<T, true, APPEND>(a, passes, G, grid, block, smem, st)

@@ -216,7 +216,7 @@ def test_append_refusals(cell):
     for dim in (0, -1, 513):
         assert append(cell=cell, dim=dim) == nf.NF_ERR_UNSUPPORTED_HIDDEN
     for bad in ({"kc": None}, {"vc": None}, {"k": None}, {"v": None}, {"q": None}, {"q_out": None}, {"q": None, "q_out": None, "qw": L},
-                {"cell": 3}, {"cell": -1}, {"pages": -1}, {"pages": 1 << 31}, {"page": 0}, {"page": -1}, {"seqs": -1}, {"seqs": 1 << 31},
+                {"cell": 3}, {"cell": -1}, {"pages": -1}, {"pages": 1 << 31}, {"page": 0}, {"page": -1}, {"seqs": -1}, {"seqs": (1 << 30) + 1},
                 {"width": -1}, {"stride": 6}, {"stride": -1}, {"kind": 2}, {"tokens": -1}, {"tokens": 1 << 31}, {"past": None}, {"table": None},
                 {"k": hd(None, HK)}, {"v": hd(D, HQ)}, {"q_out": hd(E, HK)}, {"kc": pg(None, J)}, {"kc": pg(A, J, slot=-1)}, {"kc": pg(A, J, page=BIG)},
                 {"qw": L, "eps": 0.0}, {"kw_": L, "eps": math.nan}, {"rates": None}, {"layout": 3}, {"magnitude": math.nan},

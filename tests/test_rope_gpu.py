@@ -254,3 +254,15 @@ def test_refusals():
     big = torch.zeros(1, 1, 1, 520, dtype=BF, device="cuda")
     with pytest.raises(nf.NFError):
         nf.rope_fwd(big, None, p[:1, :1], rates)
+
+
+def test_strides_of_single_dimensions_do_not_count():
+    # one head, one token or one batch whose stride is no whole vector: the same bits as from contiguous rows
+    g = gen(8)
+    rates = nf.rope_rates(64)
+    for shape, strides in (((3, 7, 1, 64), (7 * 64, 64, 13)), ((5, 1, 4, 64), (256, 3, 64)), ((1, 9, 2, 64), (5, 128, 64))):
+        x = heads(g, *shape)
+        odd = torch.zeros(2000 * 8, dtype=BF, device="cuda").as_strided(shape, strides)
+        odd.copy_(x)
+        p = torch.arange(shape[1], device="cuda")
+        assert torch.equal(nf.rope_fwd(odd, None, p, rates)[0], nf.rope_fwd(x, None, p, rates)[0])
