@@ -824,8 +824,9 @@ def kv_append(k, v, k_cache, v_cache, table, past, starts=None, rates=None, posi
     cache before the call (negative: padding, nothing is written); starts: int32
     [seqs + 1], where its new tokens begin (None: one token per sequence).
     Tokens behind starts[seqs] are padding; a token without a page in the cache
-    is not stored; what a slot holds that two tokens of a call share is not defined.  k (and q) are normalized where their weight is given and
-    turned where rates are, by the token's place in its sequence unless
+    is not stored; what a slot holds that two tokens of a call share is not
+    defined.  k (and q) are normalized where their weight is given and turned
+    where rates are, by the token's place in its sequence unless
     positions [tokens] are given."""
     if stream is not None:
         return _on(stream, kv_append, k, v, k_cache, v_cache, table, past, starts, rates, positions, q, q_weight,

@@ -95,14 +95,14 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) heads_grad_rows(const
     const LaneVectors<W, INTER, FULL> v(j, FULL ? 2 * W * GT : a.dim, pairs);
     float* table = reinterpret_cast<float*>(ring + kStages * kSlot) + warp_in * 2 * pairs;
 
-    uint4 wa = make_uint4(0, 0, 0, 0), wb = wa;
-    if (v.has_a()) wa = ld_param(static_cast<const T*>(s.weight) + v.a);
-    if (v.has_b()) wb = ld_param(static_cast<const T*>(s.weight) + v.b);
     float2 dwx[P], dwy[P];
 #pragma unroll
     for (int i = 0; i < P; ++i) dwx[i] = dwy[i] = make_float2(0.f, 0.f);
 
-    if (r.first < r.end) {
+    if (r.first < r.end) {  // a call without rows may have null pointers
+        uint4 wa = make_uint4(0, 0, 0, 0), wb = wa;
+        if (v.has_a()) wa = ld_param(static_cast<const T*>(s.weight) + v.a);
+        if (v.has_b()) wb = ld_param(static_cast<const T*>(s.weight) + v.b);
         const float mean_of = 1.f / (FULL ? 2 * W * GT : a.dim);
         uint32_t token = static_cast<uint32_t>(r.first / per_token);
         int pass = static_cast<int>(r.first - static_cast<int64_t>(token) * per_token), left = static_cast<int>(r.end - r.first);
@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(kWarps * 32) heads_grad_elements(const __grid_
 #pragma unroll
     for (int k = 0; k < kPerLane; ++k) {
         dw[k] = 0.f;
-        w[k] = lane + 32 * k < dim ? load_element(static_cast<const T*>(s.weight) + lane + 32 * k) : 0.f;
+        w[k] = r.first < r.end && lane + 32 * k < dim ? load_element(static_cast<const T*>(s.weight) + lane + 32 * k) : 0.f;
     }
     uint32_t token = static_cast<uint32_t>(r.first / s.heads), batch = divide(token, a.by_tokens), at = token - batch * a.tokens;
     int head = static_cast<int>(r.first - static_cast<int64_t>(token) * s.heads);

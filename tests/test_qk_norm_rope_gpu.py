@@ -197,3 +197,19 @@ def test_refusals():
         kw = dict(dq_out=d, dk_out=d.clone(), q=q, k=q.clone(), q_weight=w, k_weight=w, positions=p, rates=rates) | change
         with pytest.raises(error):
             nf.qk_rmsnorm_rope_bwd(**kw)
+
+
+@pytest.mark.parametrize("dim", [64, 200, 63, 400])
+@pytest.mark.parametrize("kind", [nf.NF_BF16, nf.NF_F32])
+def test_gradient_without_rows_reads_nothing(kind, dim):
+    # null pointers for all that has no rows, the weights too: the weights' gradients are zeros
+    n = nf.nf_qk_rmsnorm_rope_bwd_workspace_size(dim)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    dw = torch.full((2, dim), 7.0, device="cuda")
+    q, k = nf.Heads(None, 0, 6 * dim, dim, 4), nf.Heads(None, 0, 6 * dim, dim, 2)
+    for sets in (1, 2):
+        dw.fill_(7.0)
+        two = (lambda x: x) if sets == 2 else (lambda x: None)
+        assert nf.nf_qk_rmsnorm_rope_bwd(q, dw[0].data_ptr(), q, q, None, two(k), two(dw[1].data_ptr()), two(k), two(k), None, kind, 2, 0,
+                                         dim, 1e-6, None, ws.data_ptr(), n, torch.cuda.current_stream().cuda_stream) == nf.NF_OK
+        assert not dw[:sets].any() and (dw[sets:] == 7.0).all()
