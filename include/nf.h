@@ -475,7 +475,7 @@ typedef struct {
     int64_t batch_stride; /* in elements */
     int64_t token_stride;
     int64_t head_stride;
-    int32_t heads;        /* 1 or more */
+    int32_t heads;        /* 1 to 2^20 */
 } nf_heads;
 
 /* Which elements of a head are a pair i, i < dim / 2. */

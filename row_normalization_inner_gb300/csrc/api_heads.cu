@@ -16,6 +16,7 @@ namespace {
 constexpr int64_t kMostStride = int64_t{1} << 40;
 constexpr int64_t kMostRows = 0x7FFFFFFF;
 constexpr int64_t kMostSeqs = 1 << 30;
+constexpr int64_t kMostHeads = 1 << 20;  // of a set: the kernels step from head to head in 32 bits
 
 // What a set of rows covers: up to three dimensions over rows of `inner`
 // bytes.  Extents fit 128 bits whatever the arguments.
@@ -113,7 +114,7 @@ struct Regions {
 
 bool stride_ok(int64_t s) { return s >= 0 && s <= kMostStride; }
 bool heads_ok(const nf_heads* h) {
-    return h->heads >= 1 && stride_ok(h->batch_stride) && stride_ok(h->token_stride) && stride_ok(h->head_stride);
+    return h->heads >= 1 && h->heads <= kMostHeads && stride_ok(h->batch_stride) && stride_ok(h->token_stride) && stride_ok(h->head_stride);
 }
 Region region_of(const nf_heads* h, int64_t batch, int64_t tokens, int64_t dim, int64_t size) {
     return region(h->data, batch, tokens, h->heads, h->batch_stride, h->token_stride, h->head_stride, dim, size);

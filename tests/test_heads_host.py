@@ -151,6 +151,15 @@ def test_refusals(call):
         assert call(**bad) == nf.NF_ERR_MISALIGNED, bad
 
 
+@pytest.mark.parametrize("call", [fwd, bwd, norm, norm_grad])
+def test_many_heads_are_refused(call):
+    for heads in ((1 << 20) + 1, 2 ** 31 - 1):
+        many = {x: nf.Heads(at, 0, 0, 64, heads) for x, at in (("q", 1 << 40), ("q_out", 2 << 40), ("dqo", 3 << 40))}
+        if call is not norm_grad:
+            del many["dqo"]
+        assert call(batch=1, tokens=1, k=None, k_out=None, **many, **({"dko": None} if call is norm_grad else {})) == nf.NF_ERR_INVALID_ARG
+
+
 @pytest.mark.parametrize("call", [fwd, bwd, norm])
 def test_nothing_to_do(call):
     assert call(tokens=0, q=hd(None), q_out=hd(None), k=hd(None, HK), k_out=hd(None, HK), rates=None, positions=None) == nf.NF_OK
