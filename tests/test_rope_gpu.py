@@ -260,7 +260,7 @@ def test_strides_of_single_dimensions_do_not_count():
     # one head, one token or one batch whose stride is no whole vector: the same bits as from contiguous rows
     g = gen(8)
     rates = nf.rope_rates(64)
-    for shape, strides in (((3, 7, 1, 64), (7 * 64, 64, 13)), ((5, 1, 4, 64), (256, 3, 64)), ((1, 9, 2, 64), (5, 128, 64))):
+    for shape, strides in (((3, 7, 1, 64), (7 * 64, 64, 13, 1)), ((5, 1, 4, 64), (256, 3, 64, 1)), ((1, 9, 2, 64), (5, 128, 64, 1))):
         x = heads(g, *shape)
         odd = torch.zeros(2000 * 8, dtype=BF, device="cuda").as_strided(shape, strides)
         odd.copy_(x)
