@@ -38,7 +38,8 @@ struct HeadSegment {
     int groups_of_token;  //   each on so many groups of lanes
     int groups_factor;
     bool rotate;
-    bool cache;   // out is a paged cache
+    bool cache;      // out is a paged cache
+    bool with_next;  // its one share of a token has the next segment's rows too, in the second half of its passes
 };
 
 // The gradient of one set of normalized heads.
@@ -96,6 +97,8 @@ cudaError_t launch_heads_bf16(HeadsArgs& a, int sms, cudaStream_t st);
 cudaError_t launch_heads_f32(HeadsArgs& a, int sms, cudaStream_t st);
 cudaError_t launch_append_bf16(HeadsArgs& a, int sms, cudaStream_t st);
 cudaError_t launch_append_f32(HeadsArgs& a, int sms, cudaStream_t st);
+cudaError_t launch_append_8_bf16(HeadsArgs& a, int sms, cudaStream_t st);
+cudaError_t launch_append_8_f32(HeadsArgs& a, int sms, cudaStream_t st);
 
 struct HeadsGradArgs {
     HeadGradSegment seg[2];

@@ -45,27 +45,32 @@ __device__ __forceinline__ float about_inverse(float d) {
 }
 
 // The scale of a row whose largest |y| has the bits `top`; NaN where that is not finite.
-template <bool INT8>
-__device__ __forceinline__ float row_scale(uint32_t top) {
-    constexpr float most = INT8 ? 127.f : 448.f;
-    return finite_bits(top) ? fmaxf(quotient(__uint_as_float(top), most, 1.f / most), kScaleMin) : __uint_as_float(0x7FC00000u);
+__device__ __forceinline__ float row_scale(bool int8, uint32_t top) {
+    const float most = int8 ? 127.f : 448.f, inverse = int8 ? 1.f / 127.f : 1.f / 448.f;
+    return finite_bits(top) ? fmaxf(quotient(__uint_as_float(top), most, inverse), kScaleMin) : __uint_as_float(0x7FC00000u);
 }
 
-template <bool INT8>
-__device__ __forceinline__ uint32_t quant2(float y0, float y1, float scale, float inverse) {
-    const float a = quotient(y0, scale, inverse), b = quotient(y1, scale, inverse);
-    if constexpr (INT8) return (static_cast<uint32_t>(__float2int_rn(a)) & 0xFF) | ((static_cast<uint32_t>(__float2int_rn(b)) & 0xFF) << 8);
+// Two elements in 8 bits, in the lower half of the result's 16 bits each's byte.
+__device__ __forceinline__ uint32_t e4m3_pair(float a, float b) {
     uint16_t v;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(v) : "f"(b), "f"(a));
     return v;
 }
+// |y| <= 127 to the nearest integer, ties to even, in the lower 8 bits of the
+// result: where fp32 numbers are one apart, the sum's own rounding is that.
+__device__ __forceinline__ uint32_t int8_bits(float y) { return __float_as_uint(y + 0x1.8p23f); }
+__device__ __forceinline__ uint32_t int8_pair(float a, float b) { return __byte_perm(int8_bits(a), int8_bits(b), 0x0040); }
 
+// W elements (divided by the row's scale) in 8 bits; `keep`: all bits, or none.
 template <bool INT8, int W>
-__device__ __forceinline__ void store_quantized(uint8_t* p, const float (&v)[W], float scale, float inverse) {
+__device__ __forceinline__ void store_8(uint8_t* p, const float (&v)[W], uint32_t keep) {
     uint32_t q[W / 4];
 #pragma unroll
-    for (int i = 0; i < W / 4; ++i)
-        q[i] = quant2<INT8>(v[4 * i], v[4 * i + 1], scale, inverse) | (quant2<INT8>(v[4 * i + 2], v[4 * i + 3], scale, inverse) << 16);
+    for (int i = 0; i < W / 4; ++i) {
+        const float *f = v + 4 * i;
+        const uint32_t lower = INT8 ? int8_pair(f[0], f[1]) : e4m3_pair(f[0], f[1]), upper = INT8 ? int8_pair(f[2], f[3]) : e4m3_pair(f[2], f[3]);
+        q[i] = __byte_perm(lower, upper, 0x5410) & keep;
+    }
     if constexpr (W == 8) *reinterpret_cast<uint2*>(p) = make_uint2(q[0], q[1]);
     else *reinterpret_cast<uint32_t*>(p) = q[0];
 }
@@ -77,27 +82,34 @@ __device__ __forceinline__ float largest(float a, float b, float c) {
     return d;
 }
 
-// A row in 8 bits, and its scale.  All lanes of its group call this.
-template <bool INT8, bool INTER, int GT, int P>
-__device__ __forceinline__ void store_row_8(uint8_t* to, float* scale_to, float2 (&x)[P], float2 (&y)[P], int G, int lane, bool here, bool first_lane,
-                                            const LaneVectors<2 * P, INTER, GT != 0>& v) {
+// A row in 8 bits, and its scale; with a NaN or an infinity its elements are zeros.
+// All lanes of its group call this.
+template <bool INTER, int GT, int P>
+__device__ __forceinline__ void store_row_8(bool int8, uint8_t* to, float* scale_to, float2 (&x)[P], float2 (&y)[P], int G, int lane, bool here,
+                                            bool first_lane, const LaneVectors<2 * P, INTER, GT != 0>& v) {
     float m = 0.f;
 #pragma unroll
     for (int i = 0; i < P; ++i) m = largest(largest(m, x[i].x, x[i].y), y[i].x, y[i].y);
     uint32_t top = __float_as_uint(m) & 0x7FFFFFFFu;  // as integers: a NaN stands above every number here too
     top = max_lanes<GT>(top, G, lane);
-    const float scale = row_scale<INT8>(top);
-    float inverse = about_inverse(scale);
-    if (!finite_bits(top)) {  // stored as zeros
-        inverse = 0.f;
+    const float scale = row_scale(int8, top), by = about_inverse(scale);
+    const float2 d = make_float2(-scale, -scale), inverse = make_float2(by, by);
 #pragma unroll
-        for (int i = 0; i < P; ++i) x[i] = y[i] = make_float2(0.f, 0.f);
+    for (int i = 0; i < P; ++i) {  // quotient(), two at a time
+        const float2 qx = __fmul2_rn(x[i], inverse), qy = __fmul2_rn(y[i], inverse);
+        x[i] = __ffma2_rn(__ffma2_rn(qx, d, x[i]), inverse, qx);
+        y[i] = __ffma2_rn(__ffma2_rn(qy, d, y[i]), inverse, qy);
     }
     float a[2 * P], b[2 * P];
     in_order<2 * P, INTER>(x, y, a, b);
-    const float divisor = finite_bits(top) ? scale : 1.f;
-    if (here && v.has_a()) store_quantized<INT8>(to + v.a, a, divisor, inverse);
-    if (here && v.has_b()) store_quantized<INT8>(to + v.b, b, divisor, inverse);
+    const uint32_t keep = finite_bits(top) ? 0xFFFFFFFFu : 0u;
+    if (int8) {
+        if (here && v.has_a()) store_8<true>(to + v.a, a, keep);
+        if (here && v.has_b()) store_8<true>(to + v.b, b, keep);
+    } else {
+        if (here && v.has_a()) store_8<false>(to + v.a, a, keep);
+        if (here && v.has_b()) store_8<false>(to + v.b, b, keep);
+    }
     if (here && first_lane) *scale_to = scale;
 }
 
@@ -153,18 +165,27 @@ __device__ __forceinline__ Place find_place(const HeadsArgs& a, int token, int l
     return place_in(a, token, lo, first, first >= 0 && first <= token && token < behind ? past : -1);
 }
 
+// What a kernel is compiled for: the code that stores rows in 8 bits takes
+// registers that other calls' rows want (an append of 8192 tokens of 32 + 8 + 8
+// heads to a bf16 cache 34.0 us, with both in one kernel 34.7).
+constexpr int kNoCache = 0, kCacheOfType = 1, kCache8Bits = 2;
+
 // Warps of a CTA at most, and CTAs that the registers of an SM hold (80 a thread,
 // some spilled).  With 3, 5 (of 96 registers) and 9 warps 16384 tokens of 64 + 8
 // heads take 97, 95 and 95 us, of 32 + 8 heads 50, 52 and 52 turned and 54, 57 and
-// 57 normalized too, an append to an 8-bit cache (8192 tokens of 64 + 8 + 8) 62, 70
-// and 67.
+// 57 normalized too.  An append to an 8-bit cache (8192 tokens of 64 + 8 + 8) takes
+// 59 us, with six CTAs of more registers 62.
 constexpr int kMaxWarps = 3;
 constexpr int kMinCtas = 7;
+// Rows in 8 bits take twice the instructions: a share has half as many of them,
+// so that its warp is not the one that the others' CTA waits for.
+constexpr int rows_8(int rows) { return rows > 1 ? rows / 2 : 1; }
 // Shares of four rows per SM from which these are taken rather than single rows
 // (us, four rows / one): 256 tokens of 32 + 8 heads, five to an SM, turned 2.4 /
-// 2.7, normalized too 3.0 / 3.1, 1024 tokens 4.3 / 6.0 and 5.0 / 6.8; appended, 256
-// tokens with 8 + 8 heads, seven to an SM, 3.8 / 3.5, 1024 tokens 8.0 / 8.8.
-constexpr int64_t many_shares(bool append) { return append ? 8 : 4; }
+// 2.7, normalized too 3.0 / 3.1, 1024 tokens 4.3 / 6.0 and 5.0 / 6.8; appended with
+// 8 + 8 heads, 320 tokens, six to an SM, 3.6 / 3.5, to an 8-bit cache 4.4 / 3.6,
+// 384 tokens 3.7 / 4.4 and 4.5 / 4.9.
+constexpr int64_t many_shares(bool append) { return append ? 7 : 4; }
 
 // 1 over a row's root mean square.
 template <typename T, bool INTER, int GT>
@@ -212,15 +233,16 @@ constexpr int kMaxTokens = 8;  // of a CTA
 // do), its warps their shares: N rows for each group of lanes, of queries, keys
 // or values.  A share is part of a token, pass after pass of 32 / G heads; or,
 // where a token has fewer heads, several tokens, each on as many groups as it
-// needs, so that a few heads fill a warp too.  The angles are computed once for
+// needs, so that a few heads fill a warp too.  An append's share of two passes of
+// keys takes the values' two as well.  The angles are computed once for
 // all the warps that need them, while the rows are on their way.
 // GT: lanes of a group, each with both its vectors; 0: a power of two that the
 // host gives, some lanes without one or both.
 // SEVERAL: the CTA has several tokens.
-template <typename T, bool INTER, bool APPEND, int GT, int N, bool SEVERAL>
+template <typename T, bool INTER, int CACHE, int GT, int N, bool SEVERAL>
 __global__ void __launch_bounds__(kMaxWarps * 32, kMinCtas) heads_rows(const __grid_constant__ HeadsArgs a, int lanes) {
     constexpr int W = Elem<T, INTER>::W, P = W / 2;
-    constexpr bool FULL = GT != 0;
+    constexpr bool FULL = GT != 0, APPEND = CACHE != kNoCache;
     const int G = FULL ? GT : lanes;
     extern __shared__ float4 tables[];  // [per_cta][2][pairs]
     __shared__ Place places[APPEND ? SEVERAL ? kMaxTokens : 1 : 1];
@@ -234,6 +256,11 @@ __global__ void __launch_bounds__(kMaxWarps * 32, kMinCtas) heads_rows(const __g
     if (!real) share = 0;
     while (share >= a.seg[si].shares) share -= a.seg[si++].shares;
     const HeadSegment& s = a.seg[si];
+    constexpr int H = APPEND && N > 1 && !SEVERAL ? N / 2 : N;  // rows of a half
+    const bool both = H < N && s.with_next;                     // keys in the first half, values in the second
+    constexpr int M = CACHE == kCache8Bits ? rows_8(N) : N;     // rows of a share that goes to the cache
+    const int most = both ? H : s.cache ? M : N;
+    const HeadSegment& s2 = a.seg[H < N ? si + both : si];
     // The lane's token in the CTA and its first head, how far its next head is, and
     // how many heads the share has for a group at most.  Lanes without a row of
     // their own (behind the last whole group, or the last token) are not `mine`:
@@ -242,12 +269,12 @@ __global__ void __launch_bounds__(kMaxWarps * 32, kMinCtas) heads_rows(const __g
     bool mine, whole;  // whole: every group has N rows
     if (!SEVERAL || s.per_token) {
         if (SEVERAL) nth = share / s.per_token;
-        const int first = (share - (SEVERAL ? nth * s.per_token : 0)) * N * rows;
+        const int first = (share - (SEVERAL ? nth * s.per_token : 0)) * most * rows;
         if (SEVERAL) real = real && nth < tokens;
         mine = (FULL && 32 % (GT ? GT : 1) == 0) || group < rows;
         head = first + (mine ? group : 0);
-        passes = min(N, (s.heads - first + rows - 1) / rows);
-        whole = real && first + N * rows <= s.heads;
+        passes = min(most, (s.heads - first + rows - 1) / rows);
+        whole = real && first + most * rows <= s.heads;
     } else {
         const int in_share = (group * s.groups_factor) >> 10, first = share * s.tokens_of_share;  // group / groups_of_token
         nth = first + in_share;
@@ -257,7 +284,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, kMinCtas) heads_rows(const __g
         step = s.groups_of_token;
         head = mine ? group - in_share * step : 0;
         passes = (s.heads + step - 1) / step;
-        whole = real && s.heads == N * step;
+        whole = real && s.heads == most * step;
     }
     if (SEVERAL && !real) nth = 0;
     const uint32_t token = first_token + nth;
@@ -283,11 +310,28 @@ __global__ void __launch_bounds__(kMaxWarps * 32, kMinCtas) heads_rows(const __g
     uint4 xa[N], xb[N];
     {
         const T* in = static_cast<const T*>(s.in) + batch * s.in_batch + at * s.in_token;
-        if (FULL && whole) {
+        if (H < N && both) {
+            const T* in2 = static_cast<const T*>(s2.in) + at * s2.in_token;
+#pragma unroll
+            for (int p = 0; p < H; ++p) {
+                xa[p] = xb[p] = xa[H + p] = xb[H + p] = make_uint4(0, 0, 0, 0);
+                if (p < passes) {
+                    const int h = whole ? head + p * step : min(head + p * step, s.heads - 1);
+                    const T *row = in + h * s.in_head, *row2 = in2 + h * s2.in_head;
+                    if (v.has_a()) xa[p] = ld_stream(row + v.a);
+                    if (v.has_b()) xb[p] = ld_stream(row + v.b);
+                    if (v.has_a()) xa[H + p] = ld_stream(row2 + v.a);
+                    if (v.has_b()) xb[H + p] = ld_stream(row2 + v.b);
+                }
+            }
+        } else if (FULL && whole) {
             const T* row = in + head * s.in_head;
             const int64_t further = step * s.in_head;
 #pragma unroll
-            for (int p = 0; p < N; ++p, row += further) xa[p] = ld_stream(row + v.a), xb[p] = ld_stream(row + v.b);
+            for (int p = 0; p < N; ++p, row += further) {
+                if (M < N && p == M && s.cache) break;
+                xa[p] = ld_stream(row + v.a), xb[p] = ld_stream(row + v.b);
+            }
         } else {
 #pragma unroll
             for (int p = 0; p < N; ++p) {
@@ -343,13 +387,25 @@ __global__ void __launch_bounds__(kMaxWarps * 32, kMinCtas) heads_rows(const __g
     T* out = static_cast<T*>(s.out);
     if (APPEND && s.cache) {
         const int64_t cell = page * s.out_batch + place.slot * s.out_token;
-        if (a.format != kCacheSame) {
+        if constexpr (CACHE == kCache8Bits) {
+            const bool int8 = a.format == kCacheInt8;
+            if (H < N && both) {  // the values first: they need no factors, whose registers the keys take then
+                uint8_t* q = static_cast<uint8_t*>(s2.out) + page * s2.out_batch + place.slot * s2.out_token + head * s2.out_head;
+                float* scale = s2.scale + page * s2.scale_page + place.slot * s2.scale_slot + head * s2.scale_head;
+#pragma unroll
+                for (int p = 0; p < H; ++p, q += step * s2.out_head, scale += step * s2.scale_head) {
+                    if (p >= passes) break;
+                    float2 x[P], y[P];
+                    Elem<T, INTER>::unpack(xa[H % N + p], xb[H % N + p], x, y);
+                    store_row_8<INTER, GT, P>(int8, q, scale, x, y, G, lane, mine && head + p * step < s.heads, j == 0, v);
+                }
+            }
             LaneFactors<W, INTER, FULL> f;
             if (weight || pairs) f.read(weight, table, pairs, v);
             uint8_t* q = static_cast<uint8_t*>(s.out) + cell + head * s.out_head;
             float* scale = s.scale + page * s.scale_page + place.slot * s.scale_slot + head * s.scale_head;
 #pragma unroll
-            for (int p = 0; p < N; ++p, q += step * s.out_head, scale += step * s.scale_head) {
+            for (int p = 0; p < M; ++p, q += step * s.out_head, scale += step * s.scale_head) {
                 if (p >= passes) break;
                 float2 x[P], y[P];
                 if (weight) {
@@ -360,9 +416,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, kMinCtas) heads_rows(const __g
                 } else {
                     Elem<T, INTER>::unpack(xa[p], xb[p], x, y);
                 }
-                const bool here = mine && head + p * step < s.heads;
-                if (a.format == kCacheInt8) store_row_8<true, INTER, GT, P>(q, scale, x, y, G, lane, here, j == 0, v);
-                else store_row_8<false, INTER, GT, P>(q, scale, x, y, G, lane, here, j == 0, v);
+                store_row_8<INTER, GT, P>(int8, q, scale, x, y, G, lane, mine && head + p * step < s.heads, j == 0, v);
             }
             return;
         }
@@ -377,10 +431,24 @@ __global__ void __launch_bounds__(kMaxWarps * 32, kMinCtas) heads_rows(const __g
             if (half) turn_rows<T, INTER, GT, true, (N + 1) / 2>(xa, xb, rstd, f, G, lane, mean_of, a.eps);
             else turn_rows<T, INTER, GT, true, N>(xa, xb, rstd, f, G, lane, mean_of, a.eps);
         } else {
-            turn_rows<T, INTER, GT, false, N>(xa, xb, rstd, f, G, lane, mean_of, a.eps);
+            if (H < N && both) turn_rows<T, INTER, GT, false, H>(xa, xb, rstd, f, G, lane, mean_of, a.eps);
+            else turn_rows<T, INTER, GT, false, N>(xa, xb, rstd, f, G, lane, mean_of, a.eps);
         }
     }
-    if (FULL && whole) {
+    if (H < N && both) {
+        T* out2 = static_cast<T*>(s2.out) + page * s2.out_batch + place.slot * s2.out_token;
+#pragma unroll
+        for (int p = 0; p < H; ++p) {
+            const int h = head + p * step;
+            if (mine && h < s.heads) {
+                T *row = out + h * s.out_head, *row2 = out2 + h * s2.out_head;
+                if (v.has_a()) st_stream(row + v.a, xa[p]);
+                if (v.has_b()) st_stream(row + v.b, xb[p]);
+                if (v.has_a()) st_stream(row2 + v.a, xa[H + p]);
+                if (v.has_b()) st_stream(row2 + v.b, xb[H + p]);
+            }
+        }
+    } else if (FULL && whole) {
         if (mine) {
             T* row = out + head * s.out_head;
             const int64_t further = step * s.out_head;
@@ -459,11 +527,11 @@ __global__ void __launch_bounds__(kWarps * 32) heads_elements(const __grid_const
                 for (int i = lane; i < dim; i += 32) top = max(top, __float_as_uint(fabsf(row[i])));
                 top = __reduce_max_sync(0xFFFFFFFFu, top);
                 const bool int8 = a.format == kCacheInt8, fine = finite_bits(top);
-                const float scale = int8 ? row_scale<true>(top) : row_scale<false>(top), inverse = about_inverse(scale);
+                const float scale = row_scale(int8, top), inverse = about_inverse(scale);
                 uint8_t* out = static_cast<uint8_t*>(s.out) + first;
                 for (int i = lane; i < dim; i += 32) {
-                    const uint32_t q = int8 ? quant2<true>(row[i], 0.f, scale, inverse) : quant2<false>(row[i], 0.f, scale, inverse);
-                    out[i] = fine ? static_cast<uint8_t>(q) : 0;
+                    const float q = quotient(row[i], scale, inverse);
+                    out[i] = fine ? static_cast<uint8_t>(int8 ? int8_bits(q) : e4m3_pair(q, 0.f)) : 0;
                 }
                 if (lane == 0) s.scale[page * s.scale_page + place.slot * s.scale_slot + head * s.scale_head] = scale;
             } else {
@@ -504,15 +572,30 @@ inline void share_out_tokens(HeadsArgs& a, int tokens, int passes, int rows) {
     a.shares = 0;
     for (int i = 0; i < a.segments; ++i) {
         HeadSegment& s = a.seg[i];
-        s.per_token = (s.heads + rows * passes - 1) / (rows * passes);
+        const int most = s.cache && a.format != kCacheSame ? rows_8(passes) : passes;
+        s.per_token = (s.heads + rows * most - 1) / (rows * most);
         s.shares = tokens * s.per_token;
+        s.with_next = false;
         if (tokens > 1) {
-            s.groups_of_token = (s.heads + passes - 1) / passes;
+            s.groups_of_token = (s.heads + most - 1) / most;
             s.groups_factor = 1024 / s.groups_of_token + 1;  // n * this >> 10 is n / groups_of_token for n and that below 32
             s.tokens_of_share = std::min(tokens, rows / s.groups_of_token);
             if (s.tokens_of_share > 1) s.per_token = 0, s.shares = (tokens + s.tokens_of_share - 1) / s.tokens_of_share;
         }
         a.shares += s.shares;
+    }
+    if (tokens > 1 || passes == 1 || a.segments < 2 || !a.seg[a.segments - 1].cache) return;
+    // Keys and values together, where that takes fewer CTAs, or fewer warps of the
+    // one (8192 tokens of 32 + 8 + 8 heads to an 8-bit cache 38 us, apart 48); else
+    // such a share only lasts longer than the others (64 + 8 + 8 heads 74, apart 62).
+    HeadSegment &k = a.seg[a.segments - 2], &v = a.seg[a.segments - 1];
+    const int half = rows * passes / 2, joined = (k.heads + half - 1) / half, shares = a.shares - k.shares - v.shares + joined;
+    const auto turns = [](int n) { return (n + kMaxWarps - 1) / kMaxWarps; };
+    if (turns(shares) < turns(a.shares) || (shares < a.shares && a.shares <= kMaxWarps)) {
+        k.with_next = true;
+        k.shares = k.per_token = joined;
+        v.shares = 0;
+        a.shares = shares;
     }
 }
 
@@ -542,31 +625,32 @@ inline int share_out(HeadsArgs& a, int rows, int64_t many, int sms) {
     return 4;
 }
 
-template <typename T, bool INTER, bool APPEND, int GT>
+template <typename T, bool INTER, int CACHE, int GT>
 cudaError_t launch_rows(const HeadsArgs& a, int passes, int G, dim3 grid, dim3 block, size_t smem, cudaStream_t st) {
-    return passes == 1      ? launch_args(heads_rows<T, INTER, APPEND, GT, 1, false>, grid, block, smem, st, a, G)
-           : a.per_cta == 1 ? launch_args(heads_rows<T, INTER, APPEND, GT, 4, false>, grid, block, smem, st, a, G)
-                            : launch_args(heads_rows<T, INTER, APPEND, GT, 4, true>, grid, block, smem, st, a, G);
+    return passes == 1      ? launch_args(heads_rows<T, INTER, CACHE, GT, 1, false>, grid, block, smem, st, a, G)
+           : a.per_cta == 1 ? launch_args(heads_rows<T, INTER, CACHE, GT, 4, false>, grid, block, smem, st, a, G)
+                            : launch_args(heads_rows<T, INTER, CACHE, GT, 4, true>, grid, block, smem, st, a, G);
 }
 
 // The head sizes with kernels of their own: 64, 80, 96, 112, 128, 192 and 256.
-template <typename T, bool INTER, bool APPEND>
+template <typename T, bool INTER, int CACHE>
 cudaError_t launch_lanes(const HeadsArgs& a, int passes, int lanes, dim3 grid, dim3 block, size_t smem, cudaStream_t st) {
     const int own = own_lanes<Elem<T, INTER>::W>(a.dim);
 #define NF_LANES(n) \
-    if (own == n) return launch_rows<T, INTER, APPEND, n>(a, passes, n, grid, block, smem, st);
+    if (own == n) return launch_rows<T, INTER, CACHE, n>(a, passes, n, grid, block, smem, st);
     if constexpr (sizeof(T) == 2) {
         NF_EACH_LANES_bf16(NF_LANES)
     } else {
         NF_EACH_LANES_f32(NF_LANES)
     }
 #undef NF_LANES
-    return launch_rows<T, INTER, APPEND, 0>(a, passes, lanes, grid, block, smem, st);
+    return launch_rows<T, INTER, CACHE, 0>(a, passes, lanes, grid, block, smem, st);
 }
 
-template <typename T, bool APPEND>
+template <typename T, int CACHE>
 cudaError_t launch_heads_rows(HeadsArgs& a, int sms, cudaStream_t st) {
     constexpr int W = Elem<T, false>::W;
+    constexpr bool APPEND = CACHE != kNoCache;
     if (APPEND) a.by_page = Divider(a.page_size);
     a.by_tokens = Divider(a.tokens);
     if (!whole_vectors(a, W)) {
@@ -586,8 +670,8 @@ cudaError_t launch_heads_rows(HeadsArgs& a, int sms, cudaStream_t st) {
     a.by_turns = Divider(a.turns);
     const dim3 grid((a.total + a.per_cta - 1) / a.per_cta * a.turns), block(warps * 32);
     const size_t smem = a.per_cta * a.rope.pairs * sizeof(float2);
-    return a.rope.interleaved ? launch_lanes<T, true, APPEND>(a, passes, G, grid, block, smem, st)
-                              : launch_lanes<T, false, APPEND>(a, passes, G, grid, block, smem, st);
+    return a.rope.interleaved ? launch_lanes<T, true, CACHE>(a, passes, G, grid, block, smem, st)
+                              : launch_lanes<T, false, CACHE>(a, passes, G, grid, block, smem, st);
 }
 
 }  // namespace

@@ -3,6 +3,6 @@
 
 namespace nf {
 
-cudaError_t launch_heads_f32(HeadsArgs& a, int sms, cudaStream_t st) { return launch_heads_rows<float, false>(a, sms, st); }
+cudaError_t launch_heads_f32(HeadsArgs& a, int sms, cudaStream_t st) { return launch_heads_rows<float, kNoCache>(a, sms, st); }
 
 }  // namespace nf

@@ -335,3 +335,35 @@ def test_refusals():
             nf.kv_append(**(base | change))
     torch.cuda.synchronize()
     assert all(a is None or torch.equal(a, b) for a, b in zip(before, s.copy()))
+
+
+TOGETHER = [  # shares with keys and values: tokens enough for four rows to a warp, past and new as below
+    (32, 8, 128, 128), (40, 10, 128, 64), (32, 4, 80, 80), (6, 6, 72, 48), (3, 3, 112, 112), (1, 13, 64, 64), (32, 8, 256, 256),
+]
+
+
+@pytest.mark.parametrize("cell", ["same", E4M3, INT8])
+@pytest.mark.parametrize("kind", [BF, F32])
+@pytest.mark.parametrize("hq,hk,dim,rot", TOGETHER)
+def test_keys_and_values_in_one_share(hq, hk, dim, rot, kind, cell):
+    test_append([9, 500, 0], [700, 1, 803], 64, hq, hk, dim, rot, kind, cell)
+
+
+@pytest.mark.parametrize("cell", ["same", E4M3])
+@pytest.mark.parametrize("hq,hk,dim", [(32, 8, 128), (32, 4, 80), (40, 10, 128)])
+def test_padding_beside_keys_and_values_in_one_share(hq, hk, dim, cell):
+    g = gen(28)
+    past = [(-1 if n % 5 == 3 else 3 * n) for n in range(170)]
+    s = Step(g, past, [n % 17 for n in range(170)], 8, hq, hk, dim, BF, None if cell == "same" else cell)
+    gone = torch.arange(0, 170, 7)
+    s.table[gone.cuda(), 1] = s.pages + 5
+    before = s.copy()
+    q_out = torch.full_like(s.q, 9.0)
+    s.call(q=s.q, rates=rates_of(dim), q_out=q_out)
+    used = s.used()
+    stored = used & ~((s.seq % 7 == 0) & (s.place // 8 == 1))
+    assert torch.all(q_out[~used] == 9.0)
+    y, size = turn(s.q, s.place, frequencies(dim))
+    close(q_out[used], y[used], TURN * size[used])
+    y, size = turn(s.k, s.place, frequencies(dim))
+    s.check(before, y, TURN * size, stored)
