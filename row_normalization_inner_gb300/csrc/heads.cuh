@@ -16,8 +16,7 @@
 // the share of a turn per position, in units of 2^-64, so that the 64-bit
 // product position * rate IS the angle modulo a turn: exact for every position
 // up to the rate's own rounding (2^-65 turns per position), with no reduction
-// of large angles, no table of angles and no limit to a context.  Its signed
-// value over 2^63 is the angle in half turns, which sincospif takes.
+// of large angles, no table of angles and no limit to a context.
 #pragma once
 
 #include "common.cuh"
@@ -85,17 +84,34 @@ __device__ __forceinline__ float load_element(const float* p) { return *p; }
 __device__ __forceinline__ void store_element(uint16_t* p, float f) { *p = static_cast<uint16_t>(pack2(f, 0.f) & 0xFFFF); }
 __device__ __forceinline__ void store_element(float* p, float f) { *p = f; }
 
-// (cos, sin) of a pair at a position, both times `magnitude`.  sincospif takes
-// the angle's upper 24 bits, which fp32 holds exactly; the rest, below 2^-24 half
-// turns, turns its result on to first order (what is left out is below 2^-46).
+// (cos, sin) of a pair at a position, both times `magnitude`.  The angle's upper
+// 32 bits are a quarter and the rest to it, x in [-1/2, 1/2] quarters, exactly;
+// on that the Taylor series of sin and cos of h x, h = pi / 2, to x^9 and x^10
+// (what is left out is below 2^-29 and 2^-30), the sine's first coefficient in two parts.  Both are
+// off by 1.25 steps of 2^-24 at most over 4 million angles (0.28 in the square mean,
+// rounding alone 0.24).  With sincospif and its angle set right by a product the
+// gradient of 777 tokens of 20 + 4 fp32 heads of 80 took 6.6 us for 6.2, 16384
+// tokens of 64 + 8 normalized heads of 128 97.9 for 97.3.
 __device__ __forceinline__ float2 turn_of(uint64_t rate, int64_t position, float magnitude, float direction) {
-    const uint64_t angle = rate * static_cast<uint64_t>(position);
-    const int64_t upper = static_cast<int64_t>(angle + (1ull << 39)) >> 40;
-    const int64_t rest = static_cast<int64_t>(angle - (static_cast<uint64_t>(upper) << 40));
-    float s, c;
-    sincospif(static_cast<float>(static_cast<int32_t>(upper)) * 0x1p-23f, &s, &c);
-    const float r = __ll2float_rn(rest) * (3.14159265f * 0x1p-63f);
-    return make_float2((c - s * r) * magnitude, (s + c * r) * magnitude * direction);
+    constexpr double h = 1.57079632679489661923, h2 = h * h, h3 = h * h2, h4 = h2 * h2;
+    constexpr float first = static_cast<float>(h), rest = static_cast<float>(h - static_cast<double>(first));
+    const uint32_t angle = static_cast<uint32_t>((rate * static_cast<uint64_t>(position) + (1ull << 31)) >> 32);
+    const uint32_t quarter = (angle + (1u << 29)) >> 30;
+    const float x = static_cast<float>(static_cast<int32_t>(angle - (quarter << 30))) * 0x1p-30f, z = x * x;
+    float s = static_cast<float>(h4 * h4 * h / 362880);
+    s = fmaf(s, z, static_cast<float>(-h3 * h4 / 5040));
+    s = fmaf(s, z, static_cast<float>(h * h4 / 120));
+    s = fmaf(s, z, static_cast<float>(-h3 / 6));
+    s = fmaf(x, first, x * fmaf(s, z, rest));
+    float c = static_cast<float>(-h4 * h4 * h2 / 3628800);
+    c = fmaf(c, z, static_cast<float>(h4 * h4 / 40320));
+    c = fmaf(c, z, static_cast<float>(-h2 * h4 / 720));
+    c = fmaf(c, z, static_cast<float>(h4 / 24));
+    c = fmaf(c, z, static_cast<float>(-h2 / 2));
+    c = fmaf(c, z, 1.f);
+    const float cosine = __uint_as_float(__float_as_uint(quarter & 1 ? s : c) ^ ((quarter + 1 & 2) << 30));
+    const float sine = __uint_as_float(__float_as_uint(quarter & 1 ? c : s) ^ ((quarter & 2) << 30));
+    return make_float2(cosine * magnitude, sine * (magnitude * direction));
 }
 
 __device__ __forceinline__ int64_t position_at(const Rotation& r, uint32_t batch, uint32_t token) {
