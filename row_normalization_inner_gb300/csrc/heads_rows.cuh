@@ -228,6 +228,9 @@ __device__ __forceinline__ void turn_rows(uint4 (&a)[M], uint4 (&b)[M], const fl
 }
 
 constexpr int kMaxTokens = 8;  // of a CTA
+// One token, with keys and values in one share or not; several; several with
+// both in one share (the code for that took 8% where it was not used).
+constexpr int kOneToken = 0, kSeveralTokens = 1, kSeveralJoined = 2;
 
 // A CTA takes `per_cta` tokens (several CTAs take turns where there is more to
 // do), its warps their shares: N rows for each group of lanes, of queries, keys
@@ -238,11 +241,11 @@ constexpr int kMaxTokens = 8;  // of a CTA
 // all the warps that need them, while the rows are on their way.
 // GT: lanes of a group, each with both its vectors; 0: a power of two that the
 // host gives, some lanes without one or both.
-// SEVERAL: the CTA has several tokens.
-template <typename T, bool INTER, int CACHE, int GT, int N, bool SEVERAL>
+// TOKENS: what a CTA has.
+template <typename T, bool INTER, int CACHE, int GT, int N, int TOKENS>
 __global__ void __launch_bounds__(kMaxWarps * 32, kMinCtas) heads_rows(const __grid_constant__ HeadsArgs a, int lanes) {
     constexpr int W = Elem<T, INTER>::W, P = W / 2;
-    constexpr bool FULL = GT != 0, APPEND = CACHE != kNoCache;
+    constexpr bool FULL = GT != 0, APPEND = CACHE != kNoCache, SEVERAL = TOKENS != kOneToken;
     const int G = FULL ? GT : lanes;
     extern __shared__ float4 tables[];  // [per_cta][2][pairs]
     __shared__ Place places[APPEND ? SEVERAL ? kMaxTokens : 1 : 1];
@@ -256,8 +259,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32, kMinCtas) heads_rows(const __g
     if (!real) share = 0;
     while (share >= a.seg[si].shares) share -= a.seg[si++].shares;
     const HeadSegment& s = a.seg[si];
-    constexpr int H = APPEND && N > 1 && !SEVERAL ? N / 2 : N;  // rows of a half
-    const bool both = H < N && s.with_next;                     // keys in the first half, values in the second
+    constexpr int H = APPEND && N > 1 && TOKENS != kSeveralTokens ? N / 2 : N;  // rows of a half
+    const bool both = H < N && s.with_next;                                     // keys in the first half, values in the second
     constexpr int M = CACHE == kCache8Bits ? rows_8(N) : N;     // rows of a share that goes to the cache
     const int most = both ? H : s.cache ? M : N;
     const HeadSegment& s2 = a.seg[H < N ? si + both : si];
@@ -566,70 +569,95 @@ bool whole_vectors(const HeadsArgs& a, int W) {
     return true;
 }
 
-// Shares the rows of `tokens` tokens out among warps.
+// How one set's rows of `tokens` tokens are shared out, `most` rows to a group.
+inline void share_out_set(HeadSegment& s, int tokens, int most, int rows) {
+    s.with_next = false;
+    s.per_token = (s.heads + rows * most - 1) / (rows * most);
+    s.shares = tokens * s.per_token;
+    if (tokens == 1) return;
+    s.groups_of_token = (s.heads + most - 1) / most;
+    s.groups_factor = 1024 / s.groups_of_token + 1;  // n * this >> 10 is n / groups_of_token for n and that below 32
+    s.tokens_of_share = std::min(tokens, rows / s.groups_of_token);
+    if (s.tokens_of_share > 1) s.per_token = 0, s.shares = (tokens + s.tokens_of_share - 1) / s.tokens_of_share;
+}
+
+inline int turns_of(int shares) { return (shares + kMaxWarps - 1) / kMaxWarps; }
+
+// Shares the rows of `tokens` tokens out among warps, `passes` to a group.
 inline void share_out_tokens(HeadsArgs& a, int tokens, int passes, int rows) {
     a.per_cta = tokens;
     a.shares = 0;
     for (int i = 0; i < a.segments; ++i) {
         HeadSegment& s = a.seg[i];
-        const int most = s.cache && a.format != kCacheSame ? rows_8(passes) : passes;
-        s.per_token = (s.heads + rows * most - 1) / (rows * most);
-        s.shares = tokens * s.per_token;
-        s.with_next = false;
-        if (tokens > 1) {
-            s.groups_of_token = (s.heads + most - 1) / most;
-            s.groups_factor = 1024 / s.groups_of_token + 1;  // n * this >> 10 is n / groups_of_token for n and that below 32
-            s.tokens_of_share = std::min(tokens, rows / s.groups_of_token);
-            if (s.tokens_of_share > 1) s.per_token = 0, s.shares = (tokens + s.tokens_of_share - 1) / s.tokens_of_share;
-        }
+        share_out_set(s, tokens, s.cache && a.format != kCacheSame ? rows_8(passes) : passes, rows);
         a.shares += s.shares;
     }
-    if (tokens > 1 || passes == 1 || a.segments < 2 || !a.seg[a.segments - 1].cache) return;
-    // Keys and values together, where that takes fewer CTAs, or fewer warps of the
-    // one (8192 tokens of 32 + 8 + 8 heads to an 8-bit cache 38 us, apart 48); else
-    // such a share only lasts longer than the others (64 + 8 + 8 heads 74, apart 62).
-    HeadSegment &k = a.seg[a.segments - 2], &v = a.seg[a.segments - 1];
-    const int half = rows * passes / 2, joined = (k.heads + half - 1) / half, shares = a.shares - k.shares - v.shares + joined;
-    const auto turns = [](int n) { return (n + kMaxWarps - 1) / kMaxWarps; };
-    if (turns(shares) < turns(a.shares) || (shares < a.shares && a.shares <= kMaxWarps)) {
-        k.with_next = true;
-        k.shares = k.per_token = joined;
-        v.shares = 0;
-        a.shares = shares;
-    }
+}
+
+// An append's keys and values together, where that takes fewer CTAs, or fewer
+// warps of a token's one (8192 tokens of 32 + 8 + 8 heads to an 8-bit cache 38 us,
+// apart 40); else such a share only lasts longer than the others (64 + 8 + 8 heads
+// 63, apart 59).
+inline bool join_keys_and_values(HeadsArgs& a, int passes, int rows) {
+    if (a.segments < 2 || !a.seg[a.segments - 1].cache) return false;
+    HeadSegment &k = a.seg[a.segments - 2], &v = a.seg[a.segments - 1], joined = k;
+    share_out_set(joined, a.per_cta, passes / 2, rows);
+    const int shares = a.shares - k.shares - v.shares + joined.shares;
+    if (turns_of(shares) == turns_of(a.shares) && !(a.per_cta == 1 && shares < a.shares && a.shares <= kMaxWarps)) return false;
+    k = joined;
+    k.with_next = true;
+    v.shares = 0;
+    a.shares = shares;
+    return true;
 }
 
 // Rows of a group to a share, and the tokens to a CTA.  Four rows where that
 // leaves every SM its warps: they are in flight together and spread what a warp
 // does before them.  Then the tokens that take the fewest instructions each (some
 // 300 for a share before its rows, 90 for 32 angles, which every CTA of the tokens
-// computes).
+// computes), by a tenth.  Several tokens' keys and values are joined where there
+// are more warps than run at a time (appends of 8 + 1 + 1 heads, us, joined / apart:
+// 8192 tokens 12.8 / 15.3, 2500 6.3 / 7.2, 2200 5.0 / 4.6) and that is a fifth
+// less than token by token (16 + 4 + 4 heads, an eighth less, 24.0 and 21.1).
 inline int share_out(HeadsArgs& a, int rows, int64_t many, int sms) {
     const auto shares = [&] { return (static_cast<int64_t>(a.total) + a.per_cta - 1) / a.per_cta * a.shares; };
+    const auto cost = [&] { return (300.0 * a.shares + 90.0 * turns_of(a.shares) * ((a.per_cta * a.rope.pairs + 31) / 32)) / a.per_cta; };
     share_out_tokens(a, 1, 4, rows);
+    join_keys_and_values(a, 4, rows);
     if (shares() < many * sms) {
         share_out_tokens(a, 1, 1, rows);
         return 1;
     }
-    const int angles = (a.rope.pairs + 31) / 32;
+    const double one = cost();
+    const auto most = [&](int tokens) { return tokens <= kMaxTokens && tokens * a.rope.pairs <= 1024; };
+    double least = one;
+    int64_t warps = shares();
     int best = 1;
-    double least = 300.0 * a.shares + 90.0 * ((a.shares + kMaxWarps - 1) / kMaxWarps) * angles;
-    for (int tokens = 2; tokens <= kMaxTokens && tokens * a.rope.pairs <= 1024; ++tokens) {
+    bool joined = true;
+    for (int tokens = 2; most(tokens); ++tokens) {
         share_out_tokens(a, tokens, 4, rows);
         if (shares() < many * sms) break;
-        const int turns = (a.shares + kMaxWarps - 1) / kMaxWarps;
-        const double cost = (300.0 * a.shares + 90.0 * turns * ((tokens * a.rope.pairs + 31) / 32)) / tokens;
-        if (cost < 0.9 * least) best = tokens, least = cost;
+        if (cost() < 0.9 * least) best = tokens, least = cost(), warps = shares(), joined = false;
+    }
+    for (int tokens = 2; warps > (kMinCtas + 1) * kMaxWarps * sms && most(tokens); ++tokens) {
+        share_out_tokens(a, tokens, 4, rows);
+        if (!join_keys_and_values(a, 4, rows)) continue;
+        if (shares() < many * sms) break;
+        if (cost() < 0.9 * least && cost() < 0.8 * one) best = tokens, least = cost(), joined = true;
     }
     share_out_tokens(a, best, 4, rows);
+    if (joined) join_keys_and_values(a, 4, rows);
     return 4;
 }
 
 template <typename T, bool INTER, int CACHE, int GT>
 cudaError_t launch_rows(const HeadsArgs& a, int passes, int G, dim3 grid, dim3 block, size_t smem, cudaStream_t st) {
-    return passes == 1      ? launch_args(heads_rows<T, INTER, CACHE, GT, 1, false>, grid, block, smem, st, a, G)
-           : a.per_cta == 1 ? launch_args(heads_rows<T, INTER, CACHE, GT, 4, false>, grid, block, smem, st, a, G)
-                            : launch_args(heads_rows<T, INTER, CACHE, GT, 4, true>, grid, block, smem, st, a, G);
+    if (passes == 1) return launch_args(heads_rows<T, INTER, CACHE, GT, 1, kOneToken>, grid, block, smem, st, a, G);
+    if (a.per_cta == 1) return launch_args(heads_rows<T, INTER, CACHE, GT, 4, kOneToken>, grid, block, smem, st, a, G);
+    if constexpr (CACHE != kNoCache) {
+        if (a.seg[a.segments - 2].with_next) return launch_args(heads_rows<T, INTER, CACHE, GT, 4, kSeveralJoined>, grid, block, smem, st, a, G);
+    }
+    return launch_args(heads_rows<T, INTER, CACHE, GT, 4, kSeveralTokens>, grid, block, smem, st, a, G);
 }
 
 // The head sizes with kernels of their own: 64, 80, 96, 112, 128, 192 and 256.
@@ -665,7 +693,7 @@ cudaError_t launch_heads_rows(HeadsArgs& a, int sms, cudaStream_t st) {
     }
     const int G = lanes_of<W>(a.dim), rows = 32 / G;
     const int passes = share_out(a, rows, many_shares(APPEND), sms);
-    a.turns = (a.shares + kMaxWarps - 1) / kMaxWarps;
+    a.turns = turns_of(a.shares);
     const int warps = (a.shares + a.turns - 1) / a.turns;
     a.by_turns = Divider(a.turns);
     const dim3 grid((a.total + a.per_cta - 1) / a.per_cta * a.turns), block(warps * 32);

@@ -367,3 +367,28 @@ def test_padding_beside_keys_and_values_in_one_share(hq, hk, dim, cell):
     close(q_out[used], y[used], TURN * size[used])
     y, size = turn(s.k, s.place, frequencies(dim))
     s.check(before, y, TURN * size, stored)
+
+
+@pytest.mark.parametrize("cell", ["same", E4M3, INT8])
+@pytest.mark.parametrize("kind", [BF, F32])
+@pytest.mark.parametrize("hq,hk,dim,rot", [(8, 1, 128, 128), (5, 1, 64, 64), (8, 2, 64, 32), (7, 1, 80, 80), (8, 2, 72, 48), (3, 1, 256, 256)])
+def test_keys_and_values_of_several_tokens_in_one_share(hq, hk, dim, rot, kind, cell):
+    # more warps than run at a time, padded sequences and missing pages among them
+    g = gen(hq + dim)
+    past = [(-1 if n % 5 == 3 else 7 * n) for n in range(200)]
+    s = Step(g, past, [(n * 37) % 131 for n in range(200)], 16, hq, hk, dim, kind, None if cell == "same" else cell, order="heads first")
+    gone = torch.arange(0, 200, 7)
+    s.table[gone.cuda(), 1] = s.pages + 5
+    before = s.copy()
+    q_out = torch.full_like(s.q, 9.0)
+    s.call(q=s.q, rates=rates_of(rot), q_weight=s.qw, k_weight=s.kw, eps=EPS, q_out=q_out)
+    used = s.used()
+    stored = used & ~((s.seq % 7 == 0) & (s.place // 16 == 1))
+    assert torch.all(q_out[~used] == 9.0)
+
+    def rows(x, w):
+        y, size = turn(normed(x, w, EPS), s.place, frequencies(rot))
+        return y, (NORM + TURN) * size
+    y, error = rows(s.q, s.qw)
+    close(q_out[used], y[used], error[used])
+    s.check(before, *rows(s.k, s.kw), stored)
