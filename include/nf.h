@@ -493,8 +493,9 @@ typedef enum {
  * rates: the share of a turn per position, f_i / (2 pi), modulo 1 and in units
  * of 2^-64 (nf_rope_rates makes them).  The 64-bit product rate * p is then the
  * angle modulo a turn with no reduction of large angles: it is off by p * 2^-65
- * turns at most, beside what the rates' own rounding is off.  Positions are
- * any integers, negative ones too. */
+ * turns at most, beside what the rates' own rounding is off.  Its sine and cosine are
+ * within 2^-22 of their values, however small these are.  Positions are any
+ * integers, negative ones too. */
 typedef struct {
     const uint64_t* rates;  /* device, [dim / 2] */
     int32_t dim;

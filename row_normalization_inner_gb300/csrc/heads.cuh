@@ -85,19 +85,22 @@ __device__ __forceinline__ void store_element(uint16_t* p, float f) { *p = stati
 __device__ __forceinline__ void store_element(float* p, float f) { *p = f; }
 
 // (cos, sin) of a pair at a position, both times `magnitude`.  The angle's upper
-// 32 bits are a quarter and the rest to it, x in [-1/2, 1/2] quarters, exactly;
-// on that the Taylor series of sin and cos of h x, h = pi / 2, to x^9 and x^10
-// (what is left out is below 2^-29 and 2^-30), the sine's first coefficient in two parts.  Both are
-// off by 1.25 steps of 2^-24 at most over 4 million angles (0.28 in the square mean,
-// rounding alone 0.24).  With sincospif and its angle set right by a product the
-// gradient of 777 tokens of 20 + 4 fp32 heads of 80 took 6.6 us for 6.2, 16384
-// tokens of 64 + 8 normalized heads of 128 97.9 for 97.3.
+// 32 bits (rounded) are a quarter and the rest to it; that and the lower 32 (signed)
+// are x in [-1/2, 1/2] quarters, off by 1.5 * 2^-24 of itself at most.  On it the Taylor
+// series of sin and cos of h x, h = pi / 2, to x^9 and x^10 (what is left out is
+// below 2^-29 and 2^-30), the sine's first coefficient in two parts.  Both are off by
+// 1.25 steps of 2^-24 at most over 4 million angles (0.28 in the square mean, rounding
+// alone 0.24), and by 2.2 of their own value, however small: the slow pairs of the
+// first positions turn by 1e-6, of which the upper 32 bits alone keep nine.  x as one
+// 64-bit integer made to a float is off by 2^-24 and takes 3% in calls of few heads.
 __device__ __forceinline__ float2 turn_of(uint64_t rate, int64_t position, float magnitude, float direction) {
     constexpr double h = 1.57079632679489661923, h2 = h * h, h3 = h * h2, h4 = h2 * h2;
     constexpr float first = static_cast<float>(h), rest = static_cast<float>(h - static_cast<double>(first));
-    const uint32_t angle = static_cast<uint32_t>((rate * static_cast<uint64_t>(position) + (1ull << 31)) >> 32);
-    const uint32_t quarter = (angle + (1u << 29)) >> 30;
-    const float x = static_cast<float>(static_cast<int32_t>(angle - (quarter << 30))) * 0x1p-30f, z = x * x;
+    const uint64_t angle = rate * static_cast<uint64_t>(position);
+    const uint32_t upper = static_cast<uint32_t>((angle + (1ull << 31)) >> 32);
+    const int32_t lower = static_cast<int32_t>(static_cast<uint32_t>(angle));
+    const uint32_t quarter = (upper + (1u << 29)) >> 30;
+    const float x = fmaf(static_cast<float>(lower), 0x1p-62f, static_cast<float>(static_cast<int32_t>(upper - (quarter << 30))) * 0x1p-30f), z = x * x;
     float s = static_cast<float>(h4 * h4 * h / 362880);
     s = fmaf(s, z, static_cast<float>(-h3 * h4 / 5040));
     s = fmaf(s, z, static_cast<float>(h * h4 / 120));
