@@ -493,7 +493,7 @@ typedef enum {
  * rates: the share of a turn per position, f_i / (2 pi), modulo 1 and in units
  * of 2^-64 (nf_rope_rates makes them).  The 64-bit product rate * p is then the
  * angle modulo a turn with no reduction of large angles: it is off by p * 2^-65
- * turns at most, beside what the rates' own rounding is off.  Its sine and cosine are
+ * turns at most, the rates' own rounding p times.  Its sine and cosine are
  * within 2^-22 of their values, however small these are.  Positions are any
  * integers, negative ones too. */
 typedef struct {
@@ -520,7 +520,8 @@ typedef struct {
  *                   0.1 ln(factor) + 1) */
 typedef enum { NF_ROPE_PLAIN = 0, NF_ROPE_LINEAR = 1, NF_ROPE_NTK = 2, NF_ROPE_PARTS = 3 } nf_rope_scaling;
 
-/* Host only: writes dim / 2 rates to host memory.  dim even, 2 to
+/* Host only: writes dim / 2 rates to host memory, each the nearest to its
+ * frequency's share of a turn.  dim even, 2 to
  * NF_HEAD_MAX_DIM; base > 1, factor >= 1, length > 0, 0 <= low < high, all
  * finite (those that the scaling uses). */
 nf_status nf_rope_rates(uint64_t* rates, int32_t dim, double base, nf_rope_scaling scaling, double factor,

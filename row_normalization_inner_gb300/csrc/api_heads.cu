@@ -9,6 +9,7 @@
 #include "../../include/nf.h"
 #include "heads.h"
 #include "internal.h"
+#include "pair.h"
 
 namespace nf {
 namespace {
@@ -233,15 +234,17 @@ bool pages_ok(const nf_pages* c, bool scaled) {
            (!scaled || (stride_ok(c->scale_page_stride) && stride_ok(c->scale_slot_stride) && stride_ok(c->scale_head_stride)));
 }
 
-// Radians per position to the share of a turn in units of 2^-64, modulo a turn.
-uint64_t rate_of(double frequency) {
-    double turns = std::fabs(frequency) / (2.0 * 3.14159265358979323846);
-    turns -= std::floor(turns);
+// Radians per position to the share of a turn in units of 2^-64, modulo a turn:
+// the nearest one, as far as 104 bits tell.
+uint64_t rate_of(Pair frequency) {
+    const bool back = frequency.hi < 0.0;
+    const Pair turns = (back ? -frequency : frequency) / two_pi();
+    const Pair part = turns - std::floor(turns.hi);  // in [-2^-53, 1)
     // in two halves, as 2^64 itself is not an integer that fits
-    const double high = std::floor(turns * 0x1p32);
-    const double low = (turns * 0x1p32 - high) * 0x1p32;
-    const uint64_t rate = (static_cast<uint64_t>(high) << 32) + static_cast<uint64_t>(std::llround(low));
-    return frequency < 0.0 ? ~rate + 1 : rate;
+    const double high = std::floor(part.hi * 0x1p32);
+    const Pair low = scaled(scaled(part, 32) - high, 32);
+    const uint64_t rate = (static_cast<uint64_t>(static_cast<int64_t>(high)) << 32) + static_cast<uint64_t>(std::llround(low.hi + low.lo));
+    return back ? ~rate + 1 : rate;
 }
 
 }  // namespace
@@ -256,21 +259,19 @@ nf_status nf_rope_rates(uint64_t* rates, int32_t dim, double base, nf_rope_scali
     if (!rates || dim < 2 || dim % 2 || dim > kHeadMaxDim || !(std::isfinite(base) && base > 1.0)) return NF_ERR_INVALID_ARG;
     if (scaling < NF_ROPE_PLAIN || scaling > NF_ROPE_PARTS) return NF_ERR_INVALID_ARG;
     if (scaling != NF_ROPE_PLAIN && !(std::isfinite(factor) && factor >= 1.0)) return NF_ERR_INVALID_ARG;
-    if (scaling == NF_ROPE_NTK) {
-        if (dim < 4) return NF_ERR_INVALID_ARG;
-        base *= std::pow(factor, dim / (dim - 2.0));
-        if (!std::isfinite(base)) return NF_ERR_INVALID_ARG;
-    }
+    if (scaling == NF_ROPE_NTK && (dim < 4 || !std::isfinite(base * std::pow(factor, dim / (dim - 2.0))))) return NF_ERR_INVALID_ARG;
     if (scaling == NF_ROPE_PARTS &&
         !(std::isfinite(length) && length > 0.0 && std::isfinite(low) && std::isfinite(high) && low >= 0.0 && low < high))
         return NF_ERR_INVALID_ARG;
+    Pair log_base = logarithm(base);
+    if (scaling == NF_ROPE_NTK) log_base = log_base + logarithm(factor) * static_cast<double>(dim) / static_cast<double>(dim - 2);
     for (int i = 0; i < dim / 2; ++i) {
-        double f = std::pow(base, -2.0 * i / dim);
-        if (scaling == NF_ROPE_LINEAR) f /= factor;
+        Pair f = exponential(log_base * (-2.0 * i) / static_cast<double>(dim));
+        if (scaling == NF_ROPE_LINEAR) f = f / factor;
         if (scaling == NF_ROPE_PARTS) {
-            const double turns = length * f / (2.0 * 3.14159265358979323846);
-            const double keep = std::fmin(std::fmax((turns - low) / (high - low), 0.0), 1.0);
-            f *= keep + (1.0 - keep) / factor;
+            const Pair keep = (f * length / two_pi() - low) / (Pair(high) - low), slow = f / factor;
+            if (keep.hi <= 0.0) f = slow;
+            else if (keep.hi < 1.0) f = slow + keep * (f - slow);
         }
         rates[i] = rate_of(f);
     }
