@@ -465,7 +465,8 @@ nf_status nf_token_logprob_bwd(void* dlogits, int64_t dstride, const void* logit
  * slower ones.  Strides are not negative.  The rows of an output are apart: in
  * the order of its strides, each dimension steps over the ones inside it.  An
  * output overlaps nothing but where it says so; sets whose rows lie between
- * one another's (the queries and keys of one projection) do not overlap.
+ * one another's (the queries and keys of one projection) do not overlap.  Sets
+ * of three strides each that 256 steps do not tell apart count as overlapping.
  * batch * tokens * heads, over all sets of a call, is below 2^31.  Types:
  * NF_BF16 and NF_F32, one for a call, its weights included.                   */
 #define NF_HEAD_MAX_DIM 512

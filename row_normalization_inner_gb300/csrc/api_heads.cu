@@ -2,6 +2,7 @@
 // As in api.cu, every argument is checked before anything is launched.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <utility>
@@ -47,26 +48,57 @@ bool same(const Region& a, const Region& b) {
     return true;
 }
 
-// Whether two sets share no byte, as far as one step of a common stride tells:
-// their extents are apart; or both step by the same stride in a dimension, every
-// dimension outside steps by whole multiples of it, and within one step the
-// extents of what is inside are apart.
+// Whether two sets share a byte.  A row of b begins `at` bytes behind one of a, at = the
+// distance of their bases and so many of every stride: of b's forwards, of a's back.
+// The strides are gone through from the largest to the smallest, each only as often
+// as what is left of them can make up for; for sets of rows that are apart that is a few times, and
+// where it is not, `tries` run out and the sets are taken to overlap.
+struct Meeting {
+    struct Step {
+        Wide by, least, most;  // so many of it
+        Wide low, high;        // what the steps behind this one come to
+    };
+    Step steps[6];
+    int n = 0, tries = 256;
+    Wide first, last;  // the distances at which two rows share a byte
+
+    Meeting(const Region& a, const Region& b) : first(1 - static_cast<Wide>(b.inner)), last(static_cast<Wide>(a.inner) - 1) {
+        for (int d = 0; d < 3; ++d) {
+            if (a.stride[d]) add(a.stride[d], 1 - static_cast<Wide>(a.n[d]), 0);
+            if (b.stride[d]) add(b.stride[d], 0, static_cast<Wide>(b.n[d]) - 1);
+        }
+        std::sort(steps, steps + n, [](const Step& x, const Step& y) { return x.by > y.by; });
+        Wide low = 0, high = 0;
+        for (int i = n - 1; i >= 0; --i) {
+            steps[i].low = low, steps[i].high = high;
+            low += steps[i].by * steps[i].least, high += steps[i].by * steps[i].most;
+        }
+    }
+    void add(Wide by, Wide least, Wide most) {  // a stride that both have is one step
+        for (int i = 0; i < n; ++i)
+            if (steps[i].by == by) {
+                steps[i].least += least, steps[i].most += most;
+                return;
+            }
+        steps[n++] = {by, least, most, 0, 0};
+    }
+    static Wide down(Wide x, Wide by) { return x >= 0 ? x / by : -((by - 1 - x) / by); }
+    bool at(Wide distance, int i = 0) {
+        if (i == n) return first <= distance && distance <= last;
+        const Step& s = steps[i];
+        Wide from = -down(distance + s.high - first, s.by), to = down(last - s.low - distance, s.by);
+        if (from < s.least) from = s.least;
+        if (to > s.most) to = s.most;
+        for (Wide k = from; k <= to; ++k)
+            if (--tries < 0 || at(distance + k * s.by, i + 1)) return true;
+        return false;
+    }
+};
 bool apart(const Region& a, const Region& b) {
     if (!a.base || !b.base) return true;
     const Wide delta = static_cast<Wide>(b.base) - static_cast<Wide>(a.base);
     if (delta >= a.extent(0) || -delta >= b.extent(0)) return true;
-    for (int d = 0; d < 3; ++d) {
-        const int64_t step = a.stride[d] ? a.stride[d] : b.stride[d];
-        if (step == 0 || (a.stride[d] && b.stride[d] && a.stride[d] != b.stride[d])) continue;
-        bool whole = true;
-        for (int o = 0; o < d; ++o) whole = whole && a.stride[o] % step == 0 && b.stride[o] % step == 0;
-        if (!whole) continue;
-        Wide at = delta % step;
-        if (at < 0) at += step;
-        const Wide ea = a.extent(d + 1), eb = b.extent(d + 1);
-        if (at >= ea && at + eb <= step) return true;
-    }
-    return false;
+    return !Meeting(a, b).at(delta);
 }
 
 // Whether an output's own rows are apart: in the order of the strides, each
