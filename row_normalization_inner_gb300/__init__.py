@@ -765,8 +765,9 @@ def rope_fwd(q, k, positions, rates, layout: str = "half", magnitude: float = 1.
     need no copy); k may be None.  positions: int32 or int64, [batch, tokens] or
     [tokens].  rates: rope_rates' (2 * len(rates) elements of a head are
     turned, the rest left as they are).  layout: a pair is elements i and
-    i + len(rates) ("half") or 2i and 2i + 1 ("interleaved").  q_out may be q;
-    outputs made here are parts of one allocation."""
+    i + len(rates) ("half") or 2i and 2i + 1 ("interleaved").  q_out may be q.
+    Outputs made here of up to 32 MB together are parts of one allocation, which
+    lives as long as either of them; give q_out and k_out to hold them apart."""
     if stream is not None:
         return _on(stream, rope_fwd, q, k, positions, rates, layout, magnitude, q_out, k_out)
     return _result((_native or _helpers()).rope(q, k, positions, rates, layout, magnitude, q_out, k_out, False),
@@ -775,7 +776,8 @@ def rope_fwd(q, k, positions, rates, layout: str = "half", magnitude: float = 1.
 
 def rope_bwd(dq_out, dk_out, positions, rates, layout: str = "half", magnitude: float = 1.0, dq=None, dk=None,
              stream=None):
-    """Gradient of rope_fwd for q and k: (dq, dk), given that of its outputs.  dq may be dq_out."""
+    """Gradient of rope_fwd for q and k: (dq, dk), given that of its outputs.
+    dq may be dq_out; their memory as rope_fwd's outputs'."""
     if stream is not None:
         return _on(stream, rope_bwd, dq_out, dk_out, positions, rates, layout, magnitude, dq, dk)
     return _result((_native or _helpers()).rope(dq_out, dk_out, positions, rates, layout, magnitude, dq, dk, True),
@@ -787,7 +789,8 @@ def qk_rmsnorm_rope_fwd(q, k, q_weight, k_weight, positions=None, rates=None, ep
     """RMSNorm of each query and key head (weights [head_dim], one for all
     heads of a kind), turned by the tokens' positions in the same pass (rates
     None: not turned).  Returns (q_out, k_out).  Tensors as for rope_fwd, the
-    weights of their type; k and k_weight may be None; q_out may be q."""
+    weights of their type; k and k_weight may be None; q_out may be q.  The
+    outputs' memory as rope_fwd's."""
     if stream is not None:
         return _on(stream, qk_rmsnorm_rope_fwd, q, k, q_weight, k_weight, positions, rates, eps, layout, magnitude,
                    q_out, k_out)
@@ -800,7 +803,8 @@ def qk_rmsnorm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, positions=None
                         stream=None):
     """Gradient of qk_rmsnorm_rope_fwd, given that of its outputs and its
     inputs: (dq, dk, dq_weight, dk_weight), the weights' in fp32.  dq may be
-    dq_out or q.  The workspace (nf_qk_rmsnorm_rope_bwd_workspace_size bytes)
+    dq_out or q.  The memory of dq and dk as rope_fwd's outputs', the weights'
+    gradients in one allocation.  The workspace (nf_qk_rmsnorm_rope_bwd_workspace_size bytes)
     is allocated here when not given."""
     if stream is not None:
         return _on(stream, qk_rmsnorm_rope_bwd, dq_out, dk_out, q, k, q_weight, k_weight, positions, rates, eps, layout,
