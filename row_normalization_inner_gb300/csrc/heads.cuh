@@ -97,10 +97,9 @@ __device__ __forceinline__ float2 turn_of(uint64_t rate, int64_t position, float
     constexpr double h = 1.57079632679489661923, h2 = h * h, h3 = h * h2, h4 = h2 * h2;
     constexpr float first = static_cast<float>(h), rest = static_cast<float>(h - static_cast<double>(first));
     const uint64_t angle = rate * static_cast<uint64_t>(position);
-    const uint32_t upper = static_cast<uint32_t>((angle + (1ull << 31)) >> 32);
-    const int32_t lower = static_cast<int32_t>(static_cast<uint32_t>(angle));
-    const uint32_t quarter = (upper + (1u << 29)) >> 30;
-    const float x = fmaf(static_cast<float>(lower), 0x1p-62f, static_cast<float>(static_cast<int32_t>(upper - (quarter << 30))) * 0x1p-30f), z = x * x;
+    const uint32_t upper = static_cast<uint32_t>((angle + (1ull << 31)) >> 32), quarter = (upper + (1u << 29)) >> 30;
+    const int32_t rest_of_upper = static_cast<int32_t>(upper << 2), lower = static_cast<int32_t>(static_cast<uint32_t>(angle));
+    const float x = fmaf(static_cast<float>(lower), 0x1p-62f, static_cast<float>(rest_of_upper) * 0x1p-32f), z = x * x;
     float s = static_cast<float>(h4 * h4 * h / 362880);
     s = fmaf(s, z, static_cast<float>(-h3 * h4 / 5040));
     s = fmaf(s, z, static_cast<float>(h * h4 / 120));
