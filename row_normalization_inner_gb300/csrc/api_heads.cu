@@ -28,9 +28,9 @@ struct Region {
     int64_t n[3];       // sizes, outer first
     int64_t stride[3];  // in bytes; 0 for dimensions of one
     int64_t inner;
-    Wide extent(int from) const {
+    Wide extent() const {
         Wide e = inner;
-        for (int i = from; i < 3; ++i) e += static_cast<Wide>(n[i] - 1) * stride[i];
+        for (int i = 0; i < 3; ++i) e += static_cast<Wide>(n[i] - 1) * stride[i];
         return e;
     }
 };
@@ -51,8 +51,9 @@ bool same(const Region& a, const Region& b) {
 // Whether two sets share a byte.  A row of b begins `at` bytes behind one of a, at = the
 // distance of their bases and so many of every stride: of b's forwards, of a's back.
 // The strides are gone through from the largest to the smallest, each only as often
-// as what is left of them can make up for; for sets of rows that are apart that is a few times, and
-// where it is not, `tries` run out and the sets are taken to overlap.
+// as what is left of them can make up for.  For sets whose rows do not share bytes
+// among themselves that is a few times; where it is not, `tries` run out and the
+// sets are taken to overlap.
 struct Meeting {
     struct Step {
         Wide by, least, most;  // so many of it
@@ -94,11 +95,23 @@ struct Meeting {
         return false;
     }
 };
-bool apart(const Region& a, const Region& b) {
-    if (!a.base || !b.base) return true;
+
+__attribute__((noinline)) bool meet(const Region& a, const Region& b) {
     const Wide delta = static_cast<Wide>(b.base) - static_cast<Wide>(a.base);
-    if (delta >= a.extent(0) || -delta >= b.extent(0)) return true;
-    return !Meeting(a, b).at(delta);
+    // Mostly (queries beside keys in one buffer) a stride that both have says it at once: within one step of it, what the
+    // strides that are no whole multiples of it cover is apart.  (The checks of a rotation in place 0.2 us so, 0.8 without.)
+    for (int d = 0; d < 3; ++d) {
+        const int64_t step = a.stride[d];
+        if (step == 0 || step != b.stride[d] || delta <= -step || delta >= step) continue;
+        Wide ea = a.inner, eb = b.inner;
+        for (int o = 0; o < 3; ++o) {
+            if (a.stride[o] >= step ? a.stride[o] % step : 1) ea += static_cast<Wide>(a.n[o] - 1) * a.stride[o];
+            if (b.stride[o] >= step ? b.stride[o] % step : 1) eb += static_cast<Wide>(b.n[o] - 1) * b.stride[o];
+        }
+        const Wide at = delta < 0 ? delta + step : delta;
+        if (at >= ea && at + eb <= step) return false;
+    }
+    return Meeting(a, b).at(delta);
 }
 
 // Whether an output's own rows are apart: in the order of the strides, each
@@ -123,12 +136,14 @@ struct Regions {
     Region r[kMost];
     bool out[kMost];
     int own[kMost];  // an input that the output may be, or the output it may stand for
+    Wide behind[kMost];  // the first address behind it
     int n = 0;
     // `twin`: outputs and inputs of the same twin may be one another
     void add(const Region& x, bool is_out, int twin = 0) {
         if (!x.base) return;
         r[n] = x;
         out[n] = is_out;
+        behind[n] = x.base + x.extent();
         own[n++] = twin;
     }
     bool sound() const {
@@ -136,9 +151,9 @@ struct Regions {
             if (!out[i]) continue;
             if (!rows_apart(r[i])) return false;
             for (int j = 0; j < n; ++j) {
-                if (j == i || (out[j] && j < i) || apart(r[i], r[j])) continue;
+                if (j == i || (out[j] && j < i) || r[j].base >= behind[i] || r[i].base >= behind[j]) continue;
                 if (!out[j] && own[i] && own[i] == own[j] && same(r[i], r[j])) continue;
-                return false;
+                if (meet(r[i], r[j])) return false;
             }
         }
         return true;
