@@ -1,9 +1,9 @@
 // What the kernels on attention heads share: the lanes' vectors of a row, and
 // the angles.
 //
-// A row is one head of one token, `dim` elements.  A group of G lanes (a power
-// of two) holds it, each lane two 16-byte vectors a and b, chosen so that a
-// lane can turn its elements without another's:
+// A row is one head of one token, `dim` elements.  A group of G lanes (of which
+// sizes, stands at the end of this file) holds it, each lane two 16-byte vectors a
+// and b, chosen so that a lane can turn its elements without another's:
 //   half layout (pairs i, i + pairs):  a = elements j W.., b = pairs + j W..
 //     for lane j below pairs / W, then the elements behind the rotated ones,
 //     two vectors to a lane;

@@ -660,7 +660,7 @@ cudaError_t launch_rows(const HeadsArgs& a, int passes, int G, dim3 grid, dim3 b
     return launch_args(heads_rows<T, INTER, CACHE, GT, 4, kSeveralTokens>, grid, block, smem, st, a, G);
 }
 
-// The head sizes with kernels of their own: 64, 80, 96, 112, 128, 192 and 256.
+// The head sizes with kernels of their own: 64, 80, 96, 112 and 128, in bf16 192 and 256 too.
 template <typename T, bool INTER, int CACHE>
 cudaError_t launch_lanes(const HeadsArgs& a, int passes, int lanes, dim3 grid, dim3 block, size_t smem, cudaStream_t st) {
     const int own = own_lanes<Elem<T, INTER>::W>(a.dim);
