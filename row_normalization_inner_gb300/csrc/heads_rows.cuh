@@ -7,8 +7,8 @@
 //   scale = max(max|y| / Q, 2^-100), q = y / scale rounded to nearest
 //
 // Bound by memory: each element is read once and written once (16384 tokens of
-// 64 + 8 heads of 128 in bf16: turned 89.6 us, 6.74 TB/s, a copy's rate; normalized
-// too 97.4 us, 6.2 TB/s).  A group of lanes holds a row (heads.cuh), so that its
+// 64 + 8 heads of 128 in bf16: turned 89.0 us, 6.8 TB/s, a copy's rate; normalized
+// too 96.5 us, 6.3 TB/s).  A group of lanes holds a row (heads.cuh), so that its
 // sums stay in the warp; a warp has four rows of every group in flight.  What it
 // does before them -- its share, addresses, angles, weights -- is a good half of
 // its instructions and the reason for most of what follows: the angles are
